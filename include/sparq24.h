@@ -362,6 +362,100 @@ sparq24_status sparq24_fp8_gemm(const uint8_t* a, const float* scale_a, int64_t 
                                 const uint8_t* b, const float* scale_b, int64_t n, int64_t k,
                                 float* c, hipStream_t stream);
 
+/* The dense INT8 side's GEMM [PD §2, §3: INT8 with one scale per row]: c
+ * [M][N] = (sum_k a[m][k] b[n][k]) * scale_a[m] * scale_b[n] (+ bias[n]) with a
+ * [M][K] and b [N][K] the int8 codes and per-row scales of sparq24_quantize
+ * (INT, at most 8 bits): one scale per token and one per output channel.  The
+ * sums are int32 and exact (codes of -128 too), so no order or split of K
+ * changes a bit; then one rounding to fp32, the two fp32 scale multiplies in
+ * that order, the bias add (fp32 [N], or NULL for none) and one rounding to
+ * c_dtype (sparq24_dtype).  lda and ldb are the bytes between rows (a multiple
+ * of 16 where there is more than one row, at least K), ldc the elements
+ * between rows of c (at least N).  a, b, c 16-byte aligned; scales and bias
+ * 4-byte.  K % 16 == 0 and K <= SPARQ24_MAX_INT8_K (SHAPE); K == 0 gives the
+ * bias or zeros.  Any M and N (M <= 64 streams b once, larger M runs MFMA
+ * tiles).  Workspace protocol as above. */
+#define SPARQ24_MAX_INT8_K 131056
+sparq24_status sparq24_int8_gemm(const int8_t* a, int64_t lda, const float* scale_a, int64_t m,
+                                 const int8_t* b, int64_t ldb, const float* scale_b, int64_t n,
+                                 int64_t k, const float* bias, int32_t c_dtype, void* c,
+                                 int64_t ldc, void* ws, size_t* ws_bytes, hipStream_t stream);
+
+/* Paged 8-bit key/value cache: the quantized storage of attention's K and V
+ * [PD §1, §2: K and V are operands produced online], one scale per block of
+ * tokens and kv head.
+ *   k: codes [blocks][heads][tokens][dim], v: codes [blocks][heads][dim][tokens]
+ *   (each reduction of attention, q.k along dim and p.v along the tokens, is
+ *   contiguous), k_scale and v_scale: fp32 [blocks][heads].
+ * fmt: SPARQ24_Q_INT (8 bits: int8, qmax 127) or SPARQ24_Q_FP8_E4M3 (qmax 448).
+ * tokens: a power of two, 16..256; dim: 64, 128, 192 or 256; blocks >= 1. */
+typedef struct {
+  void* k;
+  float* k_scale;
+  void* v;
+  float* v_scale;
+  int32_t fmt;
+  int64_t blocks, heads, tokens, dim;
+} sparq24_kvcache;
+
+/* The sequences of one call.  Sequence b has seq_lens[b] tokens in the cache,
+ * the call's new tokens included as its last ones; position p of it lives in
+ * block block_table[b * table_stride + p / tokens].  The call's token rows
+ * (new keys and values, or queries) are [total]: rows cu_tokens[b] ..
+ * cu_tokens[b + 1] - 1 belong to sequence b (device int32 [seqs + 1],
+ * ascending), or total / seqs rows each where cu_tokens is NULL.  Sequences
+ * may have no rows or no tokens.  Positions at or past max_blocks * tokens (or
+ * 2^31 - 256) and entries outside 0 .. blocks - 1 name no storage: nothing is
+ * written there and attention sees no token there.  All arrays are device int32. */
+typedef struct {
+  const int32_t* block_table;
+  int64_t max_blocks, table_stride;
+  const int32_t* seq_lens;
+  const int32_t* cu_tokens;
+  int64_t seqs, total;
+} sparq24_kvseqs;
+
+/* Appends token rows to the cache.  k and v: batch = total tokens, rows = kv
+ * heads, k = dim (any batch and row strides, k_stride 1), fp32, bf16 or fp16,
+ * both of one type.  The i-th of a sequence's n rows becomes position
+ * seq_lens[b] - n + i.  Per touched block and head, with amax the largest
+ * |element| that the block receives (NaN left out): cand = fp32(amax / qmax),
+ * 0 where amax < 2^-64; the new scale s is cand where the block's first token
+ * is among the new ones, else max(old scale, cand); new codes are
+ * encode(fp32(x * fp32(1 / s))) (nearest even, saturating; NaN as 0); where s
+ * grew, the codes before the new ones become encode(fp32(code * fp32(old *
+ * fp32(1 / s)))), otherwise they stay.  Codes behind the last new token stay
+ * as they are.  Calling it again with the same arguments changes nothing.  A
+ * block must receive tokens of one sequence only in a call (else its codes
+ * and scale are unspecified, those of other blocks are not). */
+sparq24_status sparq24_kv_append(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs,
+                                 const sparq24_tensor* k, const sparq24_tensor* v,
+                                 hipStream_t stream);
+
+/* Attention of query rows over the cached tokens.  q: batch = total tokens,
+ * rows = query heads (a multiple of the kv heads; query head h reads kv head
+ * h / (rows / heads)), k = dim, bf16 or fp16, any batch and row strides.  The
+ * i-th of a sequence's n query tokens is at position seq_lens[b] - n + i.
+ * With s_t = scale * <q, K_t>, K_t and V_t the stored codes times their block's
+ * scale, out = sum_t exp(s_t) V_t / sum_t exp(s_t) over the visible tokens t:
+ * all of the sequence, or with causal = 1 those up to the query's position,
+ * and of these the last `window` ones where window > 0 (needs causal).
+ * out [total][query heads][dim] in q's type; lse [total][query heads] fp32 (or
+ * NULL) receives log sum_t exp(s_t).  A row that sees no token gets zeros and
+ * -inf.  Rows of out and lse that belong to no sequence stay as they are.
+ * What is stored in no visible place (behind a sequence, before its window)
+ * does not reach the result, whatever its bits; a visible e4m3 NaN code gives
+ * NaN.  scale: finite, > 0.  Block scales: 0, or 2^-80 and above.
+ * Arithmetic: codes and queries enter fp16 MFMAs exactly, the weights exp(s_t)
+ * are rounded to fp16 (2^-11), all sums, maxima and scores are fp32.
+ * Workspace: partial results of sequences that are split along their tokens,
+ * none where max_blocks * tokens <= 256.  Concurrent calls, and graphs that may
+ * replay at the same time, need workspaces of their own. */
+sparq24_status sparq24_kv_attention(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs,
+                                    const sparq24_tensor* q, float scale, int32_t causal,
+                                    int64_t window, void* out, float* lse, void* ws,
+                                    size_t* ws_bytes, hipStream_t stream);
+
 /* Wanda's input-channel norms [PD §2]: norms[k] = fp32(sqrt(sum over all
  * (b, r) of x[b][r][k]^2)), the sum in fp64 (fixed order), the square root in
  * fp64, then rounded once.  x is an activation [tokens, channels] given with

@@ -6,6 +6,7 @@ ABI, see ``include/sparq24.h``); :mod:`.binding` marshals torch tensors into
 it.  Build with ``python -m pruning_quantization_amd.build``.
 """
 from .binding import (  # noqa: F401
+    KVCache,
     Sparq24Error,
     SYMBOLS,
     bits_per_element,
@@ -16,6 +17,10 @@ from .binding import (  # noqa: F401
     error_energy,
     fp8_gemm,
     hadamard,
+    int8_gemm,
+    kv_append,
+    kv_attention,
+    kv_cache,
     lib,
     operator_error,
     predict_R,

@@ -14,8 +14,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_double, c_int32, c_int64, c_size_t, c_uint8, c_void_p
-from typing import Optional, Sequence, Tuple, Union
+from ctypes import POINTER, c_double, c_float, c_int32, c_int64, c_size_t, c_uint8, c_void_p
+from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -49,6 +49,18 @@ class CSide(ctypes.Structure):
     _fields_ = [("pattern", c_int32), ("q", CQSpec)]
 
 
+class CKvCache(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("k_scale", c_void_p), ("v", c_void_p), ("v_scale", c_void_p),
+                ("fmt", c_int32), ("blocks", c_int64), ("heads", c_int64), ("tokens", c_int64),
+                ("dim", c_int64)]
+
+
+class CKvSeqs(ctypes.Structure):
+    _fields_ = [("block_table", c_void_p), ("max_blocks", c_int64), ("table_stride", c_int64),
+                ("seq_lens", c_void_p), ("cu_tokens", c_void_p), ("seqs", c_int64),
+                ("total", c_int64)]
+
+
 #: Every symbol the C header declares.
 SYMBOLS = ("sparq24_prune_compress", "sparq24_quantize", "sparq24_prune_quantize",
            "sparq24_error_energy", "sparq24_predict_R", "sparq24_col_l2norm", "sparq24_copy",
@@ -57,7 +69,8 @@ SYMBOLS = ("sparq24_prune_compress", "sparq24_quantize", "sparq24_prune_quantize
            "sparq24_prune_quantize_rot", "sparq24_predict_R_rot", "sparq24_operator_error",
            "sparq24_sparse_gemm", "sparq24_dense_gemm", "sparq24_fp8_gemm",
            "sparq24_bits_per_element", "sparq24_status_string", "sparq24_version",
-           "sparq24_predict_R_noalloc")
+           "sparq24_predict_R_noalloc", "sparq24_int8_gemm", "sparq24_kv_append",
+           "sparq24_kv_attention")
 
 _lib = None
 
@@ -97,6 +110,12 @@ def lib(path: Optional[str] = None):
         "sparq24_dense_gemm": [T, T, c_void_p, c_void_p],
         "sparq24_fp8_gemm": [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_int64,
                              c_void_p, c_void_p],
+        "sparq24_int8_gemm": [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                              c_int64, c_int64, c_void_p, c_int32, c_void_p, c_int64, c_void_p,
+                              POINTER(c_size_t), c_void_p],
+        "sparq24_kv_append": [POINTER(CKvCache), POINTER(CKvSeqs), T, T, c_void_p],
+        "sparq24_kv_attention": [POINTER(CKvCache), POINTER(CKvSeqs), T, c_float, c_int32, c_int64,
+                                 c_void_p, c_void_p, c_void_p, POINTER(c_size_t), c_void_p],
         "sparq24_quantize_rot": [T, c_int32, Q, c_void_p, c_void_p, c_void_p, c_void_p,
                                  POINTER(c_size_t), c_void_p],
         "sparq24_prune_quantize_rot": [T, c_int32, c_int32, Q, c_void_p, c_void_p, c_void_p,
@@ -623,6 +642,207 @@ def fp8_gemm(codes_a: torch.Tensor, scale_a: torch.Tensor, codes_b: torch.Tensor
                                 scale_b.data_ptr(), n, k, out.data_ptr(), _stream(codes_a))
     _check("sparq24_fp8_gemm", st)
     return out
+
+
+def _on_device(*ts: Optional[torch.Tensor]):
+    """Checks that all tensors are on one GPU and returns it."""
+    dev = ts[0].device
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {dev}")
+    return dev
+
+
+def _call(fn: str, dev: torch.device, *args) -> None:
+    """Calls ``fn`` with the device's current stream, that device current."""
+    f = getattr(lib(), fn)
+    if dev.index == torch.cuda.current_device():
+        st = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    _check(fn, st)
+
+
+def _vector(t: torch.Tensor, n: int, dtype: torch.dtype, name: str) -> int:
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} with {n} elements, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def int8_gemm(codes_a: torch.Tensor, scale_a: torch.Tensor, codes_b: torch.Tensor,
+              scale_b: torch.Tensor, bias: Optional[torch.Tensor] = None,
+              dtype: torch.dtype = torch.float32,
+              out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C = diag(scale_a) (A B^T) diag(scale_b) (+ bias) from int8 codes
+    [..., K], [N, K] and per-row scales of :func:`quantize` (INT, at most 8
+    bits), exact int32 sums -> ``dtype`` (fp32, bf16 or fp16) [..., N].  K is a
+    multiple of 16; the rows of either operand and of ``out`` may be strided;
+    ``bias`` is fp32 [N]."""
+    dev = _on_device(codes_a, scale_a, codes_b, scale_b, bias, out)
+    if codes_a.dtype != torch.int8 or codes_b.dtype != torch.int8:
+        raise TypeError(f"int8 codes expected, got {codes_a.dtype} and {codes_b.dtype}")
+    if codes_b.dim() != 2 or codes_a.dim() < 1 or codes_a.shape[-1] != codes_b.shape[1]:
+        raise ValueError(f"shapes {tuple(codes_a.shape)} and {tuple(codes_b.shape)} do not multiply")
+    n, k = codes_b.shape
+    a = codes_a if codes_a.dim() == 2 else codes_a.view(-1, k)
+    m = a.shape[0]
+    if k > 1 and ((m and a.stride(1) != 1) or (n and codes_b.stride(1) != 1)):
+        raise ValueError("codes must be contiguous along K")
+    if out is None:
+        out = torch.empty(*codes_a.shape[:-1], n, dtype=dtype, device=dev)
+    elif out.shape != (*codes_a.shape[:-1], n):
+        raise ValueError(f"out has shape {tuple(out.shape)}")
+    if out.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {out.dtype}")
+    c = out if out.dim() == 2 else out.view(-1, n)
+    if n > 1 and m and c.stride(1) != 1:
+        raise ValueError("out must be contiguous along N")
+    _call("sparq24_int8_gemm", dev, a.data_ptr(), a.stride(0),
+          _vector(scale_a, m, torch.float32, "scale_a"), m, codes_b.data_ptr(), codes_b.stride(0),
+          _vector(scale_b, n, torch.float32, "scale_b"), n, k,
+          None if bias is None else _vector(bias, n, torch.float32, "bias"), _DT[out.dtype],
+          c.data_ptr(), c.stride(0), None, None)
+    return out
+
+
+class KVCache(NamedTuple):
+    """Paged 8-bit key/value cache: ``k`` codes [blocks, kv heads, tokens, dim],
+    ``v`` codes [blocks, kv heads, dim, tokens] (int8, or e4m3 as uint8) and one
+    fp32 scale per block and kv head for each.  :func:`kv_cache` allocates one."""
+
+    k: torch.Tensor
+    k_scale: torch.Tensor
+    v: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def kv_cache(blocks: int, heads: int, dim: int, tokens: int = 64, q: QLike = ("int", 8),
+             device: Union[str, torch.device] = "cuda") -> KVCache:
+    """An empty cache pool of ``blocks`` blocks of ``tokens`` tokens (a power of
+    two, 16..256) in INT8 or FP8 (``q``: ("int", 8) or "fp8")."""
+    qs = qspec(q)
+    if qs.fmt not in (Q_INT, Q_FP8) or (qs.fmt == Q_INT and qs.bits != 8):
+        raise ValueError("a cache holds ('int', 8) or 'fp8' codes")
+    dt = torch.int8 if qs.fmt == Q_INT else torch.uint8
+    return KVCache(torch.zeros(blocks, heads, tokens, dim, dtype=dt, device=device),
+                   torch.zeros(blocks, heads, dtype=torch.float32, device=device),
+                   torch.zeros(blocks, heads, dim, tokens, dtype=dt, device=device),
+                   torch.zeros(blocks, heads, dtype=torch.float32, device=device))
+
+
+def _c_cache(cache: KVCache) -> CKvCache:
+    k, ks, v, vs = cache
+    if k.dim() != 4 or v.dim() != 4:
+        raise ValueError("cache codes must be [blocks, heads, tokens, dim] and [blocks, heads, dim, tokens]")
+    blocks, heads, tokens, dim = k.shape
+    if v.shape != (blocks, heads, dim, tokens) or k.dtype != v.dtype:
+        raise ValueError(f"cache codes {tuple(k.shape)} {k.dtype} and {tuple(v.shape)} {v.dtype} do not match")
+    if k.dtype not in (torch.int8, torch.uint8):
+        raise TypeError(f"cache codes are int8 or uint8 (e4m3), got {k.dtype}")
+    if not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("cache codes must be contiguous")
+    n = blocks * heads
+    return CKvCache(k.data_ptr(), _vector(ks, n, torch.float32, "k_scale"), v.data_ptr(),
+                    _vector(vs, n, torch.float32, "v_scale"),
+                    Q_INT if k.dtype == torch.int8 else Q_FP8, blocks, heads, tokens, dim)
+
+
+def _c_seqs(x: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+            cu_tokens: Optional[torch.Tensor]) -> CKvSeqs:
+    """Sequences of the token rows ``x``: [total, heads, dim] with ``cu_tokens``,
+    or [seqs, n, heads, dim]."""
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or (
+            block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [seqs, max blocks] with contiguous rows")
+    seqs, width = block_table.shape
+    if cu_tokens is None:
+        if x.dim() != 4 or x.shape[0] != seqs:
+            raise ValueError(f"without cu_tokens token rows are [seqs, n, heads, dim], got {tuple(x.shape)}")
+        total = seqs * x.shape[1]
+    else:
+        if x.dim() != 3:
+            raise ValueError(f"with cu_tokens token rows are [total, heads, dim], got {tuple(x.shape)}")
+        total = x.shape[0]
+    return CKvSeqs(block_table.data_ptr() if width else None, width, block_table.stride(0),
+                   _vector(seq_lens, seqs, torch.int32, "seq_lens"),
+                   None if cu_tokens is None else _vector(cu_tokens, seqs + 1, torch.int32, "cu_tokens"),
+                   seqs, total)
+
+
+def _c_rows(x: torch.Tensor) -> CTensor:
+    """Descriptor of token rows: one batch entry per token."""
+    if x.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    if x.dim() == 4:
+        a, n = x.shape[:2]
+        if a > 1 and n > 1 and x.stride(0) != n * x.stride(1):
+            raise ValueError("the sequences of token rows must be evenly spaced (or contiguous)")
+        total, ts = a * n, x.stride(1) if n > 1 else x.stride(0)
+    else:
+        total, ts = x.shape[0], x.stride(0)
+    heads, dim = x.shape[-2:]
+    if dim > 1 and x.stride(-1) != 1:
+        raise ValueError("token rows must be contiguous along dim")
+    return CTensor(x.data_ptr(), _DT[x.dtype], total, heads, dim, ts, x.stride(-2), 1)
+
+
+def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
+              seq_lens: torch.Tensor, cu_tokens: Optional[torch.Tensor] = None) -> None:
+    """Quantizes new key and value rows into ``cache``, in place.
+
+    ``k`` and ``v`` are [seqs, n, kv heads, dim], or [total, kv heads, dim] with
+    int32 offsets ``cu_tokens`` [seqs + 1]; ``seq_lens`` int32 [seqs] counts the
+    tokens of each sequence with the new ones included, so the new rows become
+    its last positions; position p lives in block ``block_table[b, p // tokens]``
+    (int32).  A block's scale grows when a new element exceeds it, and the
+    block's earlier codes are then coded again."""
+    dev = _on_device(k, v, block_table, seq_lens, cu_tokens, *cache)
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError(f"k {tuple(k.shape)} {k.dtype} and v {tuple(v.shape)} {v.dtype} do not match")
+    c, q = _c_cache(cache), _c_seqs(k, block_table, seq_lens, cu_tokens)
+    _call("sparq24_kv_append", dev, c, q, _c_rows(k), _c_rows(v))
+
+
+def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
+                 seq_lens: torch.Tensor, cu_tokens: Optional[torch.Tensor] = None,
+                 scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                 return_lse: bool = False, out: Optional[torch.Tensor] = None,
+                 lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Attention of query rows over the cached tokens -> out in q's type and
+    shape, or (out, lse) with ``return_lse``.
+
+    ``q`` (bf16 or fp16) is [seqs, n, heads, dim], or [total, heads, dim] with
+    ``cu_tokens``; heads is a multiple of the cache's kv heads; the other
+    arguments are those of :func:`kv_append`, whose tokens are visible: a
+    sequence's n queries sit at its last n positions.  ``causal``: a query sees
+    the tokens up to its own; ``window`` > 0: the last ``window`` of these.
+    ``scale`` defaults to dim ** -0.5.  A row that sees nothing gives zeros and
+    an lse of -inf."""
+    dev = _on_device(q, block_table, seq_lens, cu_tokens, out, lse, workspace, *cache)
+    c, s, x = _c_cache(cache), _c_seqs(q, block_table, seq_lens, cu_tokens), _c_rows(q)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape and type")
+    if lse is None:
+        if return_lse:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+    elif lse.shape != q.shape[:-1] or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 of q's shape without dim")
+    args = (c, s, x, q.shape[-1] ** -0.5 if scale is None else float(scale), int(bool(causal)),
+            int(window), out.data_ptr(), _ptr(lse))
+    if workspace is None:
+        n = c_size_t(0)
+        _call("sparq24_kv_attention", dev, *args, None, n)
+        ws = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
+    else:
+        ws, n = workspace, c_size_t(workspace.numel() * workspace.element_size())
+    _call("sparq24_kv_attention", dev, *args, _ptr(ws), n if ws is not None else None)
+    return (out, lse) if return_lse else out
 
 
 def col_l2norm(x: torch.Tensor, out: Optional[torch.Tensor] = None, workspace=None):

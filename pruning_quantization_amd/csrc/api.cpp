@@ -777,6 +777,146 @@ sparq24_status sparq24_fp8_gemm(const uint8_t* a, const float* scale_a, int64_t 
   return launched(launch_fp8_gemm(a, k, scale_a, m, k, b, k, scale_b, n, c, n, stream));
 }
 
+sparq24_status sparq24_int8_gemm(const int8_t* a, int64_t lda, const float* scale_a, int64_t m,
+                                 const int8_t* b, int64_t ldb, const float* scale_b, int64_t n,
+                                 int64_t k, const float* bias, int32_t c_dtype, void* c,
+                                 int64_t ldc, void* ws, size_t* ws_bytes, hipStream_t stream) {
+  if (m < 0 || n < 0 || k < 0) return SPARQ24_ERR_INVALID;
+  if (c_dtype != SPARQ24_F32 && c_dtype != SPARQ24_BF16 && c_dtype != SPARQ24_F16)
+    return SPARQ24_ERR_INVALID;
+  if (k % 16 || k > SPARQ24_MAX_INT8_K) return SPARQ24_ERR_SHAPE;
+  if (m > INT32_MAX || n > INT32_MAX) return SPARQ24_ERR_UNSUPPORTED;
+  if ((m > 1 && lda < k) || (n > 1 && ldb < k) || (m > 1 && ldc < n))
+    return SPARQ24_ERR_UNSUPPORTED;
+  if ((m > 1 && lda % 16) || (n > 1 && ldb % 16)) return SPARQ24_ERR_ALIGN;
+  const Int8Gemm g{a, b, m > 1 ? lda : k, n > 1 ? ldb : k, scale_a, scale_b, bias,
+                   m, n, k, c, m > 1 ? ldc : n, c_dtype};
+  bool query;
+  CHECK(workspace(ws, ws_bytes, 0, query));
+  if (query) return SPARQ24_OK;
+  if (m == 0 || n == 0) return SPARQ24_OK;
+  if (((m + 15) / 16) * ((n + 15) / 16) > INT32_MAX) return SPARQ24_ERR_UNSUPPORTED;
+  if ((k && (!a || !b)) || !scale_a || !scale_b || !c) return SPARQ24_ERR_INVALID;
+  if (!aligned16(a) || !aligned16(b) || !aligned16(c) || ((uintptr_t)scale_a & 3u) ||
+      ((uintptr_t)scale_b & 3u) || ((uintptr_t)bias & 3u))
+    return SPARQ24_ERR_ALIGN;
+  CHECK(device_ok());
+  return launched(launch_int8_gemm(g, stream));
+}
+
+namespace {
+// Cache and sequences of the kv calls.  empty: no token rows, nothing to do.
+sparq24_status check_kv(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs, KvCache& c,
+                        KvSeqs& q, bool& empty) {
+  if (!cache || !seqs) return SPARQ24_ERR_INVALID;
+  if (cache->fmt < SPARQ24_Q_NONE || cache->fmt > SPARQ24_Q_NVFP4) return SPARQ24_ERR_INVALID;
+  if (cache->fmt != SPARQ24_Q_INT && cache->fmt != SPARQ24_Q_FP8_E4M3) return SPARQ24_ERR_UNSUPPORTED;
+  if (cache->blocks < 0 || cache->heads < 0 || seqs->seqs < 0 || seqs->total < 0 ||
+      seqs->max_blocks < 0 || seqs->table_stride < 0)
+    return SPARQ24_ERR_INVALID;
+  const int64_t T = cache->tokens, D = cache->dim;
+  if (T < 16 || T > 256 || (T & (T - 1))) return SPARQ24_ERR_SHAPE;
+  if (D != 64 && D != 128 && D != 192 && D != 256) return SPARQ24_ERR_SHAPE;
+  if (cache->blocks < 1 || cache->heads < 1) return SPARQ24_ERR_SHAPE;
+  if (cache->blocks > INT32_MAX || cache->heads > 65535 || seqs->total > INT32_MAX ||
+      seqs->seqs > INT32_MAX / 2 / cache->heads || seqs->max_blocks > INT32_MAX)
+    return SPARQ24_ERR_UNSUPPORTED;
+  if (seqs->seqs > 1 && seqs->table_stride < seqs->max_blocks) return SPARQ24_ERR_UNSUPPORTED;
+  if (!seqs->cu_tokens && seqs->seqs && seqs->total % seqs->seqs) return SPARQ24_ERR_SHAPE;
+  empty = seqs->seqs == 0 || seqs->total == 0;
+  c = KvCache{(uint8_t*)cache->k, cache->k_scale, (uint8_t*)cache->v, cache->v_scale,
+              cache->blocks, (int)cache->heads, (int)D, __builtin_ctz((unsigned)T),
+              cache->fmt == SPARQ24_Q_FP8_E4M3};
+  const int64_t cap = seqs->max_blocks * T;
+  const int64_t most = INT32_MAX - 255;  // positions and tile ends are 32-bit in the kernels
+  q = KvSeqs{seqs->block_table, seqs->table_stride, cap < most ? cap : most,
+             seqs->seq_lens, seqs->cu_tokens, seqs->seqs, seqs->total,
+             seqs->seqs ? seqs->total / seqs->seqs : 0};
+  return SPARQ24_OK;
+}
+
+sparq24_status check_kv_pointers(const KvCache& c, const KvSeqs& q) {
+  if (!c.k || !c.ks || !c.v || !c.vs || !q.lens || (q.cap && !q.table)) return SPARQ24_ERR_INVALID;
+  if (!aligned16(c.k) || !aligned16(c.v) || ((uintptr_t)c.ks & 3u) || ((uintptr_t)c.vs & 3u) ||
+      ((uintptr_t)q.lens & 3u) || ((uintptr_t)q.table & 3u) || ((uintptr_t)q.cu & 3u))
+    return SPARQ24_ERR_ALIGN;
+  return SPARQ24_OK;
+}
+
+// Token rows [total][heads][dim]; ts, hs: bytes between tokens and heads.
+sparq24_status check_kv_rows(const sparq24_tensor* x, int64_t total, int64_t dim, int64_t& ts,
+                             int64_t& hs) {
+  if (!x) return SPARQ24_ERR_INVALID;
+  if (x->dtype != SPARQ24_F32 && x->dtype != SPARQ24_BF16 && x->dtype != SPARQ24_F16)
+    return SPARQ24_ERR_INVALID;
+  if (x->batch < 0 || x->rows < 0 || x->k < 0) return SPARQ24_ERR_INVALID;
+  if (x->batch_stride < 0 || x->row_stride < 0 || x->k_stride < 0) return SPARQ24_ERR_INVALID;
+  if (x->batch != total || x->k != dim) return SPARQ24_ERR_SHAPE;
+  if (x->k_stride != 1) return SPARQ24_ERR_UNSUPPORTED;
+  const int es = esize(x->dtype);
+  ts = total > 1 ? x->batch_stride * es : 0;
+  hs = x->rows > 1 ? x->row_stride * es : 0;
+  if (ts % 16 || hs % 16) return SPARQ24_ERR_ALIGN;
+  return SPARQ24_OK;
+}
+}  // namespace
+
+sparq24_status sparq24_kv_append(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs,
+                                 const sparq24_tensor* k, const sparq24_tensor* v,
+                                 hipStream_t stream) {
+  KvCache c;
+  KvSeqs q;
+  bool empty;
+  CHECK(check_kv(cache, seqs, c, q, empty));
+  KvRows kr, vr;
+  CHECK(check_kv_rows(k, q.total, c.dim, kr.ts, kr.hs));
+  CHECK(check_kv_rows(v, q.total, c.dim, vr.ts, vr.hs));
+  if (k->rows != c.heads || v->rows != c.heads) return SPARQ24_ERR_SHAPE;
+  if (k->dtype != v->dtype) return SPARQ24_ERR_UNSUPPORTED;
+  if (empty) return SPARQ24_OK;
+  if (q.total / (1 << c.tsh) + 2 * q.seqs > INT32_MAX) return SPARQ24_ERR_UNSUPPORTED;
+  CHECK(check_kv_pointers(c, q));
+  if (!k->data || !v->data) return SPARQ24_ERR_INVALID;
+  if (!aligned16(k->data) || !aligned16(v->data)) return SPARQ24_ERR_ALIGN;
+  kr.x = (const char*)k->data;
+  vr.x = (const char*)v->data;
+  CHECK(device_ok());
+  return launched(launch_kv_append(c, q, kr, vr, k->dtype, stream));
+}
+
+sparq24_status sparq24_kv_attention(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs,
+                                    const sparq24_tensor* q, float scale, int32_t causal,
+                                    int64_t window, void* out, float* lse, void* ws,
+                                    size_t* ws_bytes, hipStream_t stream) {
+  KvAttn a;
+  bool empty;
+  CHECK(check_kv(cache, seqs, a.c, a.q, empty));
+  CHECK(check_kv_rows(q, a.q.total, a.c.dim, a.ts, a.hs));
+  if (q->dtype == SPARQ24_F32) return SPARQ24_ERR_UNSUPPORTED;
+  if (q->rows < 1 || q->rows % a.c.heads) return SPARQ24_ERR_SHAPE;
+  if (!(scale > 0.0f) || scale > 3.0e38f || (causal != 0 && causal != 1) || window < 0)
+    return SPARQ24_ERR_INVALID;
+  if (window && !causal) return SPARQ24_ERR_INVALID;
+  // row counts (tokens times query heads) are 32-bit in the kernels
+  if (q->rows > INT32_MAX || a.q.total * q->rows > INT32_MAX / 2) return SPARQ24_ERR_UNSUPPORTED;
+  a.x = (const char*)q->data;
+  a.dtype = q->dtype;
+  a.heads = (int)q->rows;
+  a.scale = scale;
+  a.causal = causal;
+  a.window = window > INT32_MAX ? INT32_MAX : (int)window;
+  a.out = (char*)out;
+  a.lse = lse;
+  bool query;
+  CHECK(workspace(ws, ws_bytes, empty ? 0 : kv_attn_workspace(a), query));
+  if (query || empty) return SPARQ24_OK;
+  CHECK(check_kv_pointers(a.c, a.q));
+  if (!a.x || !a.out) return SPARQ24_ERR_INVALID;
+  if (!aligned16(a.x) || !aligned16(a.out) || ((uintptr_t)lse & 3u)) return SPARQ24_ERR_ALIGN;
+  CHECK(device_ok());
+  return launched(launch_kv_attn(a, ws, stream));
+}
+
 sparq24_status sparq24_col_l2norm(const sparq24_tensor* x, float* norms, void* ws,
                                   size_t* ws_bytes, hipStream_t stream) {
   RowDesc d;

@@ -1,0 +1,669 @@
+// Paged 8-bit key/value cache: append of new token rows, and attention of
+// query rows over the cached tokens.  Layout and conventions: kv_common.hpp.
+#include "dispatch.hpp"
+#include "kv_common.hpp"
+
+namespace sparq24 {
+
+// ---------------------------------------------------------------------------
+// Append.  One workgroup per touched block, kv head and side (K, V).  With
+// amax the absolute maximum of the block's new elements (NaN left out):
+//   cand = amax < 2^-64 ? 0 : fp32(amax / qmax)
+//   s    = the block begins with a new token ? cand : max(s_old, cand)
+//   code = encode(fp32(x * fp32(1 / s)));  a NaN element is coded as 0
+// and where s > s_old the codes before the new ones become
+//   encode(fp32(code * fp32(s_old * fp32(1 / s)))).
+// Codes behind the new ones stay as they are.
+// ---------------------------------------------------------------------------
+template <bool FP8>
+__device__ inline uint32_t kv_encode(float y) {
+  constexpr float q = FP8 ? 448.0f : 127.0f;
+  y = y == y ? __builtin_amdgcn_fmed3f(y, -q, q) : 0.0f;
+  if constexpr (FP8) return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, 0.0f, 0u, false) & 0xFFu;
+  else return __float_as_uint(y + kRoundMagic) & 0xFFu;
+}
+template <bool FP8>
+__device__ inline float kv_decode(uint32_t c) {
+  if constexpr (FP8) return dec_e4m3(c);
+  else return (float)(int8_t)c;
+}
+
+template <class DT, bool FP8>
+__global__ __launch_bounds__(kBlock) void k_kv_append(KvCache c, KvSeqs q, KvRows kr, KvRows vr) {
+  extern __shared__ uint8_t tile[];  // V: codes [D][T + 4]
+  __shared__ float red[kBlock / 64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int T = 1 << c.tsh, D = c.dim;
+  int64_t b, j;
+  const bool found = find_sequence(q.seqs, blockIdx.x, lane, b, j, [&](int64_t i) -> int64_t {
+    const SeqRows r = seq_rows(q, i);
+    const int p0 = r.len > r.n ? r.len - r.n : 0;
+    const int64_t end = r.len < q.cap ? r.len : q.cap;
+    return r.n > 0 && p0 < end ? ((end - 1) >> c.tsh) - (p0 >> c.tsh) + 1 : 0;
+  });
+  if (!found) return;
+  const SeqRows r = seq_rows(q, b);
+  const int p0 = r.len > r.n ? r.len - r.n : 0;
+  const int64_t cend = r.len < q.cap ? r.len : q.cap;
+  const int64_t page = (p0 >> c.tsh) + j;
+  const int64_t blk = q.table[b * q.table_stride + page];
+  if (blk < 0 || blk >= c.blocks) return;
+  const int64_t base = page << c.tsh;
+  const int o0 = base < p0 ? (int)(p0 - base) : 0;
+  const int o1 = cend - base < T ? (int)(cend - base) : T;  // new codes: rows o0 .. o1 - 1
+  const int head = blockIdx.y;
+  const bool side_v = blockIdx.z != 0;
+  const KvRows rows = side_v ? vr : kr;
+  // row of the block's row o: position base + o is new token base + o - (len - n)
+  const int64_t row0 = r.first + (base - ((int64_t)r.len - r.n));
+  const char* x = rows.x + row0 * rows.ts + head * rows.hs;
+  const int upr = D / 8, units = (o1 - o0) * upr;
+
+  float am = 0.0f;
+  for (int i = tid; i < units; i += kBlock) {
+    Unit<DT> u;
+    load_unit(u, x + (int64_t)(o0 + i / upr) * rows.ts + (i % upr) * 8 * DT::ESIZE);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) am = __builtin_fmaxf(am, __builtin_fabsf(u.f(e)));
+  }
+  am = __uint_as_float(wave_max_u32<64>(__float_as_uint(am)));
+  if (lane == 0) red[tid >> 6] = am;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kBlock / 64; ++i) am = __builtin_fmaxf(am, red[i]);
+
+  float* sp = (side_v ? c.vs : c.ks) + blk * c.heads + head;
+  const float old = o0 ? *sp : 0.0f;
+  const float cand = am >= 0x1p-64f ? am / (FP8 ? 448.0f : 127.0f) : 0.0f;
+  const float s = cand > old ? cand : old;
+  const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+  __syncthreads();  // every thread has read the old scale
+  if (tid == 0) *sp = s;
+  uint8_t* codes = (side_v ? c.v : c.k) + (blk * c.heads + head) * (int64_t)T * D;
+  if (o0 && s > old) {  // code what the block held again, to the grown scale
+    const float ratio = old * inv;
+    if (side_v) {
+      for (int i = tid; i < D * o0; i += kBlock) {
+        uint8_t* p = codes + (i / o0) * T + i % o0;
+        *p = (uint8_t)kv_encode<FP8>(kv_decode<FP8>(*p) * ratio);
+      }
+    } else {
+      for (int i = tid; i < o0 * D; i += kBlock)
+        codes[i] = (uint8_t)kv_encode<FP8>(kv_decode<FP8>(codes[i]) * ratio);
+    }
+  }
+  const int pitch = T + 4;
+  for (int i = tid; i < units; i += kBlock) {
+    Unit<DT> u;
+    const int o = o0 + i / upr, d = (i % upr) * 8;
+    load_unit(u, x + (int64_t)o * rows.ts + d * DT::ESIZE);
+    uint32_t code[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) code[e] = kv_encode<FP8>(u.f(e) * inv);
+    if (side_v) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) tile[(d + e) * pitch + o] = (uint8_t)code[e];
+    } else {
+      uint32_t* p = (uint32_t*)(codes + o * D + d);
+      p[0] = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
+      p[1] = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
+    }
+  }
+  if (!side_v) return;
+  __syncthreads();
+  // whole dwords where the new rows cover them, bytes at the ragged ends
+  const int q0 = o0 >> 2, nq = ((o1 + 3) >> 2) - q0;
+  for (int i = tid; i < D * nq; i += kBlock) {
+    const int d = i / nq, t = (q0 + i % nq) * 4;
+    if (t >= o0 && t + 4 <= o1) {
+      *(uint32_t*)(codes + d * T + t) = *(const uint32_t*)(tile + d * pitch + t);
+    } else {
+      for (int e = t < o0 ? o0 : t; e < (t + 4 < o1 ? t + 4 : o1); ++e)
+        codes[d * T + e] = tile[d * pitch + e];
+    }
+  }
+}
+
+hipError_t launch_kv_append(const KvCache& c, const KvSeqs& q, const KvRows& k, const KvRows& v,
+                            int dtype, hipStream_t s) {
+  const int64_t T = 1ll << c.tsh;
+  // n tokens touch at most (n + T - 2) / T + 1 blocks
+  const int64_t most = q.cu ? (q.total + q.seqs * (T - 2)) / T + q.seqs
+                            : q.seqs * ((q.nper + T - 2) / T + 1);
+  const size_t shmem = (size_t)c.dim * (size_t)(T + 4);
+  const dim3 grid((unsigned)most, (unsigned)c.heads, 2);
+  return with_dtype(dtype, [&]<class DT>() {
+    auto go = [&](auto kern) {
+      if (shmem > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void*)kern,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)shmem);
+        if (e != hipSuccess) return e;
+      }
+      hipLaunchKernelGGL(kern, grid, dim3(kBlock), shmem, s, c, q, k, v);
+      return hipGetLastError();
+    };
+    return c.fp8 ? go(k_kv_append<DT, true>) : go(k_kv_append<DT, false>);
+  });
+}
+
+// ---------------------------------------------------------------------------
+// Attention.  For query row i of sequence b at position pos = len - n + i and
+// kv head j = h / g (g query heads per kv head), over the visible tokens t:
+//   s_t = scale * ks[blk(t)] * (q . kcode_t),  p_t = exp(s_t),
+//   o = (sum_t p_t vs[blk(t)] vcode_t) / (sum_t p_t).
+// Both products run on v_mfma_f32_16x16x32_f16 with the codes widened exactly
+// to fp16.  Transposed throughout, so that no operand is rearranged:
+//   S^T [token][row] = K Q^T    lane: row c = lane % 16, tokens 4 h + i
+//   O^T [dim][row]   = V^T P^T  lane: row c, dims 4 h + i  (h = lane / 16)
+// A tile is 64 tokens.  Rows of the four 16-token MFMA tiles are dealt so that
+// lane group h gets the scores of tokens 16h .. 16h + 15, which are exactly
+// the k slots in which it supplies P^T, and one 16-byte run of a V row.
+// The block scales ride on the exponent: with w_t = p_t vs, w = exp2(s_t log2e
+// + log2 vs - m) feeds the second product, and the sum of p_t is the sum of
+// w / vs, so neither scale costs an instruction per score and w stays in
+// fp16's range whatever the scales are.  A query row is multiplied by a power
+// of two that puts its largest element at 2^13 (exact: fp16 then holds every
+// bf16 or fp16 element down to 2^-27 of it in full).  Scores, m, sums and O are
+// fp32; w is rounded to fp16 (relative 2^-11, below bf16's own rounding and
+// at fp16's).
+// ---------------------------------------------------------------------------
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+typedef float f32x2v __attribute__((ext_vector_type(2)));
+typedef unsigned u32x4v __attribute__((ext_vector_type(4)));
+
+// Eight codes (two dwords) as fp16, exactly.
+template <bool FP8>
+__device__ inline f16x8_t widen8(uint32_t a, uint32_t b) {
+  f16x2_t r[4];
+  if constexpr (FP8) {
+    r[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false);
+    r[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
+    r[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false);
+    r[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
+  } else {
+    // 0x6400 | (code + 128) is the fp16 number 1024 + 128 + code
+    const f16x2_t off = {(_Float16)1152.0f, (_Float16)1152.0f};
+    const uint32_t ua = a ^ 0x80808080u, ub = b ^ 0x80808080u;
+    r[0] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, ua, 0x04010400u)) - off;
+    r[1] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, ua, 0x04030402u)) - off;
+    r[2] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, ub, 0x04010400u)) - off;
+    r[3] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, ub, 0x04030402u)) - off;
+  }
+  return f16x8_t{r[0].x, r[0].y, r[1].x, r[1].y, r[2].x, r[2].y, r[3].x, r[3].y};
+}
+
+constexpr int kKvTile = 64;
+constexpr float kTopSet = 8.0f;    // a new reference puts the largest w at 2^8 ...
+constexpr float kTopMost = 15.0f;  // ... and stands until one would pass 2^15
+// One fma from score to exponent rounds m, not the exponent: the same factor for
+// every token, harmless until the rounding itself is large.  From here on the
+// exponent is the difference of the rounded terms, so the largest stays in range.
+constexpr float kFarTop = 65536.0f;
+constexpr float kNegInf = -__builtin_inff();
+
+// Work of one launch: item = ((sequence, chunk, row tile), kv head).
+struct KvAttnArgs {
+  KvAttn a;
+  int g;            // query heads per kv head
+  int rb;           // rows (token, head of the group) per row tile
+  int64_t target;   // items that the launch aims at
+  int64_t items;    // items that it has room for
+  int cmin;         // least tiles of a chunk
+  int* plan;        // [seqs][2]: first item / kv heads, chunks
+  float* ml;        // [items][rb][2]: reference and sum of a split row tile
+  float* po;        // [items][rb][D]
+};
+
+struct KvWork {
+  int rows, rt, lo, tiles;  // rows, row tiles, first tile, tiles of the visible range
+};
+// First position that a query at pos sees (window 0: all).
+__device__ inline int first_seen(int pos, int window) {
+  return window && pos >= window ? pos - window + 1 : 0;
+}
+__device__ inline KvWork kv_work(const KvAttnArgs& w, const SeqRows& r) {
+  KvWork k;
+  k.rows = r.n * w.g;
+  k.rt = (k.rows + w.rb - 1) / w.rb;
+  const int hi = (int)(r.len < w.a.q.cap ? r.len : w.a.q.cap);
+  const int lo = first_seen(r.len - r.n, w.a.window);
+  k.lo = lo / kKvTile;
+  k.tiles = hi > lo ? (hi + kKvTile - 1) / kKvTile - k.lo : 0;
+  return k;
+}
+
+struct KvItem {
+  SeqRows r;
+  KvWork k;
+  int64_t seq, slot;
+  int chunk, chunks, len, rt, head;  // len: tiles of a chunk
+};
+__device__ inline bool kv_item(const KvAttnArgs& w, int64_t id, int lane, KvItem& it) {
+  const int H = w.a.c.heads;
+  const int64_t seqs = w.a.q.seqs;
+  int64_t all = 0;
+  for (int64_t b0 = 0; b0 < seqs; b0 += 64) {
+    const int64_t b = b0 + lane;
+    int64_t c = 0;
+    if (b < seqs) {
+      const KvWork k = kv_work(w, seq_rows(w.a.q, b));
+      c = (int64_t)k.rt * k.tiles;
+    }
+    all += __shfl(wave_scan_sum(c, lane), 63, 64);
+  }
+  int64_t len = (all * H + w.target - 1) / w.target;
+  len = len < w.cmin ? w.cmin : (len + 3) / 4 * 4;  // four waves share a chunk
+  it.len = (int)len;
+  int64_t local;
+  if (!find_sequence(seqs, id / H, lane, it.seq, local, [&](int64_t b) -> int64_t {
+        const KvWork k = kv_work(w, seq_rows(w.a.q, b));
+        const int64_t ch = (k.tiles + len - 1) / len;
+        return k.rt * (ch > 1 ? ch : 1);
+      }))
+    return false;
+  it.r = seq_rows(w.a.q, it.seq);
+  it.k = kv_work(w, it.r);
+  it.chunks = (int)((it.k.tiles + len - 1) / len);
+  if (it.chunks < 1) it.chunks = 1;
+  it.chunk = (int)(local / it.k.rt);
+  it.rt = (int)(local % it.k.rt);
+  it.head = (int)(id % H);
+  it.slot = id;
+  if (w.plan && local == 0 && it.head == 0 && threadIdx.x == 0) {
+    w.plan[2 * it.seq] = (int)(id / H);
+    w.plan[2 * it.seq + 1] = it.chunks;
+  }
+  return true;
+}
+
+__device__ inline void kv_store_out(const KvAttn& a, int64_t o, float v) {
+  if (a.dtype == 1) ((__bf16*)a.out)[o] = (__bf16)v;
+  else ((_Float16*)a.out)[o] = (_Float16)v;
+}
+
+// Few rows per kv head (decoding): QT tiles of 16 rows, four waves that take
+// the chunk's tiles in turn, K and V straight from memory into MFMA operands.
+// Bound by the cache's bytes.
+template <int D, int QT, bool FP8>
+__global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
+  constexpr int NS = D / 64, NU = D / 16;
+  const KvAttn& a = p.a;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, c16 = lane & 15, h = lane >> 4;
+  KvItem it;
+  if (!kv_item(p, blockIdx.x, lane, it)) return;
+  const int H = a.c.heads, tsh = a.c.tsh, T = 1 << tsh;
+  const int pos0 = it.r.len - it.r.n;  // position of the first query token
+  const int hi_all = (int)(it.r.len < a.q.cap ? it.r.len : a.q.cap);
+
+  // query rows of this lane's column, in fp16 times a power of two
+  f16x8_t qf[QT][2 * NS];
+  float cq[QT];
+  int lim[QT], low[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    const int r = it.rt * p.rb + 16 * t + c16;
+    const bool valid = r < it.k.rows;
+    const int i = valid ? r / p.g : 0, hq = valid ? it.head * p.g + r % p.g : 0;
+    const int pos = pos0 + i;
+    lim[t] = !valid ? -1 : (a.causal && pos + 1 < hi_all ? pos + 1 : hi_all) - 1;
+    low[t] = first_seen(pos, a.window);
+    const char* x = a.x + (it.r.first + (int64_t)i) * a.ts + hq * a.hs + 32 * h;
+    u32x4v raw[NS][2];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      raw[s][0] = *(const u32x4v*)(x + 128 * s);
+      raw[s][1] = *(const u32x4v*)(x + 128 * s + 16);
+    }
+    float f[NS][16], am = 0.0f;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t v = (raw[s][e / 8][(e % 8) / 2] >> (16 * (e & 1))) & 0xFFFFu;
+        f[s][e] = a.dtype == 1 ? BF16T::to_f32(v) : F16T::to_f32(v);
+        am = __builtin_fmaxf(am, __builtin_fabsf(f[s][e]));
+      }
+    am = __builtin_fmaxf(am, __shfl_xor(am, 16, 64));
+    am = __builtin_fmaxf(am, __shfl_xor(am, 32, 64));
+    int ex = (int)(__float_as_uint(am) >> 23);           // 0: zero or subnormal, 255: inf
+    ex = ex < 64 ? 64 : (ex > 254 ? 127 : ex);
+    const float up = __uint_as_float((uint32_t)(127 + 13 - (ex - 127)) << 23);
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) qf[t][2 * s + e / 8][e % 8] = (_Float16)(f[s][e] * up);
+    cq[t] = a.scale * 1.44269504088896340736f * __uint_as_float((uint32_t)(127 - 13 + (ex - 127)) << 23);
+  }
+
+  f32x4v o[QT][NU];
+  float m[QT], l[QT];
+  bool far = false;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    m[t] = kNegInf;
+    l[t] = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) o[t][u] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // tiles that some row of the row tile sees, within the chunk
+  const int r0 = it.rt * p.rb, r1 = r0 + 16 * QT < it.k.rows ? r0 + 16 * QT : it.k.rows;
+  const int i0 = r0 / p.g, i1 = (r1 - 1) / p.g;
+  const int hi = a.causal && pos0 + i1 + 1 < hi_all ? pos0 + i1 + 1 : hi_all;
+  const int lo = first_seen(pos0 + i0, a.window);
+  const int least = a.causal && pos0 + i0 + 1 < hi ? pos0 + i0 + 1 : hi;           // below: seen by all rows
+  const int from = first_seen(pos0 + i1, a.window);  // from here on: by all
+  int t0 = it.k.lo + it.chunk * it.len, t1 = t0 + it.len;
+  if (t1 > it.k.lo + it.k.tiles) t1 = it.k.lo + it.k.tiles;
+  if (t0 < lo / kKvTile) t0 = lo / kKvTile;
+  if (t1 > (hi + kKvTile - 1) / kKvTile) t1 = (hi + kKvTile - 1) / kKvTile;
+  const int* table = a.q.table + it.seq * a.q.table_stride;
+  const int64_t bhead = (int64_t)T * D;
+
+  for (int tt = t0 + wv; tt < t1; tt += 4) {
+    const int b0 = tt * kKvTile;
+    // block of this lane group's 16 tokens; groups that no row sees (their scales
+    // may be anything) and groups without a block read block 0, masked
+    const int gp = b0 + 16 * h;
+    int64_t blk = gp < hi && gp + 16 > lo ? table[gp >> tsh] : -1;
+    const bool there = blk >= 0 && blk < a.c.blocks;
+    blk = there ? blk * H + it.head : it.head;
+    const uint64_t away = __ballot(!there);
+    const int src = 16 * (c16 >> 2);
+    const int64_t kblk = __shfl(blk, src, 64);
+    const int krow = ((b0 + src) & (T - 1)) + (c16 & 3);
+    const uint8_t* kp = a.c.k + kblk * bhead + (int64_t)krow * D + 16 * h;
+    const uint8_t* vp = a.c.v + blk * bhead + (int64_t)c16 * T + (gp & (T - 1));
+    u32x4v kr[4][NS], vr[NU];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) kr[mt][s] = *(const u32x4v*)(kp + 4 * mt * D + 64 * s);
+    const float ks = a.c.ks[blk], vs = a.c.vs[blk];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) vr[u] = *(const u32x4v*)(vp + (int64_t)u * 16 * T);
+
+    f32x4v sc[QT][4];
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) sc[t][mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const f16x8_t k0 = widen8<FP8>(kr[mt][s][0], kr[mt][s][1]);
+        const f16x8_t k1 = widen8<FP8>(kr[mt][s][2], kr[mt][s][3]);
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+          sc[t][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[t][2 * s], sc[t][mt], 0, 0, 0);
+          sc[t][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[t][2 * s + 1], sc[t][mt], 0, 0, 0);
+        }
+      }
+
+    const bool edge = away != 0 || b0 + kKvTile > least || b0 < from;
+    // a zero scale counts as 2^-80: its codes are zeros
+    const float vse = vs < 0x1p-80f ? 0x1p-80f : vs;
+    const float lv = there ? __builtin_amdgcn_logf(vse) : 0.0f;
+    const float rv = there ? 1.0f / vse : 1.0f;
+    f16x8_t pf[QT][2];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      float ck = there ? cq[t] * ks : 1.0f;
+      ck = ck < 0x1p-120f ? 0x1p-120f : ck;
+      if (edge) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tok = gp + 4 * mt + e;
+            if (!there || tok > lim[t] || tok < low[t]) sc[t][mt][e] = kNegInf;
+          }
+      }
+      float mx = kNegInf;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx = __builtin_fmaxf(mx, sc[t][mt][e]);
+      mx = __builtin_fmaf(mx, ck, lv);
+      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16, 64));
+      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
+      if (__any(mx - m[t] > kTopMost)) {  // -inf - -inf is NaN: no new reference
+        const float nm = mx - m[t] > kTopMost ? mx - kTopSet : m[t];
+        const float al = nm == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[t] - nm);
+        m[t] = nm;
+        far |= __any(__builtin_fabsf(nm) > kFarTop && nm != kNegInf);
+        l[t] *= al;
+#pragma unroll
+        for (int u = 0; u < NU; ++u) o[t][u] *= al;
+      }
+      const float ref = m[t] == kNegInf ? 0.0f : m[t], off = lv - ref;
+      if (far) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[t][mt][e] = __builtin_fmaf(sc[t][mt][e], ck, lv) - ref;
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[t][mt][e] = __builtin_fmaf(sc[t][mt][e], ck, off);
+      }
+      float sum = 0.0f;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = __builtin_amdgcn_exp2f(sc[t][mt][e]);
+          sum += w;
+          pf[t][mt / 2][4 * (mt & 1) + e] = (_Float16)w;
+        }
+      l[t] = __builtin_fmaf(sum, rv, l[t]);
+    }
+    if constexpr (FP8) {
+      if (edge) {  // codes that nobody sees can be NaN: 0 * NaN must not reach O
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t keep = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tok = gp + 4 * q + e;
+            if (there && tok < hi && tok >= lo) keep |= 0xFFu << (8 * e);
+          }
+#pragma unroll
+          for (int u = 0; u < NU; ++u) vr[u][q] &= keep;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const f16x8_t v0 = widen8<FP8>(vr[u][0], vr[u][1]), v1 = widen8<FP8>(vr[u][2], vr[u][3]);
+#pragma unroll
+      for (int t = 0; t < QT; ++t) {
+        o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[t][0], o[t][u], 0, 0, 0);
+        o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[t][1], o[t][u], 0, 0, 0);
+      }
+    }
+  }
+
+  // the four waves' parts of each row meet in LDS, in wave order
+  constexpr int PITCH = D + 4;
+  __shared__ float os[4][16][PITCH];
+  __shared__ float mls[4][16][2];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    l[t] += __shfl_xor(l[t], 16, 64);
+    l[t] += __shfl_xor(l[t], 32, 64);
+    if (t) __syncthreads();
+    if (h == 0) {
+      mls[wv][c16][0] = m[t];
+      mls[wv][c16][1] = l[t];
+    }
+#pragma unroll
+    for (int u = 0; u < NU; ++u) *(f32x4v*)&os[wv][c16][16 * u + 4 * h] = o[t][u];
+    __syncthreads();
+    const int row = threadIdx.x >> 4, sub = threadIdx.x & 15;
+    const int r = it.rt * p.rb + 16 * t + row;
+    if (r < it.k.rows) {
+      float top = kNegInf, f[4], sum = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) top = __builtin_fmaxf(top, mls[q][row][0]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f[q] = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mls[q][row][0] - top);
+        sum += mls[q][row][1] * f[q];
+      }
+      const int64_t tok = it.r.first + r / p.g, hq = it.head * p.g + r % p.g;
+      const bool split = it.chunks > 1;
+      const float inv = split ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum);
+      const int64_t base = split ? (it.slot * p.rb + 16 * t + row) * D : (tok * a.heads + hq) * D;
+#pragma unroll
+      for (int e = 0; e < D / 16; ++e) {
+        const int d = sub + 16 * e;
+        float v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v += os[q][row][d] * f[q];
+        if (split) p.po[base + d] = v;
+        else kv_store_out(a, base + d, v * inv);
+      }
+      if (sub == 0) {
+        if (split) {
+          float* ml = p.ml + (it.slot * p.rb + 16 * t + row) * 2;
+          ml[0] = sum == sum ? top : -kNegInf;  // NaN has the last word in the join
+          ml[1] = sum;
+        } else if (a.lse) {
+          a.lse[tok * a.heads + hq] =
+              sum == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
+        }
+      }
+    }
+  }
+}
+
+// Joins the chunks of split sequences: one wave per (token, query head).
+__global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs p, int D) {
+  const KvAttn& a = p.a;
+  const int lane = threadIdx.x & 63;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (id >= a.q.total * a.heads) return;
+  const int64_t tok = id / a.heads;
+  const int hq = (int)(id % a.heads);
+  int64_t seq = 0;
+  if (a.q.cu) {  // last sequence that begins at or before the token
+    int64_t lo = 0, hi = a.q.seqs;
+    while (hi - lo > 1) {
+      const int64_t mid = (lo + hi) / 2;
+      if (a.q.cu[mid] <= tok) lo = mid;
+      else hi = mid;
+    }
+    seq = lo;
+  } else {
+    seq = tok / a.q.nper;
+  }
+  const SeqRows r = seq_rows(a.q, seq);
+  if (tok < r.first || tok >= (int64_t)r.first + r.n) return;  // in no sequence
+  const int chunks = p.plan[2 * seq + 1];
+  if (chunks < 2) return;
+  const int row = (int)(tok - r.first) * p.g + hq % p.g;
+  const int nrt = (r.n * p.g + p.rb - 1) / p.rb, rt = row / p.rb, rr = row % p.rb;
+  const int head = hq / p.g;
+  const int64_t first = p.plan[2 * seq];
+  // offsets that do not ascend can ask for more items than there is room for
+  if (first < 0 || (first + (int64_t)chunks * nrt) * a.c.heads > p.items) return;
+  auto slot = [&](int c) { return ((first + (int64_t)c * nrt + rt) * a.c.heads + head) * p.rb + rr; };
+  float top = kNegInf;
+  for (int c = lane; c < chunks; c += 64) top = __builtin_fmaxf(top, p.ml[slot(c) * 2]);
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, x, 64));
+  float sum = 0.0f, v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (top != kNegInf) {
+    for (int c = 0; c < chunks; ++c) {
+      const int64_t s = slot(c);
+      const float f = __builtin_amdgcn_exp2f(p.ml[s * 2] - top);
+      if (f == 0.0f) continue;
+      sum = __builtin_fmaf(p.ml[s * 2 + 1], f, sum);
+      for (int e = 0; e < D / 64; ++e) v[e] = __builtin_fmaf(p.po[s * D + lane + 64 * e], f, v[e]);
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  for (int e = 0; e < D / 64; ++e) kv_store_out(a, id * D + lane + 64 * e, v[e] * inv);
+  if (a.lse && lane == 0)
+    a.lse[id] = sum == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
+}
+
+namespace {
+struct KvPlan {
+  int g, rb, qt, cmin;
+  int64_t target, items;  // most items of the launch
+  bool split;
+  size_t off_ml, off_po, need;
+};
+KvPlan kv_plan(const KvAttn& a) {
+  KvPlan p;
+  p.g = a.heads / a.c.heads;
+  const int64_t rows = (a.q.total + a.q.seqs - 1) / a.q.seqs * p.g;  // of a usual sequence
+  p.qt = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+  if (a.c.dim > 128 && p.qt > 2) p.qt = 2;
+  p.rb = 16 * p.qt;
+  p.cmin = 4;
+  p.target = 4 * device_cu_count();
+  const int64_t H = a.c.heads;
+  const int64_t rt = a.q.cu ? (a.q.total * p.g) / p.rb + a.q.seqs
+                            : a.q.seqs * ((a.q.nper * p.g + p.rb - 1) / p.rb);
+  const int64_t tiles = (a.q.cap + kKvTile - 1) / kKvTile;
+  p.split = tiles > p.cmin;
+  p.items = rt * H;
+  if (p.split) {
+    const int64_t more = rt * H * ((tiles + p.cmin - 1) / p.cmin);
+    p.items = more < p.target + rt * H ? more : p.target + rt * H;
+  }
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  p.off_ml = up((size_t)a.q.seqs * 8);
+  p.off_po = p.off_ml + up((size_t)p.items * p.rb * 8);
+  p.need = p.split ? p.off_po + up((size_t)p.items * p.rb * a.c.dim * 4) : 0;
+  return p;
+}
+}  // namespace
+
+size_t kv_attn_workspace(const KvAttn& a) { return kv_plan(a).need; }
+
+hipError_t launch_kv_attn(const KvAttn& a, void* ws, hipStream_t s) {
+  const KvPlan pl = kv_plan(a);
+  KvAttnArgs p;
+  p.a = a;
+  p.g = pl.g;
+  p.rb = pl.rb;
+  p.target = pl.target;
+  p.items = pl.items;
+  p.cmin = pl.split ? pl.cmin : (1 << 26);
+  p.plan = pl.split ? (int*)ws : nullptr;
+  p.ml = (float*)((char*)ws + pl.off_ml);
+  p.po = (float*)((char*)ws + pl.off_po);
+  auto run = [&]<int D, int QT>() {
+    auto k = a.c.fp8 ? k_kv_attn<D, QT, true> : k_kv_attn<D, QT, false>;
+    hipLaunchKernelGGL(k, dim3((unsigned)pl.items), dim3(256), 0, s, p);
+    return hipGetLastError();
+  };
+  auto dim = [&]<int D>() {
+    if (pl.qt == 1) return run.template operator()<D, 1>();
+    if (pl.qt == 2) return run.template operator()<D, 2>();
+    if constexpr (D <= 128) return run.template operator()<D, 4>();
+    return hipErrorInvalidValue;
+  };
+  hipError_t e;
+  switch (a.c.dim) {
+    case 64: e = dim.template operator()<64>(); break;
+    case 128: e = dim.template operator()<128>(); break;
+    case 192: e = dim.template operator()<192>(); break;
+    case 256: e = dim.template operator()<256>(); break;
+    default: return hipErrorInvalidValue;
+  }
+  if (e != hipSuccess || !pl.split) return e;
+  const int64_t waves = a.q.total * a.heads;
+  hipLaunchKernelGGL(k_kv_join, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, s, p, a.c.dim);
+  return hipGetLastError();
+}
+
+}  // namespace sparq24
