@@ -78,15 +78,185 @@ __global__ __launch_bounds__(512) void k_int8_stream(Int8Gemm g, int64_t ntn) {
   }
 }
 
+// Many rows: a BM x BN tile per workgroup, waves of WM x 64 on
+// v_mfma_i32_16x16x64_i8.  Slabs of 128 codes go from memory straight into LDS
+// (global_load_lds), S - 1 slabs ahead; their 16-byte chunks are XOR-swizzled
+// by row.  Waits and barriers as in k_gemm_dma: the fragment reads wait for
+// themselves, the slab loads by a per-wave vmcnt before the raw barrier.
+// Chunks at or past K come from zeros; rows past the ends repeat the last.
+__device__ const uint4 kInt8Zeros = {0, 0, 0, 0};
+
+// 16 outputs n .. n + 15 of row m: 16-byte stores where `wide` says that all
+// are inside and aligned, else one by one.
+template <class T>
+__device__ inline void int8_store16(const Int8Gemm& g, int64_t m, int64_t n, const i32x4_t (&acc)[4], float sa,
+                                    const float* sb, const float* bias, bool wide) {
+  typedef T t8 __attribute__((ext_vector_type(16 / sizeof(T))));
+  constexpr int V = 16 / sizeof(T);
+  T* c = (T*)g.c + m * g.ldc + n;
+  T y[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) y[e] = (T)((float)acc[e / 4][e % 4] * sa * sb[e] + bias[e]);
+  if (wide) {
+#pragma unroll
+    for (int q = 0; q < 16 / V; ++q) {
+      t8 v;
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = y[V * q + e];
+      *(t8*)(c + V * q) = v;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (n + e < g.N) c[e] = y[e];
+  }
+}
+
+template <int BM, int BN, int WM, int S>
+__global__ __launch_bounds__((BM / WM) * (BN / 64) * 64) void k_int8_tile(Int8Gemm g) {
+  constexpr int WN = 64, NWN = BN / WN, NT = (BM / WM) * NWN * 64;
+  constexpr int TI = WM / 16, TJ = 4, SK = 128;
+  constexpr int A_BYTES = BM * SK, STAGE = (BM + BN) * SK;
+  constexpr int QA = BM * 8 / NT, QB = BN * 8 / NT;
+  static_assert(QA * NT == BM * 8 && QB * NT == BN * 8 && TI % 4 == 0, "tile / thread mismatch");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[S * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w / NWN, wn = w % NWN;
+  // XCD-aware order: each XCD owns a contiguous run of tiles, walked in
+  // groups of eight row tiles, so that its L2 serves the shared slabs
+  const int64_t ntn = (g.N + BN - 1) / BN, ntm = (g.M + BM - 1) / BM, total = ntm * ntn;
+  const int64_t pid = blockIdx.x, per = total / 8;
+  const int64_t lid = pid < per * 8 ? (pid % 8) * per + pid / 8 : pid;
+  constexpr int64_t kGroupM = 8;
+  const int64_t ingroup = kGroupM * ntn, first = (lid / ingroup) * kGroupM;
+  const int64_t gsz = ntm - first < kGroupM ? ntm - first : kGroupM;
+  const int64_t m0 = (first + (lid % ingroup) % gsz) * BM, n0 = ((lid % ingroup) / gsz) * BN;
+
+  const int K = (int)g.K;
+  auto issue = [&](int buf, int k0) {
+    uint8_t* st = smem + buf * STAGE;
+#pragma unroll
+    for (int q = 0; q < QA; ++q) {
+      const int p = q * NT + tid, r = p >> 3, k = k0 + 16 * ((p & 7) ^ (r & 7));
+      const int8_t* src = g.a + (m0 + r < g.M ? m0 + r : g.M - 1) * g.lda + k;
+      __builtin_amdgcn_global_load_lds(k < K ? src : (const int8_t*)&kInt8Zeros,
+                                       (lds_void_t*)(st + (q * NT + w * 64) * 16), 16, 0, 0);
+    }
+#pragma unroll
+    for (int q = 0; q < QB; ++q) {
+      const int p = q * NT + tid, r = p >> 3, k = k0 + 16 * ((p & 7) ^ ((r & 3) | ((r >> 2) & 4)));
+      const int8_t* src = g.b + (n0 + r < g.N ? n0 + r : g.N - 1) * g.ldb + k;
+      __builtin_amdgcn_global_load_lds(k < K ? src : (const int8_t*)&kInt8Zeros,
+                                       (lds_void_t*)(st + A_BYTES + (q * NT + w * 64) * 16), 16, 0, 0);
+    }
+  };
+
+  const unsigned lds0 = (unsigned)(uintptr_t)(lds_void_t*)smem;
+  const int fr = lane & 15, h = lane >> 4;
+  i32x4_t acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+
+  const int nk = (K + SK - 1) / SK;
+#pragma unroll
+  for (int s = 0; s + 1 < S; ++s) issue(s, s * SK);
+  for (int kt = 0; kt < nk; ++kt) {
+    wait_vmcnt<(S - 2) * (QA + QB)>();  // this wave's loads of slab kt have landed
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();  // every wave's have, and slab kt - 1 is consumed
+    asm volatile("" ::: "memory");
+    issue((kt + S - 1) % S, (kt + S - 1) * SK);  // past the end: zeros
+    const unsigned so = lds0 + (unsigned)((kt % S) * STAGE);
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      const unsigned aa =
+          so + (unsigned)((wm * WM + fr) * SK + (((4 * st + h) ^ (fr & 7)) * 16));
+      // tile j's row fr is weight row 16 (fr / 4) + 4 j + fr % 4
+      const unsigned ba = so + A_BYTES +
+                          (unsigned)((wn * WN + 16 * (fr >> 2) + (fr & 3)) * SK +
+                                     (((4 * st + h) ^ ((fr & 3) | (fr & 4))) * 16));
+      i32x4_t bf[TJ], af[4];
+      asm volatile(
+          "ds_read_b128 %0, %8\n\t"
+          "ds_read_b128 %1, %8 offset:512\n\t"
+          "ds_read_b128 %2, %8 offset:1024\n\t"
+          "ds_read_b128 %3, %8 offset:1536\n\t"
+          "ds_read_b128 %4, %9\n\t"
+          "ds_read_b128 %5, %9 offset:2048\n\t"
+          "ds_read_b128 %6, %9 offset:4096\n\t"
+          "ds_read_b128 %7, %9 offset:6144\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(bf[0]), "=&v"(bf[1]), "=&v"(bf[2]), "=&v"(bf[3]), "=&v"(af[0]), "=&v"(af[1]),
+            "=&v"(af[2]), "=&v"(af[3])
+          : "v"(ba), "v"(aa)
+          : "memory");
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af[i], acc[i][j], 0, 0, 0);
+      if constexpr (TI == 8) {
+        asm volatile(
+            "ds_read_b128 %0, %4 offset:8192\n\t"
+            "ds_read_b128 %1, %4 offset:10240\n\t"
+            "ds_read_b128 %2, %4 offset:12288\n\t"
+            "ds_read_b128 %3, %4 offset:14336\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(af[0]), "=&v"(af[1]), "=&v"(af[2]), "=&v"(af[3])
+            : "v"(aa)
+            : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < TJ; ++j)
+            acc[4 + i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af[i], acc[4 + i][j], 0, 0, 0);
+      }
+    }
+  }
+  wait_vmcnt<0>();  // the slabs requested past the end land before LDS is released
+  asm volatile("" ::: "memory");
+  // lane: row 16 i + fr, outputs 16 h + 4 j + e
+  const int64_t n = n0 + wn * WN + 16 * h;
+  float sb[16], bias[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int64_t c = n + e < g.N ? n + e : g.N - 1;
+    sb[e] = g.sb[c];
+    bias[e] = g.bias ? g.bias[c] : -0.0f;  // y + -0 is y
+  }
+  auto out = [&]<class T>(T) {
+    const bool wide = n + 16 <= g.N && g.ldc * sizeof(T) % 16 == 0;
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int64_t m = m0 + wm * WM + 16 * i + fr;
+      if (m < g.M) int8_store16<T>(g, m, n, acc[i], g.sa[m], sb, bias, wide);
+    }
+  };
+  if (g.dtype == 0) out(0.0f);
+  else if (g.dtype == 1) out((__bf16)0.0f);
+  else out((_Float16)0.0f);
+}
+
 hipError_t launch_int8_gemm(const Int8Gemm& g, hipStream_t s) {
-  auto go = [&]<int MT, int NT>() {
+  auto few = [&]<int MT, int NT>() {
     const int64_t ntm = (g.M + 16 * MT - 1) / (16 * MT), ntn = (g.N + 16 * NT - 1) / (16 * NT);
     hipLaunchKernelGGL((k_int8_stream<MT, NT>), dim3((unsigned)(ntm * ntn)), dim3(512), 0, s, g, ntn);
     return hipGetLastError();
   };
-  if (g.M <= 16) return go.template operator()<1, 1>();
-  if (g.M <= 32) return go.template operator()<2, 1>();
-  return go.template operator()<4, 2>();
+  auto tile = [&]<int BM, int BN, int WM, int S>() {
+    const int64_t n = ((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN);
+    hipLaunchKernelGGL((k_int8_tile<BM, BN, WM, S>), dim3((unsigned)n), dim3((BM / WM) * (BN / 64) * 64), 0, s, g);
+    return hipGetLastError();
+  };
+  if (g.M <= 16) return few.template operator()<1, 1>();
+  if (g.M <= 32) return few.template operator()<2, 1>();
+  if (g.M <= 64) return few.template operator()<4, 2>();
+  auto tiles = [&](int bm, int bn) { return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
+  const int cus = device_cu_count();
+  if (tiles(256, 256) >= cus) return tile.template operator()<256, 256, 128, 2>();
+  if (tiles(128, 128) >= cus / 2) return tile.template operator()<128, 128, 64, 3>();
+  return tile.template operator()<64, 64, 64, 4>();
 }
 
 }  // namespace sparq24
