@@ -80,10 +80,14 @@ __global__ __launch_bounds__(512) void k_int8_stream(Int8Gemm g, int64_t ntn) {
 
 // Many rows: a BM x BN tile per workgroup, waves of WM x 64 on
 // v_mfma_i32_16x16x64_i8.  Slabs of 128 codes go from memory straight into LDS
-// (global_load_lds), S - 1 slabs ahead; their 16-byte chunks are XOR-swizzled
-// by row.  Waits and barriers as in k_gemm_dma: the fragment reads wait for
-// themselves, the slab loads by a per-wave vmcnt before the raw barrier.
-// Chunks at or past K come from zeros; rows past the ends repeat the last.
+// (global_load_lds) into two buffers; their 16-byte chunks are XOR-swizzled by
+// row.  A slab is two steps of 64 codes, and the fragments of a step are read
+// into registers while the products of the step before run, across slabs
+// too, so the matrix pipe waits for neither LDS nor the barrier: between a
+// slab's two steps every wave has its last fragments of it and the next slab
+// has landed (one barrier), and the slab after that starts into the freed
+// buffer.  Chunks at or past K come from zeros; rows past the ends repeat the
+// last.
 __device__ const uint4 kInt8Zeros = {0, 0, 0, 0};
 
 // 16 outputs n .. n + 15 of row m: 16-byte stores where `wide` says that all
@@ -112,14 +116,14 @@ __device__ inline void int8_store16(const Int8Gemm& g, int64_t m, int64_t n, con
   }
 }
 
-template <int BM, int BN, int WM, int S>
+template <int BM, int BN, int WM>
 __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64) void k_int8_tile(Int8Gemm g) {
   constexpr int WN = 64, NWN = BN / WN, NT = (BM / WM) * NWN * 64;
   constexpr int TI = WM / 16, TJ = 4, SK = 128;
   constexpr int A_BYTES = BM * SK, STAGE = (BM + BN) * SK;
   constexpr int QA = BM * 8 / NT, QB = BN * 8 / NT;
   static_assert(QA * NT == BM * 8 && QB * NT == BN * 8 && TI % 4 == 0, "tile / thread mismatch");
-  __shared__ __attribute__((aligned(16))) uint8_t smem[S * STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * STAGE];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w / NWN, wn = w % NWN;
   // XCD-aware order: each XCD owns a contiguous run of tiles, walked in
   // groups of eight row tiles, so that its L2 serves the shared slabs
@@ -134,84 +138,80 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64) void k_int8_tile(Int8Ge
   const int K = (int)g.K;
   auto issue = [&](int buf, int k0) {
     uint8_t* st = smem + buf * STAGE;
+    const bool whole = k0 + SK <= K;
 #pragma unroll
     for (int q = 0; q < QA; ++q) {
       const int p = q * NT + tid, r = p >> 3, k = k0 + 16 * ((p & 7) ^ (r & 7));
       const int8_t* src = g.a + (m0 + r < g.M ? m0 + r : g.M - 1) * g.lda + k;
-      __builtin_amdgcn_global_load_lds(k < K ? src : (const int8_t*)&kInt8Zeros,
+      __builtin_amdgcn_global_load_lds(whole || k < K ? src : (const int8_t*)&kInt8Zeros,
                                        (lds_void_t*)(st + (q * NT + w * 64) * 16), 16, 0, 0);
     }
 #pragma unroll
     for (int q = 0; q < QB; ++q) {
       const int p = q * NT + tid, r = p >> 3, k = k0 + 16 * ((p & 7) ^ ((r & 3) | ((r >> 2) & 4)));
       const int8_t* src = g.b + (n0 + r < g.N ? n0 + r : g.N - 1) * g.ldb + k;
-      __builtin_amdgcn_global_load_lds(k < K ? src : (const int8_t*)&kInt8Zeros,
+      __builtin_amdgcn_global_load_lds(whole || k < K ? src : (const int8_t*)&kInt8Zeros,
                                        (lds_void_t*)(st + A_BYTES + (q * NT + w * 64) * 16), 16, 0, 0);
     }
   };
 
-  const unsigned lds0 = (unsigned)(uintptr_t)(lds_void_t*)smem;
   const int fr = lane & 15, h = lane >> 4;
-  i32x4_t acc[TI][TJ];
+  // fragment rows: A tile i row fr; B tile j row fr is weight row
+  // 16 (fr / 4) + 4 j + fr % 4 (a lane then holds 16 adjacent outputs)
+  const uint8_t* fa = smem + (wm * WM + fr) * SK;
+  const uint8_t* fb = smem + A_BYTES + (wn * WN + 16 * (fr >> 2) + (fr & 3)) * SK;
+  const int c0 = (h ^ (fr & 7)) * 16, c1 = ((4 + h) ^ (fr & 7)) * 16;
+  i32x4_t acc[TI][TJ], a0[TI], b0[TJ], a1[TI], b1[TJ];
 #pragma unroll
   for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
 
   const int nk = (K + SK - 1) / SK;
+  issue(0, 0);
+  issue(1, SK);  // slabs past the end are zeros
+  wait_vmcnt<QA + QB>();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 #pragma unroll
-  for (int s = 0; s + 1 < S; ++s) issue(s, s * SK);
+  for (int j = 0; j < TJ; ++j) b0[j] = *(const i32x4_t*)(fb + 4 * SK * j + c0);
+#pragma unroll
+  for (int i = 0; i < TI; ++i) a0[i] = *(const i32x4_t*)(fa + 16 * SK * i + c0);
   for (int kt = 0; kt < nk; ++kt) {
-    wait_vmcnt<(S - 2) * (QA + QB)>();  // this wave's loads of slab kt have landed
+    const int cur = (kt & 1) * STAGE, nxt = STAGE - cur;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) b1[j] = *(const i32x4_t*)(fb + cur + 4 * SK * j + c1);
+#pragma unroll
+    for (int i = 0; i < TI; ++i) a1[i] = *(const i32x4_t*)(fa + cur + 16 * SK * i + c1);
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b0[j], a0[i], acc[i][j], 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < TI + TJ; ++i) {  // one read among every two or three products
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, TI * TJ / (TI + TJ), 0);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();  // every wave's have, and slab kt - 1 is consumed
+    __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    issue((kt + S - 1) % S, (kt + S - 1) * SK);  // past the end: zeros
-    const unsigned so = lds0 + (unsigned)((kt % S) * STAGE);
+    issue(kt & 1, (kt + 2) * SK);
 #pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      const unsigned aa =
-          so + (unsigned)((wm * WM + fr) * SK + (((4 * st + h) ^ (fr & 7)) * 16));
-      // tile j's row fr is weight row 16 (fr / 4) + 4 j + fr % 4
-      const unsigned ba = so + A_BYTES +
-                          (unsigned)((wn * WN + 16 * (fr >> 2) + (fr & 3)) * SK +
-                                     (((4 * st + h) ^ ((fr & 3) | (fr & 4))) * 16));
-      i32x4_t bf[TJ], af[4];
-      asm volatile(
-          "ds_read_b128 %0, %8\n\t"
-          "ds_read_b128 %1, %8 offset:512\n\t"
-          "ds_read_b128 %2, %8 offset:1024\n\t"
-          "ds_read_b128 %3, %8 offset:1536\n\t"
-          "ds_read_b128 %4, %9\n\t"
-          "ds_read_b128 %5, %9 offset:2048\n\t"
-          "ds_read_b128 %6, %9 offset:4096\n\t"
-          "ds_read_b128 %7, %9 offset:6144\n\t"
-          "s_waitcnt lgkmcnt(0)"
-          : "=&v"(bf[0]), "=&v"(bf[1]), "=&v"(bf[2]), "=&v"(bf[3]), "=&v"(af[0]), "=&v"(af[1]),
-            "=&v"(af[2]), "=&v"(af[3])
-          : "v"(ba), "v"(aa)
-          : "memory");
+    for (int j = 0; j < TJ; ++j) b0[j] = *(const i32x4_t*)(fb + nxt + 4 * SK * j + c0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < TI; ++i) a0[i] = *(const i32x4_t*)(fa + nxt + 16 * SK * i + c0);
 #pragma unroll
-        for (int j = 0; j < TJ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af[i], acc[i][j], 0, 0, 0);
-      if constexpr (TI == 8) {
-        asm volatile(
-            "ds_read_b128 %0, %4 offset:8192\n\t"
-            "ds_read_b128 %1, %4 offset:10240\n\t"
-            "ds_read_b128 %2, %4 offset:12288\n\t"
-            "ds_read_b128 %3, %4 offset:14336\n\t"
-            "s_waitcnt lgkmcnt(0)"
-            : "=&v"(af[0]), "=&v"(af[1]), "=&v"(af[2]), "=&v"(af[3])
-            : "v"(aa)
-            : "memory");
+    for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < TJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b1[j], a1[i], acc[i][j], 0, 0, 0);
 #pragma unroll
-          for (int j = 0; j < TJ; ++j)
-            acc[4 + i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af[i], acc[4 + i][j], 0, 0, 0);
-      }
+    for (int i = 0; i < TI + TJ; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(0x008, TI * TJ / (TI + TJ), 1);
     }
   }
   wait_vmcnt<0>();  // the slabs requested past the end land before LDS is released
@@ -244,9 +244,9 @@ hipError_t launch_int8_gemm(const Int8Gemm& g, hipStream_t s) {
     hipLaunchKernelGGL((k_int8_stream<MT, NT>), dim3((unsigned)(ntm * ntn)), dim3(512), 0, s, g, ntn);
     return hipGetLastError();
   };
-  auto tile = [&]<int BM, int BN, int WM, int S>() {
+  auto tile = [&]<int BM, int BN, int WM>() {
     const int64_t n = ((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN);
-    hipLaunchKernelGGL((k_int8_tile<BM, BN, WM, S>), dim3((unsigned)n), dim3((BM / WM) * (BN / 64) * 64), 0, s, g);
+    hipLaunchKernelGGL((k_int8_tile<BM, BN, WM>), dim3((unsigned)n), dim3((BM / WM) * (BN / 64) * 64), 0, s, g);
     return hipGetLastError();
   };
   if (g.M <= 16) return few.template operator()<1, 1>();
@@ -254,9 +254,9 @@ hipError_t launch_int8_gemm(const Int8Gemm& g, hipStream_t s) {
   if (g.M <= 64) return few.template operator()<4, 2>();
   auto tiles = [&](int bm, int bn) { return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
   const int cus = device_cu_count();
-  if (tiles(256, 256) >= cus) return tile.template operator()<256, 256, 128, 2>();
-  if (tiles(128, 128) >= cus / 2) return tile.template operator()<128, 128, 64, 3>();
-  return tile.template operator()<64, 64, 64, 4>();
+  if (tiles(256, 256) >= cus) return tile.template operator()<256, 256, 128>();
+  if (tiles(128, 128) >= cus / 2) return tile.template operator()<128, 128, 64>();
+  return tile.template operator()<64, 64, 64>();
 }
 
 }  // namespace sparq24
