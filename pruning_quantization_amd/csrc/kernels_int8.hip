@@ -86,10 +86,7 @@ __global__ __launch_bounds__(512) void k_int8_stream(Int8Gemm g, int64_t ntn) {
 // too, so the matrix pipe waits for neither LDS nor the barrier: between a
 // slab's two steps every wave has its last fragments of it and the next slab
 // has landed (one barrier), and the slab after that starts into the freed
-// buffer.  Chunks at or past K come from zeros; rows past the ends repeat the
-// last.
-__device__ const uint4 kInt8Zeros = {0, 0, 0, 0};
-
+// buffer.  Rows past the ends repeat the last; a rest of K is filled up with zeros.
 // 16 outputs n .. n + 15 of row m: 16-byte stores where `wide` says that all
 // are inside and aligned, else one by one.
 template <class T>
@@ -124,7 +121,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64) void k_int8_tile(Int8Ge
   constexpr int QA = BM * 8 / NT, QB = BN * 8 / NT;
   static_assert(QA * NT == BM * 8 && QB * NT == BN * 8 && TI % 4 == 0, "tile / thread mismatch");
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * STAGE];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w / NWN, wn = w % NWN;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = w / NWN, wn = w % NWN;
   // XCD-aware order: each XCD owns a contiguous run of tiles, walked in
   // groups of eight row tiles, so that its L2 serves the shared slabs
   const int64_t ntn = (g.N + BN - 1) / BN, ntm = (g.M + BM - 1) / BM, total = ntm * ntn;
@@ -135,25 +133,34 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64) void k_int8_tile(Int8Ge
   const int64_t gsz = ntm - first < kGroupM ? ntm - first : kGroupM;
   const int64_t m0 = (first + (lid % ingroup) % gsz) * BM, n0 = ((lid % ingroup) / gsz) * BN;
 
-  const int K = (int)g.K;
-  auto issue = [&](int buf, int k0) {
-    uint8_t* st = smem + buf * STAGE;
-    const bool whole = k0 + SK <= K;
+  // Loads of a slab: 32-bit offsets from the tile's first rows (row strides of
+  // 8 MiB and more go to k_int8_stream).
+  const int K = (int)g.K, rows_a = (int)(g.M - m0 < BM ? g.M - m0 : BM), rows_b = (int)(g.N - n0 < BN ? g.N - n0 : BN);
+  const int8_t *base_a = g.a + m0 * g.lda, *base_b = g.b + n0 * g.ldb;
+  unsigned off_a[QA], off_b[QB];
 #pragma unroll
-    for (int q = 0; q < QA; ++q) {
-      const int p = q * NT + tid, r = p >> 3, k = k0 + 16 * ((p & 7) ^ (r & 7));
-      const int8_t* src = g.a + (m0 + r < g.M ? m0 + r : g.M - 1) * g.lda + k;
-      __builtin_amdgcn_global_load_lds(whole || k < K ? src : (const int8_t*)&kInt8Zeros,
-                                       (lds_void_t*)(st + (q * NT + w * 64) * 16), 16, 0, 0);
-    }
+  for (int q = 0; q < QA; ++q) {
+    const int p = q * NT + tid, r = p >> 3, m = r < rows_a ? r : rows_a - 1;
+    off_a[q] = (unsigned)m * (unsigned)g.lda + 16 * ((p & 7) ^ (r & 7));
+  }
 #pragma unroll
-    for (int q = 0; q < QB; ++q) {
-      const int p = q * NT + tid, r = p >> 3, k = k0 + 16 * ((p & 7) ^ ((r & 3) | ((r >> 2) & 4)));
-      const int8_t* src = g.b + (n0 + r < g.N ? n0 + r : g.N - 1) * g.ldb + k;
-      __builtin_amdgcn_global_load_lds(whole || k < K ? src : (const int8_t*)&kInt8Zeros,
-                                       (lds_void_t*)(st + A_BYTES + (q * NT + w * 64) * 16), 16, 0, 0);
-    }
-  };
+  for (int q = 0; q < QB; ++q) {
+    const int p = q * NT + tid, r = p >> 3, n = r < rows_b ? r : rows_b - 1;
+    off_b[q] = (unsigned)n * (unsigned)g.ldb + 16 * ((p & 7) ^ ((r & 3) | ((r >> 2) & 4)));
+  }
+#define SPARQ24_INT8_SLAB(buf, k0)                                                             \
+  {                                                                                            \
+    uint8_t* st = smem + (buf) * STAGE + w * 1024;                                             \
+    const int8_t *ka = base_a + (k0), *kb = base_b + (k0);                                     \
+    _Pragma("unroll") for (int q = 0; q < QA; ++q) {                                           \
+      const int8_t* src = ka + off_a[q];                                                       \
+      __builtin_amdgcn_global_load_lds(src, (lds_void_t*)(st + q * NT * 16), 16, 0, 0);        \
+    }                                                                                          \
+    _Pragma("unroll") for (int q = 0; q < QB; ++q) {                                           \
+      const int8_t* src = kb + off_b[q];                                                       \
+      __builtin_amdgcn_global_load_lds(src, (lds_void_t*)(st + A_BYTES + q * NT * 16), 16, 0, 0); \
+    }                                                                                          \
+  }
 
   const int fr = lane & 15, h = lane >> 4;
   // fragment rows: A tile i row fr; B tile j row fr is weight row
@@ -167,55 +174,79 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64) void k_int8_tile(Int8Ge
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
 
-  const int nk = (K + SK - 1) / SK;
-  issue(0, 0);
-  issue(1, SK);  // slabs past the end are zeros
-  wait_vmcnt<QA + QB>();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-#pragma unroll
-  for (int j = 0; j < TJ; ++j) b0[j] = *(const i32x4_t*)(fb + 4 * SK * j + c0);
-#pragma unroll
-  for (int i = 0; i < TI; ++i) a0[i] = *(const i32x4_t*)(fa + 16 * SK * i + c0);
-  for (int kt = 0; kt < nk; ++kt) {
-    const int cur = (kt & 1) * STAGE, nxt = STAGE - cur;
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) b1[j] = *(const i32x4_t*)(fb + cur + 4 * SK * j + c1);
-#pragma unroll
-    for (int i = 0; i < TI; ++i) a1[i] = *(const i32x4_t*)(fa + cur + 16 * SK * i + c1);
-#pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int j = 0; j < TJ; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b0[j], a0[i], acc[i][j], 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < TI + TJ; ++i) {  // one read among every two or three products
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, TI * TJ / (TI + TJ), 0);
-    }
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+#define SPARQ24_INT8_READ(fa_, fb_, at, c)                                                     \
+  {                                                                                            \
+    _Pragma("unroll") for (int j = 0; j < TJ; ++j) fb_[j] = *(const i32x4_t*)(fb + (at) + 4 * SK * j + (c)); \
+    _Pragma("unroll") for (int i = 0; i < TI; ++i) fa_[i] = *(const i32x4_t*)(fa + (at) + 16 * SK * i + (c)); \
+  }
+#define SPARQ24_INT8_MULTIPLY(fa_, fb_)                                                        \
+  {                                                                                            \
+    _Pragma("unroll") for (int i = 0; i < TI; ++i) _Pragma("unroll") for (int j = 0; j < TJ; ++j) \
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb_[j], fa_[i], acc[i][j], 0, 0, 0); \
+  }
+  const int nk = K / SK;  // whole slabs
+  if (nk) {
+    SPARQ24_INT8_SLAB(0, 0);
+    SPARQ24_INT8_SLAB(1, nk > 1 ? SK : 0);  // past the end: the last one again
+    wait_vmcnt<QA + QB>();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    issue(kt & 1, (kt + 2) * SK);
+    SPARQ24_INT8_READ(a0, b0, 0, c0);
+    for (int kt = 0; kt < nk; ++kt) {
+      const int cur = (kt & 1) * STAGE, nxt = STAGE - cur;
+      SPARQ24_INT8_READ(a1, b1, cur, c1);
+      SPARQ24_INT8_MULTIPLY(a0, b0);
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) b0[j] = *(const i32x4_t*)(fb + nxt + 4 * SK * j + c0);
+      for (int i = 0; i < TI + TJ; ++i) {  // a read among every two or three products
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, TI * TJ / (TI + TJ), 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      SPARQ24_INT8_SLAB(kt & 1, (kt + 2 < nk ? kt + 2 : nk - 1) * SK);
+      SPARQ24_INT8_READ(a0, b0, nxt, c0);
+      SPARQ24_INT8_MULTIPLY(a1, b1);
 #pragma unroll
-    for (int i = 0; i < TI; ++i) a0[i] = *(const i32x4_t*)(fa + nxt + 16 * SK * i + c0);
+      for (int i = 0; i < QA + QB; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 1);
+      }
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int j = 0; j < TJ; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b1[j], a1[i], acc[i][j], 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < TI + TJ; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
-      __builtin_amdgcn_sched_group_barrier(0x008, TI * TJ / (TI + TJ), 1);
+      for (int i = 0; i < TI + TJ; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+        __builtin_amdgcn_sched_group_barrier(0x008, (TI * TJ - QA - QB) / (TI + TJ), 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
+    wait_vmcnt<0>();  // the slabs requested past the end have landed
+    __syncthreads();
   }
-  wait_vmcnt<0>();  // the slabs requested past the end land before LDS is released
-  asm volatile("" ::: "memory");
+  if (K % SK) {  // the rest of K, filled up with zeros
+    auto fill = [&](uint8_t* at, const int8_t* src, unsigned off, int chunk) {
+      i32x4_t v = {0, 0, 0, 0};
+      if (nk * SK + chunk < K) v = *(const i32x4_t*)(src + nk * SK + off);
+      *(i32x4_t*)at = v;
+    };
+#pragma unroll
+    for (int q = 0; q < QA; ++q) {
+      const int p = q * NT + tid;
+      fill(smem + p * 16, base_a, off_a[q], 16 * ((p & 7) ^ ((p >> 3) & 7)));
+    }
+#pragma unroll
+    for (int q = 0; q < QB; ++q) {
+      const int p = q * NT + tid, r = p >> 3;
+      fill(smem + A_BYTES + p * 16, base_b, off_b[q], 16 * ((p & 7) ^ ((r & 3) | ((r >> 2) & 4))));
+    }
+    __syncthreads();
+    SPARQ24_INT8_READ(a0, b0, 0, c0);
+    SPARQ24_INT8_READ(a1, b1, 0, c1);
+    SPARQ24_INT8_MULTIPLY(a0, b0);
+    SPARQ24_INT8_MULTIPLY(a1, b1);
+  }
   // lane: row 16 i + fr, outputs 16 h + 4 j + e
   const int64_t n = n0 + wn * WN + 16 * h;
   float sb[16], bias[16];
