@@ -20,42 +20,104 @@ __device__ inline void int8_store(const Int8Gemm& g, int64_t m, int64_t n, int a
   else ((_Float16*)g.c)[o] = (_Float16)y;
 }
 
-// Few rows: the weight is streamed once, straight into MFMA operands.  A
-// workgroup owns 16 MT x 16 NT outputs, its 8 waves take 256-byte runs of K
-// in turn, and their int32 sums meet in LDS.  Bound by the weight's bytes.
-template <int MT, int NT>
-__global__ __launch_bounds__(512) void k_int8_stream(Int8Gemm g, int64_t ntn) {
-  constexpr int W = 8, RUN = 256;
-  __shared__ i32x4_t red[W][MT * NT][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = lane & 15, h = lane >> 4;
+// Few rows: the weight is streamed once.  A workgroup owns 16 MT x 16 NT
+// outputs; each of its W waves takes slabs of 128 codes of K in turn, with S
+// buffers of its own in LDS (chunks XOR-swizzled by row) that it fills with
+// global_load_lds S - 1 slabs ahead, so no wave waits for another until the
+// int32 sums meet in LDS.  Through LDS because an MFMA operand straight from
+// memory gives adjacent lanes adjacent rows, which the address unit takes at one
+// lane (16 bytes) a cycle: 34 GB/s per CU measured, against 64 bytes a
+// cycle in row order.  Bound by the weight's bytes, for one or two row tiles
+// of a small weight by the launch and the latency of the first slabs.
+template <int MT, int NT, int W, int S>
+__global__ __launch_bounds__(64 * W) void k_int8_stream(Int8Gemm g, int64_t ntn) {
+  constexpr int SK = 128, QA = 2 * MT, QB = 2 * NT, STAGE = (MT + NT) * 16 * SK;
+  constexpr int BYTES = W * S * STAGE > W * MT * NT * 1024 ? W * S * STAGE : W * MT * NT * 1024;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[BYTES];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, h = lane >> 4;
   const int64_t m0 = (blockIdx.x / ntn) * (16 * MT), n0 = (blockIdx.x % ntn) * (16 * NT);
-  const int8_t* ar[MT];
-  const int8_t* br[NT];
+  uint8_t* mine = smem + w * S * STAGE;
+  const int64_t last_m = g.M - 1 - m0, last_n = g.N - 1 - n0;
+  const int8_t *base_a = g.a + m0 * g.lda, *base_b = g.b + n0 * g.ldb;
+  // eight rows of a slab per load; rows past the ends repeat the last, unused
+  int64_t off_a[QA], off_b[QB];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {  // rows past the end repeat the last one, unused
-    const int64_t m = m0 + 16 * i + c;
-    ar[i] = g.a + (m < g.M ? m : g.M - 1) * g.lda;
+  for (int q = 0; q < QA; ++q) {
+    const int64_t r = 8 * q + (lane >> 3);
+    off_a[q] = (r < last_m ? r : last_m) * g.lda + 16 * ((lane & 7) ^ (int)(r & 7));
   }
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t n = n0 + 16 * j + c;
-    br[j] = g.b + (n < g.N ? n : g.N - 1) * g.ldb;
+  for (int q = 0; q < QB; ++q) {
+    const int64_t r = 8 * q + (lane >> 3);
+    off_b[q] = (r < last_n ? r : last_n) * g.ldb + 16 * ((lane & 7) ^ (int)(r & 7));
+  }
+#define SPARQ24_INT8_FETCH(buf, k0)                                                            \
+  {                                                                                            \
+    uint8_t* st = mine + (buf) * STAGE;                                                        \
+    const int8_t *ka = base_a + (k0), *kb = base_b + (k0);                                     \
+    _Pragma("unroll") for (int q = 0; q < QB; ++q) {                                           \
+      const int8_t* src = kb + off_b[q];                                                       \
+      __builtin_amdgcn_global_load_lds(src, (lds_void_t*)(st + QA * 1024 + q * 1024), 16, 0, 0); \
+    }                                                                                          \
+    _Pragma("unroll") for (int q = 0; q < QA; ++q) {                                           \
+      const int8_t* src = ka + off_a[q];                                                       \
+      __builtin_amdgcn_global_load_lds(src, (lds_void_t*)(st + q * 1024), 16, 0, 0);           \
+    }                                                                                          \
   }
   i32x4_t acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
-  for (int64_t kb = w * RUN; kb < g.K; kb += W * RUN) {
+  const int K = (int)g.K, nk = K / SK;  // whole slabs
+  if (w < nk) {
+    const int last = nk - 1 - (nk - 1 - w) % W;  // this wave's last slab, asked for again past the end
 #pragma unroll
-    for (int s = 0; s < RUN / 64; ++s) {
-      const int64_t k = kb + 64 * s + 16 * h;
+    for (int s = 0; s + 1 < S; ++s) SPARQ24_INT8_FETCH(s, (w + s * W < last ? w + s * W : last) * SK);
+    int buf = 0;
+    for (int kt = w; kt < nk; kt += W) {
+      const int next = kt + (S - 1) * W;
+      const int to = buf == 0 ? S - 1 : buf - 1;
+      SPARQ24_INT8_FETCH(to, (next < last ? next : last) * SK);
+      wait_vmcnt<(S - 1) * (QA + QB)>();
+      asm volatile("" ::: "memory");
+      const uint8_t* st = mine + buf * STAGE + c * SK;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        i32x4_t af[MT], bf[NT];
+        const int ch = ((4 * x + h) ^ (c & 7)) * 16;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) af[i] = *(const i32x4_t*)(st + 16 * SK * i + ch);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) bf[j] = *(const i32x4_t*)(st + 16 * SK * (MT + j) + ch);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i], bf[j], acc[i][j], 0, 0, 0);
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the buffer is read before it is filled again
+      asm volatile("" ::: "memory");
+      buf = buf + 1 == S ? 0 : buf + 1;
+    }
+    wait_vmcnt<0>();  // what was asked for past the end has landed
+    asm volatile("" ::: "memory");
+  }
+  if (w == nk % W) {  // the rest of K, zeros behind it
+    for (int k = nk * SK + 16 * h; k - 16 * h < K; k += 64) {
       const i32x4_t zero = {0, 0, 0, 0};
       i32x4_t af[MT], bf[NT];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) af[i] = k < g.K ? *(const i32x4_t*)(ar[i] + k) : zero;
+      for (int i = 0; i < MT; ++i) {
+        const int64_t r = 16 * i + c;
+        af[i] = k < K ? *(const i32x4_t*)(base_a + (r < last_m ? r : last_m) * g.lda + k) : zero;
+      }
 #pragma unroll
-      for (int j = 0; j < NT; ++j) bf[j] = k < g.K ? *(const i32x4_t*)(br[j] + k) : zero;
+      for (int j = 0; j < NT; ++j) {
+        const int64_t r = 16 * j + c;
+        bf[j] = k < K ? *(const i32x4_t*)(base_b + (r < last_n ? r : last_n) * g.ldb + k) : zero;
+      }
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -63,15 +125,17 @@ __global__ __launch_bounds__(512) void k_int8_stream(Int8Gemm g, int64_t ntn) {
           acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i], bf[j], acc[i][j], 0, 0, 0);
     }
   }
+  __syncthreads();  // every wave is done with its buffers
+  i32x4_t* red = (i32x4_t*)smem;  // [W][MT * NT][64]
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) red[w][i * NT + j][lane] = acc[i][j];
+    for (int j = 0; j < NT; ++j) red[(w * MT * NT + i * NT + j) * 64 + lane] = acc[i][j];
   __syncthreads();
   for (int t = w; t < MT * NT; t += W) {
-    i32x4_t s = red[0][t][lane];
+    i32x4_t s = red[t * 64 + lane];
 #pragma unroll
-    for (int q = 1; q < W; ++q) s += red[q][t][lane];
+    for (int q = 1; q < W; ++q) s += red[(q * MT * NT + t) * 64 + lane];
     const int64_t m = m0 + 16 * (t / NT) + 4 * h, n = n0 + 16 * (t % NT) + c;
 #pragma unroll
     for (int e = 0; e < 4; ++e) int8_store(g, m + e, n, s[e]);
@@ -81,12 +145,22 @@ __global__ __launch_bounds__(512) void k_int8_stream(Int8Gemm g, int64_t ntn) {
 // Many rows: a BM x BN tile per workgroup, waves of WM x 64 on
 // v_mfma_i32_16x16x64_i8.  Slabs of 128 codes go from memory straight into LDS
 // (global_load_lds) into two buffers; their 16-byte chunks are XOR-swizzled by
-// row.  A slab is two steps of 64 codes, and the fragments of a step are read
-// into registers while the products of the step before run, across slabs
-// too, so the matrix pipe waits for neither LDS nor the barrier: between a
+// row.  A slab is two steps of 64 codes.  Rows past the ends repeat the last; a
+// rest of K is filled up with zeros.  Two schedules:
+// Mixed (small tiles, several workgroups per CU): the fragments of a step are
+// read while the products of the step before run, across slabs too; between a
 // slab's two steps every wave has its last fragments of it and the next slab
 // has landed (one barrier), and the slab after that starts into the freed
-// buffer.  Rows past the ends repeat the last; a rest of K is filled up with zeros.
+// buffer.
+// In turns (PP, eight waves, two per SIMD): waves 4..7 run half a step behind
+// waves 0..3, with a barrier after every half, so on each SIMD one wave
+// multiplies (at raised priority) while the other reads and requests slabs.
+// With phases p between barriers, waves 0..3 read step s at p = 2 s, waves
+// 4..7 at 2 s + 1.  Slab t + 1 is requested by the reads of step 2 t, when both
+// groups have read all of slab t - 1 (phases up to 4 t - 1), and waited for at
+// the end of phase 4 t + 3, before anyone reads it.
+// 4096 x 14336 x 4096, bf16 out: mixed 267 us, in turns 253 us; bound by LDS
+// (192 KB of fragments and 64 KB of slabs for 2048 cycles of products per slab).
 // 16 outputs n .. n + 15 of row m: 16-byte stores where `wide` says that all
 // are inside and aligned, else one by one.
 template <class T>
@@ -113,7 +187,7 @@ __device__ inline void int8_store16(const Int8Gemm& g, int64_t m, int64_t n, con
   }
 }
 
-template <int BM, int BN, int WM>
+template <int BM, int BN, int WM, bool PP>
 __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64) void k_int8_tile(Int8Gemm g) {
   constexpr int WN = 64, NWN = BN / WN, NT = (BM / WM) * NWN * 64;
   constexpr int TI = WM / 16, TJ = 4, SK = 128;
@@ -185,7 +259,43 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64) void k_int8_tile(Int8Ge
         acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb_[j], fa_[i], acc[i][j], 0, 0, 0); \
   }
   const int nk = K / SK;  // whole slabs
-  if (nk) {
+  auto barrier = [] {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr int kLgkm0 = 0xC07F, kAll0 = 0x0070;  // s_waitcnt lgkmcnt(0); with vmcnt(0)
+  if (PP && nk) {
+    const bool late = w >= 4;
+    SPARQ24_INT8_SLAB(0, 0);
+    SPARQ24_INT8_SLAB(1, nk > 1 ? SK : 0);  // past the end: the last one again
+    wait_vmcnt<0>();
+    barrier();
+    if (late) barrier();
+    for (int kt = 0; kt < nk; ++kt) {
+      const int cur = (kt & 1) * STAGE;
+      SPARQ24_INT8_READ(a0, b0, cur, c0);
+      if (kt) SPARQ24_INT8_SLAB((kt & 1) ^ 1, (kt + 1 < nk ? kt + 1 : nk - 1) * SK);
+      __builtin_amdgcn_s_waitcnt(kLgkm0);
+      barrier();
+      __builtin_amdgcn_s_setprio(1);
+      SPARQ24_INT8_MULTIPLY(a0, b0);
+      __builtin_amdgcn_s_setprio(0);
+      barrier();
+      SPARQ24_INT8_READ(a0, b0, cur, c1);
+      if (late) __builtin_amdgcn_s_waitcnt(kAll0);
+      else __builtin_amdgcn_s_waitcnt(kLgkm0);
+      barrier();
+      __builtin_amdgcn_s_setprio(1);
+      SPARQ24_INT8_MULTIPLY(a0, b0);
+      __builtin_amdgcn_s_setprio(0);
+      if (!late) wait_vmcnt<0>();
+      barrier();
+    }
+    if (!late) barrier();
+  } else if (nk) {
     SPARQ24_INT8_SLAB(0, 0);
     SPARQ24_INT8_SLAB(1, nk > 1 ? SK : 0);  // past the end: the last one again
     wait_vmcnt<QA + QB>();
@@ -222,6 +332,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64) void k_int8_tile(Int8Ge
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+  }
+  if (nk) {
     wait_vmcnt<0>();  // the slabs requested past the end have landed
     __syncthreads();
   }
@@ -270,24 +382,51 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64) void k_int8_tile(Int8Ge
 }
 
 hipError_t launch_int8_gemm(const Int8Gemm& g, hipStream_t s) {
-  auto few = [&]<int MT, int NT>() {
+  auto few = [&]<int MT, int NT, int W, int S>() {
     const int64_t ntm = (g.M + 16 * MT - 1) / (16 * MT), ntn = (g.N + 16 * NT - 1) / (16 * NT);
-    hipLaunchKernelGGL((k_int8_stream<MT, NT>), dim3((unsigned)(ntm * ntn)), dim3(512), 0, s, g, ntn);
+    hipLaunchKernelGGL((k_int8_stream<MT, NT, W, S>), dim3((unsigned)(ntm * ntn)), dim3(64 * W), 0, s, g, ntn);
     return hipGetLastError();
   };
-  auto tile = [&]<int BM, int BN, int WM>() {
+  auto tile = [&]<int BM, int BN, int WM, bool PP>() {
     const int64_t n = ((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN);
-    hipLaunchKernelGGL((k_int8_tile<BM, BN, WM>), dim3((unsigned)n), dim3((BM / WM) * (BN / 64) * 64), 0, s, g);
+    hipLaunchKernelGGL((k_int8_tile<BM, BN, WM, PP>), dim3((unsigned)n), dim3((BM / WM) * (BN / 64) * 64), 0, s, g);
     return hipGetLastError();
   };
-  if (g.M <= 16) return few.template operator()<1, 1>();
-  if (g.M <= 32) return few.template operator()<2, 1>();
-  if (g.M <= 64) return few.template operator()<4, 2>();
   auto tiles = [&](int bm, int bn) { return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
+  // k_int8_stream takes about 2.3 us + 1.5 us per 16-row group of a and b that a
+  // CU streams (K = 4096): (1, 1) and (1, 4) for 1 x 4096 and 1 x 14336: 6.0, 11.3;
+  // (2, 2) 7.6, (4, 2) 9.3, (4, 4) 13.7 us for 64, 128, 256 x 4096.  Past one round
+  // of (4, 4) on every CU (100 x 14336: 27 us) the tiles win (21 us).
   const int cus = device_cu_count();
-  if (tiles(256, 256) >= cus) return tile.template operator()<256, 256, 128>();
-  if (tiles(128, 128) >= cus / 2) return tile.template operator()<128, 128, 64>();
-  return tile.template operator()<64, 64, 64>();
+  const bool far_rows = g.lda >= (1 << 23) || g.ldb >= (1 << 23);  // past the tiles' 32-bit offsets
+  int mt = 0, nt = 0;
+  int64_t best = INT64_MAX;
+  for (int i = 1; i <= 4; i *= 2)
+    for (int j = 1; j <= 4; j *= 2) {
+      const int64_t rounds = (tiles(16 * i, 16 * j) + cus - 1) / cus;
+      if (rounds * (i + j) < best) best = rounds * (i + j), mt = i, nt = j;
+    }
+  if (best <= 8 || far_rows) {
+    switch (mt * 8 + nt) {
+      case 9: return few.template operator()<1, 1, 8, 3>();
+      case 10: return few.template operator()<1, 2, 8, 2>();
+      case 12: return few.template operator()<1, 4, 8, 2>();
+      case 17: return few.template operator()<2, 1, 8, 2>();
+      case 18: return few.template operator()<2, 2, 8, 2>();
+      case 20: return few.template operator()<2, 4, 4, 2>();
+      case 33: return few.template operator()<4, 1, 8, 2>();
+      case 34: return few.template operator()<4, 2, 4, 2>();
+      default: return few.template operator()<4, 4, 4, 2>();
+    }
+  }
+  // The largest tile that still gives every CU one, else four small ones per CU
+  // (a 64 x 64 tile takes 32 KB of LDS), else the middle.  At K = 4096, us for
+  // 256 x 256 / 256 x 128 / 128 x 128 / 64 x 64: 4096 x 14336: 256 / 284 / 304 /
+  // 416; 2048 x 4096: 49 / 37 / 41 / 58; 1024 x 4096: 46 / 30 / 27 / 26.
+  if (tiles(256, 256) >= cus) return tile.template operator()<256, 256, 128, true>();
+  if (tiles(256, 128) >= cus) return tile.template operator()<256, 128, 64, false>();
+  if (tiles(64, 64) > 4 * cus) return tile.template operator()<128, 128, 64, false>();
+  return tile.template operator()<64, 64, 64, false>();
 }
 
 }  // namespace sparq24
