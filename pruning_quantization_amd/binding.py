@@ -13,7 +13,9 @@ each one.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+import struct
 from ctypes import POINTER, c_double, c_float, c_int32, c_int64, c_size_t, c_uint8, c_void_p
 from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
@@ -113,8 +115,9 @@ def lib(path: Optional[str] = None):
         "sparq24_int8_gemm": [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
                               c_int64, c_int64, c_void_p, c_int32, c_void_p, c_int64, c_void_p,
                               POINTER(c_size_t), c_void_p],
-        "sparq24_kv_append": [POINTER(CKvCache), POINTER(CKvSeqs), T, T, c_void_p],
-        "sparq24_kv_attention": [POINTER(CKvCache), POINTER(CKvSeqs), T, c_float, c_int32, c_int64,
+        # descriptors by address: packed bytes, or byref() of the structures
+        "sparq24_kv_append": [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p],
+        "sparq24_kv_attention": [c_void_p, c_void_p, c_void_p, c_float, c_int32, c_int64,
                                  c_void_p, c_void_p, c_void_p, POINTER(c_size_t), c_void_p],
         "sparq24_quantize_rot": [T, c_int32, Q, c_void_p, c_void_p, c_void_p, c_void_p,
                                  POINTER(c_size_t), c_void_p],
@@ -644,26 +647,35 @@ def fp8_gemm(codes_a: torch.Tensor, scale_a: torch.Tensor, codes_b: torch.Tensor
     return out
 
 
-def _on_device(*ts: Optional[torch.Tensor]):
-    """Checks that all tensors are on one GPU and returns it."""
-    dev = ts[0].device
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    if dev.type != "cuda":
-        raise ValueError(f"tensors must be on a GPU, got {dev}")
-    return dev
+# The calls below are made once per layer and decoded token, so their marshalling
+# is kept short: descriptors are packed as bytes (layouts of CKvCache, CKvSeqs
+# and CTensor) instead of built as ctypes structures.
+_PACK_KVCACHE = struct.Struct("PPPPi4xqqqq").pack
+_PACK_KVSEQS = struct.Struct("PqqPPqq").pack
+_PACK_TENSOR = struct.Struct("Pi4xqqqqqq").pack
 
 
-def _call(fn: str, dev: torch.device, *args) -> None:
+def _device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    """Checks that all tensors are on one GPU and returns its index."""
+    i = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != i:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    if i < 0:
+        raise ValueError(f"tensors must be on a GPU, got {first.device}")
+    return i
+
+
+def _call(fn: str, dev: int, *args) -> None:
     """Calls ``fn`` with the device's current stream, that device current."""
-    f = getattr(lib(), fn)
-    if dev.index == torch.cuda.current_device():
-        st = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    f = getattr(_lib or lib(), fn)
+    if dev == torch._C._cuda_getDevice():
+        st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
-    _check(fn, st)
+            st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        raise Sparq24Error(fn, st)
 
 
 def _vector(t: torch.Tensor, n: int, dtype: torch.dtype, name: str) -> int:
@@ -682,30 +694,37 @@ def int8_gemm(codes_a: torch.Tensor, scale_a: torch.Tensor, codes_b: torch.Tenso
     bits), exact int32 sums -> ``dtype`` (fp32, bf16 or fp16) [..., N].  K is a
     multiple of 16; the rows of either operand and of ``out`` may be strided;
     ``bias`` is fp32 [N]."""
-    dev = _on_device(codes_a, scale_a, codes_b, scale_b, bias, out)
+    dev = _device(codes_a, scale_a, codes_b, scale_b, bias, out)
     if codes_a.dtype != torch.int8 or codes_b.dtype != torch.int8:
         raise TypeError(f"int8 codes expected, got {codes_a.dtype} and {codes_b.dtype}")
-    if codes_b.dim() != 2 or codes_a.dim() < 1 or codes_a.shape[-1] != codes_b.shape[1]:
-        raise ValueError(f"shapes {tuple(codes_a.shape)} and {tuple(codes_b.shape)} do not multiply")
+    lead = codes_a.shape
+    if codes_b.dim() != 2 or not lead or lead[-1] != codes_b.shape[1]:
+        raise ValueError(f"shapes {tuple(lead)} and {tuple(codes_b.shape)} do not multiply")
     n, k = codes_b.shape
-    a = codes_a if codes_a.dim() == 2 else codes_a.view(-1, k)
+    a = codes_a if len(lead) == 2 else codes_a.view(math.prod(lead[:-1]), k)
     m = a.shape[0]
-    if k > 1 and ((m and a.stride(1) != 1) or (n and codes_b.stride(1) != 1)):
+    lda, a1 = a.stride()
+    ldb, b1 = codes_b.stride()
+    if k > 1 and ((m and a1 != 1) or (n and b1 != 1)):
         raise ValueError("codes must be contiguous along K")
     if out is None:
-        out = torch.empty(*codes_a.shape[:-1], n, dtype=dtype, device=dev)
-    elif out.shape != (*codes_a.shape[:-1], n):
+        c = out = codes_a.new_empty((m, n), dtype=dtype)
+        if len(lead) != 2:
+            out = c.view(*lead[:-1], n)
+    elif out.shape != (*lead[:-1], n):
         raise ValueError(f"out has shape {tuple(out.shape)}")
+    else:
+        c = out if len(lead) == 2 else out.view(m, n)
+    ldc, c1 = c.stride()
+    if n > 1 and m and c1 != 1:
+        raise ValueError("out must be contiguous along N")
     if out.dtype not in _DT:
         raise TypeError(f"unsupported dtype {out.dtype}")
-    c = out if out.dim() == 2 else out.view(-1, n)
-    if n > 1 and m and c.stride(1) != 1:
-        raise ValueError("out must be contiguous along N")
-    _call("sparq24_int8_gemm", dev, a.data_ptr(), a.stride(0),
-          _vector(scale_a, m, torch.float32, "scale_a"), m, codes_b.data_ptr(), codes_b.stride(0),
+    _call("sparq24_int8_gemm", dev, a.data_ptr(), lda,
+          _vector(scale_a, m, torch.float32, "scale_a"), m, codes_b.data_ptr(), ldb,
           _vector(scale_b, n, torch.float32, "scale_b"), n, k,
           None if bias is None else _vector(bias, n, torch.float32, "bias"), _DT[out.dtype],
-          c.data_ptr(), c.stride(0), None, None)
+          c.data_ptr(), ldc, None, None)
     return out
 
 
@@ -734,60 +753,73 @@ def kv_cache(blocks: int, heads: int, dim: int, tokens: int = 64, q: QLike = ("i
                    torch.zeros(blocks, heads, dtype=torch.float32, device=device))
 
 
-def _c_cache(cache: KVCache) -> CKvCache:
+def _c_cache(cache: KVCache):
+    """(sparq24_kvcache as bytes, shape of the K codes)."""
     k, ks, v, vs = cache
-    if k.dim() != 4 or v.dim() != 4:
+    shape = k.shape
+    if len(shape) != 4 or v.dim() != 4:
         raise ValueError("cache codes must be [blocks, heads, tokens, dim] and [blocks, heads, dim, tokens]")
-    blocks, heads, tokens, dim = k.shape
+    blocks, heads, tokens, dim = shape
     if v.shape != (blocks, heads, dim, tokens) or k.dtype != v.dtype:
-        raise ValueError(f"cache codes {tuple(k.shape)} {k.dtype} and {tuple(v.shape)} {v.dtype} do not match")
-    if k.dtype not in (torch.int8, torch.uint8):
+        raise ValueError(f"cache codes {tuple(shape)} {k.dtype} and {tuple(v.shape)} {v.dtype} do not match")
+    if k.dtype == torch.int8:
+        fmt = Q_INT
+    elif k.dtype == torch.uint8:
+        fmt = Q_FP8
+    else:
         raise TypeError(f"cache codes are int8 or uint8 (e4m3), got {k.dtype}")
     if not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError("cache codes must be contiguous")
     n = blocks * heads
-    return CKvCache(k.data_ptr(), _vector(ks, n, torch.float32, "k_scale"), v.data_ptr(),
-                    _vector(vs, n, torch.float32, "v_scale"),
-                    Q_INT if k.dtype == torch.int8 else Q_FP8, blocks, heads, tokens, dim)
+    return _PACK_KVCACHE(k.data_ptr(), _vector(ks, n, torch.float32, "k_scale"), v.data_ptr(),
+                         _vector(vs, n, torch.float32, "v_scale"), fmt, blocks, heads, tokens,
+                         dim), shape
 
 
 def _c_seqs(x: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
-            cu_tokens: Optional[torch.Tensor]) -> CKvSeqs:
-    """Sequences of the token rows ``x``: [total, heads, dim] with ``cu_tokens``,
-    or [seqs, n, heads, dim]."""
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or (
-            block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [seqs, max blocks] with contiguous rows")
+            cu_tokens: Optional[torch.Tensor]):
+    """(sparq24_kvseqs as bytes, (sequences, table width, token rows, bool
+    cu_tokens)) of the token rows ``x``: [total, heads, dim] with
+    ``cu_tokens``, or [seqs, n, heads, dim]."""
+    if block_table.dim() != 2 or block_table.dtype != torch.int32:
+        raise ValueError("block_table must be int32 [seqs, max blocks]")
     seqs, width = block_table.shape
+    stride, inner = block_table.stride()
+    if width > 1 and inner != 1:
+        raise ValueError("block_table must have contiguous rows")
+    shape = x.shape
     if cu_tokens is None:
-        if x.dim() != 4 or x.shape[0] != seqs:
-            raise ValueError(f"without cu_tokens token rows are [seqs, n, heads, dim], got {tuple(x.shape)}")
-        total = seqs * x.shape[1]
+        if len(shape) != 4 or shape[0] != seqs:
+            raise ValueError(f"without cu_tokens token rows are [seqs, n, heads, dim], got {tuple(shape)}")
+        total, cu = seqs * shape[1], 0
     else:
-        if x.dim() != 3:
-            raise ValueError(f"with cu_tokens token rows are [total, heads, dim], got {tuple(x.shape)}")
-        total = x.shape[0]
-    return CKvSeqs(block_table.data_ptr() if width else None, width, block_table.stride(0),
-                   _vector(seq_lens, seqs, torch.int32, "seq_lens"),
-                   None if cu_tokens is None else _vector(cu_tokens, seqs + 1, torch.int32, "cu_tokens"),
-                   seqs, total)
+        if len(shape) != 3:
+            raise ValueError(f"with cu_tokens token rows are [total, heads, dim], got {tuple(shape)}")
+        total, cu = shape[0], _vector(cu_tokens, seqs + 1, torch.int32, "cu_tokens")
+    return _PACK_KVSEQS(block_table.data_ptr() if width else 0, width, stride,
+                        _vector(seq_lens, seqs, torch.int32, "seq_lens"), cu, seqs,
+                        total), (seqs, width, total, cu != 0)
 
 
-def _c_rows(x: torch.Tensor) -> CTensor:
-    """Descriptor of token rows: one batch entry per token."""
+def _c_rows(x: torch.Tensor) -> bytes:
+    """sparq24_tensor of token rows as bytes: one batch entry per token."""
     if x.dtype not in _DT:
         raise TypeError(f"unsupported dtype {x.dtype}")
-    if x.dim() == 4:
-        a, n = x.shape[:2]
-        if a > 1 and n > 1 and x.stride(0) != n * x.stride(1):
+    shape, stride = x.shape, x.stride()
+    if len(shape) == 4:
+        a, n = shape[0], shape[1]
+        if a > 1 and n > 1 and stride[0] != n * stride[1]:
             raise ValueError("the sequences of token rows must be evenly spaced (or contiguous)")
-        total, ts = a * n, x.stride(1) if n > 1 else x.stride(0)
+        total, ts = a * n, stride[1] if n > 1 else stride[0]
     else:
-        total, ts = x.shape[0], x.stride(0)
-    heads, dim = x.shape[-2:]
-    if dim > 1 and x.stride(-1) != 1:
+        total, ts = shape[0], stride[0]
+    if shape[-1] > 1 and stride[-1] != 1:
         raise ValueError("token rows must be contiguous along dim")
-    return CTensor(x.data_ptr(), _DT[x.dtype], total, heads, dim, ts, x.stride(-2), 1)
+    return _PACK_TENSOR(x.data_ptr(), _DT[x.dtype], total, shape[-2], shape[-1], ts, stride[-2], 1)
+
+
+#: Workspace bytes of kv_attention by everything they depend on (shapes only).
+_kv_workspace: dict = {}
 
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
@@ -800,11 +832,11 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: tor
     its last positions; position p lives in block ``block_table[b, p // tokens]``
     (int32).  A block's scale grows when a new element exceeds it, and the
     block's earlier codes are then coded again."""
-    dev = _on_device(k, v, block_table, seq_lens, cu_tokens, *cache)
+    dev = _device(k, v, block_table, seq_lens, cu_tokens, *cache)
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError(f"k {tuple(k.shape)} {k.dtype} and v {tuple(v.shape)} {v.dtype} do not match")
-    c, q = _c_cache(cache), _c_seqs(k, block_table, seq_lens, cu_tokens)
-    _call("sparq24_kv_append", dev, c, q, _c_rows(k), _c_rows(v))
+    _call("sparq24_kv_append", dev, _c_cache(cache)[0],
+          _c_seqs(k, block_table, seq_lens, cu_tokens)[0], _c_rows(k), _c_rows(v))
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
@@ -822,26 +854,32 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     the tokens up to its own; ``window`` > 0: the last ``window`` of these.
     ``scale`` defaults to dim ** -0.5.  A row that sees nothing gives zeros and
     an lse of -inf."""
-    dev = _on_device(q, block_table, seq_lens, cu_tokens, out, lse, workspace, *cache)
-    c, s, x = _c_cache(cache), _c_seqs(q, block_table, seq_lens, cu_tokens), _c_rows(q)
+    dev = _device(q, block_table, seq_lens, cu_tokens, out, lse, workspace, *cache)
+    c, shape = _c_cache(cache)
+    s, sizes = _c_seqs(q, block_table, seq_lens, cu_tokens)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = q.new_empty(q.shape)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's shape and type")
     if lse is None:
         if return_lse:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+            lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
     elif lse.shape != q.shape[:-1] or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 of q's shape without dim")
-    args = (c, s, x, q.shape[-1] ** -0.5 if scale is None else float(scale), int(bool(causal)),
-            int(window), out.data_ptr(), _ptr(lse))
-    if workspace is None:
-        n = c_size_t(0)
-        _call("sparq24_kv_attention", dev, *args, None, n)
-        ws = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
-    else:
-        ws, n = workspace, c_size_t(workspace.numel() * workspace.element_size())
-    _call("sparq24_kv_attention", dev, *args, _ptr(ws), n if ws is not None else None)
+    args = (c, s, _c_rows(q), q.shape[-1] ** -0.5 if scale is None else float(scale),
+            1 if causal else 0, int(window), out.data_ptr(), None if lse is None else lse.data_ptr())
+    ws = workspace
+    if ws is None:
+        key = (dev, *sizes, q.shape[-2], *shape[1:])
+        n = _kv_workspace.get(key)
+        if n is None:
+            size = c_size_t(0)
+            _call("sparq24_kv_attention", dev, *args, None, size)
+            n = _kv_workspace[key] = size.value
+        if n:
+            ws = q.new_empty(n, dtype=torch.uint8)
+    _call("sparq24_kv_attention", dev, *args, None if ws is None else ws.data_ptr(),
+          None if ws is None else c_size_t(ws.numel() * ws.element_size()))
     return (out, lse) if return_lse else out
 
 

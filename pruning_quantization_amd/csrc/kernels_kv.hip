@@ -208,6 +208,7 @@ struct KvAttnArgs {
   KvAttn a;
   int g;            // query heads per kv head
   int rb;           // rows (token, head of the group) per row tile
+  int above, most;  // sequences with more than `above` and at most `most` rows
   int64_t target;   // items that the launch aims at
   int64_t items;    // items that it has room for
   int cmin;         // least tiles of a chunk
@@ -226,6 +227,10 @@ __device__ inline int first_seen(int pos, int window) {
 __device__ inline KvWork kv_work(const KvAttnArgs& w, const SeqRows& r) {
   KvWork k;
   k.rows = r.n * w.g;
+  if (k.rows <= w.above || k.rows > w.most) {
+    k.rows = k.rt = k.lo = k.tiles = 0;
+    return k;
+  }
   k.rt = (k.rows + w.rb - 1) / w.rb;
   const int hi = (int)(r.len < w.a.q.cap ? r.len : w.a.q.cap);
   const int lo = first_seen(r.len - r.n, w.a.window);
@@ -268,7 +273,7 @@ __device__ inline bool kv_item(const KvAttnArgs& w, int64_t id, int lane, KvItem
   it.chunks = (int)((it.k.tiles + len - 1) / len);
   if (it.chunks < 1) it.chunks = 1;
   it.chunk = (int)(local / it.k.rt);
-  it.rt = (int)(local % it.k.rt);
+  it.rt = it.k.rt - 1 - (int)(local % it.k.rt);  // the last rows see the most: first
   it.head = (int)(id % H);
   it.slot = id;
   if (w.plan && local == 0 && it.head == 0 && threadIdx.x == 0) {
@@ -283,6 +288,148 @@ __device__ inline void kv_store_out(const KvAttn& a, int64_t o, float v) {
   else ((_Float16*)a.out)[o] = (_Float16)v;
 }
 
+// Query row r of the row tile (column c of the MFMA tiles), in fp16 times a power
+// of two: elements d(j) .. d(j) + 7 of lane group h into qf[j].
+struct KvRow {
+  float c;       // scale * log2 e / that power of two
+  int lim, low;  // last and first position seen (lim -1: no row)
+};
+template <int NJ, class F>
+__device__ inline KvRow kv_query(const KvAttnArgs& p, const KvItem& it, int r, f16x8_t (&qf)[NJ], F&& d) {
+  const KvAttn& a = p.a;
+  const bool valid = r < it.k.rows;
+  const int i = valid ? r / p.g : 0, hq = valid ? it.head * p.g + r % p.g : 0;
+  const int pos = it.r.len - it.r.n + i;
+  const int hi_all = (int)(it.r.len < a.q.cap ? it.r.len : a.q.cap);
+  KvRow row;
+  row.lim = !valid ? -1 : (a.causal && pos + 1 < hi_all ? pos + 1 : hi_all) - 1;
+  row.low = first_seen(pos, a.window);
+  const char* x = a.x + (it.r.first + (int64_t)i) * a.ts + hq * a.hs;
+  u32x4v raw[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) raw[j] = *(const u32x4v*)(x + 2 * d(j));
+  float am = 0.0f;
+  auto at = [&](int j, int e) {
+    const uint32_t v = (raw[j][e / 2] >> (16 * (e & 1))) & 0xFFFFu;
+    return a.dtype == 1 ? BF16T::to_f32(v) : F16T::to_f32(v);
+  };
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) am = __builtin_fmaxf(am, __builtin_fabsf(at(j, e)));
+  am = __builtin_fmaxf(am, __shfl_xor(am, 16, 64));
+  am = __builtin_fmaxf(am, __shfl_xor(am, 32, 64));
+  int ex = (int)(__float_as_uint(am) >> 23);  // 0: zero or subnormal, 255: inf
+  ex = ex < 64 ? 64 : (ex > 254 ? 127 : ex);
+  const float up = __uint_as_float((uint32_t)(127 + 13 - (ex - 127)) << 23);
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) qf[j][e] = (_Float16)(at(j, e) * up);
+  row.c = a.scale * 1.44269504088896340736f * __uint_as_float((uint32_t)(127 - 13 + (ex - 127)) << 23);
+  return row;
+}
+
+// Block scales of the 16 tokens of a lane group.  A zero scale counts as 2^-80:
+// its codes are zeros.
+struct KvScales {
+  bool there;
+  float ks, lv, rv;  // K scale, log2 and reciprocal of V's
+};
+__device__ inline KvScales kv_scales(bool there, float ks, float vs) {
+  KvScales k;
+  const float vse = vs < 0x1p-80f ? 0x1p-80f : vs;
+  k.there = there;
+  k.ks = ks;
+  k.lv = there ? __builtin_amdgcn_logf(vse) : 0.0f;
+  k.rv = there ? 1.0f / vse : 1.0f;
+  return k;
+}
+
+// Scores of a tile (lane: one row, tokens tok0 .. tok0 + 15) to weights: masks
+// (where `edge`), the row's reference m, the sum l and the rescaling of O.
+template <int NU>
+__device__ inline void kv_weights(f32x4v (&sc)[4], const KvRow& row, const KvScales& k, int tok0, bool edge,
+                                  float& m, float& l, f32x4v (&o)[NU], bool& far, f16x8_t (&pf)[2]) {
+  float ck = k.there ? row.c * k.ks : 1.0f;
+  ck = ck < 0x1p-120f ? 0x1p-120f : ck;
+  if (edge) {
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int tok = tok0 + 4 * mt + e;
+        if (!k.there || tok > row.lim || tok < row.low) sc[mt][e] = kNegInf;
+      }
+  }
+  float mx = kNegInf;
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mx = __builtin_fmaxf(mx, sc[mt][e]);
+  mx = __builtin_fmaf(mx, ck, k.lv);
+  mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16, 64));
+  mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
+  if (__any(mx - m > kTopMost)) {  // -inf - -inf is NaN: no new reference
+    const float nm = mx - m > kTopMost ? mx - kTopSet : m;
+    const float al = nm == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - nm);
+    m = nm;
+    far |= __any(__builtin_fabsf(nm) > kFarTop && nm != kNegInf);
+    l *= al;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) o[u] *= al;
+  }
+  const float ref = m == kNegInf ? 0.0f : m, off = k.lv - ref;
+  if (far) {
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[mt][e] = __builtin_fmaf(sc[mt][e], ck, k.lv) - ref;
+  } else {
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[mt][e] = __builtin_fmaf(sc[mt][e], ck, off);
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float w = __builtin_amdgcn_exp2f(sc[mt][e]);
+      sum += w;
+      pf[mt / 2][4 * (mt & 1) + e] = (_Float16)w;
+    }
+  l = __builtin_fmaf(sum, k.rv, l);
+}
+
+__device__ inline float kv_lse(float top, float sum) {
+  return sum == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
+}
+
+// Tiles and limits of a row tile within its chunk.
+struct KvRange {
+  int t0, t1;       // tiles
+  int lo, hi;       // tokens that some row sees
+  int least, from;  // tokens from .. least - 1 are seen by every row
+};
+__device__ inline KvRange kv_range(const KvAttnArgs& p, const KvItem& it, int r0, int r1) {
+  const KvAttn& a = p.a;
+  const int pos0 = it.r.len - it.r.n, i0 = r0 / p.g, i1 = (r1 - 1) / p.g;
+  const int hi_all = (int)(it.r.len < a.q.cap ? it.r.len : a.q.cap);
+  KvRange k;
+  k.hi = a.causal && pos0 + i1 + 1 < hi_all ? pos0 + i1 + 1 : hi_all;
+  k.lo = first_seen(pos0 + i0, a.window);
+  k.least = a.causal && pos0 + i0 + 1 < k.hi ? pos0 + i0 + 1 : k.hi;
+  k.from = first_seen(pos0 + i1, a.window);
+  k.t0 = it.k.lo + it.chunk * it.len;
+  k.t1 = k.t0 + it.len;
+  if (k.t1 > it.k.lo + it.k.tiles) k.t1 = it.k.lo + it.k.tiles;
+  if (k.t0 < k.lo / kKvTile) k.t0 = k.lo / kKvTile;
+  if (k.t1 > (k.hi + kKvTile - 1) / kKvTile) k.t1 = (k.hi + kKvTile - 1) / kKvTile;
+  return k;
+}
+
 // Few rows per kv head (decoding): QT tiles of 16 rows, four waves that take
 // the chunk's tiles in turn, K and V straight from memory into MFMA operands.
 // Bound by the cache's bytes.
@@ -294,48 +441,12 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
   KvItem it;
   if (!kv_item(p, blockIdx.x, lane, it)) return;
   const int H = a.c.heads, tsh = a.c.tsh, T = 1 << tsh;
-  const int pos0 = it.r.len - it.r.n;  // position of the first query token
-  const int hi_all = (int)(it.r.len < a.q.cap ? it.r.len : a.q.cap);
-
-  // query rows of this lane's column, in fp16 times a power of two
   f16x8_t qf[QT][2 * NS];
-  float cq[QT];
-  int lim[QT], low[QT];
+  KvRow row[QT];
 #pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    const int r = it.rt * p.rb + 16 * t + c16;
-    const bool valid = r < it.k.rows;
-    const int i = valid ? r / p.g : 0, hq = valid ? it.head * p.g + r % p.g : 0;
-    const int pos = pos0 + i;
-    lim[t] = !valid ? -1 : (a.causal && pos + 1 < hi_all ? pos + 1 : hi_all) - 1;
-    low[t] = first_seen(pos, a.window);
-    const char* x = a.x + (it.r.first + (int64_t)i) * a.ts + hq * a.hs + 32 * h;
-    u32x4v raw[NS][2];
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      raw[s][0] = *(const u32x4v*)(x + 128 * s);
-      raw[s][1] = *(const u32x4v*)(x + 128 * s + 16);
-    }
-    float f[NS][16], am = 0.0f;
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const uint32_t v = (raw[s][e / 8][(e % 8) / 2] >> (16 * (e & 1))) & 0xFFFFu;
-        f[s][e] = a.dtype == 1 ? BF16T::to_f32(v) : F16T::to_f32(v);
-        am = __builtin_fmaxf(am, __builtin_fabsf(f[s][e]));
-      }
-    am = __builtin_fmaxf(am, __shfl_xor(am, 16, 64));
-    am = __builtin_fmaxf(am, __shfl_xor(am, 32, 64));
-    int ex = (int)(__float_as_uint(am) >> 23);           // 0: zero or subnormal, 255: inf
-    ex = ex < 64 ? 64 : (ex > 254 ? 127 : ex);
-    const float up = __uint_as_float((uint32_t)(127 + 13 - (ex - 127)) << 23);
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) qf[t][2 * s + e / 8][e % 8] = (_Float16)(f[s][e] * up);
-    cq[t] = a.scale * 1.44269504088896340736f * __uint_as_float((uint32_t)(127 - 13 + (ex - 127)) << 23);
-  }
+  for (int t = 0; t < QT; ++t)
+    row[t] = kv_query(p, it, it.rt * p.rb + 16 * t + c16, qf[t],
+                      [&](int j) { return 64 * (j / 2) + 16 * h + 8 * (j & 1); });
 
   f32x4v o[QT][NU];
   float m[QT], l[QT];
@@ -348,21 +459,13 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
     for (int u = 0; u < NU; ++u) o[t][u] = f32x4v{0.f, 0.f, 0.f, 0.f};
   }
 
-  // tiles that some row of the row tile sees, within the chunk
   const int r0 = it.rt * p.rb, r1 = r0 + 16 * QT < it.k.rows ? r0 + 16 * QT : it.k.rows;
-  const int i0 = r0 / p.g, i1 = (r1 - 1) / p.g;
-  const int hi = a.causal && pos0 + i1 + 1 < hi_all ? pos0 + i1 + 1 : hi_all;
-  const int lo = first_seen(pos0 + i0, a.window);
-  const int least = a.causal && pos0 + i0 + 1 < hi ? pos0 + i0 + 1 : hi;           // below: seen by all rows
-  const int from = first_seen(pos0 + i1, a.window);  // from here on: by all
-  int t0 = it.k.lo + it.chunk * it.len, t1 = t0 + it.len;
-  if (t1 > it.k.lo + it.k.tiles) t1 = it.k.lo + it.k.tiles;
-  if (t0 < lo / kKvTile) t0 = lo / kKvTile;
-  if (t1 > (hi + kKvTile - 1) / kKvTile) t1 = (hi + kKvTile - 1) / kKvTile;
+  const KvRange rg = kv_range(p, it, r0, r1);
+  const int lo = rg.lo, hi = rg.hi;
   const int* table = a.q.table + it.seq * a.q.table_stride;
   const int64_t bhead = (int64_t)T * D;
 
-  for (int tt = t0 + wv; tt < t1; tt += 4) {
+  for (int tt = rg.t0 + wv; tt < rg.t1; tt += 4) {
     const int b0 = tt * kKvTile;
     // block of this lane group's 16 tokens; groups that no row sees (their scales
     // may be anything) and groups without a block read block 0, masked
@@ -403,65 +506,11 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
         }
       }
 
-    const bool edge = away != 0 || b0 + kKvTile > least || b0 < from;
-    // a zero scale counts as 2^-80: its codes are zeros
-    const float vse = vs < 0x1p-80f ? 0x1p-80f : vs;
-    const float lv = there ? __builtin_amdgcn_logf(vse) : 0.0f;
-    const float rv = there ? 1.0f / vse : 1.0f;
+    const bool edge = away != 0 || b0 + kKvTile > rg.least || b0 < rg.from;
+    const KvScales kk = kv_scales(there, ks, vs);
     f16x8_t pf[QT][2];
 #pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      float ck = there ? cq[t] * ks : 1.0f;
-      ck = ck < 0x1p-120f ? 0x1p-120f : ck;
-      if (edge) {
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tok = gp + 4 * mt + e;
-            if (!there || tok > lim[t] || tok < low[t]) sc[t][mt][e] = kNegInf;
-          }
-      }
-      float mx = kNegInf;
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx = __builtin_fmaxf(mx, sc[t][mt][e]);
-      mx = __builtin_fmaf(mx, ck, lv);
-      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16, 64));
-      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
-      if (__any(mx - m[t] > kTopMost)) {  // -inf - -inf is NaN: no new reference
-        const float nm = mx - m[t] > kTopMost ? mx - kTopSet : m[t];
-        const float al = nm == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[t] - nm);
-        m[t] = nm;
-        far |= __any(__builtin_fabsf(nm) > kFarTop && nm != kNegInf);
-        l[t] *= al;
-#pragma unroll
-        for (int u = 0; u < NU; ++u) o[t][u] *= al;
-      }
-      const float ref = m[t] == kNegInf ? 0.0f : m[t], off = lv - ref;
-      if (far) {
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[t][mt][e] = __builtin_fmaf(sc[t][mt][e], ck, lv) - ref;
-      } else {
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[t][mt][e] = __builtin_fmaf(sc[t][mt][e], ck, off);
-      }
-      float sum = 0.0f;
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float w = __builtin_amdgcn_exp2f(sc[t][mt][e]);
-          sum += w;
-          pf[t][mt / 2][4 * (mt & 1) + e] = (_Float16)w;
-        }
-      l[t] = __builtin_fmaf(sum, rv, l[t]);
-    }
+    for (int t = 0; t < QT; ++t) kv_weights<NU>(sc[t], row[t], kk, gp, edge, m[t], l[t], o[t], far, pf[t]);
     if constexpr (FP8) {
       if (edge) {  // codes that nobody sees can be NaN: 0 * NaN must not reach O
 #pragma unroll
@@ -534,20 +583,211 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
           ml[0] = sum == sum ? top : -kNegInf;  // NaN has the last word in the join
           ml[1] = sum;
         } else if (a.lse) {
-          a.lse[tok * a.heads + hq] =
-              sum == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
+          a.lse[tok * a.heads + hq] = kv_lse(top, sum);
         }
       }
     }
   }
 }
 
-// Joins the chunks of split sequences: one wave per (token, query head).
-__global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs p, int D) {
+// Many rows per kv head (prompts): four waves of 16 QT rows each share every
+// tile, which is widened once into LDS as fp16 (K [64][D], V [D][64], 16-byte
+// chunks XOR-swizzled by row), one tile ahead of its use, its codes loaded one
+// tile ahead of that.  Per tile a wave reads 2 * 64 * D * 2 bytes of fragments
+// for 4 QT MFMAs of each 16 tokens x 32 elements; QT balances these reads, the
+// softmax and the products within the registers of two waves per SIMD.
+template <int D>
+struct KvPromptShape {
+  static constexpr int QT = D == 64 ? 3 : 2, WAVES = D <= 128 ? 2 : 1;  // waves per SIMD
+};
+
+template <int D, bool FP8>
+__global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAttnArgs p) {
+  constexpr int QT = KvPromptShape<D>::QT, NJ = D / 32, NU = D / 16, KC = D / 16, NQ = D / 64;
+  constexpr int K_BYTES = kKvTile * D * 2, BUF = 2 * K_BYTES;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * BUF];
   const KvAttn& a = p.a;
-  const int lane = threadIdx.x & 63;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (id >= a.q.total * a.heads) return;
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c16 = lane & 15, h = lane >> 4;
+  KvItem it;
+  if (!kv_item(p, blockIdx.x, lane, it)) return;
+  const int H = a.c.heads, tsh = a.c.tsh, T = 1 << tsh;
+
+  const int w0 = it.rt * p.rb + 16 * QT * wv;  // this wave's first row
+  f16x8_t qf[QT][NJ];
+  KvRow row[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t)
+    row[t] = kv_query(p, it, w0 + 16 * t + c16, qf[t], [&](int j) { return 32 * j + 8 * h; });
+  f32x4v o[QT][NU];
+  float m[QT], l[QT];
+  bool far = false;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    m[t] = kNegInf;
+    l[t] = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) o[t][u] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  }
+  const int r0 = it.rt * p.rb, r1 = r0 + p.rb < it.k.rows ? r0 + p.rb : it.k.rows;
+  const KvRange rg = kv_range(p, it, r0, r1);
+  // what this wave's own rows see (none: rows past the end)
+  const int w1 = w0 + 16 * QT < it.k.rows ? w0 + 16 * QT : it.k.rows;
+  KvRange mine = rg;
+  if (w0 < w1) mine = kv_range(p, it, w0, w1);
+  else mine.hi = 0;
+
+  const int* table = a.q.table + it.seq * a.q.table_stride;
+  const int64_t bhead = (int64_t)T * D;
+  // Block (times kv heads, plus the head) of lane group h's 16 tokens of a tile,
+  // or -1 where no row sees them or there is none.
+  auto block_of = [&](int tt) -> int64_t {
+    const int gp = tt * kKvTile + 16 * h;
+    if (tt >= rg.t1 || gp >= rg.hi || gp + 16 <= rg.lo) return -1;
+    const int64_t b = table[gp >> tsh];
+    return b >= 0 && b < a.c.blocks ? b * H + it.head : -1;
+  };
+  u32x4v kr[NQ], vr[NQ];
+  // Codes of a tile: K chunk tid + 256 q is row (token) / KC, 16 elements; V chunk
+  // tid + 256 q is row (dim) / 4, tokens 16 (tid % 4).
+  auto fetch = [&](int tt, int64_t blk) {
+    const int64_t safe = blk < 0 ? it.head : blk;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const int i = tid + 256 * q, r = i / KC;
+      const int64_t b = __shfl(safe, 16 * (r >> 4), 64);
+      kr[q] = *(const u32x4v*)(a.c.k + b * bhead + (int64_t)((tt * kKvTile + r) & (T - 1)) * D + 16 * (i % KC));
+    }
+    const int64_t b = __shfl(safe, 16 * (tid & 3), 64);
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+      vr[q] = *(const u32x4v*)(a.c.v + b * bhead + (int64_t)(tid / 4 + 64 * q) * T +
+                               ((tt * kKvTile + 16 * (tid & 3)) & (T - 1)));
+  };
+  auto widen = [&](int tt, int64_t blk, uint8_t* buf) {
+    if constexpr (FP8) {  // codes that nobody sees can be NaN: 0 * NaN must not reach O
+      const int tok = tt * kKvTile + 16 * (tid & 3);
+      const bool none = __shfl((int)(blk < 0), 16 * (tid & 3), 64);
+      if (none || tok + 16 > rg.hi || tok < rg.lo) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          uint32_t keep = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!none && tok + 4 * d + e < rg.hi && tok + 4 * d + e >= rg.lo) keep |= 0xFFu << (8 * e);
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) vr[q][d] &= keep;
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const int i = tid + 256 * q, r = i / KC, c = 2 * (i % KC), z = (r & 3) | ((r >> 2) & 4);
+      uint8_t* k = buf + r * (2 * D);
+      *(f16x8_t*)(k + (c ^ z) * 16) = widen8<FP8>(kr[q][0], kr[q][1]);
+      *(f16x8_t*)(k + ((c + 1) ^ z) * 16) = widen8<FP8>(kr[q][2], kr[q][3]);
+      const int d = tid / 4 + 64 * q, x = 2 * (tid & 3);
+      uint8_t* v = buf + K_BYTES + d * 128;
+      *(f16x8_t*)(v + (x ^ (d & 7)) * 16) = widen8<FP8>(vr[q][0], vr[q][1]);
+      *(f16x8_t*)(v + ((x + 1) ^ (d & 7)) * 16) = widen8<FP8>(vr[q][2], vr[q][3]);
+    }
+  };
+
+  if (rg.t0 < rg.t1) {
+    int64_t blk = block_of(rg.t0), blk1 = block_of(rg.t0 + 1);
+    fetch(rg.t0, blk);
+    widen(rg.t0, blk, smem);
+    float ks = a.c.ks[blk < 0 ? it.head : blk], vs = a.c.vs[blk < 0 ? it.head : blk];
+    fetch(rg.t0 + 1, blk1);  // past the end: block 0, unused
+    int64_t blk2 = block_of(rg.t0 + 2);
+    __syncthreads();
+    for (int tt = rg.t0; tt < rg.t1; ++tt) {
+      const uint8_t* buf = smem + ((tt - rg.t0) & 1) * BUF;
+      const int b0 = tt * kKvTile;
+      const float ks1 = a.c.ks[blk1 < 0 ? it.head : blk1], vs1 = a.c.vs[blk1 < 0 ? it.head : blk1];
+      if (b0 < mine.hi && b0 + kKvTile > mine.lo) {
+        f32x4v sc[QT][4];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+          const int r = 16 * (c16 >> 2) + 4 * mt + (c16 & 3);
+          const uint8_t* k = buf + r * (2 * D);
+          const int z = (r & 3) | ((r >> 2) & 4);
+#pragma unroll
+          for (int t = 0; t < QT; ++t) sc[t][mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const f16x8_t kf = *(const f16x8_t*)(k + ((4 * j + h) ^ z) * 16);
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+              sc[t][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[t][j], sc[t][mt], 0, 0, 0);
+          }
+        }
+        const bool edge = __any(blk < 0) || b0 + kKvTile > mine.least || b0 < mine.from;
+        const KvScales kk = kv_scales(blk >= 0, ks, vs);
+        f16x8_t pf[QT][2];
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+          kv_weights<NU>(sc[t], row[t], kk, b0 + 16 * h, edge, m[t], l[t], o[t], far, pf[t]);
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+          const int d = 16 * u + c16;
+          const uint8_t* v = buf + K_BYTES + d * 128;
+          const f16x8_t v0 = *(const f16x8_t*)(v + ((2 * h) ^ (d & 7)) * 16);
+          const f16x8_t v1 = *(const f16x8_t*)(v + ((2 * h + 1) ^ (d & 7)) * 16);
+#pragma unroll
+          for (int t = 0; t < QT; ++t) {
+            o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[t][0], o[t][u], 0, 0, 0);
+            o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[t][1], o[t][u], 0, 0, 0);
+          }
+        }
+      }
+      if (tt + 1 < rg.t1) {
+        widen(tt + 1, blk1, smem + ((tt + 1 - rg.t0) & 1) * BUF);
+        fetch(tt + 2, blk2);
+        blk = blk1;
+        blk1 = blk2;
+        blk2 = block_of(tt + 3);
+        ks = ks1;
+        vs = vs1;
+      }
+      __syncthreads();
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    l[t] += __shfl_xor(l[t], 16, 64);
+    l[t] += __shfl_xor(l[t], 32, 64);
+    const int r = w0 + 16 * t + c16;
+    if (r >= it.k.rows) continue;
+    const int64_t tok = it.r.first + r / p.g, hq = it.head * p.g + r % p.g;
+    if (it.chunks > 1) {
+      const int64_t at = it.slot * p.rb + (r - r0);
+#pragma unroll
+      for (int u = 0; u < NU; ++u) *(f32x4v*)(p.po + at * D + 16 * u + 4 * h) = o[t][u];
+      if (h == 0) {
+        p.ml[at * 2] = l[t] == l[t] ? m[t] : -kNegInf;  // NaN has the last word in the join
+        p.ml[at * 2 + 1] = l[t];
+      }
+    } else {
+      const float inv = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
+      const int64_t at = (tok * a.heads + hq) * D;
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) kv_store_out(a, at + 16 * u + 4 * h + e, o[t][u][e] * inv);
+      if (a.lse && h == 0) a.lse[tok * a.heads + hq] = kv_lse(m[t], l[t]);
+    }
+  }
+}
+
+// Joins the chunks of split sequences: one workgroup per (token, query head), the
+// chunks dealt to its four waves, whose sums meet in wave order.
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many) {
+  constexpr int V = D / 64;
+  const KvAttn& a = few.a;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int64_t id = blockIdx.x;
   const int64_t tok = id / a.heads;
   const int hq = (int)(id % a.heads);
   int64_t seq = 0;
@@ -564,6 +804,7 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs p, int D) {
   }
   const SeqRows r = seq_rows(a.q, seq);
   if (tok < r.first || tok >= (int64_t)r.first + r.n) return;  // in no sequence
+  const KvAttnArgs& p = r.n * few.g <= few.most ? few : many;
   const int chunks = p.plan[2 * seq + 1];
   if (chunks < 2) return;
   const int row = (int)(tok - r.first) * p.g + hq % p.g;
@@ -572,98 +813,143 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs p, int D) {
   const int64_t first = p.plan[2 * seq];
   // offsets that do not ascend can ask for more items than there is room for
   if (first < 0 || (first + (int64_t)chunks * nrt) * a.c.heads > p.items) return;
-  auto slot = [&](int c) { return ((first + (int64_t)c * nrt + rt) * a.c.heads + head) * p.rb + rr; };
+  const int64_t at0 = ((first + nrt - 1 - rt) * a.c.heads + head) * p.rb + rr;
+  const int64_t step = (int64_t)nrt * a.c.heads * p.rb;
   float top = kNegInf;
-  for (int c = lane; c < chunks; c += 64) top = __builtin_fmaxf(top, p.ml[slot(c) * 2]);
+  for (int c = lane; c < chunks; c += 64) top = __builtin_fmaxf(top, p.ml[(at0 + c * step) * 2]);
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, x, 64));
-  float sum = 0.0f, v[4] = {0.f, 0.f, 0.f, 0.f};
+  float sum = 0.0f, v[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) v[e] = 0.0f;
   if (top != kNegInf) {
-    for (int c = 0; c < chunks; ++c) {
-      const int64_t s = slot(c);
+#pragma unroll 4
+    for (int c = wv; c < chunks; c += 4) {
+      const int64_t s = at0 + c * step;
       const float f = __builtin_amdgcn_exp2f(p.ml[s * 2] - top);
-      if (f == 0.0f) continue;
       sum = __builtin_fmaf(p.ml[s * 2 + 1], f, sum);
-      for (int e = 0; e < D / 64; ++e) v[e] = __builtin_fmaf(p.po[s * D + lane + 64 * e], f, v[e]);
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(p.po[s * D + lane * V + e], f, v[e]);
     }
   }
+  __shared__ float part[4][D], sums[4];
+#pragma unroll
+  for (int e = 0; e < V; ++e) part[wv][lane * V + e] = v[e];
+  if (lane == 0) sums[wv] = sum;
+  __syncthreads();
+  sum = sums[0] + sums[1] + sums[2] + sums[3];
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  for (int e = 0; e < D / 64; ++e) kv_store_out(a, id * D + lane + 64 * e, v[e] * inv);
-  if (a.lse && lane == 0)
-    a.lse[id] = sum == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
+  for (int d = threadIdx.x; d < D; d += 256)
+    kv_store_out(a, id * D + d, (part[0][d] + part[1][d] + part[2][d] + part[3][d]) * inv);
+  if (a.lse && threadIdx.x == 0) a.lse[id] = kv_lse(top, sum);
 }
 
 namespace {
+// Row shapes of the prompt kernel by head dim (KvPromptShape).
+int prompt_rows(int dim) { return 64 * (dim == 64 ? 3 : 2); }
+
 struct KvPlan {
-  int g, rb, qt, cmin;
-  int64_t target, items;  // most items of the launch
-  bool split;
-  size_t off_ml, off_po, need;
+  KvAttnArgs few, many;
+  int qt;                   // 16-row tiles of the few-rows kernel
+  bool run_few, run_many, split;
+  size_t need;
 };
-KvPlan kv_plan(const KvAttn& a) {
+
+// Which kernels run, their row tiles and the room for split results, from what
+// the host knows (shapes; lengths and offsets stay on the device).  Sequences of
+// at most 64 rows per kv head (query tokens times heads of the group) go to the
+// few-rows kernel, the others to the prompt kernel; without offsets all have the
+// same count, with offsets both may be needed.
+KvPlan kv_plan(const KvAttn& a, char* ws) {
+  constexpr int kNever = 1 << 26;  // tiles of a chunk that nothing reaches
   KvPlan p;
-  p.g = a.heads / a.c.heads;
-  const int64_t rows = (a.q.total + a.q.seqs - 1) / a.q.seqs * p.g;  // of a usual sequence
-  p.qt = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-  if (a.c.dim > 128 && p.qt > 2) p.qt = 2;
-  p.rb = 16 * p.qt;
-  p.cmin = 4;
-  p.target = 4 * device_cu_count();
-  const int64_t H = a.c.heads;
-  const int64_t rt = a.q.cu ? (a.q.total * p.g) / p.rb + a.q.seqs
-                            : a.q.seqs * ((a.q.nper * p.g + p.rb - 1) / p.rb);
+  const int g = a.heads / a.c.heads;
+  const int64_t H = a.c.heads, rows = a.q.nper * g, cus = device_cu_count();
+  const int usual = (int)(a.q.cu ? (g < 64 ? g : 64) : (rows < 64 ? rows : 64));
+  p.qt = usual <= 16 ? 1 : (usual <= 32 || a.c.dim > 128 ? 2 : 4);
+  const int limit = 64;
+  p.run_few = a.q.cu || rows <= limit;
+  p.run_many = a.q.cu ? a.q.total * g > limit : rows > limit;
   const int64_t tiles = (a.q.cap + kKvTile - 1) / kKvTile;
-  p.split = tiles > p.cmin;
-  p.items = rt * H;
-  if (p.split) {
-    const int64_t more = rt * H * ((tiles + p.cmin - 1) / p.cmin);
-    p.items = more < p.target + rt * H ? more : p.target + rt * H;
-  }
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  p.off_ml = up((size_t)a.q.seqs * 8);
-  p.off_po = p.off_ml + up((size_t)p.items * p.rb * 8);
-  p.need = p.split ? p.off_po + up((size_t)p.items * p.rb * a.c.dim * 4) : 0;
+  size_t off = up((size_t)a.q.seqs * 8);
+  p.split = false;
+  auto lay = [&](KvAttnArgs& w, bool run, int rb, int above, int most, int cmin, int64_t target, int64_t rt) {
+    w.a = a;
+    w.g = g;
+    w.rb = rb;
+    w.above = above;
+    w.most = most;
+    w.target = target;
+    const bool split = run && tiles > cmin && (most == limit || rt * H < target);
+    w.cmin = split ? cmin : kNever;
+    w.items = rt * H;
+    w.plan = (int*)ws;
+    if (split) {
+      const int64_t all = rt * H * ((tiles + cmin - 1) / cmin);
+      w.items = all < target + rt * H ? all : target + rt * H;
+      w.ml = (float*)(ws + off);
+      off += up((size_t)w.items * rb * 8);
+      w.po = (float*)(ws + off);
+      off += up((size_t)w.items * rb * a.c.dim * 4);
+      p.split = true;
+    } else {
+      w.ml = w.po = nullptr;
+    }
+  };
+  const int rbf = 16 * p.qt, rbm = prompt_rows(a.c.dim);
+  int64_t rtf = a.q.seqs * ((rows + rbf - 1) / rbf), rtm = a.q.seqs * ((rows + rbm - 1) / rbm);
+  if (a.q.cu) {  // n rows make at most n / rb + 1 tiles
+    rtf = a.q.total * g / rbf + a.q.seqs;
+    const int64_t most = a.q.seqs * ((limit + rbf - 1) / rbf), longer = a.q.total * g / limit;
+    if (rtf > most) rtf = most;
+    rtm = a.q.total * g / rbm + (longer < a.q.seqs ? longer : a.q.seqs);
+  }
+  lay(p.few, p.run_few, rbf, 0, limit, 4, 4 * cus, rtf);
+  lay(p.many, p.run_many, rbm, limit, INT32_MAX, 4, (a.c.dim <= 128 ? 2 : 1) * cus, rtm);
+  p.need = p.split ? off : 0;
+  if (!p.split) p.few.plan = p.many.plan = nullptr;
   return p;
 }
 }  // namespace
 
-size_t kv_attn_workspace(const KvAttn& a) { return kv_plan(a).need; }
+size_t kv_attn_workspace(const KvAttn& a) { return kv_plan(a, nullptr).need; }
 
 hipError_t launch_kv_attn(const KvAttn& a, void* ws, hipStream_t s) {
-  const KvPlan pl = kv_plan(a);
-  KvAttnArgs p;
-  p.a = a;
-  p.g = pl.g;
-  p.rb = pl.rb;
-  p.target = pl.target;
-  p.items = pl.items;
-  p.cmin = pl.split ? pl.cmin : (1 << 26);
-  p.plan = pl.split ? (int*)ws : nullptr;
-  p.ml = (float*)((char*)ws + pl.off_ml);
-  p.po = (float*)((char*)ws + pl.off_po);
-  auto run = [&]<int D, int QT>() {
-    auto k = a.c.fp8 ? k_kv_attn<D, QT, true> : k_kv_attn<D, QT, false>;
-    hipLaunchKernelGGL(k, dim3((unsigned)pl.items), dim3(256), 0, s, p);
-    return hipGetLastError();
-  };
+  const KvPlan p = kv_plan(a, (char*)ws);
   auto dim = [&]<int D>() {
-    if (pl.qt == 1) return run.template operator()<D, 1>();
-    if (pl.qt == 2) return run.template operator()<D, 2>();
-    if constexpr (D <= 128) return run.template operator()<D, 4>();
-    return hipErrorInvalidValue;
+    if (p.run_many) {
+      auto k = a.c.fp8 ? k_kv_prompt<D, true> : k_kv_prompt<D, false>;
+      hipLaunchKernelGGL(k, dim3((unsigned)p.many.items), dim3(256), 0, s, p.many);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    if (p.run_few) {
+      auto few = [&]<int QT>() {
+        auto k = a.c.fp8 ? k_kv_attn<D, QT, true> : k_kv_attn<D, QT, false>;
+        hipLaunchKernelGGL(k, dim3((unsigned)p.few.items), dim3(256), 0, s, p.few);
+        return hipGetLastError();
+      };
+      hipError_t e;
+      if (p.qt == 1) e = few.template operator()<1>();
+      else if (p.qt == 2) e = few.template operator()<2>();
+      else if constexpr (D <= 128) e = few.template operator()<4>();
+      else e = hipErrorInvalidValue;
+      if (e != hipSuccess) return e;
+    }
+    if (p.split) {
+      hipLaunchKernelGGL((k_kv_join<D>), dim3((unsigned)(a.q.total * a.heads)), dim3(256), 0, s, p.few, p.many);
+      return hipGetLastError();
+    }
+    return hipSuccess;
   };
-  hipError_t e;
   switch (a.c.dim) {
-    case 64: e = dim.template operator()<64>(); break;
-    case 128: e = dim.template operator()<128>(); break;
-    case 192: e = dim.template operator()<192>(); break;
-    case 256: e = dim.template operator()<256>(); break;
+    case 64: return dim.template operator()<64>();
+    case 128: return dim.template operator()<128>();
+    case 192: return dim.template operator()<192>();
+    case 256: return dim.template operator()<256>();
     default: return hipErrorInvalidValue;
   }
-  if (e != hipSuccess || !pl.split) return e;
-  const int64_t waves = a.q.total * a.heads;
-  hipLaunchKernelGGL(k_kv_join, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, s, p, a.c.dim);
-  return hipGetLastError();
 }
 
 }  // namespace sparq24

@@ -165,12 +165,14 @@ def rows(heads=2, dim=64, total=6, dtype=B.BF16, ts=None, hs=None, data=FAKE, ks
 
 
 def append(L, c=None, s=None, k=None, v=None):
-    return L.sparq24_kv_append(c or cache(), s or seqs(), k or rows(), v or rows(), None)
+    R = ctypes.byref
+    return L.sparq24_kv_append(R(c or cache()), R(s or seqs()), R(k or rows()), R(v or rows()), None)
 
 
 def attend(L, c=None, s=None, q=None, scale=0.125, causal=1, window=0, out=FAKE, lse=None, ws=FAKE, nb=1 << 40):
-    n = None if nb is None else ctypes.c_size_t(nb)
-    return L.sparq24_kv_attention(c or cache(), s or seqs(), q or rows(heads=6), scale, causal,
+    n = ctypes.c_size_t(nb) if isinstance(nb, int) else nb
+    R = ctypes.byref
+    return L.sparq24_kv_attention(R(c or cache()), R(s or seqs()), R(q or rows(heads=6)), scale, causal,
                                   window, out, lse, ws, n, None)
 
 
@@ -219,13 +221,12 @@ def test_attention_refusals_and_workspace(L):
     assert attend(L, q=rows(heads=6, data=None)) == INVALID
     big = seqs(max_blocks=64, table_stride=64)
     n = ctypes.c_size_t(0)
-    assert L.sparq24_kv_attention(cache(), big, rows(heads=6), 0.1, 1, 0, None, None, None, n, None) == OK
+    assert attend(L, s=big, out=None, ws=None, nb=n) == OK
     assert n.value > 0
     assert attend(L, s=big, nb=n.value - 1) == WORKSPACE and attend(L, s=big, nb=None) == WORKSPACE
     assert attend(L, s=big, ws=FAKE + 8) == ALIGN
     # 256 tokens at most: no split, no workspace
-    assert L.sparq24_kv_attention(cache(), seqs(max_blocks=8, table_stride=8), rows(heads=6), 0.1, 1, 0, None,
-                                  None, None, n, None) == OK
+    assert attend(L, s=seqs(max_blocks=8, table_stride=8), out=None, ws=None, nb=n) == OK
     assert n.value == 0
     assert attend(L, s=seqs(total=0), q=rows(heads=6, total=0, data=None), out=None) == OK
     assert attend(L, s=seqs(total=2 ** 28, seqs=2 ** 20), q=rows(heads=64, total=2 ** 28)) == UNSUPPORTED
@@ -255,6 +256,15 @@ def test_binding_refusals():
         B.kv_attention(x, c, table, lens)
     with pytest.raises(ValueError, match="int"):
         B.kv_cache(3, 2, 64, 16, q=("int", 4), device="cpu")
+    # the packed descriptors are the C structures
+    r = B.CKvCache.from_buffer_copy(B._c_cache(c)[0])
+    assert (r.k, r.v_scale, r.fmt, r.blocks, r.heads, r.tokens, r.dim) == (
+        c.k.data_ptr(), c.v_scale.data_ptr(), B.Q_INT, 3, 2, 16, 64)
+    packed, sizes = B._c_seqs(x, table, lens, None)
+    r = B.CKvSeqs.from_buffer_copy(packed)
+    assert (r.block_table, r.max_blocks, r.table_stride, r.seq_lens, r.cu_tokens, r.seqs, r.total) == (
+        table.data_ptr(), 4, 4, lens.data_ptr(), None, 2, 2) and sizes == (2, 4, 2, False)
+    assert len(packed) == ctypes.sizeof(B.CKvSeqs) and len(B._c_rows(x)) == ctypes.sizeof(B.CTensor)
     # descriptors: what they refuse without a device
     with pytest.raises(ValueError, match="match"):
         B._c_cache(c._replace(v=c.k))
@@ -274,5 +284,5 @@ def test_binding_refusals():
         B._c_rows(torch.zeros(3, 5, 2, 64)[:, :2])
     with pytest.raises(ValueError, match="contiguous"):
         B._c_rows(torch.zeros(3, 64, 2).transpose(1, 2))
-    r = B._c_rows(torch.zeros(7, 3, 2, 64)[:, 1:2])                # one row of each three
+    r = B.CTensor.from_buffer_copy(B._c_rows(torch.zeros(7, 3, 2, 64)[:, 1:2]))  # one row of each three
     assert (r.batch, r.rows, r.k, r.batch_stride, r.row_stride) == (7, 2, 64, 384, 64)
