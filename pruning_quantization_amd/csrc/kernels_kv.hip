@@ -239,6 +239,13 @@ __device__ inline KvWork kv_work(const KvAttnArgs& w, const SeqRows& r) {
   return k;
 }
 
+// Values that are the same in every lane, for scalar registers and branches.
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline int64_t uniform(int64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 | lo);
+}
+
 struct KvItem {
   SeqRows r;
   KvWork k;
@@ -260,7 +267,6 @@ __device__ inline bool kv_item(const KvAttnArgs& w, int64_t id, int lane, KvItem
   }
   int64_t len = (all * H + w.target - 1) / w.target;
   len = len < w.cmin ? w.cmin : (len + 3) / 4 * 4;  // four waves share a chunk
-  it.len = (int)len;
   int64_t local;
   if (!find_sequence(seqs, id / H, lane, it.seq, local, [&](int64_t b) -> int64_t {
         const KvWork k = kv_work(w, seq_rows(w.a.q, b));
@@ -268,12 +274,18 @@ __device__ inline bool kv_item(const KvAttnArgs& w, int64_t id, int lane, KvItem
         return k.rt * (ch > 1 ? ch : 1);
       }))
     return false;
+  it.seq = uniform(it.seq);
+  it.len = uniform((int)len);
   it.r = seq_rows(w.a.q, it.seq);
+  it.r.first = uniform(it.r.first);
+  it.r.n = uniform(it.r.n);
+  it.r.len = uniform(it.r.len);
   it.k = kv_work(w, it.r);
-  it.chunks = (int)((it.k.tiles + len - 1) / len);
+  it.chunks = (it.k.tiles + it.len - 1) / it.len;
   if (it.chunks < 1) it.chunks = 1;
-  it.chunk = (int)(local / it.k.rt);
-  it.rt = it.k.rt - 1 - (int)(local % it.k.rt);  // the last rows see the most: first
+  const int at = uniform((int)local);
+  it.chunk = at / it.k.rt;
+  it.rt = it.k.rt - 1 - at % it.k.rt;  // the last rows see the most: first
   it.head = (int)(id % H);
   it.slot = id;
   if (w.plan && local == 0 && it.head == 0 && threadIdx.x == 0) {
@@ -342,65 +354,99 @@ __device__ inline KvScales kv_scales(bool there, float ks, float vs) {
   k.there = there;
   k.ks = ks;
   k.lv = there ? __builtin_amdgcn_logf(vse) : 0.0f;
-  k.rv = there ? 1.0f / vse : 1.0f;
+  k.rv = there ? __builtin_amdgcn_rcpf(vse) : 1.0f;
   return k;
 }
 
-// Scores of a tile (lane: one row, tokens tok0 .. tok0 + 15) to weights: masks
-// (where `edge`), the row's reference m, the sum l and the rescaling of O.
-template <int NU>
-__device__ inline void kv_weights(f32x4v (&sc)[4], const KvRow& row, const KvScales& k, int tok0, bool edge,
-                                  float& m, float& l, f32x4v (&o)[NU], bool& far, f16x8_t (&pf)[2]) {
-  float ck = k.there ? row.c * k.ks : 1.0f;
-  ck = ck < 0x1p-120f ? 0x1p-120f : ck;
+// Over the four lane groups (lanes l ^ 16, l ^ 32).
+__device__ inline float groups_max(float v) {
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Scores of a tile (lane: QT rows, tokens tok0 .. tok0 + 15) to weights: masks
+// (where `edge`), the rows' references m, sums l and the rescaling of O.
+template <int QT, int NU>
+__device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], const KvScales& k, int tok0,
+                                  bool edge, float (&m)[QT], float (&l)[QT], f32x4v (&o)[QT][NU], int& far,
+                                  f16x8_t (&pf)[QT][2]) {
+  float ck[QT], mx[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    ck[t] = k.there ? row[t].c * k.ks : 1.0f;
+    ck[t] = ck[t] < 0x1p-120f ? 0x1p-120f : ck[t];
+  }
   if (edge) {
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      // tokens tok0 + x with first <= x <= last
+      const int first = k.there ? row[t].low - tok0 : 16, last = row[t].lim - tok0;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int x = 4 * mt + e;
+          sc[t][mt][e] = x > last || x < first ? kNegInf : sc[t][mt][e];
+        }
+    }
+  }
+  bool grow = false;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    mx[t] = kNegInf;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[t] = __builtin_fmaxf(mx[t], sc[t][mt][e]);
+    mx[t] = groups_max(__builtin_fmaf(mx[t], ck[t], k.lv));
+    grow |= mx[t] - m[t] > kTopMost;  // -inf - -inf is NaN: no new reference
+  }
+  if (__any(grow)) {
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      const float nm = mx[t] - m[t] > kTopMost ? mx[t] - kTopSet : m[t];
+      const float al = nm == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[t] - nm);
+      m[t] = nm;
+      far |= uniform((int)__any(__builtin_fabsf(nm) > kFarTop && nm != kNegInf));
+      l[t] *= al;
+#pragma unroll
+      for (int u = 0; u < NU; ++u) o[t][u] *= al;
+    }
+  }
+  if (far) {
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      const float ref = m[t] == kNegInf ? 0.0f : m[t];
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[t][mt][e] = __builtin_fmaf(sc[t][mt][e], ck[t], k.lv) - ref;
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      const float off = k.lv - (m[t] == kNegInf ? 0.0f : m[t]);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[t][mt][e] = __builtin_fmaf(sc[t][mt][e], ck[t], off);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    float sum = 0.0f;
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int tok = tok0 + 4 * mt + e;
-        if (!k.there || tok > row.lim || tok < row.low) sc[mt][e] = kNegInf;
+        const float w = __builtin_amdgcn_exp2f(sc[t][mt][e]);
+        sum += w;
+        pf[t][mt / 2][4 * (mt & 1) + e] = (_Float16)w;
       }
+    l[t] = __builtin_fmaf(sum, k.rv, l[t]);
   }
-  float mx = kNegInf;
-#pragma unroll
-  for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) mx = __builtin_fmaxf(mx, sc[mt][e]);
-  mx = __builtin_fmaf(mx, ck, k.lv);
-  mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16, 64));
-  mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
-  if (__any(mx - m > kTopMost)) {  // -inf - -inf is NaN: no new reference
-    const float nm = mx - m > kTopMost ? mx - kTopSet : m;
-    const float al = nm == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - nm);
-    m = nm;
-    far |= __any(__builtin_fabsf(nm) > kFarTop && nm != kNegInf);
-    l *= al;
-#pragma unroll
-    for (int u = 0; u < NU; ++u) o[u] *= al;
-  }
-  const float ref = m == kNegInf ? 0.0f : m, off = k.lv - ref;
-  if (far) {
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sc[mt][e] = __builtin_fmaf(sc[mt][e], ck, k.lv) - ref;
-  } else {
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sc[mt][e] = __builtin_fmaf(sc[mt][e], ck, off);
-  }
-  float sum = 0.0f;
-#pragma unroll
-  for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float w = __builtin_amdgcn_exp2f(sc[mt][e]);
-      sum += w;
-      pf[mt / 2][4 * (mt & 1) + e] = (_Float16)w;
-    }
-  l = __builtin_fmaf(sum, k.rv, l);
 }
 
 __device__ inline float kv_lse(float top, float sum) {
@@ -437,7 +483,7 @@ template <int D, int QT, bool FP8>
 __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
   constexpr int NS = D / 64, NU = D / 16;
   const KvAttn& a = p.a;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, c16 = lane & 15, h = lane >> 4;
+  const int lane = threadIdx.x & 63, wv = uniform((int)threadIdx.x >> 6), c16 = lane & 15, h = lane >> 4;
   KvItem it;
   if (!kv_item(p, blockIdx.x, lane, it)) return;
   const int H = a.c.heads, tsh = a.c.tsh, T = 1 << tsh;
@@ -450,7 +496,7 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
 
   f32x4v o[QT][NU];
   float m[QT], l[QT];
-  bool far = false;
+  int far = 0;
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
     m[t] = kNegInf;
@@ -509,8 +555,7 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
     const bool edge = away != 0 || b0 + kKvTile > rg.least || b0 < rg.from;
     const KvScales kk = kv_scales(there, ks, vs);
     f16x8_t pf[QT][2];
-#pragma unroll
-    for (int t = 0; t < QT; ++t) kv_weights<NU>(sc[t], row[t], kk, gp, edge, m[t], l[t], o[t], far, pf[t]);
+    kv_weights<QT, NU>(sc, row, kk, gp, edge, m, l, o, far, pf);
     if constexpr (FP8) {
       if (edge) {  // codes that nobody sees can be NaN: 0 * NaN must not reach O
 #pragma unroll
@@ -621,7 +666,7 @@ __global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAt
     row[t] = kv_query(p, it, w0 + 16 * t + c16, qf[t], [&](int j) { return 32 * j + 8 * h; });
   f32x4v o[QT][NU];
   float m[QT], l[QT];
-  bool far = false;
+  int far = 0;
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
     m[t] = kNegInf;
@@ -725,9 +770,7 @@ __global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAt
         const bool edge = __any(blk < 0) || b0 + kKvTile > mine.least || b0 < mine.from;
         const KvScales kk = kv_scales(blk >= 0, ks, vs);
         f16x8_t pf[QT][2];
-#pragma unroll
-        for (int t = 0; t < QT; ++t)
-          kv_weights<NU>(sc[t], row[t], kk, b0 + 16 * h, edge, m[t], l[t], o[t], far, pf[t]);
+        kv_weights<QT, NU>(sc, row, kk, b0 + 16 * h, edge, m, l, o, far, pf);
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
           const int d = 16 * u + c16;
