@@ -692,22 +692,43 @@ __global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAt
     const int64_t b = table[gp >> tsh];
     return b >= 0 && b < a.c.blocks ? b * H + it.head : -1;
   };
+  // A 16-byte LDS access takes lanes l .. l + 7 and l + 16 .. l + 23 (two lane groups)
+  // at a time, from 16 slots of 16 bytes: the xor of a row's chunks is chosen so
+  // that these sixteen lanes of a fragment read meet sixteen slots (rows c % 8 =
+  // r % 4 + 4 (r / 16 % 2) of K two chunks apart or, where rows are odd multiples of
+  // 128 bytes, in their own half; rows d % 8 of V in halves by d % 2).
+  auto k_swizzle = [](int r) {
+    return D % 128 == 0 ? 2 * ((r & 3) | ((r >> 2) & 4)) : ((r & 2) | ((r >> 2) & 4));
+  };
+  auto v_swizzle = [](int d) { return ((d >> 2) & 1) | ((d << 1) & 4); };
   u32x4v kr[NQ], vr[NQ];
+  const unsigned koff = tid * 16, voff = (tid >> 2) * T + 16 * (tid & 3);
   // Codes of a tile: K chunk tid + 256 q is row (token) / KC, 16 elements; V chunk
   // tid + 256 q is row (dim) / 4, tokens 16 (tid % 4).
   auto fetch = [&](int tt, int64_t blk) {
     const int64_t safe = blk < 0 ? it.head : blk;
+    if (tsh >= 6) {  // the tile lies in one block: scalar base, constant lane offsets
+      const uint64_t seen = __ballot(blk >= 0);  // by some group, if by any
+      const int64_t at = uniform(__shfl(safe, seen ? __ffsll((unsigned long long)seen) - 1 : 0, 64)) * bhead;
+      const int o = (tt * kKvTile) & (T - 1);
+      const uint8_t *kb = a.c.k + at + o * D, *vb = a.c.v + at + o;
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const int i = tid + 256 * q, r = i / KC;
-      const int64_t b = __shfl(safe, 16 * (r >> 4), 64);
-      kr[q] = *(const u32x4v*)(a.c.k + b * bhead + (int64_t)((tt * kKvTile + r) & (T - 1)) * D + 16 * (i % KC));
+      for (int q = 0; q < NQ; ++q) {
+        kr[q] = *(const u32x4v*)(kb + koff + q * 4096);
+        vr[q] = *(const u32x4v*)(vb + voff + q * 64 * T);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const int i = tid + 256 * q, r = i / KC;
+        const int64_t b = __shfl(safe, 16 * (r >> 4), 64);
+        kr[q] = *(const u32x4v*)(a.c.k + b * bhead + (int64_t)(r & (T - 1)) * D + 16 * (i % KC));
+      }
+      const int64_t b = __shfl(safe, 16 * (tid & 3), 64);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+        vr[q] = *(const u32x4v*)(a.c.v + b * bhead + (int64_t)(tid / 4 + 64 * q) * T + ((16 * (tid & 3)) & (T - 1)));
     }
-    const int64_t b = __shfl(safe, 16 * (tid & 3), 64);
-#pragma unroll
-    for (int q = 0; q < NQ; ++q)
-      vr[q] = *(const u32x4v*)(a.c.v + b * bhead + (int64_t)(tid / 4 + 64 * q) * T +
-                               ((tt * kKvTile + 16 * (tid & 3)) & (T - 1)));
   };
   auto widen = [&](int tt, int64_t blk, uint8_t* buf) {
     if constexpr (FP8) {  // codes that nobody sees can be NaN: 0 * NaN must not reach O
@@ -727,14 +748,18 @@ __global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAt
     }
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const int i = tid + 256 * q, r = i / KC, c = 2 * (i % KC), z = (r & 3) | ((r >> 2) & 4);
+      const int i = tid + 256 * q, r = i / KC, c = 2 * (i % KC), z = k_swizzle(r);
       uint8_t* k = buf + r * (2 * D);
-      *(f16x8_t*)(k + (c ^ z) * 16) = widen8<FP8>(kr[q][0], kr[q][1]);
-      *(f16x8_t*)(k + ((c + 1) ^ z) * 16) = widen8<FP8>(kr[q][2], kr[q][3]);
+      // which of its two chunks a thread writes first: sixteen different slots for
+      // lanes l .. l + 7 and l + 16 .. l + 23
+      const int odd = ((c >> 3) ^ (r / (256 / D))) & 1;
+      const f16x8_t k0 = widen8<FP8>(kr[q][0], kr[q][1]), k1 = widen8<FP8>(kr[q][2], kr[q][3]);
+      *(f16x8_t*)(k + ((c + odd) ^ z) * 16) = odd ? k1 : k0;
+      *(f16x8_t*)(k + ((c + 1 - odd) ^ z) * 16) = odd ? k0 : k1;
       const int d = tid / 4 + 64 * q, x = 2 * (tid & 3);
       uint8_t* v = buf + K_BYTES + d * 128;
-      *(f16x8_t*)(v + (x ^ (d & 7)) * 16) = widen8<FP8>(vr[q][0], vr[q][1]);
-      *(f16x8_t*)(v + ((x + 1) ^ (d & 7)) * 16) = widen8<FP8>(vr[q][2], vr[q][3]);
+      *(f16x8_t*)(v + (x ^ v_swizzle(d)) * 16) = widen8<FP8>(vr[q][0], vr[q][1]);
+      *(f16x8_t*)(v + ((x + 1) ^ v_swizzle(d)) * 16) = widen8<FP8>(vr[q][2], vr[q][3]);
     }
   };
 
@@ -756,7 +781,7 @@ __global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAt
         for (int mt = 0; mt < 4; ++mt) {
           const int r = 16 * (c16 >> 2) + 4 * mt + (c16 & 3);
           const uint8_t* k = buf + r * (2 * D);
-          const int z = (r & 3) | ((r >> 2) & 4);
+          const int z = k_swizzle(r);
 #pragma unroll
           for (int t = 0; t < QT; ++t) sc[t][mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -775,8 +800,8 @@ __global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAt
         for (int u = 0; u < NU; ++u) {
           const int d = 16 * u + c16;
           const uint8_t* v = buf + K_BYTES + d * 128;
-          const f16x8_t v0 = *(const f16x8_t*)(v + ((2 * h) ^ (d & 7)) * 16);
-          const f16x8_t v1 = *(const f16x8_t*)(v + ((2 * h + 1) ^ (d & 7)) * 16);
+          const f16x8_t v0 = *(const f16x8_t*)(v + ((2 * h) ^ v_swizzle(d)) * 16);
+          const f16x8_t v1 = *(const f16x8_t*)(v + ((2 * h + 1) ^ v_swizzle(d)) * 16);
 #pragma unroll
           for (int t = 0; t < QT; ++t) {
             o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[t][0], o[t][u], 0, 0, 0);
