@@ -198,8 +198,9 @@ constexpr int kKvTile = 64;
 constexpr float kTopSet = 8.0f;    // a new reference puts the largest w at 2^8 ...
 constexpr float kTopMost = 15.0f;  // ... and stands until one would pass 2^15
 // One fma from score to exponent rounds m, not the exponent: the same factor for
-// every token, harmless until the rounding itself is large.  From here on the
-// exponent is the difference of the rounded terms, so the largest stays in range.
+// every token, harmless until the rounding itself is large.  From here on every
+// tile takes the exponent as the difference of the rounded terms, so that the
+// largest stays in range.
 constexpr float kFarTop = 65536.0f;
 constexpr float kNegInf = -__builtin_inff();
 
@@ -366,12 +367,33 @@ __device__ inline float groups_max(float v) {
   return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+// State of a wave's rows over the tiles.
+template <int QT, int NU>
+struct KvState {
+  float m[QT], l[QT];  // reference (log2), sum of this lane group's tokens
+  f32x4v o[QT][NU];
+  int far;             // some row's reference is past kFarTop
+  __device__ inline void init() {
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      m[t] = kNegInf;
+      l[t] = 0.0f;
+#pragma unroll
+      for (int u = 0; u < NU; ++u) o[t][u] = f32x4v{0.f, 0.f, 0.f, 0.f};
+    }
+    far = 0;
+  }
+};
+
 // Scores of a tile (lane: QT rows, tokens tok0 .. tok0 + 15) to weights: masks
-// (where `edge`), the rows' references m, sums l and the rescaling of O.
+// (where `edge`), the rows' references, sums (fp32: a token of a small V scale can
+// have a weight that fp16 does not hold and still be most of the sum) and the
+// rescaling of O.  (Taking the weights first and forming the maxima only where
+// one passed 2^15 costs more than it saves as soon as scores spread: 847 against
+// 690 us for 8192 tokens, the maxima of 16 rows grow in most tiles.)
 template <int QT, int NU>
 __device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], const KvScales& k, int tok0,
-                                  bool edge, float (&m)[QT], float (&l)[QT], f32x4v (&o)[QT][NU], int& far,
-                                  f16x8_t (&pf)[QT][2]) {
+                                  bool edge, KvState<QT, NU>& st, f16x8_t (&pf)[QT][2]) {
   float ck[QT], mx[QT];
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
@@ -401,24 +423,25 @@ __device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], c
 #pragma unroll
       for (int e = 0; e < 4; ++e) mx[t] = __builtin_fmaxf(mx[t], sc[t][mt][e]);
     mx[t] = groups_max(__builtin_fmaf(mx[t], ck[t], k.lv));
-    grow |= mx[t] - m[t] > kTopMost;  // -inf - -inf is NaN: no new reference
+    grow |= mx[t] - st.m[t] > kTopMost;  // -inf - -inf is NaN: no new reference
   }
   if (__any(grow)) {
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      const float nm = mx[t] - m[t] > kTopMost ? mx[t] - kTopSet : m[t];
-      const float al = nm == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[t] - nm);
-      m[t] = nm;
-      far |= uniform((int)__any(__builtin_fabsf(nm) > kFarTop && nm != kNegInf));
-      l[t] *= al;
+      const bool g = mx[t] - st.m[t] > kTopMost;
+      const float nm = g ? mx[t] - kTopSet : st.m[t];
+      const float al = g ? __builtin_amdgcn_exp2f(st.m[t] - nm) : 1.0f;
+      st.m[t] = nm;
+      st.far |= uniform((int)__any(__builtin_fabsf(nm) > kFarTop && nm != kNegInf));
+      st.l[t] *= al;
 #pragma unroll
-      for (int u = 0; u < NU; ++u) o[t][u] *= al;
+      for (int u = 0; u < NU; ++u) st.o[t][u] *= al;
     }
   }
-  if (far) {
+  if (st.far) {
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      const float ref = m[t] == kNegInf ? 0.0f : m[t];
+      const float ref = st.m[t] == kNegInf ? 0.0f : st.m[t];
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -427,7 +450,7 @@ __device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], c
   } else {
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      const float off = k.lv - (m[t] == kNegInf ? 0.0f : m[t]);
+      const float off = k.lv - (st.m[t] == kNegInf ? 0.0f : st.m[t]);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -445,8 +468,14 @@ __device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], c
         sum += w;
         pf[t][mt / 2][4 * (mt & 1) + e] = (_Float16)w;
       }
-    l[t] = __builtin_fmaf(sum, k.rv, l[t]);
+    st.l[t] = __builtin_fmaf(sum, k.rv, st.l[t]);
   }
+}
+
+// Over the four lane groups, in every lane.
+__device__ inline float groups_sum(float v) {
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
 }
 
 __device__ inline float kv_lse(float top, float sum) {
@@ -494,16 +523,8 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
     row[t] = kv_query(p, it, it.rt * p.rb + 16 * t + c16, qf[t],
                       [&](int j) { return 64 * (j / 2) + 16 * h + 8 * (j & 1); });
 
-  f32x4v o[QT][NU];
-  float m[QT], l[QT];
-  int far = 0;
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    m[t] = kNegInf;
-    l[t] = 0.0f;
-#pragma unroll
-    for (int u = 0; u < NU; ++u) o[t][u] = f32x4v{0.f, 0.f, 0.f, 0.f};
-  }
+  KvState<QT, NU> st;
+  st.init();
 
   const int r0 = it.rt * p.rb, r1 = r0 + 16 * QT < it.k.rows ? r0 + 16 * QT : it.k.rows;
   const KvRange rg = kv_range(p, it, r0, r1);
@@ -555,7 +576,7 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
     const bool edge = away != 0 || b0 + kKvTile > rg.least || b0 < rg.from;
     const KvScales kk = kv_scales(there, ks, vs);
     f16x8_t pf[QT][2];
-    kv_weights<QT, NU>(sc, row, kk, gp, edge, m, l, o, far, pf);
+    kv_weights<QT, NU>(sc, row, kk, gp, edge, st, pf);
     if constexpr (FP8) {
       if (edge) {  // codes that nobody sees can be NaN: 0 * NaN must not reach O
 #pragma unroll
@@ -576,8 +597,8 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
       const f16x8_t v0 = widen8<FP8>(vr[u][0], vr[u][1]), v1 = widen8<FP8>(vr[u][2], vr[u][3]);
 #pragma unroll
       for (int t = 0; t < QT; ++t) {
-        o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[t][0], o[t][u], 0, 0, 0);
-        o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[t][1], o[t][u], 0, 0, 0);
+        st.o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[t][0], st.o[t][u], 0, 0, 0);
+        st.o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[t][1], st.o[t][u], 0, 0, 0);
       }
     }
   }
@@ -588,15 +609,14 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
   __shared__ float mls[4][16][2];
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    l[t] += __shfl_xor(l[t], 16, 64);
-    l[t] += __shfl_xor(l[t], 32, 64);
+    st.l[t] = groups_sum(st.l[t]);
     if (t) __syncthreads();
     if (h == 0) {
-      mls[wv][c16][0] = m[t];
-      mls[wv][c16][1] = l[t];
+      mls[wv][c16][0] = st.m[t];
+      mls[wv][c16][1] = st.l[t];
     }
 #pragma unroll
-    for (int u = 0; u < NU; ++u) *(f32x4v*)&os[wv][c16][16 * u + 4 * h] = o[t][u];
+    for (int u = 0; u < NU; ++u) *(f32x4v*)&os[wv][c16][16 * u + 4 * h] = st.o[t][u];
     __syncthreads();
     const int row = threadIdx.x >> 4, sub = threadIdx.x & 15;
     const int r = it.rt * p.rb + 16 * t + row;
@@ -624,9 +644,8 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
       }
       if (sub == 0) {
         if (split) {
-          float* ml = p.ml + (it.slot * p.rb + 16 * t + row) * 2;
-          ml[0] = sum == sum ? top : -kNegInf;  // NaN has the last word in the join
-          ml[1] = sum;
+          const f32x2v ml = {sum == sum ? top : -kNegInf, sum};  // NaN has the last word in the join
+          *(f32x2v*)(p.ml + (it.slot * p.rb + 16 * t + row) * 2) = ml;
         } else if (a.lse) {
           a.lse[tok * a.heads + hq] = kv_lse(top, sum);
         }
@@ -643,12 +662,17 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
 // softmax and the products within the registers of two waves per SIMD.
 template <int D>
 struct KvPromptShape {
-  static constexpr int QT = D == 64 ? 3 : 2, WAVES = D <= 128 ? 2 : 1;  // waves per SIMD
+  // 16-row tiles of a wave, waves of a workgroup, waves per SIMD
+  static constexpr int QT = 2, NW = 4, WAVES = D <= 128 ? 2 : 1;
 };
 
-template <int D, bool FP8>
-__global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAttnArgs p) {
-  constexpr int QT = KvPromptShape<D>::QT, NJ = D / 32, NU = D / 16, KC = D / 16, NQ = D / 64;
+// BIG: blocks of 64 tokens and more, so a tile lies in one block (scalar addresses
+// and scales).
+template <int D, bool FP8, bool BIG>
+__global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAttnArgs p) {
+  constexpr int QT = KvPromptShape<D>::QT, NJ = D / 32, NU = D / 16, KC = D / 16;
+  constexpr int NT = 64 * KvPromptShape<D>::NW, C = kKvTile * KC, NQ = 2 * C / NT;  // 16-code chunks of K and V
+  static_assert(C % NT == 0 || NT == 2 * C, "a wave loads K chunks or V chunks at a time");
   constexpr int K_BYTES = kKvTile * D * 2, BUF = 2 * K_BYTES;
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * BUF];
   const KvAttn& a = p.a;
@@ -664,16 +688,8 @@ __global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAt
 #pragma unroll
   for (int t = 0; t < QT; ++t)
     row[t] = kv_query(p, it, w0 + 16 * t + c16, qf[t], [&](int j) { return 32 * j + 8 * h; });
-  f32x4v o[QT][NU];
-  float m[QT], l[QT];
-  int far = 0;
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    m[t] = kNegInf;
-    l[t] = 0.0f;
-#pragma unroll
-    for (int u = 0; u < NU; ++u) o[t][u] = f32x4v{0.f, 0.f, 0.f, 0.f};
-  }
+  KvState<QT, NU> st;
+  st.init();
   const int r0 = it.rt * p.rb, r1 = r0 + p.rb < it.k.rows ? r0 + p.rb : it.k.rows;
   const KvRange rg = kv_range(p, it, r0, r1);
   // what this wave's own rows see (none: rows past the end)
@@ -684,13 +700,18 @@ __global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAt
 
   const int* table = a.q.table + it.seq * a.q.table_stride;
   const int64_t bhead = (int64_t)T * D;
-  // Block (times kv heads, plus the head) of lane group h's 16 tokens of a tile,
-  // or -1 where no row sees them or there is none.
+  // Block (times kv heads, plus the head) of a tile (BIG) or of lane group h's 16
+  // tokens of it, or -1 where no row sees them or there is none.
   auto block_of = [&](int tt) -> int64_t {
-    const int gp = tt * kKvTile + 16 * h;
-    if (tt >= rg.t1 || gp >= rg.hi || gp + 16 <= rg.lo) return -1;
+    const int gp = tt * kKvTile + (BIG ? 0 : 16 * h);
+    if (tt >= rg.t1 || gp >= rg.hi || (!BIG && gp + 16 <= rg.lo)) return -1;
     const int64_t b = table[gp >> tsh];
     return b >= 0 && b < a.c.blocks ? b * H + it.head : -1;
+  };
+  // whether lane group g's tokens of a tile are there
+  auto is_there = [&](int tt, int64_t blk, int g) {
+    const int gp = tt * kKvTile + 16 * g;
+    return blk >= 0 && (!BIG || (gp < rg.hi && gp + 16 > rg.lo));
   };
   // A 16-byte LDS access takes lanes l .. l + 7 and l + 16 .. l + 23 (two lane groups)
   // at a time, from 16 slots of 16 bytes: the xor of a row's chunks is chosen so
@@ -701,39 +722,40 @@ __global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAt
     return D % 128 == 0 ? 2 * ((r & 3) | ((r >> 2) & 4)) : ((r & 2) | ((r >> 2) & 4));
   };
   auto v_swizzle = [](int d) { return ((d >> 2) & 1) | ((d << 1) & 4); };
-  u32x4v kr[NQ], vr[NQ];
-  const unsigned koff = tid * 16, voff = (tid >> 2) * T + 16 * (tid & 3);
-  // Codes of a tile: K chunk tid + 256 q is row (token) / KC, 16 elements; V chunk
-  // tid + 256 q is row (dim) / 4, tokens 16 (tid % 4).
+  // Chunk i = tid + NT q of a tile: of K for i < C (row i / KC, 16 elements), of V
+  // above (dim (i - C) / 4, tokens 16 (i % 4)).
+  u32x4v cr[NQ];
+  auto is_k = [&](int q) { return C % NT == 0 ? q < C / NT : wv < C / 64; };
+  const unsigned koff = tid * 16, voff = (unsigned)((tid - (C % NT == 0 ? 0 : C)) >> 2) * T + 16 * (tid & 3);
   auto fetch = [&](int tt, int64_t blk) {
     const int64_t safe = blk < 0 ? it.head : blk;
-    if (tsh >= 6) {  // the tile lies in one block: scalar base, constant lane offsets
-      const uint64_t seen = __ballot(blk >= 0);  // by some group, if by any
-      const int64_t at = uniform(__shfl(safe, seen ? __ffsll((unsigned long long)seen) - 1 : 0, 64)) * bhead;
+    if constexpr (BIG) {
       const int o = (tt * kKvTile) & (T - 1);
-      const uint8_t *kb = a.c.k + at + o * D, *vb = a.c.v + at + o;
+      const uint8_t *kb = a.c.k + safe * bhead + o * D, *vb = a.c.v + safe * bhead + o;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
-        kr[q] = *(const u32x4v*)(kb + koff + q * 4096);
-        vr[q] = *(const u32x4v*)(vb + voff + q * 64 * T);
+        if (is_k(q)) cr[q] = *(const u32x4v*)(kb + koff + q * (NT * 16));
+        else cr[q] = *(const u32x4v*)(vb + voff + (C % NT == 0 ? (q - C / NT) * (NT / 4) : 0) * T);
       }
     } else {
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
-        const int i = tid + 256 * q, r = i / KC;
-        const int64_t b = __shfl(safe, 16 * (r >> 4), 64);
-        kr[q] = *(const u32x4v*)(a.c.k + b * bhead + (int64_t)(r & (T - 1)) * D + 16 * (i % KC));
+        const int i = tid + NT * q;
+        if (is_k(q)) {
+          const int r = i / KC;
+          const int64_t b = __shfl(safe, 16 * (r >> 4), 64);
+          cr[q] = *(const u32x4v*)(a.c.k + b * bhead + (int64_t)(r & (T - 1)) * D + 16 * (i % KC));
+        } else {
+          const int64_t b = __shfl(safe, 16 * (tid & 3), 64);
+          cr[q] = *(const u32x4v*)(a.c.v + b * bhead + (int64_t)((i - C) / 4) * T + ((16 * (tid & 3)) & (T - 1)));
+        }
       }
-      const int64_t b = __shfl(safe, 16 * (tid & 3), 64);
-#pragma unroll
-      for (int q = 0; q < NQ; ++q)
-        vr[q] = *(const u32x4v*)(a.c.v + b * bhead + (int64_t)(tid / 4 + 64 * q) * T + ((16 * (tid & 3)) & (T - 1)));
     }
   };
   auto widen = [&](int tt, int64_t blk, uint8_t* buf) {
     if constexpr (FP8) {  // codes that nobody sees can be NaN: 0 * NaN must not reach O
       const int tok = tt * kKvTile + 16 * (tid & 3);
-      const bool none = __shfl((int)(blk < 0), 16 * (tid & 3), 64);
+      const bool none = BIG ? !is_there(tt, blk, tid & 3) : (bool)__shfl((int)(blk < 0), 16 * (tid & 3), 64);
       if (none || tok + 16 > rg.hi || tok < rg.lo) {
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
@@ -742,24 +764,26 @@ __global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAt
           for (int e = 0; e < 4; ++e)
             if (!none && tok + 4 * d + e < rg.hi && tok + 4 * d + e >= rg.lo) keep |= 0xFFu << (8 * e);
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) vr[q][d] &= keep;
+          for (int q = 0; q < NQ; ++q)
+            if (!is_k(q)) cr[q][d] &= keep;
         }
       }
     }
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const int i = tid + 256 * q, r = i / KC, c = 2 * (i % KC), z = k_swizzle(r);
-      uint8_t* k = buf + r * (2 * D);
-      // which of its two chunks a thread writes first: sixteen different slots for
-      // lanes l .. l + 7 and l + 16 .. l + 23
-      const int odd = ((c >> 3) ^ (r / (256 / D))) & 1;
-      const f16x8_t k0 = widen8<FP8>(kr[q][0], kr[q][1]), k1 = widen8<FP8>(kr[q][2], kr[q][3]);
-      *(f16x8_t*)(k + ((c + odd) ^ z) * 16) = odd ? k1 : k0;
-      *(f16x8_t*)(k + ((c + 1 - odd) ^ z) * 16) = odd ? k0 : k1;
-      const int d = tid / 4 + 64 * q, x = 2 * (tid & 3);
-      uint8_t* v = buf + K_BYTES + d * 128;
-      *(f16x8_t*)(v + (x ^ v_swizzle(d)) * 16) = widen8<FP8>(vr[q][0], vr[q][1]);
-      *(f16x8_t*)(v + ((x + 1) ^ v_swizzle(d)) * 16) = widen8<FP8>(vr[q][2], vr[q][3]);
+      const int i = tid + NT * q;
+      const f16x8_t x0 = widen8<FP8>(cr[q][0], cr[q][1]), x1 = widen8<FP8>(cr[q][2], cr[q][3]);
+      if (is_k(q)) {
+        const int r = i / KC, c = 2 * (i % KC), z = k_swizzle(r);
+        uint8_t* k = buf + r * (2 * D);
+        *(f16x8_t*)(k + (c ^ z) * 16) = x0;
+        *(f16x8_t*)(k + ((c + 1) ^ z) * 16) = x1;
+      } else {
+        const int d = (i - C) / 4, x = 2 * (tid & 3);
+        uint8_t* v = buf + K_BYTES + d * 128;
+        *(f16x8_t*)(v + (x ^ v_swizzle(d)) * 16) = x0;
+        *(f16x8_t*)(v + ((x + 1) ^ v_swizzle(d)) * 16) = x1;
+      }
     }
   };
 
@@ -778,36 +802,34 @@ __global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAt
       if (b0 < mine.hi && b0 + kKvTile > mine.lo) {
         f32x4v sc[QT][4];
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-          const int r = 16 * (c16 >> 2) + 4 * mt + (c16 & 3);
-          const uint8_t* k = buf + r * (2 * D);
-          const int z = k_swizzle(r);
+        for (int t = 0; t < QT; ++t)
 #pragma unroll
-          for (int t = 0; t < QT; ++t) sc[t][mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
+          for (int mt = 0; mt < 4; ++mt) sc[t][mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            const f16x8_t kf = *(const f16x8_t*)(k + ((4 * j + h) ^ z) * 16);
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            const int r = 16 * (c16 >> 2) + 4 * mt + (c16 & 3);
+            const f16x8_t kf = *(const f16x8_t*)(buf + r * (2 * D) + ((4 * j + h) ^ k_swizzle(r)) * 16);
 #pragma unroll
             for (int t = 0; t < QT; ++t)
               sc[t][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[t][j], sc[t][mt], 0, 0, 0);
           }
-        }
-        const bool edge = __any(blk < 0) || b0 + kKvTile > mine.least || b0 < mine.from;
-        const KvScales kk = kv_scales(blk >= 0, ks, vs);
+        const bool there = is_there(tt, blk, h);
+        const bool edge = __any(!there) || b0 + kKvTile > mine.least || b0 < mine.from;
+        const KvScales kk = kv_scales(there, ks, vs);
         f16x8_t pf[QT][2];
-        kv_weights<QT, NU>(sc, row, kk, b0 + 16 * h, edge, m, l, o, far, pf);
+        kv_weights<QT, NU>(sc, row, kk, b0 + 16 * h, edge, st, pf);
 #pragma unroll
-        for (int u = 0; u < NU; ++u) {
-          const int d = 16 * u + c16;
-          const uint8_t* v = buf + K_BYTES + d * 128;
-          const f16x8_t v0 = *(const f16x8_t*)(v + ((2 * h) ^ v_swizzle(d)) * 16);
-          const f16x8_t v1 = *(const f16x8_t*)(v + ((2 * h + 1) ^ v_swizzle(d)) * 16);
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int t = 0; t < QT; ++t) {
-            o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[t][0], o[t][u], 0, 0, 0);
-            o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[t][1], o[t][u], 0, 0, 0);
+          for (int u = 0; u < NU; ++u) {
+            const int d = 16 * u + c16;
+            const f16x8_t vf = *(const f16x8_t*)(buf + K_BYTES + d * 128 + ((2 * h + x) ^ v_swizzle(d)) * 16);
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+              st.o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[t][x], st.o[t][u], 0, 0, 0);
           }
-        }
       }
       if (tt + 1 < rg.t1) {
         widen(tt + 1, blk1, smem + ((tt + 1 - rg.t0) & 1) * BUF);
@@ -823,27 +845,24 @@ __global__ __launch_bounds__(256, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAt
   }
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    l[t] += __shfl_xor(l[t], 16, 64);
-    l[t] += __shfl_xor(l[t], 32, 64);
+    st.l[t] = groups_sum(st.l[t]);
     const int r = w0 + 16 * t + c16;
     if (r >= it.k.rows) continue;
     const int64_t tok = it.r.first + r / p.g, hq = it.head * p.g + r % p.g;
     if (it.chunks > 1) {
       const int64_t at = it.slot * p.rb + (r - r0);
 #pragma unroll
-      for (int u = 0; u < NU; ++u) *(f32x4v*)(p.po + at * D + 16 * u + 4 * h) = o[t][u];
-      if (h == 0) {
-        p.ml[at * 2] = l[t] == l[t] ? m[t] : -kNegInf;  // NaN has the last word in the join
-        p.ml[at * 2 + 1] = l[t];
-      }
+      for (int u = 0; u < NU; ++u) *(f32x4v*)(p.po + at * D + 16 * u + 4 * h) = st.o[t][u];
+      const f32x2v ml = {st.l[t] == st.l[t] ? st.m[t] : -kNegInf, st.l[t]};  // NaN has the last word in the join
+      if (h == 0) *(f32x2v*)(p.ml + at * 2) = ml;
     } else {
-      const float inv = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
+      const float inv = st.l[t] == 0.0f ? 0.0f : 1.0f / st.l[t];
       const int64_t at = (tok * a.heads + hq) * D;
 #pragma unroll
       for (int u = 0; u < NU; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) kv_store_out(a, at + 16 * u + 4 * h + e, o[t][u][e] * inv);
-      if (a.lse && h == 0) a.lse[tok * a.heads + hq] = kv_lse(m[t], l[t]);
+        for (int e = 0; e < 4; ++e) kv_store_out(a, at + 16 * u + 4 * h + e, st.o[t][u][e] * inv);
+      if (a.lse && h == 0) a.lse[tok * a.heads + hq] = kv_lse(st.m[t], st.l[t]);
     }
   }
 }
@@ -894,8 +913,9 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many
 #pragma unroll 4
     for (int c = wv; c < chunks; c += 4) {
       const int64_t s = at0 + c * step;
-      const float f = __builtin_amdgcn_exp2f(p.ml[s * 2] - top);
-      sum = __builtin_fmaf(p.ml[s * 2 + 1], f, sum);
+      const f32x2v ml = *(const f32x2v*)(p.ml + s * 2);
+      const float f = __builtin_amdgcn_exp2f(ml[0] - top);
+      sum = __builtin_fmaf(ml[1], f, sum);
 #pragma unroll
       for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(p.po[s * D + lane * V + e], f, v[e]);
     }
@@ -914,7 +934,11 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many
 
 namespace {
 // Row shapes of the prompt kernel by head dim (KvPromptShape).
-int prompt_rows(int dim) { return 64 * (dim == 64 ? 3 : 2); }
+template <int D>
+constexpr int kPromptRows = 16 * KvPromptShape<D>::QT * KvPromptShape<D>::NW;
+int prompt_rows(int dim) {
+  return dim == 64 ? kPromptRows<64> : dim == 128 ? kPromptRows<128> : dim == 192 ? kPromptRows<192> : kPromptRows<256>;
+}
 
 struct KvPlan {
   KvAttnArgs few, many;
@@ -987,8 +1011,9 @@ hipError_t launch_kv_attn(const KvAttn& a, void* ws, hipStream_t s) {
   const KvPlan p = kv_plan(a, (char*)ws);
   auto dim = [&]<int D>() {
     if (p.run_many) {
-      auto k = a.c.fp8 ? k_kv_prompt<D, true> : k_kv_prompt<D, false>;
-      hipLaunchKernelGGL(k, dim3((unsigned)p.many.items), dim3(256), 0, s, p.many);
+      auto k = a.c.tsh >= 6 ? (a.c.fp8 ? k_kv_prompt<D, true, true> : k_kv_prompt<D, false, true>)
+                            : (a.c.fp8 ? k_kv_prompt<D, true, false> : k_kv_prompt<D, false, false>);
+      hipLaunchKernelGGL(k, dim3((unsigned)p.many.items), dim3(64 * KvPromptShape<D>::NW), 0, s, p.many);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
