@@ -362,9 +362,11 @@ __device__ inline KvScales kv_scales(bool there, float ks, float vs) {
 // Over the four lane groups (lanes l ^ 16, l ^ 32).
 __device__ inline float groups_max(float v) {
   auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-  r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  float m;
+  asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(r[0]), "v"(r[1]));
+  r = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+  asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(r[0]), "v"(r[1]));
+  return m;
 }
 
 // State of a wave's rows over the tiles.
@@ -663,7 +665,7 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
 template <int D>
 struct KvPromptShape {
   // 16-row tiles of a wave, waves of a workgroup, waves per SIMD
-  static constexpr int QT = 2, NW = 4, WAVES = D <= 128 ? 2 : 1;
+  static constexpr int QT = D <= 128 ? 1 : 2, NW = D <= 128 ? 8 : 4, WAVES = D <= 128 ? 4 : 1;
 };
 
 // BIG: blocks of 64 tokens and more, so a tile lies in one block (scalar addresses
@@ -800,6 +802,7 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
       const int b0 = tt * kKvTile;
       const float ks1 = a.c.ks[blk1 < 0 ? it.head : blk1], vs1 = a.c.vs[blk1 < 0 ? it.head : blk1];
       if (b0 < mine.hi && b0 + kKvTile > mine.lo) {
+        __builtin_amdgcn_s_setprio(1);
         f32x4v sc[QT][4];
 #pragma unroll
         for (int t = 0; t < QT; ++t)
@@ -815,11 +818,13 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
             for (int t = 0; t < QT; ++t)
               sc[t][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[t][j], sc[t][mt], 0, 0, 0);
           }
+        __builtin_amdgcn_s_setprio(0);
         const bool there = is_there(tt, blk, h);
         const bool edge = __any(!there) || b0 + kKvTile > mine.least || b0 < mine.from;
         const KvScales kk = kv_scales(there, ks, vs);
         f16x8_t pf[QT][2];
         kv_weights<QT, NU>(sc, row, kk, b0 + 16 * h, edge, st, pf);
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -830,6 +835,7 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
             for (int t = 0; t < QT; ++t)
               st.o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[t][x], st.o[t][u], 0, 0, 0);
           }
+        __builtin_amdgcn_s_setprio(0);
       }
       if (tt + 1 < rg.t1) {
         widen(tt + 1, blk1, smem + ((tt + 1 - rg.t0) & 1) * BUF);
