@@ -34,7 +34,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvCache c, KvSeqs q, KvRow
   __shared__ float red[kBlock / 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int T = 1 << c.tsh, D = c.dim;
-  int64_t b, j;
+  int b, j;
   const bool found = find_sequence(q.seqs, blockIdx.x, lane, b, j, [&](int64_t i) -> int64_t {
     const SeqRows r = seq_rows(q, i);
     const int p0 = r.len > r.n ? r.len - r.n : 0;
@@ -218,6 +218,8 @@ struct KvAttnArgs {
   float* po;        // [items][rb][D]
 };
 
+constexpr int kNever = 1 << 26;  // tiles of a chunk that nothing reaches
+
 struct KvWork {
   int rows, rt, lo, tiles;  // rows, row tiles, first tile, tiles of the visible range
 };
@@ -250,33 +252,37 @@ __device__ inline int64_t uniform(int64_t v) {
 struct KvItem {
   SeqRows r;
   KvWork k;
-  int64_t seq, slot;
-  int chunk, chunks, len, rt, head;  // len: tiles of a chunk
+  int64_t slot;
+  int seq, chunk, chunks, len, rt, head;  // len: tiles of a chunk
 };
 __device__ inline bool kv_item(const KvAttnArgs& w, int64_t id, int lane, KvItem& it) {
   const int H = w.a.c.heads;
   const int64_t seqs = w.a.q.seqs;
-  int64_t all = 0;
-  for (int64_t b0 = 0; b0 < seqs; b0 += 64) {
-    const int64_t b = b0 + lane;
-    int64_t c = 0;
-    if (b < seqs) {
-      const KvWork k = kv_work(w, seq_rows(w.a.q, b));
-      c = (int64_t)k.rt * k.tiles;
-    }
-    all += __shfl(wave_scan_sum(c, lane), 63, 64);
-  }
-  int64_t len = (all * H + w.target - 1) / w.target;
-  len = len < w.cmin ? w.cmin : (len + 3) / 4 * 4;  // four waves share a chunk
-  int64_t local;
-  if (!find_sequence(seqs, id / H, lane, it.seq, local, [&](int64_t b) -> int64_t {
+  // chunk length: all tiles of all row tiles over the items aimed at
+  int64_t len = w.cmin;
+  if (w.cmin < kNever) {
+    int64_t all = 0;
+    for (int64_t b0 = 0; b0 < seqs; b0 += 64) {
+      const int64_t b = b0 + lane;
+      int64_t c = 0;
+      if (b < seqs) {
         const KvWork k = kv_work(w, seq_rows(w.a.q, b));
-        const int64_t ch = (k.tiles + len - 1) / len;
-        return k.rt * (ch > 1 ? ch : 1);
+        c = (int64_t)k.rt * k.tiles;
+      }
+      const uint32_t n = (uint32_t)(c < kMostUnits ? c : kMostUnits);
+      all += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan_sum(n), 63);
+    }
+    len = (all * H + w.target - 1) / w.target;
+    len = len < w.cmin ? w.cmin : (len + 3) / 4 * 4;  // four waves share a chunk
+  }
+  it.len = uniform((int)len);
+  int at;
+  if (!find_sequence(seqs, id / H, lane, it.seq, at, [&](int64_t b) -> int64_t {
+        const KvWork k = kv_work(w, seq_rows(w.a.q, b));
+        const int ch = (k.tiles + it.len - 1) / it.len;
+        return (int64_t)k.rt * (ch > 1 ? ch : 1);
       }))
     return false;
-  it.seq = uniform(it.seq);
-  it.len = uniform((int)len);
   it.r = seq_rows(w.a.q, it.seq);
   it.r.first = uniform(it.r.first);
   it.r.n = uniform(it.r.n);
@@ -284,12 +290,11 @@ __device__ inline bool kv_item(const KvAttnArgs& w, int64_t id, int lane, KvItem
   it.k = kv_work(w, it.r);
   it.chunks = (it.k.tiles + it.len - 1) / it.len;
   if (it.chunks < 1) it.chunks = 1;
-  const int at = uniform((int)local);
   it.chunk = at / it.k.rt;
   it.rt = it.k.rt - 1 - at % it.k.rt;  // the last rows see the most: first
   it.head = (int)(id % H);
   it.slot = id;
-  if (w.plan && local == 0 && it.head == 0 && threadIdx.x == 0) {
+  if (w.plan && at == 0 && it.head == 0 && threadIdx.x == 0) {
     w.plan[2 * it.seq] = (int)(id / H);
     w.plan[2 * it.seq + 1] = it.chunks;
   }
@@ -531,7 +536,7 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
   const int r0 = it.rt * p.rb, r1 = r0 + 16 * QT < it.k.rows ? r0 + 16 * QT : it.k.rows;
   const KvRange rg = kv_range(p, it, r0, r1);
   const int lo = rg.lo, hi = rg.hi;
-  const int* table = a.q.table + it.seq * a.q.table_stride;
+  const int* table = a.q.table + (int64_t)it.seq * a.q.table_stride;
   const int64_t bhead = (int64_t)T * D;
 
   for (int tt = rg.t0 + wv; tt < rg.t1; tt += 4) {
@@ -700,7 +705,7 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
   if (w0 < w1) mine = kv_range(p, it, w0, w1);
   else mine.hi = 0;
 
-  const int* table = a.q.table + it.seq * a.q.table_stride;
+  const int* table = a.q.table + (int64_t)it.seq * a.q.table_stride;
   const int64_t bhead = (int64_t)T * D;
   // Block (times kv heads, plus the head) of a tile (BIG) or of lane group h's 16
   // tokens of it, or -1 where no row sees them or there is none.
@@ -873,14 +878,16 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
   }
 }
 
-// Joins the chunks of split sequences: one workgroup per (token, query head), the
-// chunks dealt to its four waves, whose sums meet in wave order.
-template <int D>
+// Joins the chunks of split sequences, W waves per (token, query head): the chunks are
+// dealt to them, and their sums meet in wave order.  Four waves where there are
+// few rows and so long chains of chunks, one where there are many.
+template <int D, int W>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many) {
   constexpr int V = D / 64;
   const KvAttn& a = few.a;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t id = blockIdx.x;
+  const int lane = threadIdx.x & 63, wv = uniform((int)threadIdx.x >> 6) % W;
+  const int64_t id = W == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + uniform((int)threadIdx.x >> 6);
+  if (W == 1 && id >= a.q.total * a.heads) return;
   const int64_t tok = id / a.heads;
   const int hq = (int)(id % a.heads);
   int64_t seq = 0;
@@ -917,7 +924,7 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many
   for (int e = 0; e < V; ++e) v[e] = 0.0f;
   if (top != kNegInf) {
 #pragma unroll 4
-    for (int c = wv; c < chunks; c += 4) {
+    for (int c = wv; c < chunks; c += W) {
       const int64_t s = at0 + c * step;
       const f32x2v ml = *(const f32x2v*)(p.ml + s * 2);
       const float f = __builtin_amdgcn_exp2f(ml[0] - top);
@@ -926,16 +933,22 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many
       for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(p.po[s * D + lane * V + e], f, v[e]);
     }
   }
-  __shared__ float part[4][D], sums[4];
+  if constexpr (W == 4) {
+    __shared__ float part[4][D], sums[4];
 #pragma unroll
-  for (int e = 0; e < V; ++e) part[wv][lane * V + e] = v[e];
-  if (lane == 0) sums[wv] = sum;
-  __syncthreads();
-  sum = sums[0] + sums[1] + sums[2] + sums[3];
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  for (int d = threadIdx.x; d < D; d += 256)
-    kv_store_out(a, id * D + d, (part[0][d] + part[1][d] + part[2][d] + part[3][d]) * inv);
-  if (a.lse && threadIdx.x == 0) a.lse[id] = kv_lse(top, sum);
+    for (int e = 0; e < V; ++e) part[wv][lane * V + e] = v[e];
+    if (lane == 0) sums[wv] = sum;
+    __syncthreads();
+    sum = sums[0] + sums[1] + sums[2] + sums[3];
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    for (int d = threadIdx.x; d < D; d += 256)
+      kv_store_out(a, id * D + d, (part[0][d] + part[1][d] + part[2][d] + part[3][d]) * inv);
+  } else {
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int e = 0; e < V; ++e) kv_store_out(a, id * D + lane * V + e, v[e] * inv);
+  }
+  if (a.lse && wv == 0 && lane == 0) a.lse[id] = kv_lse(top, sum);
 }
 
 namespace {
@@ -959,7 +972,6 @@ struct KvPlan {
 // few-rows kernel, the others to the prompt kernel; without offsets all have the
 // same count, with offsets both may be needed.
 KvPlan kv_plan(const KvAttn& a, char* ws) {
-  constexpr int kNever = 1 << 26;  // tiles of a chunk that nothing reaches
   KvPlan p;
   const int g = a.heads / a.c.heads;
   const int64_t H = a.c.heads, rows = a.q.nper * g, cus = device_cu_count();
@@ -1037,7 +1049,11 @@ hipError_t launch_kv_attn(const KvAttn& a, void* ws, hipStream_t s) {
       if (e != hipSuccess) return e;
     }
     if (p.split) {
-      hipLaunchKernelGGL((k_kv_join<D>), dim3((unsigned)(a.q.total * a.heads)), dim3(256), 0, s, p.few, p.many);
+      const int64_t rows = a.q.total * a.heads;
+      if (rows <= 16 * device_cu_count())
+        hipLaunchKernelGGL((k_kv_join<D, 4>), dim3((unsigned)rows), dim3(256), 0, s, p.few, p.many);
+      else
+        hipLaunchKernelGGL((k_kv_join<D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, p.few, p.many);
       return hipGetLastError();
     }
     return hipSuccess;

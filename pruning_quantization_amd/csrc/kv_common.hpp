@@ -36,34 +36,40 @@ __device__ inline SeqRows seq_rows(const KvSeqs& q, int64_t b) {
   return r;
 }
 
-// Inclusive sum over the wave's lanes (every lane active).
-__device__ inline int64_t wave_scan_sum(int64_t v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t u = __shfl_up(v, o, 64);
-    if (lane >= o) v += u;
-  }
+// Inclusive sum over the wave's lanes (every lane active), by DPP: within rows of
+// 16 lanes, then across them.
+__device__ inline uint32_t wave_scan_sum(uint32_t v) {
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true);   // row_shr:1
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true);   // row_shr:2
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true);   // row_shr:4
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true);   // row_shr:8
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);  // row_bcast:15
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);  // row_bcast:31
   return v;
 }
 
+// Counts of one sequence are held below 2^26, so that 64 of them add up in 32 bits
+// (the calls' size limits keep sane ones below it; offsets that do not ascend
+// can ask for more, and then get fewer units than they asked for).
+constexpr int64_t kMostUnits = (1 << 26) - 1;
+
 // The sequence that holds unit `item` when sequence b has count(b) of them in
 // order, and the unit's number within it; false if there are fewer units.
-// Every lane of the wave takes part and gets the same answer.
+// Every lane of the wave takes part and gets the same answer (scalars).
 template <class F>
-__device__ inline bool find_sequence(int64_t seqs, int64_t item, int lane, int64_t& seq,
-                                     int64_t& local, F&& count) {
+__device__ inline bool find_sequence(int64_t seqs, int64_t item, int lane, int& seq, int& local, F&& count) {
   int64_t base = 0;
   for (int64_t b0 = 0; b0 < seqs; b0 += 64) {
-    const int64_t b = b0 + lane, c = b < seqs ? count(b) : 0;
-    const int64_t end = base + wave_scan_sum(c, lane);
-    const uint64_t past = __ballot(end > item);
+    const int64_t b = b0 + lane, n = b < seqs ? count(b) : 0;
+    const uint32_t c = (uint32_t)(n < kMostUnits ? n : kMostUnits), end = wave_scan_sum(c);
+    const uint64_t past = __ballot((int64_t)end > item - base);
     if (past) {
       const int src = __ffsll((unsigned long long)past) - 1;
-      seq = b0 + src;
-      local = item - __shfl(end - c, src, 64);
+      seq = (int)b0 + src;
+      local = (int)(item - base) - __builtin_amdgcn_readlane((int)(end - c), src);
       return true;
     }
-    base = __shfl(end, 63, 64);
+    base += (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
   }
   return false;
 }
