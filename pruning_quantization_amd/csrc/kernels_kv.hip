@@ -14,13 +14,30 @@ namespace sparq24 {
 // and where s > s_old the codes before the new ones become
 //   encode(fp32(code * fp32(s_old * fp32(1 / s)))).
 // Codes behind the new ones stay as they are.
+//
+// A thread takes 4 tokens x 8 dims at a time (16-byte loads, 8 dims of a row for
+// adjacent lanes' neighbours), so that both layouts are written from packed
+// dwords: K rows directly, V through LDS as [D][T] rows in 16-byte stores.  Where
+// the new rows of a block fit one round of the workgroup (T * D <= 8192) they are
+// read once and held; larger blocks read them again for the codes, from L2.
+// Bound by HBM for prompts, by latency for single tokens.
 // ---------------------------------------------------------------------------
 template <bool FP8>
-__device__ inline uint32_t kv_encode(float y) {
+__device__ inline float kv_clamp(float y) {
   constexpr float q = FP8 ? 448.0f : 127.0f;
-  y = y == y ? __builtin_amdgcn_fmed3f(y, -q, q) : 0.0f;
-  if constexpr (FP8) return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, 0.0f, 0u, false) & 0xFFu;
-  else return __float_as_uint(y + kRoundMagic) & 0xFFu;
+  return y == y ? __builtin_amdgcn_fmed3f(y, -q, q) : 0.0f;
+}
+// Codes of four fp32 values in code units, packed little-endian.
+template <bool FP8>
+__device__ inline uint32_t kv_encode4(float a, float b, float c, float d) {
+  a = kv_clamp<FP8>(a);
+  b = kv_clamp<FP8>(b);
+  c = kv_clamp<FP8>(c);
+  d = kv_clamp<FP8>(d);
+  if constexpr (FP8) return enc_e4m3_x4(a, b, c, d);
+  const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(b + kRoundMagic), __float_as_uint(a + kRoundMagic), 0x0c0c0400u);
+  const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(d + kRoundMagic), __float_as_uint(c + kRoundMagic), 0x0c0c0400u);
+  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
 }
 template <bool FP8>
 __device__ inline float kv_decode(uint32_t c) {
@@ -30,7 +47,7 @@ __device__ inline float kv_decode(uint32_t c) {
 
 template <class DT, bool FP8>
 __global__ __launch_bounds__(kBlock) void k_kv_append(KvCache c, KvSeqs q, KvRows kr, KvRows vr) {
-  extern __shared__ uint8_t tile[];  // V: codes [D][T + 4]
+  extern __shared__ __attribute__((aligned(16))) uint8_t tile[];  // V: codes [D][T + 16]
   __shared__ float red[kBlock / 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int T = 1 << c.tsh, D = c.dim;
@@ -57,69 +74,95 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvCache c, KvSeqs q, KvRow
   // row of the block's row o: position base + o is new token base + o - (len - n)
   const int64_t row0 = r.first + (base - ((int64_t)r.len - r.n));
   const char* x = rows.x + row0 * rows.ts + head * rows.hs;
-  const int upr = D / 8, units = (o1 - o0) * upr;
+  float* sp = (side_v ? c.vs : c.ks) + blk * c.heads + head;
+  const float old = o0 ? *sp : 0.0f;
+  uint8_t* codes = (side_v ? c.v : c.k) + (blk * c.heads + head) * (int64_t)T * D;
 
-  float am = 0.0f;
-  for (int i = tid; i < units; i += kBlock) {
-    Unit<DT> u;
-    load_unit(u, x + (int64_t)(o0 + i / upr) * rows.ts + (i % upr) * 8 * DT::ESIZE);
+  // quad i: tokens 4 g .. 4 g + 3 (those outside o0 .. o1 - 1 left out), dims 8 d ..
+  const unsigned upr = D / 8, g0 = o0 >> 2, quads = (((o1 + 3) >> 2) - g0) * upr;
+  const int pitch = T + 16;
+  auto load = [&](unsigned i, Unit<DT>(&u)[4]) {
+    const int o = 4 * (g0 + i / upr), d = 8 * (i % upr);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) am = __builtin_fmaxf(am, __builtin_fabsf(u.f(e)));
+    for (int e = 0; e < 4; ++e) {
+      if (o + e >= o0 && o + e < o1) load_unit(u[e], x + (int64_t)(o + e) * rows.ts + d * DT::ESIZE);
+      else zero_unit(u[e]);
+    }
+  };
+  float am = 0.0f;
+  auto widest = [&](const Unit<DT>(&u)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int f = 0; f < 8; ++f) am = __builtin_fmaxf(am, __builtin_fabsf(u[e].f(f)));
+  };
+  auto store = [&](unsigned i, const Unit<DT>(&u)[4], float inv) {
+    const int o = 4 * (g0 + i / upr), d = 8 * (i % upr);
+    if (side_v) {
+#pragma unroll
+      for (int f = 0; f < 8; ++f)
+        *(uint32_t*)(tile + (d + f) * pitch + o) =
+            kv_encode4<FP8>(u[0].f(f) * inv, u[1].f(f) * inv, u[2].f(f) * inv, u[3].f(f) * inv);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint2 w;
+        w.x = kv_encode4<FP8>(u[e].f(0) * inv, u[e].f(1) * inv, u[e].f(2) * inv, u[e].f(3) * inv);
+        w.y = kv_encode4<FP8>(u[e].f(4) * inv, u[e].f(5) * inv, u[e].f(6) * inv, u[e].f(7) * inv);
+        if (o + e >= o0 && o + e < o1) *(uint2*)(codes + (o + e) * D + d) = w;
+      }
+    }
+  };
+  Unit<DT> held[4];
+  const bool once = quads <= kBlock;
+  if (once) {
+    if (tid < (int)quads) {
+      load(tid, held);
+      widest(held);
+    }
+  } else {
+    for (unsigned i = tid; i < quads; i += kBlock) {
+      load(i, held);
+      widest(held);
+    }
   }
   am = __uint_as_float(wave_max_u32<64>(__float_as_uint(am)));
   if (lane == 0) red[tid >> 6] = am;
-  __syncthreads();
+  __syncthreads();  // (every thread has read the old scale, too)
 #pragma unroll
   for (int i = 0; i < kBlock / 64; ++i) am = __builtin_fmaxf(am, red[i]);
 
-  float* sp = (side_v ? c.vs : c.ks) + blk * c.heads + head;
-  const float old = o0 ? *sp : 0.0f;
   const float cand = am >= 0x1p-64f ? am / (FP8 ? 448.0f : 127.0f) : 0.0f;
   const float s = cand > old ? cand : old;
   const float inv = s > 0.0f ? 1.0f / s : 0.0f;
-  __syncthreads();  // every thread has read the old scale
   if (tid == 0) *sp = s;
-  uint8_t* codes = (side_v ? c.v : c.k) + (blk * c.heads + head) * (int64_t)T * D;
   if (o0 && s > old) {  // code what the block held again, to the grown scale
     const float ratio = old * inv;
-    if (side_v) {
-      for (int i = tid; i < D * o0; i += kBlock) {
-        uint8_t* p = codes + (i / o0) * T + i % o0;
-        *p = (uint8_t)kv_encode<FP8>(kv_decode<FP8>(*p) * ratio);
-      }
-    } else {
-      for (int i = tid; i < o0 * D; i += kBlock)
-        codes[i] = (uint8_t)kv_encode<FP8>(kv_decode<FP8>(codes[i]) * ratio);
+    for (int i = tid; i < D * o0; i += kBlock) {
+      uint8_t* p = side_v ? codes + (i / o0) * T + i % o0 : codes + i;
+      *p = (uint8_t)kv_encode4<FP8>(kv_decode<FP8>(*p) * ratio, 0.f, 0.f, 0.f);
     }
   }
-  const int pitch = T + 4;
-  for (int i = tid; i < units; i += kBlock) {
-    Unit<DT> u;
-    const int o = o0 + i / upr, d = (i % upr) * 8;
-    load_unit(u, x + (int64_t)o * rows.ts + d * DT::ESIZE);
-    uint32_t code[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) code[e] = kv_encode<FP8>(u.f(e) * inv);
-    if (side_v) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) tile[(d + e) * pitch + o] = (uint8_t)code[e];
-    } else {
-      uint32_t* p = (uint32_t*)(codes + o * D + d);
-      p[0] = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
-      p[1] = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
+  if (once) {
+    if (tid < (int)quads) store(tid, held, inv);
+  } else {
+    for (unsigned i = tid; i < quads; i += kBlock) {
+      load(i, held);
+      store(i, held, inv);
     }
   }
   if (!side_v) return;
   __syncthreads();
-  // whole dwords where the new rows cover them, bytes at the ragged ends
-  const int q0 = o0 >> 2, nq = ((o1 + 3) >> 2) - q0;
+  // 16-byte chunks that the new rows cover whole, bytes at the ragged ends
+  const int q0 = o0 >> 4, nq = ((o1 + 15) >> 4) - q0;
   for (int i = tid; i < D * nq; i += kBlock) {
-    const int d = i / nq, t = (q0 + i % nq) * 4;
-    if (t >= o0 && t + 4 <= o1) {
-      *(uint32_t*)(codes + d * T + t) = *(const uint32_t*)(tile + d * pitch + t);
+    const int d = i / nq, t = (q0 + i % nq) * 16;
+    const uint8_t* from = tile + d * pitch + t;
+    uint8_t* to = codes + d * T + t;
+    if (t >= o0 && t + 16 <= o1) {
+      *(uint4*)to = *(const uint4*)from;
     } else {
-      for (int e = t < o0 ? o0 : t; e < (t + 4 < o1 ? t + 4 : o1); ++e)
-        codes[d * T + e] = tile[d * pitch + e];
+      for (int e = t < o0 ? o0 - t : 0; e < (t + 16 < o1 ? 16 : o1 - t); ++e) to[e] = from[e];
     }
   }
 }
@@ -130,7 +173,7 @@ hipError_t launch_kv_append(const KvCache& c, const KvSeqs& q, const KvRows& k, 
   // n tokens touch at most (n + T - 2) / T + 1 blocks
   const int64_t most = q.cu ? (q.total + q.seqs * (T - 2)) / T + q.seqs
                             : q.seqs * ((q.nper + T - 2) / T + 1);
-  const size_t shmem = (size_t)c.dim * (size_t)(T + 4);
+  const size_t shmem = (size_t)c.dim * (size_t)(T + 16);
   const dim3 grid((unsigned)most, (unsigned)c.heads, 2);
   return with_dtype(dtype, [&]<class DT>() {
     auto go = [&](auto kern) {
@@ -1015,7 +1058,12 @@ KvPlan kv_plan(const KvAttn& a, char* ws) {
     if (rtf > most) rtf = most;
     rtm = a.q.total * g / rbm + (longer < a.q.seqs ? longer : a.q.seqs);
   }
-  lay(p.few, p.run_few, rbf, 0, limit, 4, 4 * cus, rtf);
+  // chunks even out ragged lengths, but the join walks them: at most 64 of a
+  // sequence and head, at most eight items per CU (64 sequences of 300..16384
+  // tokens: 248 / 227 / 219 us at two / four / eight; one of 131071: 61 / 65 / 80)
+  int64_t aim = 64 * a.q.seqs * H;
+  aim = aim < 2 * cus ? 2 * cus : (aim > 8 * cus ? 8 * cus : aim);
+  lay(p.few, p.run_few, rbf, 0, limit, 4, aim, rtf);
   lay(p.many, p.run_many, rbm, limit, INT32_MAX, 4, (a.c.dim <= 128 ? 2 : 1) * cus, rtm);
   p.need = p.split ? off : 0;
   if (!p.split) p.few.plan = p.many.plan = nullptr;
