@@ -292,6 +292,16 @@ __device__ inline int64_t uniform(int64_t v) {
   return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 | lo);
 }
 
+// Holds a value that is the same in all lanes in a scalar register.  The compiler knows
+// that it is, but may move such arithmetic into vector registers all the same,
+// here behind the divisions of kv_item: that cost the prompt kernel 20 registers,
+// reloaded in its loop (a prompt of 8192 tokens: 930 us instead of 662).
+__device__ inline int scalar(int v) {
+  v = uniform(v);
+  asm("" : "+s"(v));
+  return v;
+}
+
 struct KvItem {
   SeqRows r;
   KvWork k;
@@ -333,9 +343,9 @@ __device__ inline bool kv_item(const KvAttnArgs& w, int64_t id, int lane, KvItem
   it.k = kv_work(w, it.r);
   it.chunks = (it.k.tiles + it.len - 1) / it.len;
   if (it.chunks < 1) it.chunks = 1;
-  it.chunk = at / it.k.rt;
-  it.rt = it.k.rt - 1 - at % it.k.rt;  // the last rows see the most: first
-  it.head = (int)(id % H);
+  it.chunk = scalar(at / it.k.rt);
+  it.rt = scalar(it.k.rt - 1 - at % it.k.rt);  // the last rows see the most: first
+  it.head = scalar((int)(id % H));
   it.slot = id;
   if (w.plan && at == 0 && it.head == 0 && threadIdx.x == 0) {
     w.plan[2 * it.seq] = (int)(id / H);
@@ -552,7 +562,7 @@ __device__ inline KvRange kv_range(const KvAttnArgs& p, const KvItem& it, int r0
   if (k.t1 > it.k.lo + it.k.tiles) k.t1 = it.k.lo + it.k.tiles;
   if (k.t0 < k.lo / kKvTile) k.t0 = k.lo / kKvTile;
   if (k.t1 > (k.hi + kKvTile - 1) / kKvTile) k.t1 = (k.hi + kKvTile - 1) / kKvTile;
-  return k;
+  return {scalar(k.t0), scalar(k.t1), scalar(k.lo), scalar(k.hi), scalar(k.least), scalar(k.from)};
 }
 
 // Few rows per kv head (decoding): QT tiles of 16 rows, four waves that take
@@ -704,12 +714,15 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
   }
 }
 
-// Many rows per kv head (prompts): four waves of 16 QT rows each share every
-// tile, which is widened once into LDS as fp16 (K [64][D], V [D][64], 16-byte
-// chunks XOR-swizzled by row), one tile ahead of its use, its codes loaded one
-// tile ahead of that.  Per tile a wave reads 2 * 64 * D * 2 bytes of fragments
-// for 4 QT MFMAs of each 16 tokens x 32 elements; QT balances these reads, the
-// softmax and the products within the registers of two waves per SIMD.
+// Many rows per kv head (prompts): the waves of a workgroup hold 16 QT rows each and
+// share every tile, which is widened once into LDS as fp16 (K [64][D], V [D][64],
+// 16-byte chunks XOR-swizzled by row), one tile ahead of its use, its codes loaded
+// one tile ahead of that.  Bound by the matrix and vector units in turn: per tile,
+// 16 rows and head of 128 a wave issues 32 MFMAs (512 cycles of its SIMD's matrix
+// unit) and about 130 vector instructions of softmax, and four waves per SIMD overlap
+// the one's products with the other's softmax.  A causal prompt of 8192 tokens, 32
+// heads over 8: 648 us (849 Tflop/s of 1985 that such MFMAs reach alone); two
+// waves of 32 rows per SIMD 686, three 16-row tiles a wave 2330 (spills).
 template <int D>
 struct KvPromptShape {
   // 16-row tiles of a wave, waves of a workgroup, waves per SIMD
@@ -750,16 +763,17 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
 
   const int* table = a.q.table + (int64_t)it.seq * a.q.table_stride;
   const int64_t bhead = (int64_t)T * D;
-  // Block (times kv heads, plus the head) of a tile (BIG) or of lane group h's 16
-  // tokens of it, or -1 where no row sees them or there is none.
-  auto block_of = [&](int tt) -> int64_t {
+  // Block of a tile (BIG) or of lane group h's 16 tokens of it, or -1 where no row
+  // sees them or there is none; its place among blocks and heads (0's if none).
+  auto block_of = [&](int tt) -> int {
     const int gp = tt * kKvTile + (BIG ? 0 : 16 * h);
     if (tt >= rg.t1 || gp >= rg.hi || (!BIG && gp + 16 <= rg.lo)) return -1;
-    const int64_t b = table[gp >> tsh];
-    return b >= 0 && b < a.c.blocks ? b * H + it.head : -1;
+    const int b = table[gp >> tsh];
+    return b >= 0 && b < a.c.blocks ? b : -1;
   };
+  auto place = [&](int blk) -> int64_t { return (int64_t)(blk < 0 ? 0 : blk) * H + it.head; };
   // whether lane group g's tokens of a tile are there
-  auto is_there = [&](int tt, int64_t blk, int g) {
+  auto is_there = [&](int tt, int blk, int g) {
     const int gp = tt * kKvTile + 16 * g;
     return blk >= 0 && (!BIG || (gp < rg.hi && gp + 16 > rg.lo));
   };
@@ -772,14 +786,20 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
     return D % 128 == 0 ? 2 * ((r & 3) | ((r >> 2) & 4)) : ((r & 2) | ((r >> 2) & 4));
   };
   auto v_swizzle = [](int d) { return ((d >> 2) & 1) | ((d << 1) & 4); };
+  // This lane's first fragments; the others lie at fixed distances, but for address
+  // bits that the swizzle turns (KX).  One register each, and not one per chunk.
+  constexpr unsigned KX = D % 128 == 0 ? 255 : 127;
+  const int kr = 16 * (c16 >> 2) + (c16 & 3);
+  const unsigned kat = kr * (2 * D) + (h ^ k_swizzle(kr)) * 16;
+  const unsigned vat = K_BYTES + c16 * 128 + ((2 * h) ^ v_swizzle(c16)) * 16;
   // Chunk i = tid + NT q of a tile: of K for i < C (row i / KC, 16 elements), of V
   // above (dim (i - C) / 4, tokens 16 (i % 4)).
   u32x4v cr[NQ];
   auto is_k = [&](int q) { return C % NT == 0 ? q < C / NT : wv < C / 64; };
   const unsigned koff = tid * 16, voff = (unsigned)((tid - (C % NT == 0 ? 0 : C)) >> 2) * T + 16 * (tid & 3);
-  auto fetch = [&](int tt, int64_t blk) {
-    const int64_t safe = blk < 0 ? it.head : blk;
+  auto fetch = [&](int tt, int blk) {
     if constexpr (BIG) {
+      const int64_t safe = place(blk);
       const int o = (tt * kKvTile) & (T - 1);
       const uint8_t *kb = a.c.k + safe * bhead + o * D, *vb = a.c.v + safe * bhead + o;
 #pragma unroll
@@ -793,16 +813,16 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
         const int i = tid + NT * q;
         if (is_k(q)) {
           const int r = i / KC;
-          const int64_t b = __shfl(safe, 16 * (r >> 4), 64);
+          const int64_t b = place(__shfl(blk, 16 * (r >> 4), 64));
           cr[q] = *(const u32x4v*)(a.c.k + b * bhead + (int64_t)(r & (T - 1)) * D + 16 * (i % KC));
         } else {
-          const int64_t b = __shfl(safe, 16 * (tid & 3), 64);
+          const int64_t b = place(__shfl(blk, 16 * (tid & 3), 64));
           cr[q] = *(const u32x4v*)(a.c.v + b * bhead + (int64_t)((i - C) / 4) * T + ((16 * (tid & 3)) & (T - 1)));
         }
       }
     }
   };
-  auto widen = [&](int tt, int64_t blk, uint8_t* buf) {
+  auto widen = [&](int tt, int blk, uint8_t* buf) {
     if constexpr (FP8) {  // codes that nobody sees can be NaN: 0 * NaN must not reach O
       const int tok = tt * kKvTile + 16 * (tid & 3);
       const bool none = BIG ? !is_there(tt, blk, tid & 3) : (bool)__shfl((int)(blk < 0), 16 * (tid & 3), 64);
@@ -838,17 +858,17 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
   };
 
   if (rg.t0 < rg.t1) {
-    int64_t blk = block_of(rg.t0), blk1 = block_of(rg.t0 + 1);
+    int blk = block_of(rg.t0), blk1 = block_of(rg.t0 + 1);
     fetch(rg.t0, blk);
     widen(rg.t0, blk, smem);
-    float ks = a.c.ks[blk < 0 ? it.head : blk], vs = a.c.vs[blk < 0 ? it.head : blk];
+    float ks = a.c.ks[place(blk)], vs = a.c.vs[place(blk)];
     fetch(rg.t0 + 1, blk1);  // past the end: block 0, unused
-    int64_t blk2 = block_of(rg.t0 + 2);
+    int blk2 = block_of(rg.t0 + 2);
     __syncthreads();
     for (int tt = rg.t0; tt < rg.t1; ++tt) {
-      const uint8_t* buf = smem + ((tt - rg.t0) & 1) * BUF;
+      const unsigned buf = ((tt - rg.t0) & 1) * BUF;
       const int b0 = tt * kKvTile;
-      const float ks1 = a.c.ks[blk1 < 0 ? it.head : blk1], vs1 = a.c.vs[blk1 < 0 ? it.head : blk1];
+      const float ks1 = a.c.ks[place(blk1)], vs1 = a.c.vs[place(blk1)];
       if (b0 < mine.hi && b0 + kKvTile > mine.lo) {
         __builtin_amdgcn_s_setprio(1);
         f32x4v sc[QT][4];
@@ -860,8 +880,8 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
-            const int r = 16 * (c16 >> 2) + 4 * mt + (c16 & 3);
-            const f16x8_t kf = *(const f16x8_t*)(buf + r * (2 * D) + ((4 * j + h) ^ k_swizzle(r)) * 16);
+            // row r = 16 (c16 / 4) + 4 mt + c16 % 4, chunk 4 j + h
+            const f16x8_t kf = *(const f16x8_t*)(smem + ((buf + kat) ^ (64 * j & KX)) + (64 * j & ~KX) + mt * (8 * D));
 #pragma unroll
             for (int t = 0; t < QT; ++t)
               sc[t][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[t][j], sc[t][mt], 0, 0, 0);
@@ -877,8 +897,8 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int u = 0; u < NU; ++u) {
-            const int d = 16 * u + c16;
-            const f16x8_t vf = *(const f16x8_t*)(buf + K_BYTES + d * 128 + ((2 * h + x) ^ v_swizzle(d)) * 16);
+            // dim 16 u + c16, chunk 2 h + x
+            const f16x8_t vf = *(const f16x8_t*)(smem + ((buf + vat) ^ (16 * x)) + u * 2048);
 #pragma unroll
             for (int t = 0; t < QT; ++t)
               st.o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[t][x], st.o[t][u], 0, 0, 0);
