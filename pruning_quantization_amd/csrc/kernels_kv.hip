@@ -719,14 +719,20 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
 // 16-byte chunks XOR-swizzled by row), one tile ahead of its use, its codes loaded
 // one tile ahead of that.  Bound by the matrix and vector units in turn: per tile,
 // 16 rows and head of 128 a wave issues 32 MFMAs (512 cycles of its SIMD's matrix
-// unit) and about 130 vector instructions of softmax, and four waves per SIMD overlap
-// the one's products with the other's softmax.  A causal prompt of 8192 tokens, 32
-// heads over 8: 648 us (849 Tflop/s of 1985 that such MFMAs reach alone); two
-// waves of 32 rows per SIMD 686, three 16-row tiles a wave 2330 (spills).
+// unit) and about 200 vector instructions (softmax, widening), and several waves per
+// SIMD overlap the one's products with the other's softmax.  A causal prompt of
+// 8192 tokens, 32 heads over 8: 647 us (850 Tflop/s; such MFMAs alone reach 1985).
+//
+// Shapes, 128 rows a workgroup each: as many waves as the registers of D allow, but
+// for D = 64, whose products are short next to the reads of a tile, two row tiles a
+// wave.  8192 tokens by themselves, 32 heads over 8 (16 over 8 above 128), int8 in
+// blocks of 64: D = 64 476 us (one row tile, four waves per SIMD: 545), 128 686
+// (two row tiles, two waves: 722), 192 642 and 256 698 (two row tiles, one wave:
+// 800 and 1072).
 template <int D>
 struct KvPromptShape {
   // 16-row tiles of a wave, waves of a workgroup, waves per SIMD
-  static constexpr int QT = D <= 128 ? 1 : 2, NW = D <= 128 ? 8 : 4, WAVES = D <= 128 ? 4 : 1;
+  static constexpr int QT = D == 64 ? 2 : 1, NW = D == 64 ? 4 : 8, WAVES = D == 128 ? 4 : 2;
 };
 
 // BIG: blocks of 64 tokens and more, so a tile lies in one block (scalar addresses
@@ -735,7 +741,7 @@ template <int D, bool FP8, bool BIG>
 __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAttnArgs p) {
   constexpr int QT = KvPromptShape<D>::QT, NJ = D / 32, NU = D / 16, KC = D / 16;
   constexpr int NT = 64 * KvPromptShape<D>::NW, C = kKvTile * KC, NQ = 2 * C / NT;  // 16-code chunks of K and V
-  static_assert(C % NT == 0 || NT == 2 * C, "a wave loads K chunks or V chunks at a time");
+  static_assert(C % 64 == 0 && 2 * C % NT == 0, "a wave loads K chunks or V chunks at a time");
   constexpr int K_BYTES = kKvTile * D * 2, BUF = 2 * K_BYTES;
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * BUF];
   const KvAttn& a = p.a;
@@ -795,8 +801,8 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
   // Chunk i = tid + NT q of a tile: of K for i < C (row i / KC, 16 elements), of V
   // above (dim (i - C) / 4, tokens 16 (i % 4)).
   u32x4v cr[NQ];
-  auto is_k = [&](int q) { return C % NT == 0 ? q < C / NT : wv < C / 64; };
-  const unsigned koff = tid * 16, voff = (unsigned)((tid - (C % NT == 0 ? 0 : C)) >> 2) * T + 16 * (tid & 3);
+  auto is_k = [&](int q) { return C % NT == 0 ? q < C / NT : wv + NT / 64 * q < C / 64; };
+  const int koff = tid * 16, voff = ((tid - C % NT) >> 2) * T + 16 * (tid & 3);
   auto fetch = [&](int tt, int blk) {
     if constexpr (BIG) {
       const int64_t safe = place(blk);
@@ -805,7 +811,7 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         if (is_k(q)) cr[q] = *(const u32x4v*)(kb + koff + q * (NT * 16));
-        else cr[q] = *(const u32x4v*)(vb + voff + (C % NT == 0 ? (q - C / NT) * (NT / 4) : 0) * T);
+        else cr[q] = *(const u32x4v*)(vb + voff + (q - C / NT) * (NT / 4) * T);
       }
     } else {
 #pragma unroll
