@@ -1,4 +1,5 @@
-"""Python binding of libsparq24 (ctypes): argument marshalling only.
+"""Python binding of libsparq24: argument marshalling only (ctypes, and native code
+for the calls of a serving step, csrc/marshal.cpp).
 
 Every step of every call runs in the HIP kernels of ``libsparq24.so``; this
 module builds the C descriptors from torch tensors, allocates outputs and
@@ -13,9 +14,7 @@ each one.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
-import struct
 from ctypes import POINTER, c_double, c_float, c_int32, c_int64, c_size_t, c_uint8, c_void_p
 from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
@@ -115,7 +114,7 @@ def lib(path: Optional[str] = None):
         "sparq24_int8_gemm": [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
                               c_int64, c_int64, c_void_p, c_int32, c_void_p, c_int64, c_void_p,
                               POINTER(c_size_t), c_void_p],
-        # descriptors by address: packed bytes, or byref() of the structures
+        # descriptors by address: byref() of the structures
         "sparq24_kv_append": [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p],
         "sparq24_kv_attention": [c_void_p, c_void_p, c_void_p, c_float, c_int32, c_int64,
                                  c_void_p, c_void_p, c_void_p, POINTER(c_size_t), c_void_p],
@@ -647,42 +646,26 @@ def fp8_gemm(codes_a: torch.Tensor, scale_a: torch.Tensor, codes_b: torch.Tensor
     return out
 
 
-# The calls below are made once per layer and decoded token, so their marshalling
-# is kept short: descriptors are packed as bytes (layouts of CKvCache, CKvSeqs
-# and CTensor) instead of built as ctypes structures.
-_PACK_KVCACHE = struct.Struct("PPPPi4xqqqq").pack
-_PACK_KVSEQS = struct.Struct("PqqPPqq").pack
-_PACK_TENSOR = struct.Struct("Pi4xqqqqqq").pack
+# The calls below are made once per layer and decoded token, so their tensors are
+# checked and described in native code (csrc/marshal.cpp): in Python that took as
+# long as the kernels.
+_serving_module = None
 
 
-def _device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
-    """Checks that all tensors are on one GPU and returns its index."""
-    i = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != i:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
-    if i < 0:
-        raise ValueError(f"tensors must be on a GPU, got {first.device}")
-    return i
-
-
-def _call(fn: str, dev: int, *args) -> None:
-    """Calls ``fn`` with the device's current stream, that device current."""
-    f = getattr(_lib or lib(), fn)
-    if dev == torch._C._cuda_getDevice():
-        st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
-    else:
-        with torch.cuda.device(dev):
-            st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if st:
-        raise Sparq24Error(fn, st)
-
-
-def _vector(t: torch.Tensor, n: int, dtype: torch.dtype, name: str) -> int:
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype} with {n} elements, got {t.dtype} "
-                         f"{tuple(t.shape)}")
-    return t.data_ptr()
+def _serving():
+    """The marshalling module of the serving calls, bound to the library."""
+    global _serving_module
+    if _serving_module is None:
+        L = lib()
+        try:
+            from . import _marshal
+        except ImportError as e:
+            raise ImportError("pruning_quantization_amd/_marshal.so not loaded: build it with "
+                              "`python -m pruning_quantization_amd.build`") from e
+        _marshal.bind(*(ctypes.cast(f, c_void_p).value for f in (
+            L.sparq24_int8_gemm, L.sparq24_kv_append, L.sparq24_kv_attention)), Sparq24Error)
+        _serving_module = _marshal
+    return _serving_module
 
 
 def int8_gemm(codes_a: torch.Tensor, scale_a: torch.Tensor, codes_b: torch.Tensor,
@@ -694,38 +677,7 @@ def int8_gemm(codes_a: torch.Tensor, scale_a: torch.Tensor, codes_b: torch.Tenso
     bits), exact int32 sums -> ``dtype`` (fp32, bf16 or fp16) [..., N].  K is a
     multiple of 16; the rows of either operand and of ``out`` may be strided;
     ``bias`` is fp32 [N]."""
-    dev = _device(codes_a, scale_a, codes_b, scale_b, bias, out)
-    if codes_a.dtype != torch.int8 or codes_b.dtype != torch.int8:
-        raise TypeError(f"int8 codes expected, got {codes_a.dtype} and {codes_b.dtype}")
-    lead = codes_a.shape
-    if codes_b.dim() != 2 or not lead or lead[-1] != codes_b.shape[1]:
-        raise ValueError(f"shapes {tuple(lead)} and {tuple(codes_b.shape)} do not multiply")
-    n, k = codes_b.shape
-    a = codes_a if len(lead) == 2 else codes_a.view(math.prod(lead[:-1]), k)
-    m = a.shape[0]
-    lda, a1 = a.stride()
-    ldb, b1 = codes_b.stride()
-    if k > 1 and ((m and a1 != 1) or (n and b1 != 1)):
-        raise ValueError("codes must be contiguous along K")
-    if out is None:
-        c = out = codes_a.new_empty((m, n), dtype=dtype)
-        if len(lead) != 2:
-            out = c.view(*lead[:-1], n)
-    elif out.shape != (*lead[:-1], n):
-        raise ValueError(f"out has shape {tuple(out.shape)}")
-    else:
-        c = out if len(lead) == 2 else out.view(m, n)
-    ldc, c1 = c.stride()
-    if n > 1 and m and c1 != 1:
-        raise ValueError("out must be contiguous along N")
-    if out.dtype not in _DT:
-        raise TypeError(f"unsupported dtype {out.dtype}")
-    _call("sparq24_int8_gemm", dev, a.data_ptr(), lda,
-          _vector(scale_a, m, torch.float32, "scale_a"), m, codes_b.data_ptr(), ldb,
-          _vector(scale_b, n, torch.float32, "scale_b"), n, k,
-          None if bias is None else _vector(bias, n, torch.float32, "bias"), _DT[out.dtype],
-          c.data_ptr(), ldc, None, None)
-    return out
+    return (_serving_module or _serving()).int8_gemm(codes_a, scale_a, codes_b, scale_b, bias, dtype, out)
 
 
 class KVCache(NamedTuple):
@@ -753,75 +705,6 @@ def kv_cache(blocks: int, heads: int, dim: int, tokens: int = 64, q: QLike = ("i
                    torch.zeros(blocks, heads, dtype=torch.float32, device=device))
 
 
-def _c_cache(cache: KVCache):
-    """(sparq24_kvcache as bytes, shape of the K codes)."""
-    k, ks, v, vs = cache
-    shape = k.shape
-    if len(shape) != 4 or v.dim() != 4:
-        raise ValueError("cache codes must be [blocks, heads, tokens, dim] and [blocks, heads, dim, tokens]")
-    blocks, heads, tokens, dim = shape
-    if v.shape != (blocks, heads, dim, tokens) or k.dtype != v.dtype:
-        raise ValueError(f"cache codes {tuple(shape)} {k.dtype} and {tuple(v.shape)} {v.dtype} do not match")
-    if k.dtype == torch.int8:
-        fmt = Q_INT
-    elif k.dtype == torch.uint8:
-        fmt = Q_FP8
-    else:
-        raise TypeError(f"cache codes are int8 or uint8 (e4m3), got {k.dtype}")
-    if not (k.is_contiguous() and v.is_contiguous()):
-        raise ValueError("cache codes must be contiguous")
-    n = blocks * heads
-    return _PACK_KVCACHE(k.data_ptr(), _vector(ks, n, torch.float32, "k_scale"), v.data_ptr(),
-                         _vector(vs, n, torch.float32, "v_scale"), fmt, blocks, heads, tokens,
-                         dim), shape
-
-
-def _c_seqs(x: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
-            cu_tokens: Optional[torch.Tensor]):
-    """(sparq24_kvseqs as bytes, (sequences, table width, token rows, bool
-    cu_tokens)) of the token rows ``x``: [total, heads, dim] with
-    ``cu_tokens``, or [seqs, n, heads, dim]."""
-    if block_table.dim() != 2 or block_table.dtype != torch.int32:
-        raise ValueError("block_table must be int32 [seqs, max blocks]")
-    seqs, width = block_table.shape
-    stride, inner = block_table.stride()
-    if width > 1 and inner != 1:
-        raise ValueError("block_table must have contiguous rows")
-    shape = x.shape
-    if cu_tokens is None:
-        if len(shape) != 4 or shape[0] != seqs:
-            raise ValueError(f"without cu_tokens token rows are [seqs, n, heads, dim], got {tuple(shape)}")
-        total, cu = seqs * shape[1], 0
-    else:
-        if len(shape) != 3:
-            raise ValueError(f"with cu_tokens token rows are [total, heads, dim], got {tuple(shape)}")
-        total, cu = shape[0], _vector(cu_tokens, seqs + 1, torch.int32, "cu_tokens")
-    return _PACK_KVSEQS(block_table.data_ptr() if width else 0, width, stride,
-                        _vector(seq_lens, seqs, torch.int32, "seq_lens"), cu, seqs,
-                        total), (seqs, width, total, cu != 0)
-
-
-def _c_rows(x: torch.Tensor) -> bytes:
-    """sparq24_tensor of token rows as bytes: one batch entry per token."""
-    if x.dtype not in _DT:
-        raise TypeError(f"unsupported dtype {x.dtype}")
-    shape, stride = x.shape, x.stride()
-    if len(shape) == 4:
-        a, n = shape[0], shape[1]
-        if a > 1 and n > 1 and stride[0] != n * stride[1]:
-            raise ValueError("the sequences of token rows must be evenly spaced (or contiguous)")
-        total, ts = a * n, stride[1] if n > 1 else stride[0]
-    else:
-        total, ts = shape[0], stride[0]
-    if shape[-1] > 1 and stride[-1] != 1:
-        raise ValueError("token rows must be contiguous along dim")
-    return _PACK_TENSOR(x.data_ptr(), _DT[x.dtype], total, shape[-2], shape[-1], ts, stride[-2], 1)
-
-
-#: Workspace bytes of kv_attention by everything they depend on (shapes only).
-_kv_workspace: dict = {}
-
-
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
               seq_lens: torch.Tensor, cu_tokens: Optional[torch.Tensor] = None) -> None:
     """Quantizes new key and value rows into ``cache``, in place.
@@ -832,11 +715,7 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: tor
     its last positions; position p lives in block ``block_table[b, p // tokens]``
     (int32).  A block's scale grows when a new element exceeds it, and the
     block's earlier codes are then coded again."""
-    dev = _device(k, v, block_table, seq_lens, cu_tokens, *cache)
-    if k.shape != v.shape or k.dtype != v.dtype:
-        raise ValueError(f"k {tuple(k.shape)} {k.dtype} and v {tuple(v.shape)} {v.dtype} do not match")
-    _call("sparq24_kv_append", dev, _c_cache(cache)[0],
-          _c_seqs(k, block_table, seq_lens, cu_tokens)[0], _c_rows(k), _c_rows(v))
+    (_serving_module or _serving()).kv_append(cache, k, v, block_table, seq_lens, cu_tokens)
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
@@ -854,33 +733,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     the tokens up to its own; ``window`` > 0: the last ``window`` of these.
     ``scale`` defaults to dim ** -0.5.  A row that sees nothing gives zeros and
     an lse of -inf."""
-    dev = _device(q, block_table, seq_lens, cu_tokens, out, lse, workspace, *cache)
-    c, shape = _c_cache(cache)
-    s, sizes = _c_seqs(q, block_table, seq_lens, cu_tokens)
-    if out is None:
-        out = q.new_empty(q.shape)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-        raise ValueError("out must be contiguous, of q's shape and type")
-    if lse is None:
-        if return_lse:
-            lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
-    elif lse.shape != q.shape[:-1] or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous fp32 of q's shape without dim")
-    args = (c, s, _c_rows(q), q.shape[-1] ** -0.5 if scale is None else float(scale),
-            1 if causal else 0, int(window), out.data_ptr(), None if lse is None else lse.data_ptr())
-    ws = workspace
-    if ws is None:
-        key = (dev, *sizes, q.shape[-2], *shape[1:])
-        n = _kv_workspace.get(key)
-        if n is None:
-            size = c_size_t(0)
-            _call("sparq24_kv_attention", dev, *args, None, size)
-            n = _kv_workspace[key] = size.value
-        if n:
-            ws = q.new_empty(n, dtype=torch.uint8)
-    _call("sparq24_kv_attention", dev, *args, None if ws is None else ws.data_ptr(),
-          None if ws is None else c_size_t(ws.numel() * ws.element_size()))
-    return (out, lse) if return_lse else out
+    return (_serving_module or _serving()).kv_attention(
+        q, cache, block_table, seq_lens, cu_tokens, scale, causal, window, return_lse, out, lse, workspace)
 
 
 def col_l2norm(x: torch.Tensor, out: Optional[torch.Tensor] = None, workspace=None):

@@ -1,9 +1,10 @@
-"""Build libsparq24.so for gfx950 in-tree with hipcc.
+"""Build libsparq24.so for gfx950 in-tree with hipcc, and the Python extension
+_marshal.so (host code) that calls it.
 
 Usage: python -m pruning_quantization_amd.build [-v]
 
 Every call recompiles all sources (objects go to ``_build/`` at the repository
-root, the library next to this file).
+root, the libraries next to this file).
 """
 from __future__ import annotations
 
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsparq24.so")
+MARSHAL_LIB = os.path.join(PKG, "_marshal.so")
 
 SOURCES = ["api.cpp", "kernels_prune.hip", "kernels_quant.hip", "kernels_energy.hip",
            "kernels_misc.hip", "kernels_operr.hip", "kernels_spgemm.hip", "kernels_int8.hip",
@@ -66,14 +68,37 @@ def _build_check(verbose: bool) -> None:
     shutil.move(CHECK_BIN + ".tmp", CHECK_BIN)
 
 
+def _build_marshal(verbose: bool) -> None:
+    """Python extension that marshals the serving calls (host code only)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = [sysconfig.get_paths()["include"], *cpp_extension.include_paths("cuda"), INCLUDE]
+    lib = cpp_extension.library_paths("cuda")[0]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(x for d in inc for x in ("-isystem", d)), os.path.join(CSRC, "marshal.cpp"), "-L", lib,
+           "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-o", MARSHAL_LIB + ".tmp"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for marshal:\n" + r.stdout + r.stderr)
+    shutil.move(MARSHAL_LIB + ".tmp", MARSHAL_LIB)
+
+
 def build(verbose: bool = False) -> str:
     if not os.path.exists(HIPCC):
         raise RuntimeError(f"hipcc not found at {HIPCC}")
     os.makedirs(OBJDIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 2, os.cpu_count() or 4)) as ex:
         chk = ex.submit(_build_check, verbose)
+        mar = ex.submit(_build_marshal, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
         chk.result()
+        mar.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "-shared", f"--offload-arch={ARCH}", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -91,6 +91,30 @@ def test_leading_dims_empty_and_zero_depth():
         assert torch.equal(z, dbi.expand(m, 20))
 
 
+def test_row_steps_of_views():
+    # the step between rows is that of whichever leading dim has more than one entry
+    a, sa, b, sb, _ = operands(4, 30, 20, 64)
+    da, dsa, db, dsb = dev(a, sa, b, sb)
+    want = V.int8_gemm(a, sa, b, sb)
+    x = da.view(5, 6, 64)
+    last = torch.from_numpy(want).view(5, 6, 20)[:, -1:]
+    scale = dsa.view(5, 6)[:, -1].contiguous()
+    got = S.int8_gemm(x[:, -1:], scale, db, dsb)                  # the last row of each sequence
+    assert got.shape == (5, 1, 20) and torch.equal(got.cpu(), last)
+    out = torch.full((5, 6, 20), 7.0, device=DEV)
+    S.int8_gemm(x[:, -1:], scale, db, dsb, out=out[:, -1:])
+    assert torch.equal(out[:, -1:].cpu(), last) and (out[:, :-1] == 7.0).all()
+    got = S.int8_gemm(x[2, 3], dsa[15:16], db, dsb)                # one row, no leading dim
+    assert got.shape == (20,) and torch.equal(got.cpu(), torch.from_numpy(want[15]))
+    one = da[7:8].as_strided((1, 64), (3, 1))                      # one row: its stride says nothing
+    same(S.int8_gemm(one, dsa[7:8], db, dsb), want[7:8], "f32")
+    same(S.int8_gemm(da, dsa, db[3:4].as_strided((1, 64), (5, 1)), dsb[3:4]), want[:, 3:4], "f32")
+    with pytest.raises(S.Sparq24Error):                            # one row's codes for all rows
+        S.int8_gemm(da[:1].expand(30, 64), dsa, db, dsb)
+    with pytest.raises(ValueError, match="evenly"):
+        S.int8_gemm(x[:, 1:3], dsa[:10], db, dsb)
+
+
 def test_nonfinite_scales_stay_in_their_row():
     for m in (5, 90):
         a, sa, b, sb, _ = operands(m, m, 40, 128)

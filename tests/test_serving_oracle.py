@@ -256,33 +256,45 @@ def test_binding_refusals():
         B.kv_attention(x, c, table, lens)
     with pytest.raises(ValueError, match="int"):
         B.kv_cache(3, 2, 64, 16, q=("int", 4), device="cpu")
-    # the packed descriptors are the C structures
-    r = B.CKvCache.from_buffer_copy(B._c_cache(c)[0])
-    assert (r.k, r.v_scale, r.fmt, r.blocks, r.heads, r.tokens, r.dim) == (
-        c.k.data_ptr(), c.v_scale.data_ptr(), B.Q_INT, 3, 2, 16, 64)
-    packed, sizes = B._c_seqs(x, table, lens, None)
-    r = B.CKvSeqs.from_buffer_copy(packed)
-    assert (r.block_table, r.max_blocks, r.table_stride, r.seq_lens, r.cu_tokens, r.seqs, r.total) == (
-        table.data_ptr(), 4, 4, lens.data_ptr(), None, 2, 2) and sizes == (2, 4, 2, False)
-    assert len(packed) == ctypes.sizeof(B.CKvSeqs) and len(B._c_rows(x)) == ctypes.sizeof(B.CTensor)
-    # descriptors: what they refuse without a device
+    # checks come before the device, so all refusals show without one
+    def attend(q=x, cache=c, table=table, lens=lens, cu=None, **kw):
+        B.kv_attention(q, cache, table, lens, cu, **kw)
+
+    for bad, what in ((c._replace(v=c.k), "match"), (c._replace(k_scale=c.k_scale[:2]), "k_scale"),
+                      (c._replace(k=c.k[:, :, ::2]), "match"), (c._replace(v_scale=c.v_scale.double()), "v_scale"),
+                      (c._replace(k=c.k.transpose(0, 1).contiguous().transpose(0, 1)), "contiguous"),
+                      (c._replace(k=c.k[0]), "blocks")):
+        with pytest.raises(ValueError, match=what):
+            attend(cache=bad)
+        with pytest.raises(ValueError, match=what):
+            B.kv_append(bad, x, x, table, lens)
+    with pytest.raises(TypeError, match="e4m3"):
+        attend(cache=c._replace(k=c.k.float(), v=c.v.float()))
+    with pytest.raises(TypeError, match="KVCache"):
+        attend(cache=c.k)
+    for kw, what in (({"table": table.long()}, "block_table"), ({"table": table[:, ::2]}, "block_table"),
+                     ({"lens": lens.long()}, "seq_lens"), ({"lens": lens[:1]}, "seq_lens"),
+                     ({"q": x[:, 0], "cu": lens}, "cu_tokens"), ({"q": x, "cu": lens}, "cu_tokens"),
+                     ({"q": x[:, 0]}, "n, heads"), ({"q": x[:1]}, "n, heads"),
+                     ({"q": torch.zeros(2, 5, 2, 64)[:, :2]}, "evenly"),
+                     ({"q": torch.zeros(2, 1, 64, 2).transpose(2, 3)}, "contiguous"),
+                     ({"out": x[:1]}, "out"), ({"out": x.float()}, "out"), ({"lse": x[..., 0]}, "lse"),
+                     ({"workspace": torch.zeros(8, 2)[:, :1]}, "workspace")):
+        with pytest.raises(ValueError, match=what):
+            attend(**kw)
+    for kw in ({"q": x.double()}, {"q": None}, {"lens": [1, 1]}, {"scale": "1"}, {"window": 1.5}):
+        with pytest.raises(TypeError):
+            attend(**kw)
     with pytest.raises(ValueError, match="match"):
-        B._c_cache(c._replace(v=c.k))
-    with pytest.raises(TypeError):
-        B._c_cache(c._replace(k=c.k.float(), v=c.v.float()))
-    with pytest.raises(ValueError, match="k_scale"):
-        B._c_cache(c._replace(k_scale=c.k_scale[:2]))
-    with pytest.raises(ValueError, match="block_table"):
-        B._c_seqs(x, table.long(), lens, None)
-    with pytest.raises(ValueError, match="seq_lens"):
-        B._c_seqs(x, table, lens.long(), None)
-    with pytest.raises(ValueError, match="cu_tokens"):
-        B._c_seqs(x[:, 0], table, lens, lens)
-    with pytest.raises(ValueError, match="n, heads"):
-        B._c_seqs(x[:, 0], table, lens, None)
-    with pytest.raises(ValueError, match="evenly"):
-        B._c_rows(torch.zeros(3, 5, 2, 64)[:, :2])
-    with pytest.raises(ValueError, match="contiguous"):
-        B._c_rows(torch.zeros(3, 64, 2).transpose(1, 2))
-    r = B.CTensor.from_buffer_copy(B._c_rows(torch.zeros(7, 3, 2, 64)[:, 1:2]))  # one row of each three
-    assert (r.batch, r.rows, r.k, r.batch_stride, r.row_stride) == (7, 2, 64, 384, 64)
+        B.kv_append(c, x, x.half(), table, lens)
+    for args, what in (((i8, f[:3], i8, f), "scale_a"), ((i8, f, i8, f.double()), "scale_b"),
+                       ((i8, f, i8[:, :16], f), "multiply"), ((i8[:, ::2], f, i8[:, ::2], f), "contiguous"),
+                       ((i8.t().contiguous().t(), f, i8, f), "contiguous"),
+                       ((torch.zeros(2, 3, 32, dtype=torch.int8)[:, :2], f, i8, f), "evenly"),
+                       ((i8, f, i8, f, f[:2]), "bias"), ((i8, f, i8, f, None, torch.float32, f), "out")):
+        with pytest.raises(ValueError, match=what):
+            B.int8_gemm(*args)
+    for args in ((i8.float(), f, i8, f), (i8, f, i8.float(), f), (i8, f, i8, f, None, torch.float64),
+                 (i8, f, i8, f, None, "fp32")):
+        with pytest.raises(TypeError):
+            B.int8_gemm(*args)
