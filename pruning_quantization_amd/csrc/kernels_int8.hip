@@ -10,14 +10,24 @@ namespace sparq24 {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
-__device__ inline void int8_store(const Int8Gemm& g, int64_t m, int64_t n, int acc) {
-  if (m >= g.M || n >= g.N) return;
-  float y = (float)acc * g.sa[m] * g.sb[n];
-  if (g.bias) y += g.bias[n];
-  const int64_t o = m * g.ldc + n;
-  if (g.dtype == 0) ((float*)g.c)[o] = y;
-  else if (g.dtype == 1) ((__bf16*)g.c)[o] = (__bf16)y;
-  else ((_Float16*)g.c)[o] = (_Float16)y;
+// Four outputs n .. n + 3 (a multiple of 4) of row m: one store where `wide` says
+// that rows are aligned for it and all are inside, else one by one.
+template <class T>
+__device__ inline void int8_store4(const Int8Gemm& g, int64_t m, int64_t n, i32x4_t acc, float sa,
+                                   const float (&sb)[4], const float (&bias)[4], bool wide) {
+  if (m >= g.M) return;
+  typedef T t4 __attribute__((ext_vector_type(4)));
+  T* c = (T*)g.c + m * g.ldc + n;
+  t4 y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = (T)((float)acc[e] * sa * sb[e] + bias[e]);
+  if (wide && n + 4 <= g.N) {
+    *(t4*)c = y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < g.N) c[e] = y[e];
+  }
 }
 
 // Few rows: the weight is streamed once.  A workgroup owns 16 MT x 16 NT
@@ -27,8 +37,11 @@ __device__ inline void int8_store(const Int8Gemm& g, int64_t m, int64_t n, int a
 // int32 sums meet in LDS.  Through LDS because an MFMA operand straight from
 // memory gives adjacent lanes adjacent rows, which the address unit takes at one
 // lane (16 bytes) a cycle: 34 GB/s per CU measured, against 64 bytes a
-// cycle in row order.  Bound by the weight's bytes, for one or two row tiles
-// of a small weight by the launch and the latency of the first slabs.
+// cycle in row order.  Bound by the weight's bytes (48 x 14336 x 4096: 12.8 us, 5.6
+// TB/s past the launch and the first slabs); of a small weight by the latter (1 x
+// 4096 x 4096: 4.5 us).  The products take b first, so that a lane holds four
+// adjacent outputs, and the scales are asked for before the slabs are read: with
+// stores one by one and scales at the end 14.7 us, 777 x 1031 x 2064 12.4 (10.6).
 template <int MT, int NT, int W, int S>
 __global__ __launch_bounds__(64 * W) void k_int8_stream(Int8Gemm g, int64_t ntn) {
   constexpr int SK = 128, QA = 2 * MT, QB = 2 * NT, STAGE = (MT + NT) * 16 * SK;
@@ -70,11 +83,49 @@ __global__ __launch_bounds__(64 * W) void k_int8_stream(Int8Gemm g, int64_t ntn)
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
-  const int K = (int)g.K, nk = K / SK;  // whole slabs
+  const int K = (int)g.K, nk = K / SK;         // whole slabs
+  const int last = nk - 1 - (nk - 1 - w) % W;  // this wave's last slab, asked for again past the end
   if (w < nk) {
-    const int last = nk - 1 - (nk - 1 - w) % W;  // this wave's last slab, asked for again past the end
 #pragma unroll
     for (int s = 0; s + 1 < S; ++s) SPARQ24_INT8_FETCH(s, (w + s * W < last ? w + s * W : last) * SK);
+  }
+  // the scales and bias of the 16 x 16 tiles t = w + W u that this wave joins
+  constexpr int U = (MT * NT + W - 1) / W;
+  float sa[U], sb[U][4], bias[U][4];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int t = w + W * u;
+    const int64_t m = 16 * (t / NT) + c, n = 16 * (t % NT) + 4 * h;
+    sa[u] = g.sa[m0 + (m < last_m ? m : last_m)];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t at = n0 + (n + e < last_n ? n + e : last_n);
+      sb[u][e] = g.sb[at];
+      bias[u][e] = g.bias ? g.bias[at] : -0.0f;  // y + -0 is y
+    }
+  }
+  if (w == nk % W) {  // the rest of K, zeros behind it, while the first slabs come
+    for (int k = nk * SK + 16 * h; k - 16 * h < K; k += 64) {
+      const i32x4_t zero = {0, 0, 0, 0};
+      i32x4_t af[MT], bf[NT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int64_t r = 16 * i + c;
+        af[i] = k < K ? *(const i32x4_t*)(base_a + (r < last_m ? r : last_m) * g.lda + k) : zero;
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int64_t r = 16 * j + c;
+        bf[j] = k < K ? *(const i32x4_t*)(base_b + (r < last_n ? r : last_n) * g.ldb + k) : zero;
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af[i], acc[i][j], 0, 0, 0);
+    }
+  }
+  if (w < nk) {
     int buf = 0;
     for (int kt = w; kt < nk; kt += W) {
       const int next = kt + (S - 1) * W;
@@ -95,7 +146,7 @@ __global__ __launch_bounds__(64 * W) void k_int8_stream(Int8Gemm g, int64_t ntn)
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int j = 0; j < NT; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i], bf[j], acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af[i], acc[i][j], 0, 0, 0);
       }
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the buffer is read before it is filled again
       asm volatile("" ::: "memory");
@@ -104,27 +155,6 @@ __global__ __launch_bounds__(64 * W) void k_int8_stream(Int8Gemm g, int64_t ntn)
     wait_vmcnt<0>();  // what was asked for past the end has landed
     asm volatile("" ::: "memory");
   }
-  if (w == nk % W) {  // the rest of K, zeros behind it
-    for (int k = nk * SK + 16 * h; k - 16 * h < K; k += 64) {
-      const i32x4_t zero = {0, 0, 0, 0};
-      i32x4_t af[MT], bf[NT];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int64_t r = 16 * i + c;
-        af[i] = k < K ? *(const i32x4_t*)(base_a + (r < last_m ? r : last_m) * g.lda + k) : zero;
-      }
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int64_t r = 16 * j + c;
-        bf[j] = k < K ? *(const i32x4_t*)(base_b + (r < last_n ? r : last_n) * g.ldb + k) : zero;
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i], bf[j], acc[i][j], 0, 0, 0);
-    }
-  }
   __syncthreads();  // every wave is done with its buffers
   i32x4_t* red = (i32x4_t*)smem;  // [W][MT * NT][64]
 #pragma unroll
@@ -132,14 +162,22 @@ __global__ __launch_bounds__(64 * W) void k_int8_stream(Int8Gemm g, int64_t ntn)
 #pragma unroll
     for (int j = 0; j < NT; ++j) red[(w * MT * NT + i * NT + j) * 64 + lane] = acc[i][j];
   __syncthreads();
-  for (int t = w; t < MT * NT; t += W) {
-    i32x4_t s = red[t * 64 + lane];
+  auto out = [&]<class T>(T) {
+    const bool wide = g.ldc % 4 == 0;
 #pragma unroll
-    for (int q = 1; q < W; ++q) s += red[(q * MT * NT + t) * 64 + lane];
-    const int64_t m = m0 + 16 * (t / NT) + 4 * h, n = n0 + 16 * (t % NT) + c;
+    for (int u = 0; u < U; ++u) {
+      const int t = w + W * u;
+      if (t >= MT * NT) break;
+      i32x4_t s = red[t * 64 + lane];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) int8_store(g, m + e, n, s[e]);
-  }
+      for (int q = 1; q < W; ++q) s += red[(q * MT * NT + t) * 64 + lane];
+      const int64_t m = m0 + 16 * (t / NT) + c, n = n0 + 16 * (t % NT) + 4 * h;  // outputs n .. n + 3 of row m
+      int8_store4<T>(g, m, n, s, sa[u], sb[u], bias[u], wide);
+    }
+  };
+  if (g.dtype == 0) out(0.0f);
+  else if (g.dtype == 1) out((__bf16)0.0f);
+  else out((_Float16)0.0f);
 }
 
 // Many rows: a BM x BN tile per workgroup, waves of WM x 64 on
@@ -159,7 +197,7 @@ __global__ __launch_bounds__(64 * W) void k_int8_stream(Int8Gemm g, int64_t ntn)
 // 4..7 at 2 s + 1.  Slab t + 1 is requested by the reads of step 2 t, when both
 // groups have read all of slab t - 1 (phases up to 4 t - 1), and waited for at
 // the end of phase 4 t + 3, before anyone reads it.
-// 4096 x 14336 x 4096, bf16 out: mixed 267 us, in turns 253 us; bound by LDS
+// 4096 x 14336 x 4096, bf16 out: mixed 267 us, in turns 229 us; bound by LDS
 // (192 KB of fragments and 64 KB of slabs for 2048 cycles of products per slab).
 // 16 outputs n .. n + 15 of row m: 16-byte stores where `wide` says that all
 // are inside and aligned, else one by one.
@@ -393,10 +431,11 @@ hipError_t launch_int8_gemm(const Int8Gemm& g, hipStream_t s) {
     return hipGetLastError();
   };
   auto tiles = [&](int bm, int bn) { return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
-  // k_int8_stream takes about 2.3 us + 1.5 us per 16-row group of a and b that a
-  // CU streams (K = 4096): (1, 1) and (1, 4) for 1 x 4096 and 1 x 14336: 6.0, 11.3;
-  // (2, 2) 7.6, (4, 2) 9.3, (4, 4) 13.7 us for 64, 128, 256 x 4096.  Past one round
-  // of (4, 4) on every CU (100 x 14336: 27 us) the tiles win (21 us).
+  // k_int8_stream takes about 2.4 us + 1.1 us per 16-row group of a and b that a
+  // CU streams (K = 4096): (1, 1) and (1, 4) for 1 x 4096 and 1 x 14336: 4.5, 11.0;
+  // (2, 2) 6.8, (2, 4) 8.0, (4, 4) 10.8 us for 64, 128, 256 x 4096.  At two rounds
+  // of (4, 4) the tiles draw level (100 x 14336: 22.8 and 22.4 us, 512 x 4096: 20.9
+  // and 21.6; with K = 1024, 777 x 2048: 11.4 and 9.2).
   const int cus = device_cu_count();
   const bool far_rows = g.lda >= (1 << 23) || g.ldb >= (1 << 23);  // past the tiles' 32-bit offsets
   int mt = 0, nt = 0;
