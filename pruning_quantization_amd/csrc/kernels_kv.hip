@@ -947,16 +947,17 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
   }
 }
 
-// Joins the chunks of split sequences, W waves per (token, query head): the chunks are
-// dealt to them, and their sums meet in wave order.  Four waves where there are
-// few rows and so long chains of chunks, one where there are many.
+// Joins the chunks of split sequences.  Few rows (W = 4), and so long chains of
+// chunks: a workgroup per (token, query head), the chunks dealt to its four waves,
+// whose sums meet in wave order.  Many (W = 0): 16 lanes per row, so that one round
+// of waves holds them all (17500 rows of 64: 7.2 us, with a wave per row 14.6).
 template <int D, int W>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many) {
-  constexpr int V = D / 64;
+  constexpr int L = W == 4 ? 64 : 16, V = D / L, F = W == 4 ? V : 4;  // lanes of a row, elements of a lane, in runs of F
   const KvAttn& a = few.a;
-  const int lane = threadIdx.x & 63, wv = uniform((int)threadIdx.x >> 6) % W;
-  const int64_t id = W == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + uniform((int)threadIdx.x >> 6);
-  if (W == 1 && id >= a.q.total * a.heads) return;
+  const int tid = threadIdx.x, wv = W == 4 ? uniform(tid >> 6) : 0, l = tid & (L - 1);
+  const int64_t id = W == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 16 + (tid >> 4);
+  if (W != 4 && id >= a.q.total * a.heads) return;
   const int64_t tok = id / a.heads;
   const int hq = (int)(id % a.heads);
   int64_t seq = 0;
@@ -985,39 +986,40 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many
   const int64_t at0 = ((first + nrt - 1 - rt) * a.c.heads + head) * p.rb + rr;
   const int64_t step = (int64_t)nrt * a.c.heads * p.rb;
   float top = kNegInf;
-  for (int c = lane; c < chunks; c += 64) top = __builtin_fmaxf(top, p.ml[(at0 + c * step) * 2]);
+  for (int c = l; c < chunks; c += L) top = __builtin_fmaxf(top, p.ml[(at0 + c * step) * 2]);
 #pragma unroll
-  for (int x = 1; x < 64; x <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, x, 64));
+  for (int x = 1; x < L; x <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, x, 64));
   float sum = 0.0f, v[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) v[e] = 0.0f;
+  auto at = [&](int e) { return F * L * (e / F) + F * l + e % F; };
   if (top != kNegInf) {
 #pragma unroll 4
-    for (int c = wv; c < chunks; c += W) {
+    for (int c = wv; c < chunks; c += W == 4 ? 4 : 1) {
       const int64_t s = at0 + c * step;
       const f32x2v ml = *(const f32x2v*)(p.ml + s * 2);
       const float f = __builtin_amdgcn_exp2f(ml[0] - top);
       sum = __builtin_fmaf(ml[1], f, sum);
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(p.po[s * D + lane * V + e], f, v[e]);
+      for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(p.po[s * D + at(e)], f, v[e]);
     }
   }
   if constexpr (W == 4) {
     __shared__ float part[4][D], sums[4];
 #pragma unroll
-    for (int e = 0; e < V; ++e) part[wv][lane * V + e] = v[e];
-    if (lane == 0) sums[wv] = sum;
+    for (int e = 0; e < V; ++e) part[wv][at(e)] = v[e];
+    if (l == 0) sums[wv] = sum;
     __syncthreads();
     sum = sums[0] + sums[1] + sums[2] + sums[3];
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    for (int d = threadIdx.x; d < D; d += 256)
+    for (int d = tid; d < D; d += 256)
       kv_store_out(a, id * D + d, (part[0][d] + part[1][d] + part[2][d] + part[3][d]) * inv);
   } else {
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-    for (int e = 0; e < V; ++e) kv_store_out(a, id * D + lane * V + e, v[e] * inv);
+    for (int e = 0; e < V; ++e) kv_store_out(a, id * D + at(e), v[e] * inv);
   }
-  if (a.lse && wv == 0 && lane == 0) a.lse[id] = kv_lse(top, sum);
+  if (a.lse && wv == 0 && l == 0) a.lse[id] = kv_lse(top, sum);
 }
 
 namespace {
@@ -1127,7 +1129,7 @@ hipError_t launch_kv_attn(const KvAttn& a, void* ws, hipStream_t s) {
       if (rows <= 16 * device_cu_count())
         hipLaunchKernelGGL((k_kv_join<D, 4>), dim3((unsigned)rows), dim3(256), 0, s, p.few, p.many);
       else
-        hipLaunchKernelGGL((k_kv_join<D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, p.few, p.many);
+        hipLaunchKernelGGL((k_kv_join<D, 0>), dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, s, p.few, p.many);
       return hipGetLastError();
     }
     return hipSuccess;
