@@ -831,7 +831,8 @@ sparq24_status check_kv(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs
   const int64_t most = INT32_MAX - 255;  // positions and tile ends are 32-bit in the kernels
   q = KvSeqs{seqs->block_table, seqs->table_stride, cap < most ? cap : most,
              seqs->seq_lens, seqs->cu_tokens, seqs->seqs, seqs->total,
-             seqs->seqs ? seqs->total / seqs->seqs : 0};
+             seqs->seqs ? seqs->total / seqs->seqs : 0, 0};
+  q.slots = (int)((q.nper + T - 2) / T + 1);
   return SPARQ24_OK;
 }
 
@@ -874,7 +875,7 @@ sparq24_status sparq24_kv_append(const sparq24_kvcache* cache, const sparq24_kvs
   if (k->rows != c.heads || v->rows != c.heads) return SPARQ24_ERR_SHAPE;
   if (k->dtype != v->dtype) return SPARQ24_ERR_UNSUPPORTED;
   if (empty) return SPARQ24_OK;
-  if (q.total / (1 << c.tsh) + 2 * q.seqs > INT32_MAX) return SPARQ24_ERR_UNSUPPORTED;
+  if (!kv_append_fits(c, q)) return SPARQ24_ERR_UNSUPPORTED;
   CHECK(check_kv_pointers(c, q));
   if (!k->data || !v->data) return SPARQ24_ERR_INVALID;
   if (!aligned16(k->data) || !aligned16(v->data)) return SPARQ24_ERR_ALIGN;
@@ -907,6 +908,7 @@ sparq24_status sparq24_kv_attention(const sparq24_kvcache* cache, const sparq24_
   a.window = window > INT32_MAX ? INT32_MAX : (int)window;
   a.out = (char*)out;
   a.lse = lse;
+  if (!empty && !kv_attn_fits(a)) return SPARQ24_ERR_UNSUPPORTED;
   bool query;
   CHECK(workspace(ws, ws_bytes, empty ? 0 : kv_attn_workspace(a), query));
   if (query || empty) return SPARQ24_OK;

@@ -51,17 +51,26 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvCache c, KvSeqs q, KvRow
   __shared__ float red[kBlock / 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int T = 1 << c.tsh, D = c.dim;
+  // Block number j of sequence b.  Without offsets each has as many slots as its
+  // rows may touch blocks; with them sequence b has those from cu[b] / T + 2 b on
+  // (n rows touch at most n / T + 2 blocks), so that no lengths are needed to find it.
   int b, j;
-  const bool found = find_sequence(q.seqs, blockIdx.x, lane, b, j, [&](int64_t i) -> int64_t {
-    const SeqRows r = seq_rows(q, i);
-    const int p0 = r.len > r.n ? r.len - r.n : 0;
-    const int64_t end = r.len < q.cap ? r.len : q.cap;
-    return r.n > 0 && p0 < end ? ((end - 1) >> c.tsh) - (p0 >> c.tsh) + 1 : 0;
-  });
-  if (!found) return;
+  if (q.cu) {
+    const int64_t u = blockIdx.x;
+    auto slot = [&](int i) -> int64_t {
+      const int at = q.cu[i];
+      return (at < 0 ? 0 : (at > q.total ? q.total : at) >> c.tsh) + 2 * (int64_t)i;
+    };
+    b = last_reached((int)q.seqs, lane, [&](int i) { return slot(i) <= u; });
+    j = (int)(u - slot(b));
+  } else {
+    b = (int)(blockIdx.x / (unsigned)q.slots);
+    j = (int)(blockIdx.x % (unsigned)q.slots);
+  }
   const SeqRows r = seq_rows(q, b);
   const int p0 = r.len > r.n ? r.len - r.n : 0;
   const int64_t cend = r.len < q.cap ? r.len : q.cap;
+  if (r.n <= 0 || p0 >= cend || j < 0 || j > ((cend - 1) >> c.tsh) - (p0 >> c.tsh)) return;
   const int64_t page = (p0 >> c.tsh) + j;
   const int64_t blk = q.table[b * q.table_stride + page];
   if (blk < 0 || blk >= c.blocks) return;
@@ -167,12 +176,19 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvCache c, KvSeqs q, KvRow
   }
 }
 
+namespace {
+constexpr int64_t kMostThreads = UINT32_MAX;  // of a grid, along x
+int64_t append_blocks(const KvCache& c, const KvSeqs& q) {
+  return q.cu ? (q.total >> c.tsh) + 2 * q.seqs : q.seqs * q.slots;
+}
+}  // namespace
+
+bool kv_append_fits(const KvCache& c, const KvSeqs& q) { return append_blocks(c, q) <= kMostThreads / kBlock; }
+
 hipError_t launch_kv_append(const KvCache& c, const KvSeqs& q, const KvRows& k, const KvRows& v,
                             int dtype, hipStream_t s) {
   const int64_t T = 1ll << c.tsh;
-  // n tokens touch at most (n + T - 2) / T + 1 blocks
-  const int64_t most = q.cu ? (q.total + q.seqs * (T - 2)) / T + q.seqs
-                            : q.seqs * ((q.nper + T - 2) / T + 1);
+  const int64_t most = append_blocks(c, q);
   const size_t shmem = (size_t)c.dim * (size_t)(T + 16);
   const dim3 grid((unsigned)most, (unsigned)c.heads, 2);
   return with_dtype(dtype, [&]<class DT>() {
@@ -256,11 +272,15 @@ struct KvAttnArgs {
   int64_t target;   // items that the launch aims at
   int64_t items;    // items that it has room for
   int cmin;         // least tiles of a chunk
+  int* starts;      // [seqs + 2] or null: first unit of each sequence, all units, len (k_kv_plan)
   int* plan;        // [seqs][2]: first item / kv heads, chunks
   float* ml;        // [items][rb][2]: reference and sum of a split row tile
   float* po;        // [items][rb][D]
 };
 
+// Sequences of at most so many tiles stay whole: a second launch that joins chunks costs
+// more (one new token on 600: 11.9 and 13.8 us, on 1024: 13.6 and 13.9).
+constexpr int kWholeTiles = 16;
 constexpr int kNever = 1 << 26;  // tiles of a chunk that nothing reaches
 
 struct KvWork {
@@ -308,34 +328,58 @@ struct KvItem {
   int64_t slot;
   int seq, chunk, chunks, len, rt, head;  // len: tiles of a chunk
 };
+// Tiles of a chunk: all tiles of all row tiles over the items aimed at.
+__device__ inline int chunk_tiles(const KvAttnArgs& w, int64_t all) {
+  int64_t len = (all * w.a.c.heads + w.target - 1) / w.target;
+  len = len < w.cmin ? w.cmin : (len + 3) / 4 * 4;  // four waves share a chunk
+  return (int)(len < kNever ? len : kNever);
+}
+__device__ inline int64_t tiles_of(const KvWork& k) {  // bounded, so that no sum leaves 64 bits
+  const int64_t c = (int64_t)k.rt * k.tiles;
+  return c < (1ll << 36) ? c : 1ll << 36;
+}
+__device__ inline int64_t units_of(const KvWork& k, int len) {
+  const int64_t ch = ((int64_t)k.tiles + len - 1) / len, n = k.rt * (ch > 1 ? ch : 1);
+  return n < kMostUnits ? n : kMostUnits;
+}
+
+// A unit is a chunk of a row tile of a sequence, an item a unit and a kv head.  Where
+// every sequence has as many units (same row counts, no chunks) a unit's place
+// follows from its number; up to kScanned sequences every workgroup adds up what
+// comes before it, in one round of loads; more have been added up by k_kv_plan.
+constexpr int kScanned = 64;
 __device__ inline bool kv_item(const KvAttnArgs& w, int64_t id, int lane, KvItem& it) {
   const int H = w.a.c.heads;
-  const int64_t seqs = w.a.q.seqs;
-  // chunk length: all tiles of all row tiles over the items aimed at
-  int64_t len = w.cmin;
-  if (w.cmin < kNever) {
-    int64_t all = 0;
-    for (int64_t b0 = 0; b0 < seqs; b0 += 64) {
-      const int64_t b = b0 + lane;
-      int64_t c = 0;
-      if (b < seqs) {
-        const KvWork k = kv_work(w, seq_rows(w.a.q, b));
-        c = (int64_t)k.rt * k.tiles;
-      }
-      const uint32_t n = (uint32_t)(c < kMostUnits ? c : kMostUnits);
-      all += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan_sum(n), 63);
-    }
-    len = (all * H + w.target - 1) / w.target;
-    len = len < w.cmin ? w.cmin : (len + 3) / 4 * 4;  // four waves share a chunk
-  }
-  it.len = uniform((int)len);
+  const int64_t seqs = w.a.q.seqs, unit = id / H;
   int at;
-  if (!find_sequence(seqs, id / H, lane, it.seq, at, [&](int64_t b) -> int64_t {
-        const KvWork k = kv_work(w, seq_rows(w.a.q, b));
-        const int ch = (k.tiles + it.len - 1) / it.len;
-        return (int64_t)k.rt * (ch > 1 ? ch : 1);
-      }))
-    return false;
+  if (w.starts) {
+    if (unit >= w.starts[seqs]) return false;
+    it.len = uniform(w.starts[seqs + 1]);
+    it.seq = last_reached((int)seqs, lane, [&](int b) { return w.starts[b] <= unit; });
+    at = (int)unit - w.starts[it.seq];
+  } else if (!w.a.q.cu && w.cmin == kNever) {
+    const int rt = (int)((w.a.q.nper * w.g + w.rb - 1) / w.rb);
+    it.len = kNever;
+    it.seq = (int)(unit / rt);
+    at = (int)(unit % rt);
+    if (it.seq >= seqs) return false;
+  } else {
+    it.len = w.cmin;
+    if (w.cmin < kNever) {
+      int64_t all = 0;
+      for (int64_t b0 = 0; b0 < seqs; b0 += 64) {
+        const int64_t b = b0 + lane;
+        const int64_t c = b < seqs ? tiles_of(kv_work(w, seq_rows(w.a.q, b))) : 0;
+        // 64 sums of 2^36 in two halves of 32 bits
+        all += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan_sum((uint32_t)c & 0xFFFFF), 63) +
+               ((int64_t)(uint32_t)__builtin_amdgcn_readlane((int)wave_scan_sum((uint32_t)(c >> 20)), 63) << 20);
+      }
+      it.len = uniform(chunk_tiles(w, all));
+    }
+    if (!find_sequence(seqs, unit, lane, it.seq, at,
+                       [&](int64_t b) { return units_of(kv_work(w, seq_rows(w.a.q, b)), it.len); }))
+      return false;
+  }
   it.r = seq_rows(w.a.q, it.seq);
   it.r.first = uniform(it.r.first);
   it.r.n = uniform(it.r.n);
@@ -348,7 +392,7 @@ __device__ inline bool kv_item(const KvAttnArgs& w, int64_t id, int lane, KvItem
   it.head = scalar((int)(id % H));
   it.slot = id;
   if (w.plan && at == 0 && it.head == 0 && threadIdx.x == 0) {
-    w.plan[2 * it.seq] = (int)(id / H);
+    w.plan[2 * it.seq] = (int)unit;
     w.plan[2 * it.seq + 1] = it.chunks;
   }
   return true;
@@ -947,6 +991,50 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
   }
 }
 
+// First units of more than kScanned sequences, a workgroup for each kernel: that each
+// of their workgroups added them up took it a round of loads per 64 sequences, twice
+// (4096 sequences of 100 tokens, one new each, with offsets: 2264 us, so 551).
+__global__ __launch_bounds__(1024) void k_kv_plan(KvAttnArgs few, KvAttnArgs many) {
+  const KvAttnArgs& w = blockIdx.x ? many : few;
+  if (!w.starts) return;
+  __shared__ int64_t part[1024];
+  const int tid = threadIdx.x;
+  const int64_t seqs = w.a.q.seqs, per = (seqs + 1023) / 1024;
+  const int64_t b0 = tid * per < seqs ? tid * per : seqs, b1 = b0 + per < seqs ? b0 + per : seqs;
+  auto scan = [&](int64_t v) {  // inclusive, over the workgroup
+    part[tid] = v;
+    for (int o = 1; o < 1024; o <<= 1) {
+      __syncthreads();
+      const int64_t u = tid >= o ? part[tid - o] : 0;
+      __syncthreads();
+      part[tid] += u;
+    }
+    __syncthreads();
+    return part[tid];
+  };
+  int len = w.cmin;
+  if (w.cmin < kNever) {
+    int64_t c = 0;
+#pragma unroll 4
+    for (int64_t b = b0; b < b1; ++b) c += tiles_of(kv_work(w, seq_rows(w.a.q, b)));
+    scan(c);
+    len = chunk_tiles(w, part[1023]);
+    __syncthreads();  // part is read before it is used again
+  }
+  int64_t n = 0;
+#pragma unroll 4
+  for (int64_t b = b0; b < b1; ++b) n += units_of(kv_work(w, seq_rows(w.a.q, b)), len);
+  int64_t at = scan(n) - n;
+  for (int64_t b = b0; b < b1; ++b) {
+    w.starts[b] = (int)(at < INT32_MAX ? at : INT32_MAX);
+    at += units_of(kv_work(w, seq_rows(w.a.q, b)), len);
+  }
+  if (tid == 1023) {
+    w.starts[seqs] = (int)(at < INT32_MAX ? at : INT32_MAX);
+    w.starts[seqs + 1] = len;
+  }
+}
+
 // Joins the chunks of split sequences.  Few rows (W = 4), and so long chains of
 // chunks: a workgroup per (token, query head), the chunks dealt to its four waves,
 // whose sums meet in wave order.  Many (W = 0): 16 lanes per row, so that one round
@@ -1033,7 +1121,7 @@ int prompt_rows(int dim) {
 struct KvPlan {
   KvAttnArgs few, many;
   int qt;                   // 16-row tiles of the few-rows kernel
-  bool run_few, run_many, split;
+  bool run_few, run_many, split, planned;
   size_t need;
 };
 
@@ -1054,7 +1142,7 @@ KvPlan kv_plan(const KvAttn& a, char* ws) {
   const int64_t tiles = (a.q.cap + kKvTile - 1) / kKvTile;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   size_t off = up((size_t)a.q.seqs * 8);
-  p.split = false;
+  p.split = p.planned = false;
   auto lay = [&](KvAttnArgs& w, bool run, int rb, int above, int most, int cmin, int64_t target, int64_t rt) {
     w.a = a;
     w.g = g;
@@ -1062,10 +1150,16 @@ KvPlan kv_plan(const KvAttn& a, char* ws) {
     w.above = above;
     w.most = most;
     w.target = target;
-    const bool split = run && tiles > cmin && (most == limit || rt * H < target);
+    const bool split = run && tiles > kWholeTiles && (most == limit || rt * H < target);
     w.cmin = split ? cmin : kNever;
     w.items = rt * H;
     w.plan = (int*)ws;
+    w.starts = nullptr;
+    if (run && a.q.seqs > kScanned && (a.q.cu || split)) {
+      w.starts = (int*)(ws + off);
+      off += up((size_t)(a.q.seqs + 2) * 4);
+      p.planned = true;
+    }
     if (split) {
       const int64_t all = rt * H * ((tiles + cmin - 1) / cmin);
       w.items = all < target + rt * H ? all : target + rt * H;
@@ -1091,18 +1185,32 @@ KvPlan kv_plan(const KvAttn& a, char* ws) {
   // tokens: 248 / 227 / 219 us at two / four / eight; one of 131071: 61 / 65 / 80)
   int64_t aim = 64 * a.q.seqs * H;
   aim = aim < 2 * cus ? 2 * cus : (aim > 8 * cus ? 8 * cus : aim);
-  lay(p.few, p.run_few, rbf, 0, limit, 4, aim, rtf);
+  // a chunk has one tile a wave at least, and four where unsplit sequences fill the
+  // card twice (64 sequences of 1024: 26 and 48 us with one; 8 of 2048: 21 and 17)
+  lay(p.few, p.run_few, rbf, 0, limit, rtf * H >= 2 * cus ? 16 : 4, aim, rtf);
   lay(p.many, p.run_many, rbm, limit, INT32_MAX, 4, (a.c.dim <= 128 ? 2 : 1) * cus, rtm);
-  p.need = p.split ? off : 0;
+  p.need = p.split || p.planned ? off : 0;
   if (!p.split) p.few.plan = p.many.plan = nullptr;
   return p;
 }
 }  // namespace
 
+bool kv_attn_fits(const KvAttn& a) {
+  const KvPlan p = kv_plan(a, nullptr);
+  const int64_t prompt = a.c.dim == 64 ? 64 * KvPromptShape<64>::NW : 64 * KvPromptShape<128>::NW;
+  return (!p.run_few || p.few.items <= kMostThreads / 256) && (!p.run_many || p.many.items <= kMostThreads / prompt) &&
+         (!p.split || a.q.total * a.heads <= kMostThreads / 16);
+}
+
 size_t kv_attn_workspace(const KvAttn& a) { return kv_plan(a, nullptr).need; }
 
 hipError_t launch_kv_attn(const KvAttn& a, void* ws, hipStream_t s) {
   const KvPlan p = kv_plan(a, (char*)ws);
+  if (p.planned) {
+    hipLaunchKernelGGL(k_kv_plan, dim3(2), dim3(1024), 0, s, p.few, p.many);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   auto dim = [&]<int D>() {
     if (p.run_many) {
       auto k = a.c.tsh >= 6 ? (a.c.fp8 ? k_kv_prompt<D, true, true> : k_kv_prompt<D, false, true>)

@@ -74,4 +74,19 @@ __device__ inline bool find_sequence(int64_t seqs, int64_t item, int lane, int& 
   return false;
 }
 
+// The last i of 0 .. n - 1 with reached(i), true for i = 0 and a prefix: the wave
+// looks at 64 places at a time, so at most 64 need one round of loads, 4096 two.
+// Every lane of the wave takes part and gets the same answer (a scalar).
+template <class F>
+__device__ inline int last_reached(int n, int lane, F&& reached) {
+  int at = 0;
+  while (n > 1) {
+    const int step = (n + 63) / 64, i = lane * step;
+    const int k = __popcll(__ballot(i < n && (i == 0 || reached(at + i)))) - 1;
+    at += k * step;
+    n = n - k * step < step ? n - k * step : step;
+  }
+  return at;
+}
+
 }  // namespace sparq24

@@ -182,6 +182,7 @@ struct KvSeqs {
   const int32_t* lens;
   const int32_t* cu;
   int64_t seqs, total, nper;
+  int slots;  // blocks that nper rows can touch
 };
 // One side (K or V) of the new token rows: strides in bytes.
 struct KvRows {
@@ -203,6 +204,8 @@ struct KvAttn {
   char* out;
   float* lse;       // or null
 };
+bool kv_append_fits(const KvCache& c, const KvSeqs& q);  // the launches' grids
+bool kv_attn_fits(const KvAttn& a);
 size_t kv_attn_workspace(const KvAttn& a);
 hipError_t launch_kv_attn(const KvAttn& a, void* ws, hipStream_t s);
 // Rotated copy of a K-contiguous operand (d.rot) into dense [B][R][K] `out`.

@@ -38,14 +38,15 @@ def stored(x, dtype):
 
 class Pool:
     """A cache in use: random codes and scales in every block, tables in any
-    order, lens tokens in each sequence."""
+    order, lens tokens in each sequence.  wide: tables that allow more than the
+    1024 tokens up to which a call splits no sequence."""
 
-    def __init__(self, seed, lens, kv=2, dim=64, tokens=16, fmt="int8", width=None, spare=2):
+    def __init__(self, seed, lens, kv=2, dim=64, tokens=16, fmt="int8", width=None, spare=2, wide=False):
         rng = self.rng = np.random.default_rng(seed)
         self.lens, self.fmt, self.tokens, self.kv, self.dim = list(lens), fmt, tokens, kv, dim
         need = [-(-max(n, 0) // tokens) for n in lens]
         blocks = max(1, sum(need) + spare)
-        width = width or max(max(need), 1)
+        width = width or max(max(need), 1025 // tokens + 1 if wide else 1)
         order = rng.permutation(blocks).astype(np.int32)
         self.table = np.full((len(lens), width), -1, np.int32)
         at = 0
@@ -200,14 +201,15 @@ def test_append_many_sequences():
 # --- attention ----------------------------------------------------------------
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("fmt", ["int8", "fp8"])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("dim,tokens,kv,group", [
     (64, 16, 2, 1), (128, 64, 2, 4), (128, 32, 1, 5), (192, 128, 1, 3), (256, 256, 1, 2), (256, 16, 2, 16),
     (64, 64, 1, 48), (128, 256, 1, 71)])
-def test_decode(dim, tokens, kv, group, dtype, fmt):
+def test_decode(dim, tokens, kv, group, dtype, fmt, wide):
     lens = [1, 2, 15, 16, 17, 63, 64, 65, 129, 511, 700]
-    p = Pool(dim + group, lens, kv, dim, tokens, fmt)
+    p = Pool(dim + group, lens, kv, dim, tokens, fmt, wide=wide)
     q, q64 = stored(p.rng.standard_normal((len(lens), 1, kv * group, dim)), dtype)
     cu = np.arange(len(lens) + 1)
     out, lse = S.kv_attention(q, p.dev(), *p.args(), return_lse=True)
@@ -216,26 +218,28 @@ def test_decode(dim, tokens, kv, group, dtype, fmt):
     assert torch.equal(out, S.kv_attention(q, p.dev(), *p.args()))          # the same bits without lse
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("kw", [{}, {"window": 1}, {"window": 37}, {"window": 200}, {"causal": False}])
 @pytest.mark.parametrize("dim,tokens,group,fmt", [(64, 16, 4, "fp8"), (128, 64, 3, "int8"), (256, 32, 1, "fp8"),
                                                   (192, 64, 2, "int8")])
-def test_chunks(dim, tokens, group, fmt, kw):
+def test_chunks(dim, tokens, group, fmt, kw, wide):
     # whole prompts, chunks behind a context, decoding, nothing, in one call
     lens = [130, 400, 77, 9, 64, 300, 1]
     news = [130, 90, 1, 0, 64, 2, 1]
-    p = Pool(dim, lens, 2, dim, tokens, fmt)
+    p = Pool(dim, lens, 2, dim, tokens, fmt, wide=wide)
     cu, dcu = offsets(news)
     q, q64 = stored(p.rng.standard_normal((cu[-1], 2 * group, dim)) * 1.5, "bf16")
     out, lse = S.kv_attention(q, p.dev(), *p.args(), cu_tokens=dcu, return_lse=True, scale=0.11, **kw)
     check_attention(out, lse, p, q64, cu, "bf16", np.float32(0.11), **kw)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("n", [2, 16, 70, 257])
 @pytest.mark.parametrize("dtype,fmt", [("bf16", "int8"), ("f16", "fp8")])
-def test_same_count_strided(n, dtype, fmt):
+def test_same_count_strided(n, dtype, fmt, wide):
     # queries cut out of a fused projection; n tokens of each sequence
     lens = [n, n + 1, n + 300]
-    p = Pool(n, lens, 2, 128, 64, fmt)
+    p = Pool(n, lens, 2, 128, 64, fmt, wide=wide)
     fused, f64 = stored(p.rng.standard_normal((3, n, 12, 128)), dtype)
     cu = np.arange(4) * n
     out = S.kv_attention(fused[:, :, :8], p.dev(), *p.args())
@@ -252,8 +256,9 @@ def test_split_along_the_tokens(fmt):
     assert not out[2].any()
 
 
-def test_rows_that_see_nothing():
-    p = Pool(4, [0, 3, 50, 40], 1, 64, 16, "int8")
+@pytest.mark.parametrize("wide", [False, True])
+def test_rows_that_see_nothing(wide):
+    p = Pool(4, [0, 3, 50, 40], 1, 64, 16, "int8", wide=wide)
     p.table[2, 1:], p.table[3, :] = 10 ** 6, -1      # a part of a table, a whole table outside the pool
     news = [2, 6, 5, 2]                               # more queries than tokens: the first see nothing
     cu, dcu = offsets(news)
@@ -265,12 +270,13 @@ def test_rows_that_see_nothing():
     check_attention(out, lse, p, q64, cu, "bf16", 0.125, window=20)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("tokens", [16, 64, 128])
-def test_garbage_in_unseen_places(tokens):
+def test_garbage_in_unseen_places(tokens, wide):
     # NaN codes behind the sequences, before the windows and in foreign blocks; NaN and
     # infinite scales in blocks that no row sees
     lens = [tokens + 3, 5, 200, 3 * tokens]
-    p = Pool(tokens, lens, 2, 64, tokens, "fp8", spare=4)
+    p = Pool(tokens, lens, 2, 64, tokens, "fp8", spare=4, wide=wide)
     q, q64 = stored(p.rng.standard_normal((4, 2, 4, 64)), "bf16")
     cu = np.arange(5) * 2
     for window in (0, 30):
@@ -289,11 +295,12 @@ def test_garbage_in_unseen_places(tokens):
         check_attention(out, lse, p, q64.reshape(8, 4, 64), cu, "bf16", 0.125, ref=tuple(want), window=window)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("fmt", ["int8", "fp8"])
-def test_scales_far_apart(fmt):
+def test_scales_far_apart(fmt, wide):
     # block scales over 40 binades and zeros, queries over many more
     lens = [500, 64, 300]
-    p = Pool(31, lens, 2, 64, 16, fmt)
+    p = Pool(31, lens, 2, 64, 16, fmt, wide=wide)
     k, ks, v, vs = (x.copy() for x in p.ref)
     vs *= np.exp2(p.rng.integers(-40, 1, vs.shape)).astype(np.float32)
     ks *= np.exp2(p.rng.integers(-20, 1, ks.shape)).astype(np.float32)
@@ -315,9 +322,10 @@ def test_scales_far_apart(fmt):
     check_attention(out, lse, p, q64[:, 0], np.arange(4), "f16", 0.125)
 
 
-def test_extreme_queries():
+@pytest.mark.parametrize("wide", [False, True])
+def test_extreme_queries(wide):
     # bf16 rows at both ends of the range, peaked and flat weights
-    p = Pool(41, [300, 300, 300, 300], 1, 128, 64, "int8")
+    p = Pool(41, [300, 300, 300, 300], 1, 128, 64, "int8", wide=wide)
     q = p.rng.standard_normal((4, 1, 2, 128))
     q[0] *= 1e30
     q[1] *= 1e-30
@@ -364,6 +372,42 @@ def test_many_sequences():
     q, q64 = stored(rng.standard_normal((cu[-1], 2, 64)), "bf16")
     out, lse = S.kv_attention(q, p.dev(), *p.args(), cu_tokens=dcu, return_lse=True)
     check_attention(out, lse, p, q64, cu, "bf16", 0.125)
+
+
+@pytest.mark.parametrize("uniform", [False, True])
+@pytest.mark.parametrize("count,kv", [(65, 1), (300, 2)])
+def test_many_sequences_some_split(count, kv, uniform):
+    # more sequences than a workgroup adds up by itself, a few of them split; 600 sequences and heads fill
+    # the card, so their chunks are longer
+    rng = np.random.default_rng(count + uniform)
+    lens = [int(x) for x in rng.integers(1, 90, count)]
+    for b, n in ((0, 2500), (count // 2, 1100), (count - 1, 1700)):
+        lens[b] = n
+    p = Pool(count, lens, kv, 64, 16, "int8")
+    news = [1] * count if uniform else [min(n, int(x)) for n, x in zip(lens, rng.integers(0, 3, count))]
+    if not uniform:
+        news[3], news[count - 1] = min(lens[3], 40), 200                 # the second: prompt rows
+    cu, dcu = offsets(news)
+    q, q64 = stored(rng.standard_normal((cu[-1], 2 * kv, 64)), "f16")
+    x, kw = (q[:, None], {}) if uniform else (q, {"cu_tokens": dcu})
+    out, lse = S.kv_attention(x, p.dev(), *p.args(), return_lse=True, **kw)
+    check_attention(out, lse, p, q64, cu, "f16", 0.125)
+
+
+@pytest.mark.parametrize("uniform", [False, True])
+def test_append_to_thousands(uniform):
+    rng = np.random.default_rng(13)
+    lens = [int(x) for x in rng.integers(2, 40, 4200)]
+    news = [2] * 4200 if uniform else [min(n, int(x)) for n, x in zip(lens, rng.integers(0, 4, 4200))]
+    p = Pool(14, lens, 1, 64, 16, "int8")
+    cu, dcu = offsets(news)
+    k, k64 = stored(p.rng.standard_normal((cu[-1], 1, 64)) * 2, "bf16")
+    cache = p.dev()
+    if uniform:
+        S.kv_append(cache, k.view(4200, 2, 1, 64), k.view(4200, 2, 1, 64), *p.args())
+    else:
+        S.kv_append(cache, k, k, *p.args(), cu_tokens=dcu)
+    unchanged(cache, V.kv_append(p.ref, k64, k64, p.table, lens, cu, "int8"))
 
 
 def test_offsets_past_32_bits():
@@ -456,7 +500,7 @@ def test_captured_steps_replay():
     # eager work and synchronizations in between; workspaces of their own
     rng = np.random.default_rng(19)
     heads, kv, dim, hidden, T = 4, 2, 64, 128, 16
-    p = Pool(20, [700, 30, 5], kv, dim, T, "int8", width=60)
+    p = Pool(20, [700, 30, 5], kv, dim, T, "int8", width=80)
     mk = lambda *s: stored(rng.standard_normal(s) * 0.1, "bf16")[0]  # noqa: E731
     w8, wo8 = S.quantize(mk((heads + 2 * kv) * dim, hidden), ("int", 8)), S.quantize(mk(hidden, heads * dim), ("int", 8))
     x = mk(3, hidden)
@@ -489,7 +533,7 @@ def test_captured_steps_replay():
 
 def test_two_streams_at_once():
     # calls on side streams with their own data give what the calls give one after the other
-    ps = [Pool(50 + i, [900 + 100 * i, 64], 2, 64, 16, "int8") for i in range(2)]
+    ps = [Pool(50 + i, [900 + 100 * i, 64], 2, 64, 16, "int8", wide=True) for i in range(2)]
     qs = [stored(p.rng.standard_normal((2, 1, 4, 64)), "bf16")[0] for p in ps]
     caches, args = [p.dev() for p in ps], [p.args() for p in ps]
     want = [S.kv_attention(q, c, *a) for q, c, a in zip(qs, caches, args)]

@@ -225,9 +225,19 @@ def test_attention_refusals_and_workspace(L):
     assert n.value > 0
     assert attend(L, s=big, nb=n.value - 1) == WORKSPACE and attend(L, s=big, nb=None) == WORKSPACE
     assert attend(L, s=big, ws=FAKE + 8) == ALIGN
-    # 256 tokens at most: no split, no workspace
+    # 1024 tokens at most: no split, no workspace
     assert attend(L, s=seqs(max_blocks=8, table_stride=8), out=None, ws=None, nb=n) == OK
     assert n.value == 0
+    # the work list of more than 64 sequences
+    many = dict(cu_tokens=FAKE, total=65)
+    assert attend(L, s=seqs(seqs=65, **many), q=rows(heads=6, total=65), out=None, ws=None, nb=n) == OK
+    assert n.value > 0
+    assert attend(L, s=seqs(seqs=64, **many), q=rows(heads=6, total=65), out=None, ws=None, nb=n) == OK
+    assert n.value == 0
+    # more workgroups than a grid has
+    most = dict(seqs=2 ** 24, total=2 ** 24)
+    assert attend(L, s=seqs(**most), q=rows(heads=6, total=2 ** 24)) == UNSUPPORTED
+    assert append(L, s=seqs(**most), k=rows(total=2 ** 24), v=rows(total=2 ** 24)) == UNSUPPORTED
     assert attend(L, s=seqs(total=0), q=rows(heads=6, total=0, data=None), out=None) == OK
     assert attend(L, s=seqs(total=2 ** 28, seqs=2 ** 20), q=rows(heads=64, total=2 ** 28)) == UNSUPPORTED
 
