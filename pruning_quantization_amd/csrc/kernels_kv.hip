@@ -254,6 +254,7 @@ __device__ inline f16x8_t widen8(uint32_t a, uint32_t b) {
 }
 
 constexpr int kKvTile = 64;
+constexpr int kFewRows = 16;       // most rows per kv head of the few-rows kernel
 constexpr float kTopSet = 8.0f;    // a new reference puts the largest w at 2^8 ...
 constexpr float kTopMost = 15.0f;  // ... and stands until one would pass 2^15
 // One fma from score to exponent rounds m, not the exponent: the same factor for
@@ -609,78 +610,107 @@ __device__ inline KvRange kv_range(const KvAttnArgs& p, const KvItem& it, int r0
   return {scalar(k.t0), scalar(k.t1), scalar(k.lo), scalar(k.hi), scalar(k.least), scalar(k.from)};
 }
 
-// Few rows per kv head (decoding): QT tiles of 16 rows, four waves that take
-// the chunk's tiles in turn, K and V straight from memory into MFMA operands.
-// Bound by the cache's bytes.
-template <int D, int QT, bool FP8>
-__global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
+// Few rows per kv head (decoding): one tile of 16 rows, four waves that take the
+// chunk's tiles in turn, K and V straight from memory into MFMA operands.  Bound by
+// the cache's bytes: 64 sequences of 300..16384 tokens, 32 heads over 8 of 128, in
+// 211 us (5.2 TB/s), 4096 of 100 in 360 (half of their last blocks is empty).
+// Three waves per SIMD there: two hold everything in registers and read long
+// sequences a little faster (214 and 221 us with the join), short ones slower (466).
+// BIG: blocks of 64 tokens and more, so a tile lies in one block (scalar addresses
+// and scales).
+template <int D, bool FP8, bool BIG>
+__global__ __launch_bounds__(256, BIG && D <= 128 ? 3 : 1) void k_kv_attn(KvAttnArgs p) {
   constexpr int NS = D / 64, NU = D / 16;
   const KvAttn& a = p.a;
   const int lane = threadIdx.x & 63, wv = uniform((int)threadIdx.x >> 6), c16 = lane & 15, h = lane >> 4;
   KvItem it;
   if (!kv_item(p, blockIdx.x, lane, it)) return;
   const int H = a.c.heads, tsh = a.c.tsh, T = 1 << tsh;
-  f16x8_t qf[QT][2 * NS];
-  KvRow row[QT];
-#pragma unroll
-  for (int t = 0; t < QT; ++t)
-    row[t] = kv_query(p, it, it.rt * p.rb + 16 * t + c16, qf[t],
-                      [&](int j) { return 64 * (j / 2) + 16 * h + 8 * (j & 1); });
+  f16x8_t qf[2 * NS];
+  const KvRow row[1] = {kv_query(p, it, it.rt * p.rb + c16, qf,
+                                 [&](int j) { return 64 * (j / 2) + 16 * h + 8 * (j & 1); })};
 
-  KvState<QT, NU> st;
+  KvState<1, NU> st;
   st.init();
 
-  const int r0 = it.rt * p.rb, r1 = r0 + 16 * QT < it.k.rows ? r0 + 16 * QT : it.k.rows;
+  const int r0 = it.rt * p.rb, r1 = r0 + 16 < it.k.rows ? r0 + 16 : it.k.rows;
   const KvRange rg = kv_range(p, it, r0, r1);
   const int lo = rg.lo, hi = rg.hi;
   const int* table = a.q.table + (int64_t)it.seq * a.q.table_stride;
   const int64_t bhead = (int64_t)T * D;
 
-  for (int tt = rg.t0 + wv; tt < rg.t1; tt += 4) {
-    const int b0 = tt * kKvTile;
-    // block of this lane group's 16 tokens; groups that no row sees (their scales
-    // may be anything) and groups without a block read block 0, masked
-    const int gp = b0 + 16 * h;
-    int64_t blk = gp < hi && gp + 16 > lo ? table[gp >> tsh] : -1;
-    const bool there = blk >= 0 && blk < a.c.blocks;
-    blk = there ? blk * H + it.head : it.head;
-    const uint64_t away = __ballot(!there);
-    const int src = 16 * (c16 >> 2);
-    const int64_t kblk = __shfl(blk, src, 64);
-    const int krow = ((b0 + src) & (T - 1)) + (c16 & 3);
-    const uint8_t* kp = a.c.k + kblk * bhead + (int64_t)krow * D + 16 * h;
-    const uint8_t* vp = a.c.v + blk * bhead + (int64_t)c16 * T + (gp & (T - 1));
-    u32x4v kr[4][NS], vr[NU];
+  // Block of a tile (BIG) or of this lane group's 16 tokens of it, or -1: what no row
+  // sees (its scales may be anything) and what has no block reads block 0, masked.
+  auto block_of = [&](int tt) -> int {
+    const int gp = tt * kKvTile + (BIG ? 0 : 16 * h);
+    int blk = tt < rg.t1 && gp < hi && gp + (BIG ? kKvTile : 16) > lo ? table[gp >> tsh] : -1;
+    if (blk >= a.c.blocks) blk = -1;
+    return BIG ? scalar(blk) : blk;
+  };
+  u32x4v kr[4][NS], vr[NU];
+  float ks = 0.0f, vs = 0.0f;
+  auto place = [&](int blk) -> int64_t { return (int64_t)(blk < 0 ? 0 : blk) * H + it.head; };
+  const unsigned koff = (16 * (c16 >> 2) + (c16 & 3)) * D + 16 * h, voff = c16 * T + 16 * h;
+  auto load_k = [&](int tt, int blk) {
+    const uint8_t* kp;
+    if constexpr (BIG) {
+      kp = a.c.k + place(blk) * bhead + ((tt * kKvTile) & (T - 1)) * D + koff;
+    } else {
+      const int src = 16 * (c16 >> 2), krow = ((tt * kKvTile + src) & (T - 1)) + (c16 & 3);
+      kp = a.c.k + place(__shfl(blk, src, 64)) * bhead + (int64_t)krow * D + 16 * h;
+    }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
       for (int s = 0; s < NS; ++s) kr[mt][s] = *(const u32x4v*)(kp + 4 * mt * D + 64 * s);
-    const float ks = a.c.ks[blk], vs = a.c.vs[blk];
+  };
+  auto load_v = [&](int tt, int blk) {
+    const uint8_t* vb = a.c.v + place(blk) * bhead;
 #pragma unroll
-    for (int u = 0; u < NU; ++u) vr[u] = *(const u32x4v*)(vp + (int64_t)u * 16 * T);
-
-    f32x4v sc[QT][4];
+    for (int u = 0; u < NU; ++u) {
+      if constexpr (BIG) vr[u] = *(const u32x4v*)(vb + ((tt * kKvTile) & (T - 1)) + 16 * T * u + voff);
+      else vr[u] = *(const u32x4v*)(vb + (int64_t)(c16 + 16 * u) * T + ((tt * kKvTile + 16 * h) & (T - 1)));
+    }
+  };
+  // K of the next tile is asked for as soon as this one's is used, V likewise, the
+  // table entry a tile earlier: each load has a tile's work to arrive in.
+  int tt = rg.t0 + wv, blk = -1, blk1 = -1;
+  if (tt < rg.t1) {
+    blk = block_of(tt);
+    blk1 = block_of(tt + 4);
+    load_k(tt, blk);
+    ks = a.c.ks[place(blk)];
+    vs = a.c.vs[place(blk)];
+    load_v(tt, blk);
+  }
+  for (; tt < rg.t1; tt += 4) {
+    const int b0 = tt * kKvTile, gp = b0 + 16 * h;
+    const bool there = blk >= 0 && (!BIG || (gp < hi && gp + 16 > lo)), more = tt + 4 < rg.t1;
+    const uint64_t away = __ballot(!there);
+    f32x4v sc[1][4];
 #pragma unroll
-    for (int t = 0; t < QT; ++t)
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) sc[t][mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
+    for (int mt = 0; mt < 4; ++mt) sc[0][mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         const f16x8_t k0 = widen8<FP8>(kr[mt][s][0], kr[mt][s][1]);
         const f16x8_t k1 = widen8<FP8>(kr[mt][s][2], kr[mt][s][3]);
-#pragma unroll
-        for (int t = 0; t < QT; ++t) {
-          sc[t][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[t][2 * s], sc[t][mt], 0, 0, 0);
-          sc[t][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[t][2 * s + 1], sc[t][mt], 0, 0, 0);
-        }
+        sc[0][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[2 * s], sc[0][mt], 0, 0, 0);
+        sc[0][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[2 * s + 1], sc[0][mt], 0, 0, 0);
       }
 
     const bool edge = away != 0 || b0 + kKvTile > rg.least || b0 < rg.from;
     const KvScales kk = kv_scales(there, ks, vs);
-    f16x8_t pf[QT][2];
-    kv_weights<QT, NU>(sc, row, kk, gp, edge, st, pf);
+    int blk2 = -1;
+    if (more) {
+      load_k(tt + 4, blk1);
+      ks = a.c.ks[place(blk1)];
+      vs = a.c.vs[place(blk1)];
+      blk2 = block_of(tt + 8);
+    }
+    f16x8_t pf[1][2];
+    kv_weights<1, NU>(sc, row, kk, gp, edge, st, pf);
     if constexpr (FP8) {
       if (edge) {  // codes that nobody sees can be NaN: 0 * NaN must not reach O
 #pragma unroll
@@ -699,60 +729,56 @@ __global__ __launch_bounds__(256) void k_kv_attn(KvAttnArgs p) {
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       const f16x8_t v0 = widen8<FP8>(vr[u][0], vr[u][1]), v1 = widen8<FP8>(vr[u][2], vr[u][3]);
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        st.o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[t][0], st.o[t][u], 0, 0, 0);
-        st.o[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[t][1], st.o[t][u], 0, 0, 0);
-      }
+      st.o[0][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[0][0], st.o[0][u], 0, 0, 0);
+      st.o[0][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[0][1], st.o[0][u], 0, 0, 0);
     }
+    if (more) load_v(tt + 4, blk1);
+    blk = blk1;
+    blk1 = blk2;
   }
 
   // the four waves' parts of each row meet in LDS, in wave order
   constexpr int PITCH = D + 4;
   __shared__ float os[4][16][PITCH];
   __shared__ float mls[4][16][2];
+  st.l[0] = groups_sum(st.l[0]);
+  if (h == 0) {
+    mls[wv][c16][0] = st.m[0];
+    mls[wv][c16][1] = st.l[0];
+  }
 #pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    st.l[t] = groups_sum(st.l[t]);
-    if (t) __syncthreads();
-    if (h == 0) {
-      mls[wv][c16][0] = st.m[t];
-      mls[wv][c16][1] = st.l[t];
+  for (int u = 0; u < NU; ++u) *(f32x4v*)&os[wv][c16][16 * u + 4 * h] = st.o[0][u];
+  __syncthreads();
+  const int at = threadIdx.x >> 4, sub = threadIdx.x & 15;
+  const int r = it.rt * p.rb + at;
+  if (r < it.k.rows) {
+    float top = kNegInf, f[4], sum = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) top = __builtin_fmaxf(top, mls[q][at][0]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      f[q] = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mls[q][at][0] - top);
+      sum += mls[q][at][1] * f[q];
     }
+    const int64_t tok = it.r.first + r / p.g, hq = it.head * p.g + r % p.g;
+    const bool split = it.chunks > 1;
+    const float inv = split ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum);
+    const int64_t base = split ? (it.slot * p.rb + at) * D : (tok * a.heads + hq) * D;
 #pragma unroll
-    for (int u = 0; u < NU; ++u) *(f32x4v*)&os[wv][c16][16 * u + 4 * h] = st.o[t][u];
-    __syncthreads();
-    const int row = threadIdx.x >> 4, sub = threadIdx.x & 15;
-    const int r = it.rt * p.rb + 16 * t + row;
-    if (r < it.k.rows) {
-      float top = kNegInf, f[4], sum = 0.0f;
+    for (int e = 0; e < D / 16; ++e) {
+      const int d = sub + 16 * e;
+      float v = 0.0f;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) top = __builtin_fmaxf(top, mls[q][row][0]);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f[q] = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mls[q][row][0] - top);
-        sum += mls[q][row][1] * f[q];
-      }
-      const int64_t tok = it.r.first + r / p.g, hq = it.head * p.g + r % p.g;
-      const bool split = it.chunks > 1;
-      const float inv = split ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum);
-      const int64_t base = split ? (it.slot * p.rb + 16 * t + row) * D : (tok * a.heads + hq) * D;
-#pragma unroll
-      for (int e = 0; e < D / 16; ++e) {
-        const int d = sub + 16 * e;
-        float v = 0.0f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v += os[q][row][d] * f[q];
-        if (split) p.po[base + d] = v;
-        else kv_store_out(a, base + d, v * inv);
-      }
-      if (sub == 0) {
-        if (split) {
-          const f32x2v ml = {sum == sum ? top : -kNegInf, sum};  // NaN has the last word in the join
-          *(f32x2v*)(p.ml + (it.slot * p.rb + 16 * t + row) * 2) = ml;
-        } else if (a.lse) {
-          a.lse[tok * a.heads + hq] = kv_lse(top, sum);
-        }
+      for (int q = 0; q < 4; ++q) v += os[q][at][d] * f[q];
+      if (split) p.po[base + d] = v;
+      else kv_store_out(a, base + d, v * inv);
+    }
+    if (sub == 0) {
+      if (split) {
+        const f32x2v ml = {sum == sum ? top : -kNegInf, sum};  // NaN has the last word in the join
+        *(f32x2v*)(p.ml + (it.slot * p.rb + at) * 2) = ml;
+      } else if (a.lse) {
+        a.lse[tok * a.heads + hq] = kv_lse(top, sum);
       }
     }
   }
@@ -1120,25 +1146,23 @@ int prompt_rows(int dim) {
 
 struct KvPlan {
   KvAttnArgs few, many;
-  int qt;                   // 16-row tiles of the few-rows kernel
   bool run_few, run_many, split, planned;
   size_t need;
 };
 
 // Which kernels run, their row tiles and the room for split results, from what
 // the host knows (shapes; lengths and offsets stay on the device).  Sequences of
-// at most 64 rows per kv head (query tokens times heads of the group) go to the
+// at most 16 rows per kv head (query tokens times heads of the group) go to the
 // few-rows kernel, the others to the prompt kernel; without offsets all have the
-// same count, with offsets both may be needed.
+// same count, with offsets both may be needed.  16 sequences of 4096 tokens, 4 kv
+// heads of 128: 32 rows 32 us in the prompt kernel, 60 in the other with two row
+// tiles a wave; 64 rows 39, and 108 with four.
 KvPlan kv_plan(const KvAttn& a, char* ws) {
   KvPlan p;
   const int g = a.heads / a.c.heads;
   const int64_t H = a.c.heads, rows = a.q.nper * g, cus = device_cu_count();
-  const int usual = (int)(a.q.cu ? (g < 64 ? g : 64) : (rows < 64 ? rows : 64));
-  p.qt = usual <= 16 ? 1 : (usual <= 32 || a.c.dim > 128 ? 2 : 4);
-  const int limit = 64;
-  p.run_few = a.q.cu || rows <= limit;
-  p.run_many = a.q.cu ? a.q.total * g > limit : rows > limit;
+  p.run_few = a.q.cu || rows <= kFewRows;
+  p.run_many = a.q.cu ? a.q.total * g > kFewRows : rows > kFewRows;
   const int64_t tiles = (a.q.cap + kKvTile - 1) / kKvTile;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   size_t off = up((size_t)a.q.seqs * 8);
@@ -1150,7 +1174,7 @@ KvPlan kv_plan(const KvAttn& a, char* ws) {
     w.above = above;
     w.most = most;
     w.target = target;
-    const bool split = run && tiles > kWholeTiles && (most == limit || rt * H < target);
+    const bool split = run && tiles > kWholeTiles && (most == kFewRows || rt * H < target);
     w.cmin = split ? cmin : kNever;
     w.items = rt * H;
     w.plan = (int*)ws;
@@ -1172,11 +1196,11 @@ KvPlan kv_plan(const KvAttn& a, char* ws) {
       w.ml = w.po = nullptr;
     }
   };
-  const int rbf = 16 * p.qt, rbm = prompt_rows(a.c.dim);
+  const int rbf = kFewRows, rbm = prompt_rows(a.c.dim);
   int64_t rtf = a.q.seqs * ((rows + rbf - 1) / rbf), rtm = a.q.seqs * ((rows + rbm - 1) / rbm);
   if (a.q.cu) {  // n rows make at most n / rb + 1 tiles
     rtf = a.q.total * g / rbf + a.q.seqs;
-    const int64_t most = a.q.seqs * ((limit + rbf - 1) / rbf), longer = a.q.total * g / limit;
+    const int64_t most = a.q.seqs * ((kFewRows + rbf - 1) / rbf), longer = a.q.total * g / kFewRows;
     if (rtf > most) rtf = most;
     rtm = a.q.total * g / rbm + (longer < a.q.seqs ? longer : a.q.seqs);
   }
@@ -1187,8 +1211,8 @@ KvPlan kv_plan(const KvAttn& a, char* ws) {
   aim = aim < 2 * cus ? 2 * cus : (aim > 8 * cus ? 8 * cus : aim);
   // a chunk has one tile a wave at least, and four where unsplit sequences fill the
   // card twice (64 sequences of 1024: 26 and 48 us with one; 8 of 2048: 21 and 17)
-  lay(p.few, p.run_few, rbf, 0, limit, rtf * H >= 2 * cus ? 16 : 4, aim, rtf);
-  lay(p.many, p.run_many, rbm, limit, INT32_MAX, 4, (a.c.dim <= 128 ? 2 : 1) * cus, rtm);
+  lay(p.few, p.run_few, rbf, 0, kFewRows, rtf * H >= 2 * cus ? 16 : 4, aim, rtf);
+  lay(p.many, p.run_many, rbm, kFewRows, INT32_MAX, 4, (a.c.dim <= 128 ? 2 : 1) * cus, rtm);
   p.need = p.split || p.planned ? off : 0;
   if (!p.split) p.few.plan = p.many.plan = nullptr;
   return p;
@@ -1220,16 +1244,10 @@ hipError_t launch_kv_attn(const KvAttn& a, void* ws, hipStream_t s) {
       if (e != hipSuccess) return e;
     }
     if (p.run_few) {
-      auto few = [&]<int QT>() {
-        auto k = a.c.fp8 ? k_kv_attn<D, QT, true> : k_kv_attn<D, QT, false>;
-        hipLaunchKernelGGL(k, dim3((unsigned)p.few.items), dim3(256), 0, s, p.few);
-        return hipGetLastError();
-      };
-      hipError_t e;
-      if (p.qt == 1) e = few.template operator()<1>();
-      else if (p.qt == 2) e = few.template operator()<2>();
-      else if constexpr (D <= 128) e = few.template operator()<4>();
-      else e = hipErrorInvalidValue;
+      auto k = a.c.tsh >= 6 ? (a.c.fp8 ? k_kv_attn<D, true, true> : k_kv_attn<D, false, true>)
+                            : (a.c.fp8 ? k_kv_attn<D, true, false> : k_kv_attn<D, false, false>);
+      hipLaunchKernelGGL(k, dim3((unsigned)p.few.items), dim3(256), 0, s, p.few);
+      const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
     if (p.split) {
