@@ -448,7 +448,7 @@ sparq24_status sparq24_kv_append(const sparq24_kvcache* cache, const sparq24_kvs
  * Arithmetic: codes and queries enter fp16 MFMAs exactly, the weights exp(s_t)
  * are rounded to fp16 (2^-11), all sums, maxima and scores are fp32.
  * Workspace: partial results of sequences that are split along their tokens and
- * the work list of more than 64 sequences; none for at most 64 where
+ * the work list of more than 128 sequences; none for at most 128 where
  * max_blocks * tokens <= 1024.  Concurrent calls, and graphs that may
  * replay at the same time, need workspaces of their own. */
 sparq24_status sparq24_kv_attention(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs,

@@ -347,8 +347,10 @@ __device__ inline int64_t units_of(const KvWork& k, int len) {
 // A unit is a chunk of a row tile of a sequence, an item a unit and a kv head.  Where
 // every sequence has as many units (same row counts, no chunks) a unit's place
 // follows from its number; up to kScanned sequences every workgroup adds up what
-// comes before it, in one round of loads; more have been added up by k_kv_plan.
-constexpr int kScanned = 64;
+// comes before it, in two rounds of loads; more have been added up by k_kv_plan
+// (one new token each, with offsets: 128 sequences of 300 31.4 us, by k_kv_plan 35.2;
+// 256 of 512 59.9 and 61.9).
+constexpr int kScanned = 128;
 __device__ inline bool kv_item(const KvAttnArgs& w, int64_t id, int lane, KvItem& it) {
   const int H = w.a.c.heads;
   const int64_t seqs = w.a.q.seqs, unit = id / H;
@@ -791,7 +793,7 @@ __global__ __launch_bounds__(256, BIG && D <= 128 ? 3 : 1) void k_kv_attn(KvAttn
 // 16 rows and head of 128 a wave issues 32 MFMAs (512 cycles of its SIMD's matrix
 // unit) and about 200 vector instructions (softmax, widening), and several waves per
 // SIMD overlap the one's products with the other's softmax.  A causal prompt of
-// 8192 tokens, 32 heads over 8: 647 us (850 Tflop/s; such MFMAs alone reach 1985).
+// 8192 tokens, 32 heads over 8: 650 us (845 Tflop/s; such MFMAs alone reach 1985).
 //
 // Shapes, 128 rows a workgroup each: as many waves as the registers of D allow, but
 // for D = 64, whose products are short next to the reads of a tile, two row tiles a

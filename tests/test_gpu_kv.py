@@ -375,7 +375,7 @@ def test_many_sequences():
 
 
 @pytest.mark.parametrize("uniform", [False, True])
-@pytest.mark.parametrize("count,kv", [(65, 1), (300, 2)])
+@pytest.mark.parametrize("count,kv", [(66, 1), (129, 1), (300, 2)])
 def test_many_sequences_some_split(count, kv, uniform):
     # more sequences than a workgroup adds up by itself, a few of them split; 600 sequences and heads fill
     # the card, so their chunks are longer

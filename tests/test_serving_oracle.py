@@ -228,11 +228,11 @@ def test_attention_refusals_and_workspace(L):
     # 1024 tokens at most: no split, no workspace
     assert attend(L, s=seqs(max_blocks=8, table_stride=8), out=None, ws=None, nb=n) == OK
     assert n.value == 0
-    # the work list of more than 64 sequences
-    many = dict(cu_tokens=FAKE, total=65)
-    assert attend(L, s=seqs(seqs=65, **many), q=rows(heads=6, total=65), out=None, ws=None, nb=n) == OK
+    # the work list of more than 128 sequences
+    many = dict(cu_tokens=FAKE, total=129)
+    assert attend(L, s=seqs(seqs=129, **many), q=rows(heads=6, total=129), out=None, ws=None, nb=n) == OK
     assert n.value > 0
-    assert attend(L, s=seqs(seqs=64, **many), q=rows(heads=6, total=65), out=None, ws=None, nb=n) == OK
+    assert attend(L, s=seqs(seqs=128, **many), q=rows(heads=6, total=129), out=None, ws=None, nb=n) == OK
     assert n.value == 0
     # more workgroups than a grid has
     most = dict(seqs=2 ** 24, total=2 ** 24)
