@@ -11,7 +11,7 @@
 
 #include <atomic>
 
-#include "launch.hpp"
+#include "launch_serving.hpp"
 
 using namespace sparq24;
 

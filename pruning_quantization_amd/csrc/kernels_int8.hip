@@ -5,6 +5,7 @@
 // multiplies, the bias and the rounding to the output type.
 #include "dispatch.hpp"
 #include "gemm_tile.hpp"
+#include "launch_serving.hpp"
 
 namespace sparq24 {
 

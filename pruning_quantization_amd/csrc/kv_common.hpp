@@ -10,6 +10,7 @@
 #pragma once
 
 #include "device_common.hpp"
+#include "launch_serving.hpp"
 
 namespace sparq24 {
 
