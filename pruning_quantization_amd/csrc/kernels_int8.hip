@@ -11,18 +11,19 @@ namespace sparq24 {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
-// Four outputs n .. n + 3 (a multiple of 4) of row m: one store where `wide` says
-// that rows are aligned for it and all are inside, else one by one.
+// Four outputs n .. n + 3 of row m: one store where all are inside (rows may begin at
+// any element, which global stores take: 777 x 1031 x 2064 10.8 us with the call,
+// 11.6 with aligned stores only), else one by one.
 template <class T>
 __device__ inline void int8_store4(const Int8Gemm& g, int64_t m, int64_t n, i32x4_t acc, float sa,
-                                   const float (&sb)[4], const float (&bias)[4], bool wide) {
+                                   const float (&sb)[4], const float (&bias)[4]) {
   if (m >= g.M) return;
-  typedef T t4 __attribute__((ext_vector_type(4)));
+  typedef T t4 __attribute__((ext_vector_type(4), aligned(sizeof(T))));
   T* c = (T*)g.c + m * g.ldc + n;
   t4 y;
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] = (T)((float)acc[e] * sa * sb[e] + bias[e]);
-  if (wide && n + 4 <= g.N) {
+  if (n + 4 <= g.N) {
     *(t4*)c = y;
   } else {
 #pragma unroll
@@ -42,7 +43,7 @@ __device__ inline void int8_store4(const Int8Gemm& g, int64_t m, int64_t n, i32x
 // TB/s past the launch and the first slabs); of a small weight by the latter (1 x
 // 4096 x 4096: 4.5 us).  The products take b first, so that a lane holds four
 // adjacent outputs, and the scales are asked for before the slabs are read: with
-// stores one by one and scales at the end 14.7 us, 777 x 1031 x 2064 12.4 (10.6).
+// stores one by one and scales at the end 14.7 us, 777 x 1031 x 2064 12.4 (9.2).
 template <int MT, int NT, int W, int S>
 __global__ __launch_bounds__(64 * W) void k_int8_stream(Int8Gemm g, int64_t ntn) {
   constexpr int SK = 128, QA = 2 * MT, QB = 2 * NT, STAGE = (MT + NT) * 16 * SK;
@@ -164,7 +165,6 @@ __global__ __launch_bounds__(64 * W) void k_int8_stream(Int8Gemm g, int64_t ntn)
     for (int j = 0; j < NT; ++j) red[(w * MT * NT + i * NT + j) * 64 + lane] = acc[i][j];
   __syncthreads();
   auto out = [&]<class T>(T) {
-    const bool wide = g.ldc % 4 == 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int t = w + W * u;
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(64 * W) void k_int8_stream(Int8Gemm g, int64_t ntn)
 #pragma unroll
       for (int q = 1; q < W; ++q) s += red[(q * MT * NT + t) * 64 + lane];
       const int64_t m = m0 + 16 * (t / NT) + c, n = n0 + 16 * (t % NT) + 4 * h;  // outputs n .. n + 3 of row m
-      int8_store4<T>(g, m, n, s, sa[u], sb[u], bias[u], wide);
+      int8_store4<T>(g, m, n, s, sa[u], sb[u], bias[u]);
     }
   };
   if (g.dtype == 0) out(0.0f);
@@ -201,11 +201,11 @@ __global__ __launch_bounds__(64 * W) void k_int8_stream(Int8Gemm g, int64_t ntn)
 // 4096 x 14336 x 4096, bf16 out: mixed 267 us, in turns 229 us; bound by LDS
 // (192 KB of fragments and 64 KB of slabs for 2048 cycles of products per slab).
 // 16 outputs n .. n + 15 of row m: 16-byte stores where `wide` says that all
-// are inside and aligned, else one by one.
+// are inside (rows may begin at any element), else one by one.
 template <class T>
 __device__ inline void int8_store16(const Int8Gemm& g, int64_t m, int64_t n, const i32x4_t (&acc)[4], float sa,
                                     const float* sb, const float* bias, bool wide) {
-  typedef T t8 __attribute__((ext_vector_type(16 / sizeof(T))));
+  typedef T t8 __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
   constexpr int V = 16 / sizeof(T);
   T* c = (T*)g.c + m * g.ldc + n;
   T y[16];
@@ -408,7 +408,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64) void k_int8_tile(Int8Ge
     bias[e] = g.bias ? g.bias[c] : -0.0f;  // y + -0 is y
   }
   auto out = [&]<class T>(T) {
-    const bool wide = n + 16 <= g.N && g.ldc * sizeof(T) % 16 == 0;
+    const bool wide = n + 16 <= g.N;
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
       const int64_t m = m0 + wm * WM + 16 * i + fr;
