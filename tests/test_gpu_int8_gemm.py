@@ -78,6 +78,19 @@ def test_strided_rows_and_out(m):
     assert (wide[:, n:] == 5.0).all(), "wrote outside its columns"
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("m", [3, 60, 300])
+def test_out_rows_at_any_element(m, dtype):
+    # rows of the output that begin at odd elements, in both kernels
+    n, k = 1100, 96
+    a, sa, b, sb, bi = operands(m + 1, m, n, k)
+    wide = torch.full((m, n + 7), 5.0, dtype=DT[dtype], device=DEV)
+    da, dsa, db, dsb, dbi = dev(a, sa, b, sb, bi)
+    S.int8_gemm(da, dsa, db, dsb, bias=dbi, out=wide[:, :n])
+    same(wide[:, :n].contiguous(), V.int8_gemm(a, sa, b, sb, bi), dtype)
+    assert (wide[:, n:] == 5.0).all(), "wrote outside its columns"
+
+
 def test_leading_dims_empty_and_zero_depth():
     a, sa, b, sb, bi = operands(3, 30, 20, 64)
     da, dsa, db, dsb, dbi = dev(a, sa, b, sb, bi)

@@ -531,6 +531,46 @@ def test_captured_steps_replay():
             assert torch.equal(a, b)
 
 
+def test_captured_many_sequences_follow_their_lengths():
+    # the work list of a replay comes from the lengths and offsets of that replay
+    rng = np.random.default_rng(23)
+    count = 140
+    lens = [int(x) for x in rng.integers(1, 90, count)]
+    lens[7] = 1900
+    p = Pool(24, lens, 1, 64, 16, "int8")
+    table, dlens = p.args()
+    news = np.ones(count, int)
+    cu, dcu = offsets(news)
+    q, q64 = stored(rng.standard_normal((count, 2, 64)), "f16")
+    k, _ = stored(rng.standard_normal((count, 1, 64)), "f16")
+    cache, other = p.dev(), p.dev()
+    S.kv_append(other, k, k, table, dlens, cu_tokens=dcu)                # warm
+    S.kv_attention(q, cache, table, dlens, cu_tokens=dcu)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        S.kv_append(other, k, k, table, dlens, cu_tokens=dcu)
+        out, lse = S.kv_attention(q, cache, table, dlens, cu_tokens=dcu, return_lse=True)
+    for step in range(4):
+        now = [max(1, n - 13 * step * (b % 3)) for b, n in enumerate(lens)]
+        take = np.ones(count, int)
+        take[3 * step], take[3 * step + 1] = 2, 0
+        cu, fresh = offsets(take)
+        dlens.copy_(torch.tensor(now, dtype=torch.int32))
+        dcu.copy_(fresh)
+        for a, b in zip(other, p.dev()):
+            a.copy_(b)
+        want = p.dev()
+        S.kv_append(want, k, k, table, dlens, cu_tokens=dcu)
+        eager, elens = S.kv_attention(q, cache, table, dlens, cu_tokens=dcu, return_lse=True)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager) and torch.equal(lse, elens)
+        for a, b in zip(other, want):
+            assert torch.equal(a, b)
+        check_attention(out, lse, type("P", (), dict(vars(p), lens=now))(), q64, cu, "f16", 0.125)
+
+
 def test_two_streams_at_once():
     # calls on side streams with their own data give what the calls give one after the other
     ps = [Pool(50 + i, [900 + 100 * i, 64], 2, 64, 16, "int8", wide=True) for i in range(2)]
