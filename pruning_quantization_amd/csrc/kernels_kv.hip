@@ -536,7 +536,9 @@ __device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], c
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       const bool g = mx[t] - st.m[t] > kTopMost;
-      const float nm = g ? mx[t] - kTopSet : st.m[t];
+      float nm = mx[t] - kTopSet;
+      nm = mx[t] - nm > kTopMost ? mx[t] : nm;  // where scores have steps of 16, mx - 8 may round to mx - 16
+      nm = g ? nm : st.m[t];
       const float al = g ? __builtin_amdgcn_exp2f(st.m[t] - nm) : 1.0f;
       st.m[t] = nm;
       st.far |= uniform((int)__any(__builtin_fabsf(nm) > kFarTop && nm != kNegInf));

@@ -1,0 +1,38 @@
+"""Cache attention at the ends of its numbers' ranges."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU, skipped there
+    pytest.skip("no GPU", allow_module_level=True)
+
+import pruning_quantization_amd as S  # noqa: E402
+from gpu_util import DEV  # noqa: E402
+
+I32 = dict(dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("wide", [False, True])
+def test_scores_of_any_size_leave_single_tokens_whole(n, wide):
+    # one visible token gives its value whatever its score is, here from 2^10 to 2^40, where the step of a
+    # score passes the distance between a reference and the largest weight: out = V, a whole number up to 64
+    # off by fp16's 2^-11 of it at most, which bf16 rounds back
+    heads, dim = 64, 64
+    k = torch.zeros(2, 1, 16, dim, dtype=torch.int8, device=DEV)
+    v = torch.zeros(2, 1, dim, 16, dtype=torch.int8, device=DEV)
+    k[..., 0] = 1
+    v[1, 0, :, 0] = torch.arange(1, dim + 1, device=DEV)
+    one = torch.ones(2, 1, device=DEV)
+    q = torch.zeros(1, n, heads, dim, dtype=torch.bfloat16, device=DEV)
+    rng = np.random.default_rng(n)
+    size = 2.0 ** np.linspace(10, 40, n * heads) * rng.uniform(1, 2, n * heads)
+    q[..., 0] = torch.from_numpy(size).to(DEV).view(1, n, heads)
+    table = torch.full((1, 80 if wide else 1), -1, **I32)
+    table[0, 0] = 1
+    lens = torch.tensor([1], **I32)
+    out = S.kv_attention(q, S.KVCache(k, one, v, one), table, lens, scale=1.0, causal=False)
+    bad = (out != v[1, 0, :, 0]).any(-1).flatten().cpu().numpy()
+    assert not bad.any(), f"wrong at log2 q = {np.log2(size[bad])}"
