@@ -220,7 +220,11 @@ hipError_t launch_kv_append(const KvCache& c, const KvSeqs& q, const KvRows& k, 
 // The block scales ride on the exponent: with w_t = p_t vs, w = exp2(s_t log2e
 // + log2 vs - m) feeds the second product, and the sum of p_t is the sum of
 // w / vs, so neither scale costs an instruction per score and w stays in
-// fp16's range whatever the scales are.  A query row is multiplied by a power
+// fp16's range whatever the scales are.  The sum is kept over 2^n, n near the
+// largest score, since a token of small values counts in it as much as any; m and n
+// are whole numbers, so that 2^(m - n) is exact.  Where a V scale is 2^28 and more
+// below the one that set m, w could leave fp32's range (2^-126) with a p_t that
+// counts: there the sum comes from the scores themselves.  A query row is multiplied by a power
 // of two that puts its largest element at 2^13 (exact: fp16 then holds every
 // bf16 or fp16 element down to 2^-27 of it in full).  Scores, m, sums and O are
 // fp32; w is rounded to fp16 (relative 2^-11, below bf16's own rounding and
@@ -262,6 +266,9 @@ constexpr float kTopMost = 15.0f;  // ... and stands until one would pass 2^15
 // tile takes the exponent as the difference of the rounded terms, so that the
 // largest stays in range.
 constexpr float kFarTop = 65536.0f;
+// Most that a weight is multiplied by for the sum: so a p_t passes 2^n by 2^35 at most,
+// and one that is lost (w < 2^-126) is below 2^-106 of it.
+constexpr float kMostFactor = 0x1p20f;
 constexpr float kNegInf = -__builtin_inff();
 
 // Work of one launch: item = ((sequence, chunk, row tile), kv head).
@@ -275,8 +282,8 @@ struct KvAttnArgs {
   int cmin;         // least tiles of a chunk
   int* starts;      // [seqs + 2] or null: first unit of each sequence, all units, len (k_kv_plan)
   int* plan;        // [seqs][2]: first item / kv heads, chunks
-  float* ml;        // [items][rb][2]: reference and sum of a split row tile
-  float* po;        // [items][rb][D]
+  float* ml;        // [items][rb][2]: reference n and sum of a split row tile
+  float* po;        // [items][rb][D]: its output by itself
 };
 
 // Sequences of at most so many tiles stay whole: a second launch that joins chunks costs
@@ -406,6 +413,22 @@ __device__ inline void kv_store_out(const KvAttn& a, int64_t o, float v) {
   else ((_Float16*)a.out)[o] = (_Float16)v;
 }
 
+// Over the four lane groups (lanes l ^ 16, l ^ 32), in every lane.
+__device__ inline float groups_max(float v) {
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  float m;
+  asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(r[0]), "v"(r[1]));
+  r = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+  asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(r[0]), "v"(r[1]));
+  return m;
+}
+__device__ inline float groups_sum(float v) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
 // Query row r of the row tile (column c of the MFMA tiles), in fp16 times a power
 // of two: elements d(j) .. d(j) + 7 of lane group h into qf[j].
 struct KvRow {
@@ -435,8 +458,7 @@ __device__ inline KvRow kv_query(const KvAttnArgs& p, const KvItem& it, int r, f
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
     for (int e = 0; e < 8; ++e) am = __builtin_fmaxf(am, __builtin_fabsf(at(j, e)));
-  am = __builtin_fmaxf(am, __shfl_xor(am, 16, 64));
-  am = __builtin_fmaxf(am, __shfl_xor(am, 32, 64));
+  am = groups_max(am);
   int ex = (int)(__float_as_uint(am) >> 23);  // 0: zero or subnormal, 255: inf
   ex = ex < 64 ? 64 : (ex > 254 ? 127 : ex);
   const float up = __uint_as_float((uint32_t)(127 + 13 - (ex - 127)) << 23);
@@ -464,26 +486,17 @@ __device__ inline KvScales kv_scales(bool there, float ks, float vs) {
   return k;
 }
 
-// Over the four lane groups (lanes l ^ 16, l ^ 32).
-__device__ inline float groups_max(float v) {
-  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  float m;
-  asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(r[0]), "v"(r[1]));
-  r = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
-  asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(r[0]), "v"(r[1]));
-  return m;
-}
-
 // State of a wave's rows over the tiles.
 template <int QT, int NU>
 struct KvState {
-  float m[QT], l[QT];  // reference (log2), sum of this lane group's tokens
+  float m[QT], e[QT], l[QT];  // reference of O (log2), 2^(m - n), sum of this lane group's tokens over 2^n
   f32x4v o[QT][NU];
-  int far;             // some row's reference is past kFarTop
+  int far;                    // some row's reference is past kFarTop
   __device__ inline void init() {
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       m[t] = kNegInf;
+      e[t] = 1.0f;
       l[t] = 0.0f;
 #pragma unroll
       for (int u = 0; u < NU; ++u) o[t][u] = f32x4v{0.f, 0.f, 0.f, 0.f};
@@ -491,6 +504,46 @@ struct KvState {
     far = 0;
   }
 };
+// log2 of a power of two, exactly.
+__device__ inline float log2_exact(float e) { return (float)((int)(__float_as_uint(e) >> 23) - 127); }
+
+// Where a factor of the weights for the sum has grown past kMostFactor: the sums'
+// references rise to the largest scores, and if a V scale is still so far below,
+// the tile's part of the sums comes straight from the scores.  was, up: e and m have
+// been raised from e = was by 2^up (which may have left e's range).
+template <int QT, int NU>
+__device__ inline void kv_sum_reference(const f32x4v (&sc)[QT][4], const float (&ck)[QT], const float (&mx)[QT],
+                                        float rv, const float (&was)[QT], const float (&up)[QT], KvState<QT, NU>& st,
+                                        float (&f)[QT]) {
+  bool apart = false;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    const float best = __builtin_floorf(groups_max(mx[t] * ck[t]));
+    const float d = log2_exact(was[t]) + up[t];      // m - n
+    float nd = __builtin_fminf(d, st.m[t] - best);  // NaN (both infinite): as it was
+    nd = __builtin_amdgcn_fmed3f(nd, -126.0f, 126.0f);
+    if (st.m[t] != kNegInf) {
+      st.l[t] *= __builtin_amdgcn_exp2f(nd - d);
+      st.e[t] = __builtin_amdgcn_ldexpf(1.0f, (int)nd);
+      f[t] = st.e[t] * rv;
+    }
+    apart |= f[t] > kMostFactor;
+  }
+  if (__any(apart)) {
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      const float ref = st.m[t] == kNegInf ? 0.0f : st.m[t], d = log2_exact(st.e[t]);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = st.far ? sc[t][mt][e] * ck[t] - ref : __builtin_fmaf(sc[t][mt][e], ck[t], -ref);
+          st.l[t] += __builtin_amdgcn_exp2f(x + d);
+        }
+      f[t] = 0.0f;
+    }
+  }
+}
 
 // Scores of a tile (lane: QT rows, tokens tok0 .. tok0 + 15) to weights: masks
 // (where `edge`), the rows' references, sums (fp32: a token of a small V scale can
@@ -501,7 +554,7 @@ struct KvState {
 template <int QT, int NU>
 __device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], const KvScales& k, int tok0,
                                   bool edge, KvState<QT, NU>& st, f16x8_t (&pf)[QT][2]) {
-  float ck[QT], mx[QT];
+  float ck[QT], mx[QT], top[QT], f[QT];  // f: factor of the weights for the sum
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
     ck[t] = k.there ? row[t].c * k.ks : 1.0f;
@@ -521,7 +574,7 @@ __device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], c
         }
     }
   }
-  bool grow = false;
+  bool turn = false;
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
     mx[t] = kNegInf;
@@ -529,23 +582,31 @@ __device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], c
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) mx[t] = __builtin_fmaxf(mx[t], sc[t][mt][e]);
-    mx[t] = groups_max(__builtin_fmaf(mx[t], ck[t], k.lv));
-    grow |= mx[t] - st.m[t] > kTopMost;  // -inf - -inf is NaN: no new reference
+    f[t] = st.e[t] * k.rv;
+    top[t] = groups_max(__builtin_fmaf(mx[t], ck[t], k.lv));
+    turn |= top[t] - st.m[t] > kTopMost;  // -inf - -inf is NaN: no new reference
+    turn |= f[t] > kMostFactor;
   }
-  if (__any(grow)) {
+  if (__any(turn)) {
+    float was[QT], up[QT];
+    bool apart = false;
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      const bool g = mx[t] - st.m[t] > kTopMost;
-      float nm = mx[t] - kTopSet;
-      nm = mx[t] - nm > kTopMost ? mx[t] : nm;  // where scores have steps of 16, mx - 8 may round to mx - 16
-      nm = g ? nm : st.m[t];
-      const float al = g ? __builtin_amdgcn_exp2f(st.m[t] - nm) : 1.0f;
-      st.m[t] = nm;
-      st.far |= uniform((int)__any(__builtin_fabsf(nm) > kFarTop && nm != kNegInf));
-      st.l[t] *= al;
+      const bool g = top[t] - st.m[t] > kTopMost;
+      float nm = __builtin_floorf(top[t]) - kTopSet;
+      nm = top[t] - nm > kTopMost ? top[t] : nm;  // where scores have steps of 16, top - 8 may round to top - 16
+      up[t] = g ? nm - st.m[t] : 0.0f;
+      was[t] = st.e[t];
+      const float al = __builtin_amdgcn_exp2f(-up[t]);
+      st.m[t] = g ? nm : st.m[t];
+      st.e[t] = __builtin_amdgcn_ldexpf(st.e[t], (int)up[t]);  // infinite at the first reference
+      st.far |= uniform((int)__any(__builtin_fabsf(st.m[t]) > kFarTop && st.m[t] != kNegInf));
 #pragma unroll
       for (int u = 0; u < NU; ++u) st.o[t][u] *= al;
+      f[t] = st.e[t] * k.rv;
+      apart |= f[t] > kMostFactor;
     }
+    if (__any(apart)) kv_sum_reference(sc, ck, mx, k.rv, was, up, st, f);
   }
   if (st.far) {
 #pragma unroll
@@ -577,14 +638,8 @@ __device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], c
         sum += w;
         pf[t][mt / 2][4 * (mt & 1) + e] = (_Float16)w;
       }
-    st.l[t] = __builtin_fmaf(sum, k.rv, st.l[t]);
+    st.l[t] = __builtin_fmaf(sum, f[t], st.l[t]);
   }
-}
-
-// Over the four lane groups, in every lane.
-__device__ inline float groups_sum(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
 }
 
 __device__ inline float kv_lse(float top, float sum) {
@@ -744,29 +799,29 @@ __global__ __launch_bounds__(256, BIG && D <= 128 ? 3 : 1) void k_kv_attn(KvAttn
   // the four waves' parts of each row meet in LDS, in wave order
   constexpr int PITCH = D + 4;
   __shared__ float os[4][16][PITCH];
-  __shared__ float mls[4][16][2];
+  __shared__ __attribute__((aligned(16))) float mls[4][16][4];  // m, n, sum
   st.l[0] = groups_sum(st.l[0]);
-  if (h == 0) {
-    mls[wv][c16][0] = st.m[0];
-    mls[wv][c16][1] = st.l[0];
-  }
+  if (h == 0) *(f32x4v*)mls[wv][c16] = f32x4v{st.m[0], st.m[0] - log2_exact(st.e[0]), st.l[0], 0.0f};
 #pragma unroll
   for (int u = 0; u < NU; ++u) *(f32x4v*)&os[wv][c16][16 * u + 4 * h] = st.o[0][u];
   __syncthreads();
-  const int at = threadIdx.x >> 4, sub = threadIdx.x & 15;
+  const int at = 4 * wv + h, sub = c16, g = scalar(p.g);  // (held over the loop, p.g's reciprocal is spilled)
   const int r = it.rt * p.rb + at;
   if (r < it.k.rows) {
-    float top = kNegInf, f[4], sum = 0.0f;
+    float top = kNegInf, most = kNegInf, f[4], sum = 0.0f;  // references of O and the sum
 #pragma unroll
-    for (int q = 0; q < 4; ++q) top = __builtin_fmaxf(top, mls[q][at][0]);
+    for (int q = 0; q < 4; ++q) {
+      top = __builtin_fmaxf(top, mls[q][at][0]);
+      most = __builtin_fmaxf(most, mls[q][at][1]);
+    }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       f[q] = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mls[q][at][0] - top);
-      sum += mls[q][at][1] * f[q];
+      sum += mls[q][at][2] * (top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mls[q][at][1] - most));
     }
-    const int64_t tok = it.r.first + r / p.g, hq = it.head * p.g + r % p.g;
+    const int64_t tok = it.r.first + r / g, hq = it.head * g + r % g;
     const bool split = it.chunks > 1;
-    const float inv = split ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum);
+    const float inv = sum == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(top - most) / sum;
     const int64_t base = split ? (it.slot * p.rb + at) * D : (tok * a.heads + hq) * D;
 #pragma unroll
     for (int e = 0; e < D / 16; ++e) {
@@ -774,15 +829,15 @@ __global__ __launch_bounds__(256, BIG && D <= 128 ? 3 : 1) void k_kv_attn(KvAttn
       float v = 0.0f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) v += os[q][at][d] * f[q];
-      if (split) p.po[base + d] = v;
+      if (split) p.po[base + d] = v * inv;
       else kv_store_out(a, base + d, v * inv);
     }
     if (sub == 0) {
       if (split) {
-        const f32x2v ml = {sum == sum ? top : -kNegInf, sum};  // NaN has the last word in the join
+        const f32x2v ml = {sum == sum ? most : -kNegInf, sum};  // NaN has the last word in the join
         *(f32x2v*)(p.ml + (it.slot * p.rb + at) * 2) = ml;
       } else if (a.lse) {
-        a.lse[tok * a.heads + hq] = kv_lse(top, sum);
+        a.lse[tok * a.heads + hq] = kv_lse(most, sum);
       }
     }
   }
@@ -1003,20 +1058,20 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
     const int r = w0 + 16 * t + c16;
     if (r >= it.k.rows) continue;
     const int64_t tok = it.r.first + r / p.g, hq = it.head * p.g + r % p.g;
+    const float inv = st.l[t] == 0.0f ? 0.0f : st.e[t] / st.l[t], most = st.m[t] - log2_exact(st.e[t]);
     if (it.chunks > 1) {
       const int64_t at = it.slot * p.rb + (r - r0);
 #pragma unroll
-      for (int u = 0; u < NU; ++u) *(f32x4v*)(p.po + at * D + 16 * u + 4 * h) = st.o[t][u];
-      const f32x2v ml = {st.l[t] == st.l[t] ? st.m[t] : -kNegInf, st.l[t]};  // NaN has the last word in the join
+      for (int u = 0; u < NU; ++u) *(f32x4v*)(p.po + at * D + 16 * u + 4 * h) = st.o[t][u] * inv;
+      const f32x2v ml = {st.l[t] == st.l[t] ? most : -kNegInf, st.l[t]};  // NaN has the last word in the join
       if (h == 0) *(f32x2v*)(p.ml + at * 2) = ml;
     } else {
-      const float inv = st.l[t] == 0.0f ? 0.0f : 1.0f / st.l[t];
       const int64_t at = (tok * a.heads + hq) * D;
 #pragma unroll
       for (int u = 0; u < NU; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) kv_store_out(a, at + 16 * u + 4 * h + e, st.o[t][u][e] * inv);
-      if (a.lse && h == 0) a.lse[tok * a.heads + hq] = kv_lse(st.m[t], st.l[t]);
+      if (a.lse && h == 0) a.lse[tok * a.heads + hq] = kv_lse(most, st.l[t]);
     }
   }
 }
@@ -1103,8 +1158,12 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many
   if (first < 0 || (first + (int64_t)chunks * nrt) * a.c.heads > p.items) return;
   const int64_t at0 = ((first + nrt - 1 - rt) * a.c.heads + head) * p.rb + rr;
   const int64_t step = (int64_t)nrt * a.c.heads * p.rb;
+  // the common reference: the largest sum's own exponent, so that no chunk's weight passes 2
   float top = kNegInf;
-  for (int c = l; c < chunks; c += L) top = __builtin_fmaxf(top, p.ml[(at0 + c * step) * 2]);
+  for (int c = l; c < chunks; c += L) {
+    const f32x2v ml = *(const f32x2v*)(p.ml + (at0 + c * step) * 2);
+    top = __builtin_fmaxf(top, ml[0] + (float)((int)(__float_as_uint(ml[1]) >> 23) - 127));
+  }
 #pragma unroll
   for (int x = 1; x < L; x <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, x, 64));
   float sum = 0.0f, v[V];
@@ -1116,8 +1175,8 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many
     for (int c = wv; c < chunks; c += W == 4 ? 4 : 1) {
       const int64_t s = at0 + c * step;
       const f32x2v ml = *(const f32x2v*)(p.ml + s * 2);
-      const float f = __builtin_amdgcn_exp2f(ml[0] - top);
-      sum = __builtin_fmaf(ml[1], f, sum);
+      const float f = ml[1] * __builtin_amdgcn_exp2f(ml[0] - top);
+      sum += f;
 #pragma unroll
       for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(p.po[s * D + at(e)], f, v[e]);
     }

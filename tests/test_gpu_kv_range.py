@@ -10,6 +10,8 @@ if not torch.cuda.is_available():  # collected on CPU, skipped there
 
 import pruning_quantization_amd as S  # noqa: E402
 from gpu_util import DEV  # noqa: E402
+from kv_check import check_attention  # noqa: E402
+from test_gpu_kv import Pool, offsets, stored  # noqa: E402
 
 I32 = dict(dtype=torch.int32, device=DEV)
 
@@ -36,3 +38,33 @@ def test_scores_of_any_size_leave_single_tokens_whole(n, wide):
     out = S.kv_attention(q, S.KVCache(k, one, v, one), table, lens, scale=1.0, causal=False)
     bad = (out != v[1, 0, :, 0]).any(-1).flatten().cpu().numpy()
     assert not bad.any(), f"wrong at log2 q = {np.log2(size[bad])}"
+
+
+# exponents of the V scales, dealt to runs of blocks in order; None: a scale of zero over codes of zero
+FAR = [(None, 0), (None, 46), (None, 48), (None, 100), (48, None), (100, None), (-70, 60), (60, -70),
+       (None, -70, 0, 100), (100, 0, -70, None)]
+
+
+@pytest.mark.parametrize("far", FAR, ids=str)
+@pytest.mark.parametrize("place", ["wave", "waves", "chunks", "prompt", "long prompt"])
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+def test_v_scales_over_the_whole_range(fmt, place, far):
+    # the softmax does not know the V scales: a block of small or no values counts in the sum beside one whose
+    # values are up to 2^170 times larger, in a wave, across the waves and chunks, and in the prompt kernel
+    lens, news, wide = {"wave": ([64, 40], [1, 1], False), "waves": ([700, 300], [1, 2], False),
+                        "chunks": ([2600, 300], [1, 1], True), "prompt": ([150, 90], [90, 20], False),
+                        "long prompt": ([1500, 200], [30, 40], True)}[place]
+    p = Pool(len(far), lens, 1, 64, 16, fmt, wide=wide)
+    k, ks, v, vs = (x.copy() for x in p.ref)
+    for row, n in zip(p.table, lens):
+        blocks = row[:-(-n // 16)]
+        for i, blk in enumerate(blocks):
+            e = far[i * len(far) // len(blocks)]
+            vs[blk] = 0 if e is None else np.exp2(e + p.rng.random())
+            if e is None:
+                v[blk] = 0
+    p.ref = (k, ks, v, vs)
+    cu, dcu = offsets(news)
+    q, q64 = stored(p.rng.standard_normal((cu[-1], 4, 64)), "bf16")
+    out, lse = S.kv_attention(q, p.dev(), *p.args(), cu_tokens=dcu, return_lse=True)
+    check_attention(out, lse, p.ref, p.table, lens, cu, q64, fmt, 0.125, 2.0 ** -8, bits=8)
