@@ -471,18 +471,21 @@ __device__ inline KvRow kv_query(const KvAttnArgs& p, const KvItem& it, int r, f
 }
 
 // Block scales of the 16 tokens of a lane group.  A zero scale counts as 2^-80:
-// its codes are zeros.
+// its codes are zeros.  A scale that is no finite number makes every score of its
+// tokens NaN, before the masks, so that it reaches the rows that see them only.
 struct KvScales {
-  bool there;
+  bool there, fine;
   float ks, lv, rv;  // K scale, log2 and reciprocal of V's
 };
 __device__ inline KvScales kv_scales(bool there, float ks, float vs) {
   KvScales k;
   const float vse = vs < 0x1p-80f ? 0x1p-80f : vs;
+  const bool fine = there && __builtin_isfinite(ks + vs);
   k.there = there;
+  k.fine = fine;
   k.ks = ks;
-  k.lv = there ? __builtin_amdgcn_logf(vse) : 0.0f;
-  k.rv = there ? __builtin_amdgcn_rcpf(vse) : 1.0f;
+  k.lv = fine ? __builtin_amdgcn_logf(vse) : 0.0f;
+  k.rv = fine ? __builtin_amdgcn_rcpf(vse) : 1.0f;
   return k;
 }
 
@@ -546,7 +549,7 @@ __device__ inline void kv_sum_reference(const f32x4v (&sc)[QT][4], const float (
 }
 
 // Scores of a tile (lane: QT rows, tokens tok0 .. tok0 + 15) to weights: masks
-// (where `edge`), the rows' references, sums (fp32: a token of a small V scale can
+// (where `edge`: a mask or a bad scale), the rows' references, sums (fp32: a token of a small V scale can
 // have a weight that fp16 does not hold and still be most of the sum) and the
 // rescaling of O.  (Taking the weights first and forming the maxima only where
 // one passed 2^15 costs more than it saves as soon as scores spread: 847 against
@@ -557,10 +560,16 @@ __device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], c
   float ck[QT], mx[QT], top[QT], f[QT];  // f: factor of the weights for the sum
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    ck[t] = k.there ? row[t].c * k.ks : 1.0f;
+    ck[t] = k.fine ? row[t].c * k.ks : 1.0f;
     ck[t] = ck[t] < 0x1p-120f ? 0x1p-120f : ck[t];
   }
   if (edge) {
+    if (__any(k.there && !k.fine)) {
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) sc[t][mt] += k.there && !k.fine ? __builtin_nanf("") : 0.0f;
+    }
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       // tokens tok0 + x with first <= x <= last
@@ -745,7 +754,6 @@ __global__ __launch_bounds__(256, BIG && D <= 128 ? 3 : 1) void k_kv_attn(KvAttn
   for (; tt < rg.t1; tt += 4) {
     const int b0 = tt * kKvTile, gp = b0 + 16 * h;
     const bool there = blk >= 0 && (!BIG || (gp < hi && gp + 16 > lo)), more = tt + 4 < rg.t1;
-    const uint64_t away = __ballot(!there);
     f32x4v sc[1][4];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) sc[0][mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
@@ -759,8 +767,8 @@ __global__ __launch_bounds__(256, BIG && D <= 128 ? 3 : 1) void k_kv_attn(KvAttn
         sc[0][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[2 * s + 1], sc[0][mt], 0, 0, 0);
       }
 
-    const bool edge = away != 0 || b0 + kKvTile > rg.least || b0 < rg.from;
     const KvScales kk = kv_scales(there, ks, vs);
+    const bool edge = __any(!kk.fine) || b0 + kKvTile > rg.least || b0 < rg.from;
     int blk2 = -1;
     if (more) {
       load_k(tt + 4, blk1);
@@ -1023,8 +1031,8 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
           }
         __builtin_amdgcn_s_setprio(0);
         const bool there = is_there(tt, blk, h);
-        const bool edge = __any(!there) || b0 + kKvTile > mine.least || b0 < mine.from;
         const KvScales kk = kv_scales(there, ks, vs);
+        const bool edge = __any(!kk.fine) || b0 + kKvTile > mine.least || b0 < mine.from;
         f16x8_t pf[QT][2];
         kv_weights<QT, NU>(sc, row, kk, b0 + 16 * h, edge, st, pf);
         __builtin_amdgcn_s_setprio(1);
