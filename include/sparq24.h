@@ -442,9 +442,9 @@ sparq24_status sparq24_kv_append(const sparq24_kvcache* cache, const sparq24_kvs
  * out [total][query heads][dim] in q's type; lse [total][query heads] fp32 (or
  * NULL) receives log sum_t exp(s_t).  A row that sees no token gets zeros and
  * -inf.  Rows of out and lse that belong to no sequence stay as they are.
- * What is stored in no visible place (behind a sequence, before its window)
- * does not reach the result, whatever its bits; a visible e4m3 NaN code gives
- * NaN.  scale: finite, > 0.  Block scales: 0, or 2^-80 to 2^126, in any mixture;
+ * What a row does not see (behind its position or its sequence, before its
+ * window) does not reach it, whatever its bits; a visible e4m3 NaN code makes a
+ * row NaN (of k) or its elements of that dim (of v).  scale: finite, > 0.  Block scales: 0, or 2^-80 to 2^126, in any mixture;
  * an infinite or NaN one makes the rows that see a token of its block NaN.
  * Arithmetic: codes and queries enter fp16 MFMAs exactly, the weights exp(s_t)
  * are rounded to fp16 (2^-11), all sums, maxima and scores are fp32.

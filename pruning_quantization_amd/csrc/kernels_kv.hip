@@ -678,6 +678,131 @@ __device__ inline KvRange kv_range(const KvAttnArgs& p, const KvItem& it, int r0
   return {scalar(k.t0), scalar(k.t1), scalar(k.lo), scalar(k.hi), scalar(k.least), scalar(k.from)};
 }
 
+// e4m3 only.  A V code can be NaN, and 0 * NaN carries it to rows that do not see it.
+// Where O holds a NaN that its sum does not explain, kv_nan_pass forms O of the wave's 16
+// rows again, with the references and sums that stand: codes that are NaN count as
+// zeros, and a second product counts those that a row sees, whose elements of O are
+// NaN then.  It takes the kernel's arguments and its item anew, hidden from the
+// compiler: shared with the loops before, which hardly ever need it, they took
+// registers from those (8192 e4m3 tokens 654 us, shared 686).
+template <int QT, int NU>
+__device__ inline bool kv_nan_values(const KvState<QT, NU>& st) {  // l: over the lane groups
+  bool nan = false;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    bool some = false;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) some |= st.o[t][u][e] != st.o[t][u][e];
+    nan |= some && st.l[t] == st.l[t];
+  }
+  return nan;
+}
+typedef __attribute__((address_space(3))) float lds_float_t;
+typedef __attribute__((address_space(4))) const KvAttnArgs const_args_t;
+// Row r (column c of the wave's tile) over tiles first, first + step, .. of its range;
+// m: its reference.  To LDS: O of the row; else O times inv to its place.
+template <int D>
+__device__ inline __attribute__((always_inline)) void kv_nan_pass(int r, int first, int step, float m, int far,
+                                                                  float inv, lds_float_t* lds) {
+  constexpr int NJ = D / 32;
+  auto args = (const_args_t*)__builtin_amdgcn_kernarg_segment_ptr();
+  int id = (int)blockIdx.x;
+  asm volatile("" : "+s"(args), "+s"(id));
+  const KvAttnArgs& p = *(const KvAttnArgs*)args;
+  const KvAttn& a = p.a;
+  const int lane = __lane_id(), c16 = lane & 15, h = lane >> 4, T = 1 << a.c.tsh;
+  KvItem it;
+  if (!kv_item(p, id, lane, it)) return;
+  f16x8_t qf[NJ];
+  const KvRow row = kv_query(p, it, r, qf, [&](int j) { return 64 * (j / 2) + 16 * h + 8 * (j & 1); });
+  const int hi = (int)(it.r.len < a.q.cap ? it.r.len : a.q.cap);
+  const int* table = a.q.table + (int64_t)it.seq * a.q.table_stride;
+  const float ref = m == kNegInf ? 0.0f : m;
+  const int r0 = it.rt * p.rb, r1 = r0 + p.rb < it.k.rows ? r0 + p.rb : it.k.rows;
+  const KvRange rg = kv_range(p, it, r0, r1);
+#pragma unroll 1
+  for (int d0 = 0; d0 < D; d0 += 64) {  // 64 dims at a time: few registers
+    f32x4v o[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) o[u] = f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int tt = rg.t0 + first; tt < rg.t1; tt += step) {
+      // this lane's K rows are of the 16 tokens of lane group c16 / 4, its V codes of its own
+      auto block = [&](int pos) -> int64_t {
+        const int b = pos < hi ? table[pos >> a.c.tsh] : -1;
+        return b >= 0 && b < a.c.blocks ? b : -1;
+      };
+      auto place = [&](int64_t b) { return (b < 0 ? 0 : b) * a.c.heads + it.head; };
+      const int b0 = tt * kKvTile, kpos = b0 + 16 * (c16 >> 2), tok0 = b0 + 16 * h;
+      const int64_t kb = block(kpos), vb = block(tok0);
+      const uint8_t* kp = a.c.k + place(kb) * T * D + (int64_t)((kpos & (T - 1)) + (c16 & 3)) * D + 16 * h;
+      const uint8_t* vp = a.c.v + place(vb) * T * D + (int64_t)(d0 + c16) * T + (tok0 & (T - 1));
+      f32x4v sc[4];
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        sc[mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NJ; j += 2) {
+          const u32x4v k = *(const u32x4v*)(kp + 4 * mt * D + 32 * j);
+          sc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8<true>(k[0], k[1]), qf[j], sc[mt], 0, 0, 0);
+          sc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8<true>(k[2], k[3]), qf[j + 1], sc[mt], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const KvScales k = kv_scales(vb >= 0, a.c.ks[place(vb)], a.c.vs[place(vb)]);
+      float ck = k.fine ? row.c * k.ks : 1.0f;
+      ck = ck < 0x1p-120f ? 0x1p-120f : ck;
+      f16x8_t pf[2], sees[2];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const bool seen = vb >= 0 && tok0 + x >= row.low && tok0 + x <= row.lim;
+        const float s = sc[x / 4][x % 4];
+        const float w = far ? __builtin_fmaf(s, ck, k.lv) - ref : __builtin_fmaf(s, ck, k.lv - ref);
+        pf[x / 8][x % 8] = seen ? (_Float16)__builtin_amdgcn_exp2f(w) : (_Float16)0.0f;
+        sees[x / 8][x % 8] = seen ? (_Float16)1.0f : (_Float16)0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const u32x4v c = *(const u32x4v*)(vp + 16 * u * T);
+        f32x4v count = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          f16x8_t v = widen8<true>(c[2 * x], c[2 * x + 1]), none;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const bool nan = v[e] != v[e];
+            none[e] = nan ? (_Float16)1.0f : (_Float16)0.0f;
+            v[e] = nan ? (_Float16)0.0f : v[e];
+          }
+          o[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pf[x], o[u], 0, 0, 0);
+          count = __builtin_amdgcn_mfma_f32_16x16x32_f16(none, sees[x], count, 0, 0, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[u][e] = count[e] > 0.0f ? __builtin_nanf("") : o[u][e];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (lds) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) lds[d0 + 16 * u + 4 * h + e] = o[u][e];
+    } else if (r < it.k.rows) {
+      const int64_t tok = it.r.first + r / p.g, hq = it.head * p.g + r % p.g;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int d = d0 + 16 * u + 4 * h + e;
+          if (it.chunks > 1) p.po[(it.slot * p.rb + (r - it.rt * p.rb)) * D + d] = o[u][e] * inv;
+          else kv_store_out(a, (tok * a.heads + hq) * D + d, o[u][e] * inv);
+        }
+    }
+  }
+}
+
 // Few rows per kv head (decoding): one tile of 16 rows, four waves that take the
 // chunk's tiles in turn, K and V straight from memory into MFMA operands.  Bound by
 // the cache's bytes: 64 sequences of 300..16384 tokens, 32 heads over 8 of 128, in
@@ -812,6 +937,10 @@ __global__ __launch_bounds__(256, BIG && D <= 128 ? 3 : 1) void k_kv_attn(KvAttn
   if (h == 0) *(f32x4v*)mls[wv][c16] = f32x4v{st.m[0], st.m[0] - log2_exact(st.e[0]), st.l[0], 0.0f};
 #pragma unroll
   for (int u = 0; u < NU; ++u) *(f32x4v*)&os[wv][c16][16 * u + 4 * h] = st.o[0][u];
+  if constexpr (FP8) {
+    if (__builtin_expect(__any(kv_nan_values(st)), 0))
+      kv_nan_pass<D>(it.rt * p.rb + c16, wv, 4, st.m[0], st.far, 0.0f, (lds_float_t*)os[wv][c16]);
+  }
   __syncthreads();
   const int at = 4 * wv + h, sub = c16, g = scalar(p.g);  // (held over the loop, p.g's reciprocal is spilled)
   const int r = it.rt * p.rb + at;
@@ -1080,6 +1209,14 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
 #pragma unroll
         for (int e = 0; e < 4; ++e) kv_store_out(a, at + 16 * u + 4 * h + e, st.o[t][u][e] * inv);
       if (a.lse && h == 0) a.lse[tok * a.heads + hq] = kv_lse(most, st.l[t]);
+    }
+  }
+  if constexpr (FP8) {
+    if (__builtin_expect(__any(kv_nan_values(st)), 0)) {
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+        kv_nan_pass<D>(w0 + 16 * t + c16, 0, 1, st.m[t], st.far, st.l[t] == 0.0f ? 0.0f : st.e[t] / st.l[t],
+                       nullptr);
     }
   }
 }

@@ -111,3 +111,35 @@ def test_scales_that_are_no_numbers_stay_with_rows_that_see_them(tokens, fmt, wh
     out, lse = S.kv_attention(q[None], p.dev(), *p.args(), return_lse=True, window=window)
     ref[0][blk], ref[2][blk] = 0, 0
     rows_apart(out, lse, sees, p, ref, [0, n], q64, fmt, window=window)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("first,n,window", SEEING)
+@pytest.mark.parametrize("dim,tokens", [(64, 16), (64, 64), (128, 16), (128, 128), (192, 32), (192, 64), (256, 16),
+                                        (256, 256)])
+def test_nan_codes_stay_with_rows_that_see_them(dim, tokens, first, n, window, wide):
+    # e4m3 NaN codes of values at two positions, in some dims each: those dims of the rows that see them are NaN,
+    # the rest is as without them; of a key's at a third: the rows that see it are NaN throughout
+    p = Pool(n + dim, [first + n], 1, dim, tokens, "fp8", wide=wide)
+    q, q64 = stored(p.rng.standard_normal((n, 4, dim)), "bf16")
+    ref = [x.copy() for x in p.ref]
+    pos = np.arange(first, first + n)
+    sees = lambda at: (pos >= at) & (pos < at + window if window else True)  # noqa: E731
+    nan = np.zeros((n, dim), bool)
+    last = first + n - 1
+    for at, dims in ((80, [3, 17, dim - 1]), (last - 1, [0, 17, 40])):
+        blk = p.table[0, at // tokens]
+        ref[2][blk, 0, dims, at % tokens] = 0
+        p.ref[2][blk, 0, dims, at % tokens] = [0x7F, 0xFF, 0x7F]
+        nan[np.ix_(sees(at), dims)] = True
+    p.ref[0][p.table[0, last // tokens], 0, last % tokens, 5] = 0xFF
+    out, lse = S.kv_attention(q[None], p.dev(), *p.args(), return_lse=True, window=window)
+    o, l = out.cpu().double().numpy().reshape(n, 4, dim), lse.cpu().double().numpy().reshape(n, 4)
+    assert np.isnan(o[-1]).all() and np.isnan(l[-1]).all()
+    o, l, nan = o[:-1], l[:-1], np.broadcast_to(nan[:-1, None], (n - 1, 4, dim))
+    assert np.array_equal(np.isnan(o), nan)
+    want, want_lse, spread, reach = V.kv_attention(q64, ref, p.table, p.lens, [0, n], "fp8", dim ** -0.5,
+                                                   window=window)
+    tol, own = bounds(ref, p.lens, "fp8", dim, spread, reach, want, 2.0 ** -8)
+    assert (np.abs(o - want[:-1]) <= tol[:-1])[~nan].all()
+    assert (np.abs(l - want_lse[:-1]) <= (own + 2.0 ** -21 * np.abs(want_lse))[:-1]).all()
