@@ -418,10 +418,11 @@ typedef struct {
  * heads, k = dim (any batch and row strides, k_stride 1), fp32, bf16 or fp16,
  * both of one type.  The i-th of a sequence's n rows becomes position
  * seq_lens[b] - n + i.  Per touched block and head, with amax the largest
- * |element| that the block receives (NaN left out): cand = fp32(amax / qmax),
- * 0 where amax < 2^-64; the new scale s is cand where the block's first token
+ * finite |element| that the block receives: cand = fp32(amax / qmax), 0 where
+ * amax < 2^-64; the new scale s is cand where the block's first token
  * is among the new ones, else max(old scale, cand); new codes are
- * encode(fp32(x * fp32(1 / s))) (nearest even, saturating; NaN as 0); where s
+ * encode(fp32(x * fp32(1 / s))) (nearest even, saturating, so infinities become
+ * +-qmax; NaN, and with s = 0 everything, as 0); where s
  * grew, the codes before the new ones become encode(fp32(code * fp32(old *
  * fp32(1 / s)))), otherwise they stay.  Codes behind the last new token stay
  * as they are.  Calling it again with the same arguments changes nothing.  A

@@ -10,8 +10,8 @@ Readings:
   multiplies and the bias add in fp32.
 * Append: one scale per block and head from the absolute maximum of what the
   block receives, never smaller than the scale of codes that stay in it; codes
-  that stay are coded again when the scale grows; NaN elements are left out of
-  the maximum and coded as 0.
+  that stay are coded again when the scale grows; elements that are not finite
+  are left out of the maximum, infinities saturate, NaN is coded as 0.
 * Attention: softmax over the visible stored values; a row that sees nothing
   gives zeros and a log-sum of -inf.
 """
@@ -75,7 +75,7 @@ def kv_append(cache, k: np.ndarray, v: np.ndarray, table: np.ndarray, lens: Sequ
                 for h in range(codes.shape[1]):
                     x = rows[cu[b] + row:cu[b] + row + o1 - o0, h].astype(np.float32)  # [new, D]
                     side = codes[blk, h].T if trans else codes[blk, h]                 # [T, D] view
-                    mag = np.abs(x[~np.isnan(x)])
+                    mag = np.abs(x[np.isfinite(x)])
                     amax = np.float32(mag.max()) if mag.size else np.float32(0)
                     s = np.float32(amax / QMAX[fmt]) if amax >= TINY_AMAX else np.float32(0)
                     old = scales[blk, h] if o0 else np.float32(0)
@@ -84,7 +84,8 @@ def kv_append(cache, k: np.ndarray, v: np.ndarray, table: np.ndarray, lens: Sequ
                     if o0 and s > old:
                         ratio = np.float32(old * inv)
                         side[:o0] = kv_encode(kv_decode(side[:o0], fmt).astype(np.float32) * ratio, fmt)
-                    side[o0:o1] = kv_encode(x * inv, fmt)
+                    with np.errstate(invalid="ignore"):
+                        side[o0:o1] = kv_encode(x * inv, fmt)
                     scales[blk, h] = s
     return kc, ks, vc, vs
 

@@ -7,10 +7,11 @@ namespace sparq24 {
 
 // ---------------------------------------------------------------------------
 // Append.  One workgroup per touched block, kv head and side (K, V).  With
-// amax the absolute maximum of the block's new elements (NaN left out):
+// amax the absolute maximum of the block's new elements (the finite ones, so that an
+// infinite element costs the block's other tokens nothing):
 //   cand = amax < 2^-64 ? 0 : fp32(amax / qmax)
 //   s    = the block begins with a new token ? cand : max(s_old, cand)
-//   code = encode(fp32(x * fp32(1 / s)));  a NaN element is coded as 0
+//   code = encode(fp32(x * fp32(1 / s)));  infinities saturate, NaN is coded as 0
 // and where s > s_old the codes before the new ones become
 //   encode(fp32(code * fp32(s_old * fp32(1 / s)))).
 // Codes behind the new ones stay as they are.
@@ -99,11 +100,14 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvCache c, KvSeqs q, KvRow
     }
   };
   float am = 0.0f;
-  auto widest = [&](const Unit<DT>(&u)[4]) {
+  auto widest = [&](const Unit<DT>(&u)[4], bool finite) {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int f = 0; f < 8; ++f) am = __builtin_fmaxf(am, __builtin_fabsf(u[e].f(f)));
+      for (int f = 0; f < 8; ++f) {
+        const float x = __builtin_fabsf(u[e].f(f));
+        am = __builtin_fmaxf(am, finite && x == __builtin_inff() ? 0.0f : x);
+      }
   };
   auto store = [&](unsigned i, const Unit<DT>(&u)[4], float inv) {
     const int o = 4 * (g0 + i / upr), d = 8 * (i % upr);
@@ -124,22 +128,38 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvCache c, KvSeqs q, KvRow
   };
   Unit<DT> held[4];
   const bool once = quads <= kBlock;
+  auto meet = [&] {  // am over the workgroup
+    am = __uint_as_float(wave_max_u32<64>(__float_as_uint(am)));
+    if (lane == 0) red[tid >> 6] = am;
+    __syncthreads();  // (every thread has read the old scale, too)
+#pragma unroll
+    for (int i = 0; i < kBlock / 64; ++i) am = __builtin_fmaxf(am, red[i]);
+  };
   if (once) {
     if (tid < (int)quads) {
       load(tid, held);
-      widest(held);
+      widest(held, false);
     }
   } else {
     for (unsigned i = tid; i < quads; i += kBlock) {
       load(i, held);
-      widest(held);
+      widest(held, false);
     }
   }
-  am = __uint_as_float(wave_max_u32<64>(__float_as_uint(am)));
-  if (lane == 0) red[tid >> 6] = am;
-  __syncthreads();  // (every thread has read the old scale, too)
-#pragma unroll
-  for (int i = 0; i < kBlock / 64; ++i) am = __builtin_fmaxf(am, red[i]);
+  meet();
+  if (am == __builtin_inff()) {  // once more, without the infinities
+    __syncthreads();             // red has been read
+    am = 0.0f;
+    if (once) {
+      if (tid < (int)quads) widest(held, true);
+    } else {
+      for (unsigned i = tid; i < quads; i += kBlock) {
+        load(i, held);
+        widest(held, true);
+      }
+    }
+    meet();
+  }
 
   const float cand = am >= 0x1p-64f ? am / (FP8 ? 448.0f : 127.0f) : 0.0f;
   const float s = cand > old ? cand : old;

@@ -1,4 +1,4 @@
-"""Cache attention at the ends of its numbers' ranges."""
+"""The cache's calls at the ends of their numbers' ranges."""
 import numpy as np
 import pytest
 
@@ -13,7 +13,7 @@ if not torch.cuda.is_available():  # collected on CPU, skipped there
 import pruning_quantization_amd as S  # noqa: E402
 from gpu_util import DEV  # noqa: E402
 from kv_check import bounds, check_attention  # noqa: E402
-from test_gpu_kv import Pool, offsets, stored  # noqa: E402
+from test_gpu_kv import Pool, offsets, stored, unchanged  # noqa: E402
 
 I32 = dict(dtype=torch.int32, device=DEV)
 
@@ -143,3 +143,25 @@ def test_nan_codes_stay_with_rows_that_see_them(dim, tokens, first, n, window, w
     tol, own = bounds(ref, p.lens, "fp8", dim, spread, reach, want, 2.0 ** -8)
     assert (np.abs(o - want[:-1]) <= tol[:-1])[~nan].all()
     assert (np.abs(l - want_lse[:-1]) <= (own + 2.0 ** -21 * np.abs(want_lse))[:-1]).all()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+@pytest.mark.parametrize("dtype,dim,tokens", [("bf16", 64, 16), ("f16", 128, 64), ("f32", 64, 256), ("f32", 256, 128)])
+def test_append_of_infinities(dtype, dim, tokens, fmt):
+    # single infinities, rows and blocks of them, next to kept tokens and alone; blocks whose rows a workgroup
+    # holds and larger ones
+    lens, news = [2 * tokens + 5, tokens + 3, 7, tokens], [tokens + 9, 3, 7, 5]
+    p = Pool(tokens + dim, lens, 2, dim, tokens, fmt)
+    cu, dcu = offsets(news)
+    rows = [p.rng.standard_normal((cu[-1], 2, dim)) * 3 for _ in range(2)]
+    for x in rows:
+        x[3, 0, 5], x[3, 1, 7], x[cu[1], :, :2], x[cu[1] + 1, 0] = np.inf, -np.inf, np.nan, -np.inf
+        x[cu[2]:cu[3], 1] = np.inf
+        x[cu[3]:, 0] = -np.inf
+        x[tokens // 2, 1, ::3] = np.inf
+    (k, k64), (v, v64) = (stored(x, dtype) for x in rows)
+    cache = p.dev()
+    S.kv_append(cache, k, v, *p.args(), cu_tokens=dcu)
+    want = V.kv_append(p.ref, k64, v64, p.table, lens, cu, fmt)
+    assert all(np.isfinite(x).all() for x in (want[1], want[3]))
+    unchanged(cache, want)
