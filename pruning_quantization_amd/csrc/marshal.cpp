@@ -300,16 +300,14 @@ PyObject* py_kv_attention(PyObject*, PyObject* const* a, Py_ssize_t argc) {
       auto call = [&](void* w, size_t* n) {
         return c_kv_attention(&c.c, &s, &x, (float)scale, causal, window, out.data_ptr(), plse, w, n, stream);
       };
-      size_t n = 0;
+      size_t n = work ? work->nbytes() : 0;
       if (!work) {
         const int e = call(nullptr, &n);
         if (e) return e;
-        if (!n) return call(nullptr, nullptr);
-        ws = at::empty({(int64_t)n}, q.options().dtype(ScalarType::Byte));
-      } else {
-        n = work->nbytes();
+        if (n) ws = at::empty({(int64_t)n}, q.options().dtype(ScalarType::Byte));
       }
-      return call(ws.data_ptr(), &n);
+      // without memory no size either: that would be the size query
+      return n ? call(ws.data_ptr(), &n) : call(nullptr, nullptr);
     });
     if (st) return failed("sparq24_kv_attention", st);
     if (!want_lse) return THPVariable_Wrap(out);

@@ -165,3 +165,19 @@ def test_append_of_infinities(dtype, dim, tokens, fmt):
     want = V.kv_append(p.ref, k64, v64, p.table, lens, cu, fmt)
     assert all(np.isfinite(x).all() for x in (want[1], want[3]))
     unchanged(cache, want)
+
+
+def test_an_empty_workspace():
+    # enough where a call needs none, refused where it needs one: never outputs that nothing wrote
+    p = Pool(3, [20, 70], 1, 64, 16, "int8")
+    q, _ = stored(p.rng.standard_normal((2, 1, 2, 64)), "bf16")
+    want = S.kv_attention(q, p.dev(), *p.args())
+    for empty in (torch.empty(0, dtype=torch.uint8, device=DEV), torch.empty(0, 4, device=DEV)):
+        out = torch.full_like(q, 7.0)
+        S.kv_attention(q, p.dev(), *p.args(), out=out, workspace=empty)
+        assert torch.equal(out, want)
+        p_wide = Pool(3, [20, 70], 1, 64, 16, "int8", wide=True)
+        out = torch.full_like(q, 7.0)
+        with pytest.raises(S.Sparq24Error, match="workspace"):
+            S.kv_attention(q, p_wide.dev(), *p_wide.args(), out=out, workspace=empty)
+        assert (out == 7).all()

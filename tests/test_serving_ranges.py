@@ -1,7 +1,12 @@
 """CPU pins of the serving oracle and the entry points at the ends of their ranges."""
+import ctypes
+
 import numpy as np
+import pytest
 
 import oracle.serving as V
+
+B = pytest.importorskip("pruning_quantization_amd.binding")
 
 
 def test_append_of_infinities_by_hand():
