@@ -247,7 +247,8 @@ def _workspace(x: torch.Tensor, query):
 
 
 def _wsarg(n):
-    return ctypes.byref(n) if n is not None else None
+    # an empty workspace has a null address: with a size beside it, that is the size query
+    return ctypes.byref(n) if n is not None and n.value else None
 
 
 def _code_dtype(q: CQSpec):
