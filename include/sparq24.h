@@ -373,7 +373,7 @@ sparq24_status sparq24_fp8_gemm(const uint8_t* a, const float* scale_a, int64_t 
  * of 16 where there is more than one row, at least K), ldc the elements
  * between rows of c (at least N).  a, b, c 16-byte aligned; scales and bias
  * 4-byte.  K % 16 == 0 and K <= SPARQ24_MAX_INT8_K (SHAPE); K == 0 gives the
- * bias or zeros.  Any M and N.  Workspace protocol as above. */
+ * bias or zeros, whatever lda and ldb.  Any M and N.  Workspace protocol as above. */
 #define SPARQ24_MAX_INT8_K 131056
 sparq24_status sparq24_int8_gemm(const int8_t* a, int64_t lda, const float* scale_a, int64_t m,
                                  const int8_t* b, int64_t ldb, const float* scale_b, int64_t n,

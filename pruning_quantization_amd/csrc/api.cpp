@@ -785,6 +785,7 @@ sparq24_status sparq24_int8_gemm(const int8_t* a, int64_t lda, const float* scal
   if (c_dtype != SPARQ24_F32 && c_dtype != SPARQ24_BF16 && c_dtype != SPARQ24_F16)
     return SPARQ24_ERR_INVALID;
   if (k % 16 || k > SPARQ24_MAX_INT8_K) return SPARQ24_ERR_SHAPE;
+  if (k == 0) lda = ldb = 0;  // no code is read
   if (m > INT32_MAX || n > INT32_MAX) return SPARQ24_ERR_UNSUPPORTED;
   if ((m > 1 && lda < k) || (n > 1 && ldb < k) || (m > 1 && ldc < n))
     return SPARQ24_ERR_UNSUPPORTED;

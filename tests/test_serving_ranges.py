@@ -27,3 +27,16 @@ def test_append_of_infinities_by_hand():
     # a block of infinities alone has no scale to count them in
     k, ks, _, _ = V.kv_append(cache, x, x, np.array([[0]], np.int32), [2], [0, 2], "fp8")
     assert ks[0, 0] == 0.0 and not k[0, 0, :2].any()
+
+
+def test_int8_gemm_of_no_codes_takes_any_strides():
+    # K = 0 reads no code: the strides of torch.empty(30, 0) are (1, 1)
+    fake, c = 0x7F0000000000, ctypes.c_size_t(0)
+    try:
+        L = B.lib()
+    except ImportError as e:
+        pytest.skip(str(e))
+    for lda, ldb in ((0, 0), (1, 1), (64, 3)):
+        st = L.sparq24_int8_gemm(None, lda, fake, 30, None, ldb, fake, 20, 0, None, 0, fake, 20, None,
+                                 ctypes.byref(c), None)
+        assert st == 0, (lda, ldb)
