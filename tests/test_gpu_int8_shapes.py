@@ -22,3 +22,78 @@ def test_no_codes(m, n):
     for a in (torch.empty(m, 0, dtype=torch.int8, device=DEV), torch.empty(m, 64, dtype=torch.int8, device=DEV)[:, :0]):
         y = S.int8_gemm(a, dsa, torch.empty(n, 0, dtype=torch.int8, device=DEV), dsb, bias=dbias)
         assert torch.equal(y, dbias.expand(m, n))
+
+
+def kernel_of(m, n, far=False):
+    """The kernel variant that a product takes: 16-row groups of a and b of the streaming kernel by its cost
+    rule, or the tile."""
+    cus = torch.cuda.get_device_properties(DEV).multi_processor_count
+    tiles = lambda a, b: -(-m // a) * -(-n // b)  # noqa: E731
+    cost, i, j = min(((-(-tiles(16 * i, 16 * j) // cus) * (i + j), i, j) for i in (1, 2, 4) for j in (1, 2, 4)),
+                     key=lambda c: c[0])
+    if cost <= 8 or far:
+        return "stream", i, j
+    for tile in ((256, 256), (256, 128)):
+        if tiles(*tile) >= cus:
+            return "tile", *tile
+    return ("tile", 128, 128) if tiles(64, 64) > 4 * cus else ("tile", 64, 64)
+
+
+# ragged in both directions, for 256 CUs
+SHAPES = [(("stream", 1, 1), 3, 777), (("stream", 1, 2), 30, 2101), (("stream", 1, 4), 33, 4201),
+          (("stream", 2, 1), 2147, 40), (("stream", 2, 2), 201, 1031), (("stream", 2, 4), 65, 4203),
+          (("stream", 2, 4), 1712, 145), (("stream", 4, 1), 610, 391), (("stream", 4, 2), 2060, 209),
+          (("stream", 4, 4), 300, 2905), (("tile", 64, 64), 1100, 1031), (("tile", 64, 64), 65, 9001),
+          (("tile", 128, 128), 2103, 2101), (("tile", 128, 128), 1101, 4203), (("tile", 256, 128), 2901, 2905),
+          (("tile", 256, 128), 705, 14003), (("tile", 256, 256), 4100, 4203), (("tile", 256, 256), 1101, 14003)]
+
+
+def test_shapes_reach_every_kernel():
+    if torch.cuda.get_device_properties(DEV).multi_processor_count != 256:
+        pytest.skip("the shapes are for 256 CUs")
+    for want, m, n in SHAPES:
+        assert kernel_of(m, n) == want, (m, n)
+
+
+# no whole slab of 128 codes, one, two, three and eight, with and without a rest
+@pytest.mark.parametrize("k", [16, 112, 128, 144, 256, 272, 400, 1024, 1040])
+@pytest.mark.parametrize("kernel,m,n", SHAPES)
+def test_every_kernel(kernel, m, n, k):
+    a, sa, b, sb, bias = operands(m + n + k, m, n, k)
+    dtype = ("f32", "bf16", "f16")[(m + k // 16) % 3]
+    da, dsa, db, dsb, dbias = dev(a, sa, b, sb, bias)
+    # the output's rows begin at any element, with room behind them that stays as it is
+    wide = torch.full((m, n + 5), 5.0, dtype=DT[dtype], device=DEV)
+    S.int8_gemm(da, dsa, db, dsb, bias=dbias, out=wide[:, :n])
+    same(wide[:, :n].contiguous(), V.int8_gemm(a, sa, b, sb, bias), dtype)
+    assert (wide[:, n:] == 5.0).all(), "wrote outside its columns"
+
+
+@pytest.mark.parametrize("k", [144, 400])
+@pytest.mark.parametrize("m,n", [(1100, 1031), (2103, 2101), (2901, 2905), (4100, 4203)])
+def test_tiles_of_strided_rows(m, n, k):
+    a, sa, b, sb, _ = operands(m + k, m, n, k)
+    da, dsa, db, dsb = dev(a, sa, b, sb)
+    wa, wb = (torch.full((r, k + 16 * s), 77, dtype=torch.int8, device=DEV) for r, s in ((m, 3), (n, 1)))
+    wa[:, :k], wb[:, :k] = da, db
+    assert kernel_of(m, n)[0] == "tile"
+    same(S.int8_gemm(wa[:, :k], dsa, wb[:, :k], dsb, dtype=torch.bfloat16), V.int8_gemm(a, sa, b, sb), "bf16")
+
+
+@pytest.mark.parametrize("far", ["a", "b"])
+@pytest.mark.parametrize("m,n", [(40, 20003), (20003, 40)])
+def test_rows_far_apart(m, n, far):
+    # row strides of 8 MiB and more pass the tiles' 32-bit offsets: the streaming kernel takes them whatever
+    # the shape
+    k, step = 272, (8 << 20) + 16
+    if (m if far == "a" else n) > 100:
+        m, n, step = min(m, 100), min(n, 100), 1 << 23
+    a, sa, b, sb, bias = operands(m + n, m, n, k)
+    da, dsa, db, dsb, dbias = dev(a, sa, b, sb, bias)
+    rows = m if far == "a" else n
+    room = torch.zeros((rows - 1) * step + k, dtype=torch.int8, device=DEV).as_strided((rows, k), (step, 1))
+    room.copy_(da if far == "a" else db)
+    if max(m, n) > 100:
+        assert kernel_of(m, n)[0] == "tile" and kernel_of(m, n, True)[0] == "stream"
+    y = S.int8_gemm(room if far == "a" else da, dsa, room if far == "b" else db, dsb, bias=dbias)
+    same(y, V.int8_gemm(a, sa, b, sb, bias), "f32")
