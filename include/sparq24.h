@@ -440,8 +440,9 @@ sparq24_status sparq24_kv_append(const sparq24_kvcache* cache, const sparq24_kvs
  * scale, out = sum_t exp(s_t) V_t / sum_t exp(s_t) over the visible tokens t:
  * all of the sequence, or with causal = 1 those up to the query's position,
  * and of these the last `window` ones where window > 0 (needs causal).
- * out [total][query heads][dim] in q's type; lse [total][query heads] fp32 (or
- * NULL) receives log sum_t exp(s_t).  A row that sees no token gets zeros and
+ * out [total][query heads][dim] in q's type (q itself may be it, where it is
+ * laid out so); lse [total][query heads] fp32 (or NULL) receives log sum_t
+ * exp(s_t).  A row that sees no token gets zeros and
  * -inf.  Rows of out and lse that belong to no sequence stay as they are.
  * What a row does not see (behind its position or its sequence, before its
  * window) does not reach it, whatever its bits; a visible e4m3 NaN code makes a

@@ -1210,29 +1210,35 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES)
     }
   }
 #pragma unroll
+  for (int t = 0; t < QT; ++t) st.l[t] = groups_sum(st.l[t]);
+  const bool again = FP8 && __any(kv_nan_values(st));  // (the queries may lie where the output goes)
+#pragma unroll
   for (int t = 0; t < QT; ++t) {
-    st.l[t] = groups_sum(st.l[t]);
     const int r = w0 + 16 * t + c16;
     if (r >= it.k.rows) continue;
     const int64_t tok = it.r.first + r / p.g, hq = it.head * p.g + r % p.g;
     const float inv = st.l[t] == 0.0f ? 0.0f : st.e[t] / st.l[t], most = st.m[t] - log2_exact(st.e[t]);
     if (it.chunks > 1) {
       const int64_t at = it.slot * p.rb + (r - r0);
+      if (!again) {
 #pragma unroll
-      for (int u = 0; u < NU; ++u) *(f32x4v*)(p.po + at * D + 16 * u + 4 * h) = st.o[t][u] * inv;
+        for (int u = 0; u < NU; ++u) *(f32x4v*)(p.po + at * D + 16 * u + 4 * h) = st.o[t][u] * inv;
+      }
       const f32x2v ml = {st.l[t] == st.l[t] ? most : -kNegInf, st.l[t]};  // NaN has the last word in the join
       if (h == 0) *(f32x2v*)(p.ml + at * 2) = ml;
     } else {
       const int64_t at = (tok * a.heads + hq) * D;
+      if (!again) {
 #pragma unroll
-      for (int u = 0; u < NU; ++u)
+        for (int u = 0; u < NU; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) kv_store_out(a, at + 16 * u + 4 * h + e, st.o[t][u][e] * inv);
+          for (int e = 0; e < 4; ++e) kv_store_out(a, at + 16 * u + 4 * h + e, st.o[t][u][e] * inv);
+      }
       if (a.lse && h == 0) a.lse[tok * a.heads + hq] = kv_lse(most, st.l[t]);
     }
   }
   if constexpr (FP8) {
-    if (__builtin_expect(__any(kv_nan_values(st)), 0)) {
+    if (__builtin_expect(again, 0)) {
 #pragma unroll
       for (int t = 0; t < QT; ++t)
         kv_nan_pass<D>(w0 + 16 * t + c16, 0, 1, st.m[t], st.far, st.l[t] == 0.0f ? 0.0f : st.e[t] / st.l[t],
