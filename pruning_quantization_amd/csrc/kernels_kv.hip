@@ -1018,7 +1018,7 @@ __global__ __launch_bounds__(256, BIG && D <= 128 ? 3 : 1) void k_kv_attn(KvAttn
 template <int D>
 struct KvPromptShape {
   // 16-row tiles of a wave, waves of a workgroup, waves per SIMD
-  static constexpr int QT = D == 64 ? 2 : 1, NW = D == 64 ? 4 : 8, WAVES = D == 128 ? 4 : 2;
+  static constexpr int QT = D == 64 ? 2 : 1, NW = D == 64 ? 4 : 8, WAVES = D == 128 ? 4 : D == 64 ? 3 : 2;
 };
 
 // BIG: blocks of 64 tokens and more, so a tile lies in one block (scalar addresses
