@@ -1017,14 +1017,16 @@ __global__ __launch_bounds__(256, BIG && D <= 128 ? 3 : 1) void k_kv_attn(KvAttn
 // 800 and 1072).
 template <int D>
 struct KvPromptShape {
-  // 16-row tiles of a wave, waves of a workgroup, waves per SIMD
-  static constexpr int QT = D == 64 ? 2 : 1, NW = D == 64 ? 4 : 8, WAVES = D == 128 ? 4 : D == 64 ? 3 : 2;
+  // 16-row tiles of a wave, waves of a workgroup, waves per SIMD (three with D = 64 in
+  // blocks of 64 and more: e4m3 410 us, with two 485; smaller blocks lose more by the
+  // registers that short chunks spill: a mixed batch 49.2 instead of 47.7)
+  static constexpr int QT = D == 64 ? 2 : 1, NW = D == 64 ? 4 : 8, WAVES = D == 128 ? 4 : 2;
 };
 
 // BIG: blocks of 64 tokens and more, so a tile lies in one block (scalar addresses
 // and scales).
 template <int D, bool FP8, bool BIG>
-__global__ __launch_bounds__(64 * KvPromptShape<D>::NW, KvPromptShape<D>::WAVES) void k_kv_prompt(KvAttnArgs p) {
+__global__ __launch_bounds__(64 * KvPromptShape<D>::NW, D == 64 && BIG ? 3 : KvPromptShape<D>::WAVES) void k_kv_prompt(KvAttnArgs p) {
   constexpr int QT = KvPromptShape<D>::QT, NJ = D / 32, NU = D / 16, KC = D / 16;
   constexpr int NT = 64 * KvPromptShape<D>::NW, C = kKvTile * KC, NQ = 2 * C / NT;  // 16-code chunks of K and V
   static_assert(C % 64 == 0 && 2 * C % NT == 0, "a wave loads K chunks or V chunks at a time");
