@@ -419,15 +419,14 @@ typedef struct {
  * both of one type.  The i-th of a sequence's n rows becomes position
  * seq_lens[b] - n + i.  Per touched block and head, with amax the largest
  * finite |element| that the block receives: cand = fp32(amax / qmax), 0 where
- * amax < 2^-64; the new scale s is cand where the block's first token
- * is among the new ones, else max(old scale, cand); new codes are
- * encode(fp32(x * fp32(1 / s))) (nearest even, saturating, so infinities become
- * +-qmax; NaN, and with s = 0 everything, as 0); where s
- * grew, the codes before the new ones become encode(fp32(code * fp32(old *
- * fp32(1 / s)))), otherwise they stay.  Codes behind the last new token stay
- * as they are.  Calling it again with the same arguments changes nothing.  A
- * block must receive tokens of one sequence only in a call (else its codes
- * and scale are unspecified, those of other blocks are not). */
+ * amax < 2^-64; the new scale s is cand where the block's first token is among
+ * the new ones, else max(old scale, cand); new codes are encode(fp32(x * fp32(1 /
+ * s))) (nearest even, saturating, so infinities become +-qmax; NaN, and with s =
+ * 0 everything, as 0); where s grew, the codes before the new ones become
+ * encode(fp32(code * fp32(old * fp32(1 / s)))), otherwise they stay.  Codes behind
+ * the last new token stay as they are.  Calling it again with the same arguments
+ * changes nothing.  A block must receive tokens of one sequence only in a call
+ * (else its codes and scale are unspecified, those of other blocks are not). */
 sparq24_status sparq24_kv_append(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs,
                                  const sparq24_tensor* k, const sparq24_tensor* v,
                                  hipStream_t stream);
@@ -442,13 +441,15 @@ sparq24_status sparq24_kv_append(const sparq24_kvcache* cache, const sparq24_kvs
  * and of these the last `window` ones where window > 0 (needs causal).
  * out [total][query heads][dim] in q's type (q itself may be it, where it is
  * laid out so); lse [total][query heads] fp32 (or NULL) receives log sum_t
- * exp(s_t).  A row that sees no token gets zeros and
- * -inf.  Rows of out and lse that belong to no sequence stay as they are.
+ * exp(s_t).  A row that sees no token gets zeros and -inf.  Rows of out and lse
+ * that belong to no sequence stay as they are.
  * What a row does not see (behind its position or its sequence, before its
  * window) does not reach it, whatever its bits; a visible e4m3 NaN code makes a
- * row NaN (of k) or its elements of that dim (of v).  scale: finite, > 0.  Block scales: 0, or 2^-80 to 2^126, in any mixture;
- * an infinite or NaN one makes the rows that see a token of its block NaN.
- * Arithmetic: codes and queries enter fp16 MFMAs exactly, the weights exp(s_t)
+ * row NaN (of k) or its elements of that dim (of v).  scale: finite, > 0.
+ * Block scales: 0, or 2^-80 to 2^126, in any mixture; an infinite or NaN one
+ * makes the rows that see a token of its block NaN.
+ * Arithmetic: codes enter fp16 MFMAs exactly, queries up to elements below 2^-27
+ * of their row's largest, which are rounded to 2^-38 of that; the weights exp(s_t)
  * are rounded to fp16 (2^-11), all sums, maxima and scores are fp32.
  * Workspace: partial results of sequences that are split along their tokens and
  * the work list of more than 128 sequences; none for at most 128 where

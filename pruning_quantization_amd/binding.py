@@ -715,7 +715,8 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: tor
     tokens of each sequence with the new ones included, so the new rows become
     its last positions; position p lives in block ``block_table[b, p // tokens]``
     (int32).  A block's scale grows when a new element exceeds it, and the
-    block's earlier codes are then coded again."""
+    block's earlier codes are then coded again.  Infinite elements saturate, NaN
+    is coded as 0; neither touches the block's scale."""
     (_serving_module or _serving()).kv_append(cache, k, v, block_table, seq_lens, cu_tokens)
 
 
@@ -733,7 +734,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     sequence's n queries sit at its last n positions.  ``causal``: a query sees
     the tokens up to its own; ``window`` > 0: the last ``window`` of these.
     ``scale`` defaults to dim ** -0.5.  A row that sees nothing gives zeros and
-    an lse of -inf."""
+    an lse of -inf.  ``out`` may be ``q``; ``workspace`` (bytes, any type) has to
+    hold what the call needs."""
     return (_serving_module or _serving()).kv_attention(
         q, cache, block_table, seq_lens, cu_tokens, scale, causal, window, return_lse, out, lse, workspace)
 

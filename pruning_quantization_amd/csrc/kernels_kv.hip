@@ -244,11 +244,12 @@ hipError_t launch_kv_append(const KvCache& c, const KvSeqs& q, const KvRows& k, 
 // largest score, since a token of small values counts in it as much as any; m and n
 // are whole numbers, so that 2^(m - n) is exact.  Where a V scale is 2^28 and more
 // below the one that set m, w could leave fp32's range (2^-126) with a p_t that
-// counts: there the sum comes from the scores themselves.  A query row is multiplied by a power
-// of two that puts its largest element at 2^13 (exact: fp16 then holds every
-// bf16 or fp16 element down to 2^-27 of it in full).  Scores, m, sums and O are
-// fp32; w is rounded to fp16 (relative 2^-11, below bf16's own rounding and
-// at fp16's).
+// counts: there the sum comes from the scores themselves.
+// A query row is multiplied by a power of two that puts its largest element at 2^13:
+// fp16 then holds every bf16 or fp16 element down to 2^-27 of it in full and rounds
+// smaller ones to 2^-38 of it, so a score is off by at most scale 2^-38 max |q| sum |K_t|.
+// Scores, m, sums and O are fp32; w is rounded to fp16 (relative 2^-11, below bf16's
+// own rounding and at fp16's).
 // ---------------------------------------------------------------------------
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -343,7 +344,7 @@ __device__ inline int64_t uniform(int64_t v) {
 // Holds a value that is the same in all lanes in a scalar register.  The compiler knows
 // that it is, but may move such arithmetic into vector registers all the same,
 // here behind the divisions of kv_item: that cost the prompt kernel 20 registers,
-// reloaded in its loop (a prompt of 8192 tokens: 930 us instead of 662).
+// reloaded in its loop (a prompt of 8192 tokens took 1.4 times as long).
 __device__ inline int scalar(int v) {
   v = uniform(v);
   asm("" : "+s"(v));
@@ -376,7 +377,8 @@ __device__ inline int64_t units_of(const KvWork& k, int len) {
 // follows from its number; up to kScanned sequences every workgroup adds up what
 // comes before it, in two rounds of loads; more have been added up by k_kv_plan
 // (one new token each, with offsets: 128 sequences of 300 31.4 us, by k_kv_plan 35.2;
-// 256 of 512 59.9 and 61.9).
+// 256 of 512 59.9 and 61.9, so the two meet somewhat above; from there on the sums of
+// every workgroup grow with the square of the sequences).
 constexpr int kScanned = 128;
 __device__ inline bool kv_item(const KvAttnArgs& w, int64_t id, int lane, KvItem& it) {
   const int H = w.a.c.heads;
@@ -572,8 +574,8 @@ __device__ inline void kv_sum_reference(const f32x4v (&sc)[QT][4], const float (
 // (where `edge`: a mask or a bad scale), the rows' references, sums (fp32: a token of a small V scale can
 // have a weight that fp16 does not hold and still be most of the sum) and the
 // rescaling of O.  (Taking the weights first and forming the maxima only where
-// one passed 2^15 costs more than it saves as soon as scores spread: 847 against
-// 690 us for 8192 tokens, the maxima of 16 rows grow in most tiles.)
+// one passed 2^15 costs more than it saves as soon as scores spread: 8192 tokens took
+// 1.23 times as long, the maxima of 16 rows grow in most tiles.)
 template <int QT, int NU>
 __device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], const KvScales& k, int tok0,
                                   bool edge, KvState<QT, NU>& st, f16x8_t (&pf)[QT][2]) {
@@ -826,9 +828,9 @@ __device__ inline __attribute__((always_inline)) void kv_nan_pass(int r, int fir
 // Few rows per kv head (decoding): one tile of 16 rows, four waves that take the
 // chunk's tiles in turn, K and V straight from memory into MFMA operands.  Bound by
 // the cache's bytes: 64 sequences of 300..16384 tokens, 32 heads over 8 of 128, in
-// 211 us (5.2 TB/s), 4096 of 100 in 360 (half of their last blocks is empty).
-// Three waves per SIMD there: two hold everything in registers and read long
-// sequences a little faster (214 and 221 us with the join), short ones slower (466).
+// 208 us (5.3 TB/s; vector instructions take a third of the cycles), 4096 of 100 in
+// 345 (half of their last blocks is empty).  Three waves per SIMD there: with two,
+// short sequences took 1.3 times as long.
 // BIG: blocks of 64 tokens and more, so a tile lies in one block (scalar addresses
 // and scales).
 template <int D, bool FP8, bool BIG>
@@ -1005,16 +1007,18 @@ __global__ __launch_bounds__(256, BIG && D <= 128 ? 3 : 1) void k_kv_attn(KvAttn
 // 16-byte chunks XOR-swizzled by row), one tile ahead of its use, its codes loaded
 // one tile ahead of that.  Bound by the matrix and vector units in turn: per tile,
 // 16 rows and head of 128 a wave issues 32 MFMAs (512 cycles of its SIMD's matrix
-// unit) and about 200 vector instructions (softmax, widening), and several waves per
-// SIMD overlap the one's products with the other's softmax.  A causal prompt of
-// 8192 tokens, 32 heads over 8: 650 us (845 Tflop/s; such MFMAs alone reach 1985).
+// unit) and 184 other vector instructions (softmax, widening), and several waves per
+// SIMD overlap the one's products with the other's softmax: by the counters the
+// matrix units are busy for 33% of the cycles, vector instructions (the MFMAs' issue
+// among them) take 62%.  A causal prompt of 8192 tokens, 32 heads over 8: 655 us (839 Tflop/s; such MFMAs alone
+// reach 1985).
 //
 // Shapes, 128 rows a workgroup each: as many waves as the registers of D allow, but
 // for D = 64, whose products are short next to the reads of a tile, two row tiles a
 // wave.  8192 tokens by themselves, 32 heads over 8 (16 over 8 above 128), int8 in
-// blocks of 64: D = 64 476 us (one row tile, four waves per SIMD: 545), 128 686
-// (two row tiles, two waves: 722), 192 642 and 256 698 (two row tiles, one wave:
-// 800 and 1072).
+// blocks of 64: D = 64 478 us (one row tile, four waves per SIMD: 1.15 times that), 128
+// 703 (two row tiles, two waves: 1.05), 192 635 and 256 703 (two row tiles, one wave:
+// 1.25 and 1.54).
 template <int D>
 struct KvPromptShape {
   // 16-row tiles of a wave, waves of a workgroup, waves per SIMD (three with D = 64 in
