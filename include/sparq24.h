@@ -447,7 +447,8 @@ sparq24_status sparq24_kv_append(const sparq24_kvcache* cache, const sparq24_kvs
  * window) does not reach it, whatever its bits; a visible e4m3 NaN code makes a
  * row NaN (of k) or its elements of that dim (of v).  scale: finite, > 0.
  * Block scales: 0, or 2^-80 to 2^126, in any mixture; an infinite or NaN one
- * makes the rows that see a token of its block NaN.
+ * makes the rows that see a token of its block NaN, an infinite or NaN query
+ * element its row.
  * Arithmetic: codes enter fp16 MFMAs exactly, queries up to elements below 2^-27
  * of their row's largest, which are rounded to 2^-38 of that; the weights exp(s_t)
  * are rounded to fp16 (2^-11), all sums, maxima and scores are fp32.

@@ -482,8 +482,10 @@ __device__ inline KvRow kv_query(const KvAttnArgs& p, const KvItem& it, int r, f
     for (int e = 0; e < 8; ++e) am = __builtin_fmaxf(am, __builtin_fabsf(at(j, e)));
   am = groups_max(am);
   int ex = (int)(__float_as_uint(am) >> 23);  // 0: zero or subnormal, 255: inf
-  ex = ex < 64 ? 64 : (ex > 254 ? 127 : ex);
-  const float up = __uint_as_float((uint32_t)(127 + 13 - (ex - 127)) << 23);
+  // an infinite element makes every score infinite or NaN, and the softmax NaN
+  const bool inf = ex > 254;
+  ex = ex < 64 ? 64 : (inf ? 127 : ex);
+  const float up = inf ? __builtin_nanf("") : __uint_as_float((uint32_t)(127 + 13 - (ex - 127)) << 23);
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
 #pragma unroll

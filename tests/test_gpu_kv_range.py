@@ -181,3 +181,40 @@ def test_an_empty_workspace():
         with pytest.raises(S.Sparq24Error, match="workspace"):
             S.kv_attention(q, p_wide.dev(), *p_wide.args(), out=out, workspace=empty)
         assert (out == 7).all()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("n", [1, 30])
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+def test_infinite_queries(fmt, n, wide):
+    # every score is infinite or NaN: a row that sees a token is NaN whatever the signs, one that sees none gives
+    # zeros, others are as they were
+    p = Pool(n, [70, 70, 0], 1, 64, 16, fmt, wide=wide)
+    p.ref[0][..., 3] = 1 if fmt == "int8" else 0x38          # keys of one sign along a dim
+    q, _ = stored(p.rng.standard_normal((3, n, 4, 64)), "bf16")
+    want, want_lse = S.kv_attention(q, p.dev(), *p.args(), return_lse=True)
+    q[0, 0, 0, 3], q[0, 0, 1, 3], q[1, n - 1, 2, 9], q[2, 0, 0, 3] = -np.inf, np.inf, np.inf, -np.inf
+    out, lse = S.kv_attention(q, p.dev(), *p.args(), return_lse=True)
+    for b, i, h in ((0, 0, 0), (0, 0, 1), (1, n - 1, 2)):
+        assert out[b, i, h].isnan().all() and lse[b, i, h].isnan()
+        out[b, i, h], lse[b, i, h] = want[b, i, h], want_lse[b, i, h]
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert not out[2].any() and torch.isneginf(lse[2]).all()
+
+
+def test_thousands_of_sequences():
+    # more than the work list's workgroup has threads: each adds up several sequences
+    rng = np.random.default_rng(3)
+    count = 2500
+    lens = [int(x) for x in rng.integers(0, 40, count)]
+    news = [min(n, int(x)) for n, x in zip(lens, rng.integers(0, 3, count))]
+    for b, n, w in ((0, 1500, 1), (1024, 1300, 2), (1301, 60, 30), (2499, 2000, 1)):
+        lens[b], news[b] = n, w
+    p = Pool(4, lens, 1, 64, 16, "int8")
+    cu, dcu = offsets(news)
+    q, q64 = stored(rng.standard_normal((cu[-1], 2, 64)), "bf16")
+    out, lse = S.kv_attention(q, p.dev(), *p.args(), cu_tokens=dcu, return_lse=True)
+    check_attention(out, lse, p.ref, p.table, lens, cu, q64, "int8", 0.125, 2.0 ** -8, bits=4)
+    q, q64 = stored(rng.standard_normal((count, 1, 2, 64)), "bf16")
+    out, lse = S.kv_attention(q, p.dev(), *p.args(), return_lse=True)
+    check_attention(out, lse, p.ref, p.table, lens, np.arange(count + 1), q64[:, 0], "int8", 0.125, 2.0 ** -8, bits=4)
