@@ -241,8 +241,10 @@ hipError_t launch_kv_append(const KvCache& c, const KvSeqs& q, const KvRows& k, 
 // + log2 vs - m) feeds the second product, and the sum of p_t is the sum of
 // w / vs, so neither scale costs an instruction per score and w stays in
 // fp16's range whatever the scales are.  The sum is kept over 2^n, n near the
-// largest score, since a token of small values counts in it as much as any; m and n
-// are whole numbers, so that 2^(m - n) is exact.  Where a V scale is 2^28 and more
+// largest score, since a token of small values counts in it as much as any; m - n is
+// a whole number, so that 2^(m - n) is exact.  (Were m itself one, the largest weight
+// would not be 2^8 and lose by its rounding to fp16: errors of peaked rows 2^-12 more.)
+// Where a V scale is 2^28 and more
 // below the one that set m, w could leave fp32's range (2^-126) with a p_t that
 // counts: there the sum comes from the scores themselves.
 // A query row is multiplied by a power of two that puts its largest element at 2^13:
@@ -545,9 +547,9 @@ __device__ inline void kv_sum_reference(const f32x4v (&sc)[QT][4], const float (
   bool apart = false;
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    const float best = __builtin_floorf(groups_max(mx[t] * ck[t]));
-    const float d = log2_exact(was[t]) + up[t];      // m - n
-    float nd = __builtin_fminf(d, st.m[t] - best);  // NaN (both infinite): as it was
+    const float best = groups_max(mx[t] * ck[t]);
+    const float d = log2_exact(was[t]) + up[t];                       // m - n
+    float nd = __builtin_fminf(d, __builtin_rintf(st.m[t] - best));  // NaN (both infinite): as it was
     nd = __builtin_amdgcn_fmed3f(nd, -126.0f, 126.0f);
     if (st.m[t] != kNegInf) {
       st.l[t] *= __builtin_amdgcn_exp2f(nd - d);
@@ -626,11 +628,13 @@ __device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], c
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       const bool g = top[t] - st.m[t] > kTopMost;
-      float nm = __builtin_floorf(top[t]) - kTopSet;
+      float nm = top[t] - kTopSet;
       nm = top[t] - nm > kTopMost ? top[t] : nm;  // where scores have steps of 16, top - 8 may round to top - 16
-      up[t] = g ? nm - st.m[t] : 0.0f;
+      const float by = g ? nm - st.m[t] : 0.0f;
+      up[t] = __builtin_rintf(by);
       was[t] = st.e[t];
-      const float al = __builtin_amdgcn_exp2f(-up[t]);
+      const float al = __builtin_amdgcn_exp2f(-by);
+      st.l[t] *= by < __builtin_inff() ? __builtin_amdgcn_exp2f(up[t] - by) : 1.0f;  // n has m's fraction
       st.m[t] = g ? nm : st.m[t];
       st.e[t] = __builtin_amdgcn_ldexpf(st.e[t], (int)up[t]);  // infinite at the first reference
       st.far |= uniform((int)__any(__builtin_fabsf(st.m[t]) > kFarTop && st.m[t] != kNegInf));

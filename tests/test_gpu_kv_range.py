@@ -218,3 +218,19 @@ def test_thousands_of_sequences():
     q, q64 = stored(rng.standard_normal((count, 1, 2, 64)), "bf16")
     out, lse = S.kv_attention(q, p.dev(), *p.args(), return_lse=True)
     check_attention(out, lse, p.ref, p.table, lens, np.arange(count + 1), q64[:, 0], "int8", 0.125, 2.0 ** -8, bits=4)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+def test_the_largest_weight_is_exact(fmt, wide, n):
+    # a row's largest weight is a power of two in fp16, so a softmax that one token has gives its value to the
+    # output's own rounding: fp16's half step, and the exponent's 2^(4 - 22) in the sum, twice
+    p = Pool(n, [1, 1, 1, 1], 4, 64, 16, fmt, wide=wide)
+    q, _ = stored(p.rng.standard_normal((4, n, 32, 64)), "f16")
+    out = S.kv_attention(q, p.dev(), *p.args(), causal=False).cpu().double().numpy()
+    for b in range(4):
+        blk = p.table[b, 0]
+        v = V.kv_decode(p.ref[2][blk, :, :, 0], fmt) * p.ref[3][blk].astype(np.float64)[:, None]
+        want = np.repeat(v, 8, 0)
+        assert (np.abs(out[b] - want) <= np.abs(want) * (2.0 ** -11 + 2.0 ** -17) + 2.0 ** -25).all()
