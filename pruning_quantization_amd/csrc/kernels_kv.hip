@@ -244,9 +244,8 @@ hipError_t launch_kv_append(const KvCache& c, const KvSeqs& q, const KvRows& k, 
 // largest score, since a token of small values counts in it as much as any; m - n is
 // a whole number, so that 2^(m - n) is exact.  (Were m itself one, the largest weight
 // would not be 2^8 and lose by its rounding to fp16: errors of peaked rows 2^-12 more.)
-// Where a V scale is 2^28 and more
-// below the one that set m, w could leave fp32's range (2^-126) with a p_t that
-// counts: there the sum comes from the scores themselves.
+// Where a V scale is 2^28 and more below the one that set m, w could leave fp32's range
+// (2^-126) with a p_t that counts: there the sum comes from the scores themselves.
 // A query row is multiplied by a power of two that puts its largest element at 2^13:
 // fp16 then holds every bf16 or fp16 element down to 2^-27 of it in full and rounds
 // smaller ones to 2^-38 of it, so a score is off by at most scale 2^-38 max |q| sum |K_t|.
@@ -575,9 +574,9 @@ __device__ inline void kv_sum_reference(const f32x4v (&sc)[QT][4], const float (
 }
 
 // Scores of a tile (lane: QT rows, tokens tok0 .. tok0 + 15) to weights: masks
-// (where `edge`: a mask or a bad scale), the rows' references, sums (fp32: a token of a small V scale can
-// have a weight that fp16 does not hold and still be most of the sum) and the
-// rescaling of O.  (Taking the weights first and forming the maxima only where
+// (where `edge`: a mask or a bad scale), the rows' references, sums (fp32: a token of a
+// small V scale can have a weight that fp16 does not hold and still be most of the
+// sum) and the rescaling of O.  (Taking the weights first and forming the maxima only where
 // one passed 2^15 costs more than it saves as soon as scores spread: 8192 tokens took
 // 1.23 times as long, the maxima of 16 rows grow in most tiles.)
 template <int QT, int NU>
@@ -1016,8 +1015,8 @@ __global__ __launch_bounds__(256, BIG && D <= 128 ? 3 : 1) void k_kv_attn(KvAttn
 // unit) and 184 other vector instructions (softmax, widening), and several waves per
 // SIMD overlap the one's products with the other's softmax: by the counters the
 // matrix units are busy for 33% of the cycles, vector instructions (the MFMAs' issue
-// among them) take 62%.  A causal prompt of 8192 tokens, 32 heads over 8: 655 us (839 Tflop/s; such MFMAs alone
-// reach 1985).
+// among them) take 62%.  A causal prompt of 8192 tokens, 32 heads over 8: 655 us (839
+// Tflop/s; such MFMAs alone reach 1985).
 //
 // Shapes, 128 rows a workgroup each: as many waves as the registers of D allow, but
 // for D = 64, whose products are short next to the reads of a tile, two row tiles a
@@ -1036,7 +1035,8 @@ struct KvPromptShape {
 // BIG: blocks of 64 tokens and more, so a tile lies in one block (scalar addresses
 // and scales).
 template <int D, bool FP8, bool BIG>
-__global__ __launch_bounds__(64 * KvPromptShape<D>::NW, D == 64 && BIG ? 3 : KvPromptShape<D>::WAVES) void k_kv_prompt(KvAttnArgs p) {
+__global__ __launch_bounds__(64 * KvPromptShape<D>::NW, D == 64 && BIG ? 3 : KvPromptShape<D>::WAVES)
+    void k_kv_prompt(KvAttnArgs p) {
   constexpr int QT = KvPromptShape<D>::QT, NJ = D / 32, NU = D / 16, KC = D / 16;
   constexpr int NT = 64 * KvPromptShape<D>::NW, C = kKvTile * KC, NQ = 2 * C / NT;  // 16-code chunks of K and V
   static_assert(C % 64 == 0 && 2 * C % NT == 0, "a wave loads K chunks or V chunks at a time");
