@@ -282,7 +282,7 @@ def _mx(x):
     a = y.abs()
     # nearest value, ties to the even code
     code = ((a > 0.25).to(torch.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5)
-            + (a >= 3.5) + (a > 5.0) + 8 * torch.signbit(y))
+            + (a >= 3.5) + (a > 5.0) + 8 * torch.signbit(y).to(torch.uint8))
     return code[..., 0::2] | (code[..., 1::2] << 4), (e + 127).to(torch.uint8)
 
 
