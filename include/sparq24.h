@@ -380,6 +380,49 @@ sparq24_status sparq24_int8_gemm(const int8_t* a, int64_t lda, const float* scal
                                  int64_t k, const float* bias, int32_t c_dtype, void* c,
                                  int64_t ldc, void* ws, size_t* ws_bytes, hipStream_t stream);
 
+/* The dense MXFP4 side's GEMM [PD §3: MXFP4, one power of two per 32 elements]:
+ * c [M][N] = sum_g 2^(scale_a[m][g] + scale_b[n][g] - 254) sum_{k in g} a[m][k]
+ * b[n][k] (+ bias[n]) over the groups g of 32 elements along K, with a [M][K/2]
+ * and b [N][K/2] the codes and scale_a [M][K/32], scale_b [N][K/32] the E8M0
+ * bytes of sparq24_quantize (MXFP4).  gfx950's v_mfma_scale_f32_16x16x128_f8f6f4
+ * takes both as they are: products are exact, sums fp32 (of a group and of all,
+ * in a fixed order that depends on M, N and K), then the bias add (fp32 [N], or
+ * NULL) and one rounding to c_dtype (sparq24_dtype).  A group whose scale byte is
+ * 255 (E8M0's NaN) makes its row of a (its column of c, for b) NaN, also where
+ * its codes are zeros.  lda and ldb are the bytes between rows of codes (a
+ * multiple of 16 where there is more than one row, at least K/2), ldc the
+ * elements between rows of c (at least N); scales are dense, at any byte.  a, b,
+ * c 16-byte aligned, bias 4-byte.  K % 32 == 0 and K <= SPARQ24_MAX_MXFP4_K
+ * (SHAPE); K == 0 gives the bias or zeros.  Any M and N.  Workspace protocol as
+ * above. */
+#define SPARQ24_MAX_MXFP4_K 131072
+sparq24_status sparq24_mxfp4_gemm(const uint8_t* a, int64_t lda, const uint8_t* scale_a, int64_t m,
+                                  const uint8_t* b, int64_t ldb, const uint8_t* scale_b, int64_t n,
+                                  int64_t k, const float* bias, int32_t c_dtype, void* c,
+                                  int64_t ldc, void* ws, size_t* ws_bytes, hipStream_t stream);
+
+/* Root-mean-square norm with the residual's addition, quantized for the next
+ * product [PD §2: the quantized side pays its online quantization]: one read of
+ * x and residual, one write of each output.  Per row of K elements:
+ *   h = x, or with a residual the sum fp32(x + residual) rounded to their type,
+ *       which is what `sum` receives and what the norm is taken of;
+ *   r = fp32(1 / sqrt(mean + eps)), mean = sum h^2 / K, all fp64 (0 where mean +
+ *       eps is 0);
+ *   y = fp32(fp32(h * r) * w), not rounded to h's type;
+ * then the row y is quantized as sparq24_quantize does (fp32 input): q INT (2..8
+ * bits) or FP8: codes [B][R][K], scales fp32 [B][R]; MXFP4 (K % 32 == 0): codes
+ * [B][R][K/2], scales E8M0 [B][R][K/32].  A row with an element of h that is
+ * infinite or NaN gets zero codes and a NaN scale (bytes 255); so does a row (a
+ * group, with MXFP4) with a y that is.  weight: [K] of weight_dtype
+ * (sparq24_dtype: fp32, or x's type).  residual and sum: x's type and shape, any
+ * strides that x may have; both or neither (NULL).  sum may be residual or x
+ * itself (the same rows at the same places), not overlap them otherwise.
+ * eps: finite, >= 0.  K <= SPARQ24_MAX_ROW_K.  K-contiguous operands only. */
+sparq24_status sparq24_rmsnorm_quantize(const sparq24_tensor* x, const sparq24_tensor* residual,
+                                        const void* weight, int32_t weight_dtype, float eps,
+                                        const sparq24_qspec* q, void* codes, void* scales,
+                                        const sparq24_tensor* sum, hipStream_t stream);
+
 /* Paged 8-bit key/value cache: the quantized storage of attention's K and V
  * [PD §1, §2: K and V are operands produced online], one scale per block of
  * tokens and kv head.
@@ -460,6 +503,48 @@ sparq24_status sparq24_kv_attention(const sparq24_kvcache* cache, const sparq24_
                                     const sparq24_tensor* q, float scale, int32_t causal,
                                     int64_t window, void* out, float* lse, void* ws,
                                     size_t* ws_bytes, hipStream_t stream);
+
+/* Paged 4-bit key/value cache: MXFP4 along the head dim, so a token's codes
+ * depend on that token alone.
+ *   k and v: codes [blocks][heads][tokens][dim/2], the even dim in the low nibble;
+ *   k_scale and v_scale: E8M0 bytes [blocks][heads][dim/32][tokens], so that the
+ *   tokens of a group of dims lie side by side.
+ * tokens, dim and blocks as in sparq24_kvcache. */
+typedef struct {
+  uint8_t* k;
+  uint8_t* k_scale;
+  uint8_t* v;
+  uint8_t* v_scale;
+  int64_t blocks, heads, tokens, dim;
+} sparq24_kvcache_mxfp4;
+
+/* Appends token rows to a 4-bit cache: arguments, positions and refusals of
+ * sparq24_kv_append.  Per token, head and 32 dims the codes and the scale byte are
+ * those of sparq24_quantize (MXFP4) of the finite elements; infinite elements
+ * saturate, NaN is coded as 0.  Nothing else is written, so a block may receive
+ * tokens of several sequences in a call, as long as each position of it receives
+ * one. */
+sparq24_status sparq24_kv_append_mxfp4(const sparq24_kvcache_mxfp4* cache,
+                                       const sparq24_kvseqs* seqs, const sparq24_tensor* k,
+                                       const sparq24_tensor* v, hipStream_t stream);
+
+/* Attention of query rows over a 4-bit cache: arguments, masks, outputs, refusals
+ * and workspace protocol of sparq24_kv_attention, K_t and V_t the stored codes
+ * times their scales.  With bf16 queries a visible V scale above 2^96 may make its
+ * rows infinite or NaN; with fp16 queries K_t and V_t are rounded to fp16, and
+ * scales above 2^13 (which no fp16 element gives) count as 2^13.  A scale byte
+ * of 255 in K or V of a token makes the rows that see the token NaN; what a row
+ * does not see does not reach it, whatever its bits.  An infinite or NaN query
+ * element makes its row NaN; a score above fp32's range does, too, one below it
+ * counts as hidden.
+ * Arithmetic: K, V and queries enter the matrix units exactly in the queries'
+ * type; the weights exp(s_t) are rounded to it (2^-8 of the weight at most in bf16,
+ * 2^-11 in fp16), all sums, maxima and scores are fp32. */
+sparq24_status sparq24_kv_attention_mxfp4(const sparq24_kvcache_mxfp4* cache,
+                                          const sparq24_kvseqs* seqs, const sparq24_tensor* q,
+                                          float scale, int32_t causal, int64_t window, void* out,
+                                          float* lse, void* ws, size_t* ws_bytes,
+                                          hipStream_t stream);
 
 /* Wanda's input-channel norms [PD §2]: norms[k] = fp32(sqrt(sum over all
  * (b, r) of x[b][r][k]^2)), the sum in fp64 (fixed order), the square root in

@@ -22,6 +22,7 @@ from .binding import (  # noqa: F401
     kv_attention,
     kv_cache,
     lib,
+    mxfp4_gemm,
     operator_error,
     predict_R,
     predict_R_noalloc,
@@ -35,6 +36,7 @@ from .binding import (  # noqa: F401
     qspec,
     quantize,
     quantize_rot,
+    rmsnorm_quantize,
     sparse_gemm,
     version,
 )

@@ -56,6 +56,11 @@ class CKvCache(ctypes.Structure):
                 ("dim", c_int64)]
 
 
+class CKvCacheMx(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("k_scale", c_void_p), ("v", c_void_p), ("v_scale", c_void_p),
+                ("blocks", c_int64), ("heads", c_int64), ("tokens", c_int64), ("dim", c_int64)]
+
+
 class CKvSeqs(ctypes.Structure):
     _fields_ = [("block_table", c_void_p), ("max_blocks", c_int64), ("table_stride", c_int64),
                 ("seq_lens", c_void_p), ("cu_tokens", c_void_p), ("seqs", c_int64),
@@ -71,7 +76,8 @@ SYMBOLS = ("sparq24_prune_compress", "sparq24_quantize", "sparq24_prune_quantize
            "sparq24_sparse_gemm", "sparq24_dense_gemm", "sparq24_fp8_gemm",
            "sparq24_bits_per_element", "sparq24_status_string", "sparq24_version",
            "sparq24_predict_R_noalloc", "sparq24_int8_gemm", "sparq24_kv_append",
-           "sparq24_kv_attention")
+           "sparq24_kv_attention", "sparq24_mxfp4_gemm", "sparq24_rmsnorm_quantize",
+           "sparq24_kv_append_mxfp4", "sparq24_kv_attention_mxfp4")
 
 _lib = None
 
@@ -118,6 +124,14 @@ def lib(path: Optional[str] = None):
         "sparq24_kv_append": [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p],
         "sparq24_kv_attention": [c_void_p, c_void_p, c_void_p, c_float, c_int32, c_int64,
                                  c_void_p, c_void_p, c_void_p, POINTER(c_size_t), c_void_p],
+        "sparq24_mxfp4_gemm": [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                               c_int64, c_int64, c_void_p, c_int32, c_void_p, c_int64, c_void_p,
+                               POINTER(c_size_t), c_void_p],
+        "sparq24_rmsnorm_quantize": [c_void_p, c_void_p, c_void_p, c_int32, c_float, c_void_p,
+                                     c_void_p, c_void_p, c_void_p, c_void_p],
+        "sparq24_kv_append_mxfp4": [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p],
+        "sparq24_kv_attention_mxfp4": [c_void_p, c_void_p, c_void_p, c_float, c_int32, c_int64,
+                                       c_void_p, c_void_p, c_void_p, POINTER(c_size_t), c_void_p],
         "sparq24_quantize_rot": [T, c_int32, Q, c_void_p, c_void_p, c_void_p, c_void_p,
                                  POINTER(c_size_t), c_void_p],
         "sparq24_prune_quantize_rot": [T, c_int32, c_int32, Q, c_void_p, c_void_p, c_void_p,
@@ -664,7 +678,9 @@ def _serving():
             raise ImportError("pruning_quantization_amd/_marshal.so not loaded: build it with "
                               "`python -m pruning_quantization_amd.build`") from e
         _marshal.bind(*(ctypes.cast(f, c_void_p).value for f in (
-            L.sparq24_int8_gemm, L.sparq24_kv_append, L.sparq24_kv_attention)), Sparq24Error)
+            L.sparq24_int8_gemm, L.sparq24_kv_append, L.sparq24_kv_attention, L.sparq24_mxfp4_gemm,
+            L.sparq24_rmsnorm_quantize, L.sparq24_kv_append_mxfp4, L.sparq24_kv_attention_mxfp4)),
+            Sparq24Error)
         _serving_module = _marshal
     return _serving_module
 
@@ -681,10 +697,51 @@ def int8_gemm(codes_a: torch.Tensor, scale_a: torch.Tensor, codes_b: torch.Tenso
     return (_serving_module or _serving()).int8_gemm(codes_a, scale_a, codes_b, scale_b, bias, dtype, out)
 
 
+def mxfp4_gemm(codes_a: torch.Tensor, scale_a: torch.Tensor, codes_b: torch.Tensor,
+               scale_b: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               dtype: torch.dtype = torch.float32,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C = A B^T (+ bias) from the MXFP4 codes [..., K/2], [N, K/2] and E8M0
+    bytes [..., K/32], [N, K/32] of :func:`quantize`, exact products in fp32 sums
+    -> ``dtype`` (fp32, bf16 or fp16) [..., N].  K is a multiple of 32; the rows
+    of either operand's codes and of ``out`` may be strided; ``bias`` is fp32
+    [N].  A scale byte of 255 makes its row (column) NaN."""
+    return (_serving_module or _serving()).mxfp4_gemm(codes_a, scale_a, codes_b, scale_b, bias, dtype, out)
+
+
+_FORMATS = {"fp8": (Q_FP8, 0), "mxfp4": (Q_MXFP4, 0), ("int", 8): (Q_INT, 8)}
+
+
+def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, q: QLike, eps: float = 1e-6,
+                     residual: Optional[torch.Tensor] = None,
+                     residual_out: Optional[torch.Tensor] = None, out=None):
+    """Root-mean-square norm of ``x`` [..., K] over its last dim, times
+    ``weight`` [K] (fp32 or x's type), quantized: q ("int", 2..8) or "fp8" ->
+    (codes [..., K], scales fp32 [...]); "mxfp4" -> (codes [..., K/2], e8m0
+    [..., K/32]), as :func:`quantize` of the normed rows in fp32.
+
+    With ``residual`` (x's shape and type) the norm is taken of x + residual,
+    rounded to their type, which is also returned: (codes, scales, sum), in
+    ``residual_out`` where given, which may be ``residual`` or ``x``.  A row with an
+    element that is infinite or NaN gets zero codes and a NaN scale (byte 255).
+    ``out``: (codes, scales) to write to."""
+    f = _FORMATS.get(q) if type(q) in (str, tuple) else None
+    if f is None:
+        s = qspec(q)
+        f = (s.fmt, s.bits)
+    codes, scales = (None, None) if out is None else out
+    return (_serving_module or _serving()).rmsnorm_quantize(x, weight, f[0], f[1], eps, residual,
+                                                            residual_out, codes, scales)
+
+
 class KVCache(NamedTuple):
-    """Paged 8-bit key/value cache: ``k`` codes [blocks, kv heads, tokens, dim],
-    ``v`` codes [blocks, kv heads, dim, tokens] (int8, or e4m3 as uint8) and one
-    fp32 scale per block and kv head for each.  :func:`kv_cache` allocates one."""
+    """Paged key/value cache; :func:`kv_cache` allocates one.
+
+    8 bits: ``k`` codes [blocks, kv heads, tokens, dim], ``v`` codes [blocks, kv
+    heads, dim, tokens] (int8, or e4m3 as uint8) and one fp32 scale per block and
+    kv head for each.  4 bits (MXFP4; the scales' type says so): ``k`` and ``v``
+    codes uint8 [blocks, kv heads, tokens, dim / 2], scales uint8 [blocks, kv
+    heads, dim / 32, tokens]."""
 
     k: torch.Tensor
     k_scale: torch.Tensor
@@ -695,10 +752,13 @@ class KVCache(NamedTuple):
 def kv_cache(blocks: int, heads: int, dim: int, tokens: int = 64, q: QLike = ("int", 8),
              device: Union[str, torch.device] = "cuda") -> KVCache:
     """An empty cache pool of ``blocks`` blocks of ``tokens`` tokens (a power of
-    two, 16..256) in INT8 or FP8 (``q``: ("int", 8) or "fp8")."""
+    two, 16..256) in INT8, FP8 or MXFP4 (``q``: ("int", 8), "fp8" or "mxfp4")."""
     qs = qspec(q)
+    if qs.fmt == Q_MXFP4:
+        return KVCache(*(torch.zeros(blocks, heads, *s, dtype=torch.uint8, device=device)
+                         for s in ((tokens, dim // 2), (dim // 32, tokens)) * 2))
     if qs.fmt not in (Q_INT, Q_FP8) or (qs.fmt == Q_INT and qs.bits != 8):
-        raise ValueError("a cache holds ('int', 8) or 'fp8' codes")
+        raise ValueError("a cache holds ('int', 8), 'fp8' or 'mxfp4' codes")
     dt = torch.int8 if qs.fmt == Q_INT else torch.uint8
     return KVCache(torch.zeros(blocks, heads, tokens, dim, dtype=dt, device=device),
                    torch.zeros(blocks, heads, dtype=torch.float32, device=device),
@@ -715,8 +775,9 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: tor
     tokens of each sequence with the new ones included, so the new rows become
     its last positions; position p lives in block ``block_table[b, p // tokens]``
     (int32).  A block's scale grows when a new element exceeds it, and the
-    block's earlier codes are then coded again.  Infinite elements saturate, NaN
-    is coded as 0; neither touches the block's scale."""
+    block's earlier codes are then coded again (8 bits; in 4 bits a token's codes
+    are its own).  Infinite elements saturate, NaN is coded as 0; neither touches
+    the scale."""
     (_serving_module or _serving()).kv_append(cache, k, v, block_table, seq_lens, cu_tokens)
 
 

@@ -24,7 +24,7 @@ MARSHAL_LIB = os.path.join(PKG, "_marshal.so")
 
 SOURCES = ["api.cpp", "kernels_prune.hip", "kernels_quant.hip", "kernels_energy.hip",
            "kernels_misc.hip", "kernels_operr.hip", "kernels_spgemm.hip", "kernels_int8.hip",
-           "kernels_kv.hip"]
+           "kernels_kv.hip", "kernels_kv_split.hip", "kernels_kv4.hip", "kernels_mxfp4.hip", "kernels_norm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -805,13 +805,79 @@ sparq24_status sparq24_int8_gemm(const int8_t* a, int64_t lda, const float* scal
   return launched(launch_int8_gemm(g, stream));
 }
 
+sparq24_status sparq24_mxfp4_gemm(const uint8_t* a, int64_t lda, const uint8_t* scale_a, int64_t m,
+                                  const uint8_t* b, int64_t ldb, const uint8_t* scale_b, int64_t n,
+                                  int64_t k, const float* bias, int32_t c_dtype, void* c,
+                                  int64_t ldc, void* ws, size_t* ws_bytes, hipStream_t stream) {
+  if (m < 0 || n < 0 || k < 0) return SPARQ24_ERR_INVALID;
+  if (c_dtype != SPARQ24_F32 && c_dtype != SPARQ24_BF16 && c_dtype != SPARQ24_F16)
+    return SPARQ24_ERR_INVALID;
+  if (k % 32 || k > SPARQ24_MAX_MXFP4_K) return SPARQ24_ERR_SHAPE;
+  if (k == 0) lda = ldb = 0;  // no code is read
+  if (m > INT32_MAX || n > INT32_MAX) return SPARQ24_ERR_UNSUPPORTED;
+  if ((m > 1 && lda < k / 2) || (n > 1 && ldb < k / 2) || (m > 1 && ldc < n))
+    return SPARQ24_ERR_UNSUPPORTED;
+  if ((m > 1 && lda % 16) || (n > 1 && ldb % 16)) return SPARQ24_ERR_ALIGN;
+  const Mxfp4Gemm g{a, b, m > 1 ? lda : k / 2, n > 1 ? ldb : k / 2, scale_a, scale_b, bias,
+                    m, n, k, c, m > 1 ? ldc : n, c_dtype};
+  bool query;
+  CHECK(workspace(ws, ws_bytes, 0, query));
+  if (query) return SPARQ24_OK;
+  if (m == 0 || n == 0) return SPARQ24_OK;
+  if (((m + 15) / 16) * ((n + 15) / 16) > INT32_MAX) return SPARQ24_ERR_UNSUPPORTED;
+  if ((k && (!a || !b || !scale_a || !scale_b)) || !c) return SPARQ24_ERR_INVALID;
+  if (!aligned16(a) || !aligned16(b) || !aligned16(c) || ((uintptr_t)bias & 3u))
+    return SPARQ24_ERR_ALIGN;
+  CHECK(device_ok());
+  return launched(launch_mxfp4_gemm(g, stream));
+}
+
+sparq24_status sparq24_rmsnorm_quantize(const sparq24_tensor* x, const sparq24_tensor* residual,
+                                        const void* weight, int32_t weight_dtype, float eps,
+                                        const sparq24_qspec* q, void* codes, void* scales,
+                                        const sparq24_tensor* sum, hipStream_t stream) {
+  RowDesc d[3];
+  const sparq24_tensor* t[3] = {x, residual, sum};
+  if (!residual != !sum) return SPARQ24_ERR_INVALID;
+  RmsNorm n{};
+  NormRows* rows[3] = {&n.x, &n.res, &n.sum};
+  for (int i = 0; i < (residual ? 3 : 1); ++i) {
+    CHECK(check_tensor(t[i], false, d[i]));
+    if (t[i]->dtype != x->dtype) return SPARQ24_ERR_UNSUPPORTED;
+    if (t[i]->batch != x->batch || t[i]->rows != x->rows || t[i]->k != x->k) return SPARQ24_ERR_SHAPE;
+    *rows[i] = NormRows{(char*)d[i].x, d[i].R, d[i].bs, d[i].rs};
+  }
+  if (weight_dtype < SPARQ24_F32 || weight_dtype > SPARQ24_F16) return SPARQ24_ERR_INVALID;
+  if (weight_dtype != SPARQ24_F32 && weight_dtype != x->dtype) return SPARQ24_ERR_UNSUPPORTED;
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return SPARQ24_ERR_INVALID;
+  CHECK(check_q(q, (1u << SPARQ24_Q_INT) | (1u << SPARQ24_Q_FP8_E4M3) | (1u << SPARQ24_Q_MXFP4),
+                n.cfmt, n.qmax));
+  if (n.cfmt == CF_INT16) return SPARQ24_ERR_UNSUPPORTED;
+  if (n.cfmt == CF_MX && x->k % 32) return SPARQ24_ERR_SHAPE;
+  if (x->k > SPARQ24_MAX_ROW_K) return SPARQ24_ERR_SHAPE;
+  n.rows = x->batch * x->rows;
+  if (n.rows > INT32_MAX) return SPARQ24_ERR_UNSUPPORTED;
+  if (n.rows * x->k == 0) return SPARQ24_OK;
+  if (!weight || !codes || !scales) return SPARQ24_ERR_INVALID;
+  if (!aligned16(weight) || !aligned16(codes) || !aligned16(scales)) return SPARQ24_ERR_ALIGN;
+  n.w = weight;
+  n.dtype = x->dtype;
+  n.wdtype = weight_dtype;
+  n.nunits = x->k / 8;
+  n.eps = eps;
+  n.codes = (char*)codes;
+  n.scales = scales;
+  CHECK(device_ok());
+  return launched(launch_rmsnorm_quantize(n, stream));
+}
+
+}  // extern "C"
+
 namespace {
-// Cache and sequences of the kv calls.  empty: no token rows, nothing to do.
-sparq24_status check_kv(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs, KvCache& c,
-                        KvSeqs& q, bool& empty) {
-  if (!cache || !seqs) return SPARQ24_ERR_INVALID;
-  if (cache->fmt < SPARQ24_Q_NONE || cache->fmt > SPARQ24_Q_NVFP4) return SPARQ24_ERR_INVALID;
-  if (cache->fmt != SPARQ24_Q_INT && cache->fmt != SPARQ24_Q_FP8_E4M3) return SPARQ24_ERR_UNSUPPORTED;
+// Sequences of the kv calls and the cache's shape.  empty: no token rows, nothing to do.
+template <class Cache>
+sparq24_status check_kv_shape(const Cache* cache, const sparq24_kvseqs* seqs, KvCache& c,
+                              KvSeqs& q, bool& empty) {
   if (cache->blocks < 0 || cache->heads < 0 || seqs->seqs < 0 || seqs->total < 0 ||
       seqs->max_blocks < 0 || seqs->table_stride < 0)
     return SPARQ24_ERR_INVALID;
@@ -825,9 +891,13 @@ sparq24_status check_kv(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs
   if (seqs->seqs > 1 && seqs->table_stride < seqs->max_blocks) return SPARQ24_ERR_UNSUPPORTED;
   if (!seqs->cu_tokens && seqs->seqs && seqs->total % seqs->seqs) return SPARQ24_ERR_SHAPE;
   empty = seqs->seqs == 0 || seqs->total == 0;
-  c = KvCache{(uint8_t*)cache->k, cache->k_scale, (uint8_t*)cache->v, cache->v_scale,
-              cache->blocks, (int)cache->heads, (int)D, __builtin_ctz((unsigned)T),
-              cache->fmt == SPARQ24_Q_FP8_E4M3};
+  c = KvCache{};
+  c.k = (uint8_t*)cache->k;
+  c.v = (uint8_t*)cache->v;
+  c.blocks = cache->blocks;
+  c.heads = (int)cache->heads;
+  c.dim = (int)D;
+  c.tsh = __builtin_ctz((unsigned)T);
   const int64_t cap = seqs->max_blocks * T;
   const int64_t most = INT32_MAX - 255;  // positions and tile ends are 32-bit in the kernels
   q = KvSeqs{seqs->block_table, seqs->table_stride, cap < most ? cap : most,
@@ -837,10 +907,31 @@ sparq24_status check_kv(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs
   return SPARQ24_OK;
 }
 
+sparq24_status check_kv(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs, KvCache& c,
+                        KvSeqs& q, bool& empty) {
+  if (!cache || !seqs) return SPARQ24_ERR_INVALID;
+  if (cache->fmt < SPARQ24_Q_NONE || cache->fmt > SPARQ24_Q_NVFP4) return SPARQ24_ERR_INVALID;
+  if (cache->fmt != SPARQ24_Q_INT && cache->fmt != SPARQ24_Q_FP8_E4M3) return SPARQ24_ERR_UNSUPPORTED;
+  CHECK(check_kv_shape(cache, seqs, c, q, empty));
+  c.ks = cache->k_scale;
+  c.vs = cache->v_scale;
+  c.fp8 = cache->fmt == SPARQ24_Q_FP8_E4M3;
+  return SPARQ24_OK;
+}
+sparq24_status check_kv(const sparq24_kvcache_mxfp4* cache, const sparq24_kvseqs* seqs, KvCache& c,
+                        KvSeqs& q, bool& empty) {
+  if (!cache || !seqs) return SPARQ24_ERR_INVALID;
+  CHECK(check_kv_shape(cache, seqs, c, q, empty));
+  c.ke = cache->k_scale;
+  c.ve = cache->v_scale;
+  return SPARQ24_OK;
+}
+
 sparq24_status check_kv_pointers(const KvCache& c, const KvSeqs& q) {
-  if (!c.k || !c.ks || !c.v || !c.vs || !q.lens || (q.cap && !q.table)) return SPARQ24_ERR_INVALID;
+  const bool bits8 = c.ks && c.vs, bits4 = c.ke && c.ve;
+  if (!c.k || !c.v || !(bits8 || bits4) || !q.lens || (q.cap && !q.table)) return SPARQ24_ERR_INVALID;
   if (!aligned16(c.k) || !aligned16(c.v) || ((uintptr_t)c.ks & 3u) || ((uintptr_t)c.vs & 3u) ||
-      ((uintptr_t)q.lens & 3u) || ((uintptr_t)q.table & 3u) || ((uintptr_t)q.cu & 3u))
+      !aligned16(c.ke) || !aligned16(c.ve) || ((uintptr_t)q.lens & 3u) || ((uintptr_t)q.table & 3u) || ((uintptr_t)q.cu & 3u))
     return SPARQ24_ERR_ALIGN;
   return SPARQ24_OK;
 }
@@ -861,11 +952,12 @@ sparq24_status check_kv_rows(const sparq24_tensor* x, int64_t total, int64_t dim
   if (ts % 16 || hs % 16) return SPARQ24_ERR_ALIGN;
   return SPARQ24_OK;
 }
-}  // namespace
-
-sparq24_status sparq24_kv_append(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs,
-                                 const sparq24_tensor* k, const sparq24_tensor* v,
-                                 hipStream_t stream) {
+// The calls on a cache of either kind, which differ in the check of the cache
+// and the launcher.
+template <class Cache, class Fits, class Launch>
+sparq24_status kv_append_any(const Cache* cache, const sparq24_kvseqs* seqs,
+                             const sparq24_tensor* k, const sparq24_tensor* v, hipStream_t stream,
+                             Fits fits, Launch launch) {
   KvCache c;
   KvSeqs q;
   bool empty;
@@ -876,20 +968,21 @@ sparq24_status sparq24_kv_append(const sparq24_kvcache* cache, const sparq24_kvs
   if (k->rows != c.heads || v->rows != c.heads) return SPARQ24_ERR_SHAPE;
   if (k->dtype != v->dtype) return SPARQ24_ERR_UNSUPPORTED;
   if (empty) return SPARQ24_OK;
-  if (!kv_append_fits(c, q)) return SPARQ24_ERR_UNSUPPORTED;
+  if (!fits(c, q)) return SPARQ24_ERR_UNSUPPORTED;
   CHECK(check_kv_pointers(c, q));
   if (!k->data || !v->data) return SPARQ24_ERR_INVALID;
   if (!aligned16(k->data) || !aligned16(v->data)) return SPARQ24_ERR_ALIGN;
   kr.x = (const char*)k->data;
   vr.x = (const char*)v->data;
   CHECK(device_ok());
-  return launched(launch_kv_append(c, q, kr, vr, k->dtype, stream));
+  return launched(launch(c, q, kr, vr, k->dtype, stream));
 }
 
-sparq24_status sparq24_kv_attention(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs,
-                                    const sparq24_tensor* q, float scale, int32_t causal,
-                                    int64_t window, void* out, float* lse, void* ws,
-                                    size_t* ws_bytes, hipStream_t stream) {
+template <class Cache, class Fits, class Size, class Launch>
+sparq24_status kv_attention_any(const Cache* cache, const sparq24_kvseqs* seqs,
+                                const sparq24_tensor* q, float scale, int32_t causal,
+                                int64_t window, void* out, float* lse, void* ws, size_t* ws_bytes,
+                                hipStream_t stream, Fits fits, Size size, Launch launch) {
   KvAttn a;
   bool empty;
   CHECK(check_kv(cache, seqs, a.c, a.q, empty));
@@ -909,15 +1002,47 @@ sparq24_status sparq24_kv_attention(const sparq24_kvcache* cache, const sparq24_
   a.window = window > INT32_MAX ? INT32_MAX : (int)window;
   a.out = (char*)out;
   a.lse = lse;
-  if (!empty && !kv_attn_fits(a)) return SPARQ24_ERR_UNSUPPORTED;
+  if (!empty && !fits(a)) return SPARQ24_ERR_UNSUPPORTED;
   bool query;
-  CHECK(workspace(ws, ws_bytes, empty ? 0 : kv_attn_workspace(a), query));
+  CHECK(workspace(ws, ws_bytes, empty ? 0 : size(a), query));
   if (query || empty) return SPARQ24_OK;
   CHECK(check_kv_pointers(a.c, a.q));
   if (!a.x || !a.out) return SPARQ24_ERR_INVALID;
   if (!aligned16(a.x) || !aligned16(a.out) || ((uintptr_t)lse & 3u)) return SPARQ24_ERR_ALIGN;
   CHECK(device_ok());
-  return launched(launch_kv_attn(a, ws, stream));
+  return launched(launch(a, ws, stream));
+}
+}  // namespace
+
+extern "C" {
+
+sparq24_status sparq24_kv_append(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs,
+                                 const sparq24_tensor* k, const sparq24_tensor* v,
+                                 hipStream_t stream) {
+  return kv_append_any(cache, seqs, k, v, stream, kv_append_fits, launch_kv_append);
+}
+
+sparq24_status sparq24_kv_append_mxfp4(const sparq24_kvcache_mxfp4* cache,
+                                       const sparq24_kvseqs* seqs, const sparq24_tensor* k,
+                                       const sparq24_tensor* v, hipStream_t stream) {
+  return kv_append_any(cache, seqs, k, v, stream, kv4_append_fits, launch_kv4_append);
+}
+
+sparq24_status sparq24_kv_attention(const sparq24_kvcache* cache, const sparq24_kvseqs* seqs,
+                                    const sparq24_tensor* q, float scale, int32_t causal,
+                                    int64_t window, void* out, float* lse, void* ws,
+                                    size_t* ws_bytes, hipStream_t stream) {
+  return kv_attention_any(cache, seqs, q, scale, causal, window, out, lse, ws, ws_bytes, stream,
+                          kv_attn_fits, kv_attn_workspace, launch_kv_attn);
+}
+
+sparq24_status sparq24_kv_attention_mxfp4(const sparq24_kvcache_mxfp4* cache,
+                                          const sparq24_kvseqs* seqs, const sparq24_tensor* q,
+                                          float scale, int32_t causal, int64_t window, void* out,
+                                          float* lse, void* ws, size_t* ws_bytes,
+                                          hipStream_t stream) {
+  return kv_attention_any(cache, seqs, q, scale, causal, window, out, lse, ws, ws_bytes, stream,
+                          kv4_attn_fits, kv4_attn_workspace, launch_kv4_attn);
 }
 
 sparq24_status sparq24_col_l2norm(const sparq24_tensor* x, float* norms, void* ws,

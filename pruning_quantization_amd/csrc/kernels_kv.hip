@@ -1,7 +1,6 @@
 // Paged 8-bit key/value cache: append of new token rows, and attention of
 // query rows over the cached tokens.  Layout and conventions: kv_common.hpp.
-#include "dispatch.hpp"
-#include "kv_common.hpp"
+#include "kv_split.hpp"
 
 namespace sparq24 {
 
@@ -197,7 +196,6 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvCache c, KvSeqs q, KvRow
 }
 
 namespace {
-constexpr int64_t kMostThreads = UINT32_MAX;  // of a grid, along x
 int64_t append_blocks(const KvCache& c, const KvSeqs& q) {
   return q.cu ? (q.total >> c.tsh) + 2 * q.seqs : q.seqs * q.slots;
 }
@@ -252,12 +250,6 @@ hipError_t launch_kv_append(const KvCache& c, const KvSeqs& q, const KvRows& k, 
 // Scores, m, sums and O are fp32; w is rounded to fp16 (relative 2^-11, below bf16's
 // own rounding and at fp16's).
 // ---------------------------------------------------------------------------
-typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x4v __attribute__((ext_vector_type(4)));
-typedef float f32x2v __attribute__((ext_vector_type(2)));
-typedef unsigned u32x4v __attribute__((ext_vector_type(4)));
-
 // Eight codes (two dwords) as fp16, exactly.
 template <bool FP8>
 __device__ inline f16x8_t widen8(uint32_t a, uint32_t b) {
@@ -279,8 +271,6 @@ __device__ inline f16x8_t widen8(uint32_t a, uint32_t b) {
   return f16x8_t{r[0].x, r[0].y, r[1].x, r[1].y, r[2].x, r[2].y, r[3].x, r[3].y};
 }
 
-constexpr int kKvTile = 64;
-constexpr int kFewRows = 16;       // most rows per kv head of the few-rows kernel
 constexpr float kTopSet = 8.0f;    // a new reference puts the largest w at 2^8 ...
 constexpr float kTopMost = 15.0f;  // ... and stands until one would pass 2^15
 // One fma from score to exponent rounds m, not the exponent: the same factor for
@@ -291,166 +281,6 @@ constexpr float kFarTop = 65536.0f;
 // Most that a weight is multiplied by for the sum: so a p_t passes 2^n by 2^35 at most,
 // and one that is lost (w < 2^-126) is below 2^-106 of it.
 constexpr float kMostFactor = 0x1p20f;
-constexpr float kNegInf = -__builtin_inff();
-
-// Work of one launch: item = ((sequence, chunk, row tile), kv head).
-struct KvAttnArgs {
-  KvAttn a;
-  int g;            // query heads per kv head
-  int rb;           // rows (token, head of the group) per row tile
-  int above, most;  // sequences with more than `above` and at most `most` rows
-  int64_t target;   // items that the launch aims at
-  int64_t items;    // items that it has room for
-  int cmin;         // least tiles of a chunk
-  int* starts;      // [seqs + 2] or null: first unit of each sequence, all units, len (k_kv_plan)
-  int* plan;        // [seqs][2]: first item / kv heads, chunks
-  float* ml;        // [items][rb][2]: reference n and sum of a split row tile
-  float* po;        // [items][rb][D]: its output by itself
-};
-
-// Sequences of at most so many tiles stay whole: a second launch that joins chunks costs
-// more (one new token on 600: 11.9 and 13.8 us, on 1024: 13.6 and 13.9).
-constexpr int kWholeTiles = 16;
-constexpr int kNever = 1 << 26;  // tiles of a chunk that nothing reaches
-
-struct KvWork {
-  int rows, rt, lo, tiles;  // rows, row tiles, first tile, tiles of the visible range
-};
-// First position that a query at pos sees (window 0: all).
-__device__ inline int first_seen(int pos, int window) {
-  return window && pos >= window ? pos - window + 1 : 0;
-}
-__device__ inline KvWork kv_work(const KvAttnArgs& w, const SeqRows& r) {
-  KvWork k;
-  k.rows = r.n * w.g;
-  if (k.rows <= w.above || k.rows > w.most) {
-    k.rows = k.rt = k.lo = k.tiles = 0;
-    return k;
-  }
-  k.rt = (k.rows + w.rb - 1) / w.rb;
-  const int hi = (int)(r.len < w.a.q.cap ? r.len : w.a.q.cap);
-  const int lo = first_seen(r.len - r.n, w.a.window);
-  k.lo = lo / kKvTile;
-  k.tiles = hi > lo ? (hi + kKvTile - 1) / kKvTile - k.lo : 0;
-  return k;
-}
-
-// Values that are the same in every lane, for scalar registers and branches.
-__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ inline int64_t uniform(int64_t v) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
-  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 | lo);
-}
-
-// Holds a value that is the same in all lanes in a scalar register.  The compiler knows
-// that it is, but may move such arithmetic into vector registers all the same,
-// here behind the divisions of kv_item: that cost the prompt kernel 20 registers,
-// reloaded in its loop (a prompt of 8192 tokens took 1.4 times as long).
-__device__ inline int scalar(int v) {
-  v = uniform(v);
-  asm("" : "+s"(v));
-  return v;
-}
-
-struct KvItem {
-  SeqRows r;
-  KvWork k;
-  int64_t slot;
-  int seq, chunk, chunks, len, rt, head;  // len: tiles of a chunk
-};
-// Tiles of a chunk: all tiles of all row tiles over the items aimed at.
-__device__ inline int chunk_tiles(const KvAttnArgs& w, int64_t all) {
-  int64_t len = (all * w.a.c.heads + w.target - 1) / w.target;
-  len = len < w.cmin ? w.cmin : (len + 3) / 4 * 4;  // four waves share a chunk
-  return (int)(len < kNever ? len : kNever);
-}
-__device__ inline int64_t tiles_of(const KvWork& k) {  // bounded, so that no sum leaves 64 bits
-  const int64_t c = (int64_t)k.rt * k.tiles;
-  return c < (1ll << 36) ? c : 1ll << 36;
-}
-__device__ inline int64_t units_of(const KvWork& k, int len) {
-  const int64_t ch = ((int64_t)k.tiles + len - 1) / len, n = k.rt * (ch > 1 ? ch : 1);
-  return n < kMostUnits ? n : kMostUnits;
-}
-
-// A unit is a chunk of a row tile of a sequence, an item a unit and a kv head.  Where
-// every sequence has as many units (same row counts, no chunks) a unit's place
-// follows from its number; up to kScanned sequences every workgroup adds up what
-// comes before it, in two rounds of loads; more have been added up by k_kv_plan
-// (one new token each, with offsets: 128 sequences of 300 31.4 us, by k_kv_plan 35.2;
-// 256 of 512 59.9 and 61.9, so the two meet somewhat above; from there on the sums of
-// every workgroup grow with the square of the sequences).
-constexpr int kScanned = 128;
-__device__ inline bool kv_item(const KvAttnArgs& w, int64_t id, int lane, KvItem& it) {
-  const int H = w.a.c.heads;
-  const int64_t seqs = w.a.q.seqs, unit = id / H;
-  int at;
-  if (w.starts) {
-    if (unit >= w.starts[seqs]) return false;
-    it.len = uniform(w.starts[seqs + 1]);
-    it.seq = last_reached((int)seqs, lane, [&](int b) { return w.starts[b] <= unit; });
-    at = (int)unit - w.starts[it.seq];
-  } else if (!w.a.q.cu && w.cmin == kNever) {
-    const int rt = (int)((w.a.q.nper * w.g + w.rb - 1) / w.rb);
-    it.len = kNever;
-    it.seq = (int)(unit / rt);
-    at = (int)(unit % rt);
-    if (it.seq >= seqs) return false;
-  } else {
-    it.len = w.cmin;
-    if (w.cmin < kNever) {
-      int64_t all = 0;
-      for (int64_t b0 = 0; b0 < seqs; b0 += 64) {
-        const int64_t b = b0 + lane;
-        const int64_t c = b < seqs ? tiles_of(kv_work(w, seq_rows(w.a.q, b))) : 0;
-        // 64 sums of 2^36 in two halves of 32 bits
-        all += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan_sum((uint32_t)c & 0xFFFFF), 63) +
-               ((int64_t)(uint32_t)__builtin_amdgcn_readlane((int)wave_scan_sum((uint32_t)(c >> 20)), 63) << 20);
-      }
-      it.len = uniform(chunk_tiles(w, all));
-    }
-    if (!find_sequence(seqs, unit, lane, it.seq, at,
-                       [&](int64_t b) { return units_of(kv_work(w, seq_rows(w.a.q, b)), it.len); }))
-      return false;
-  }
-  it.r = seq_rows(w.a.q, it.seq);
-  it.r.first = uniform(it.r.first);
-  it.r.n = uniform(it.r.n);
-  it.r.len = uniform(it.r.len);
-  it.k = kv_work(w, it.r);
-  it.chunks = (it.k.tiles + it.len - 1) / it.len;
-  if (it.chunks < 1) it.chunks = 1;
-  it.chunk = scalar(at / it.k.rt);
-  it.rt = scalar(it.k.rt - 1 - at % it.k.rt);  // the last rows see the most: first
-  it.head = scalar((int)(id % H));
-  it.slot = id;
-  if (w.plan && at == 0 && it.head == 0 && threadIdx.x == 0) {
-    w.plan[2 * it.seq] = (int)unit;
-    w.plan[2 * it.seq + 1] = it.chunks;
-  }
-  return true;
-}
-
-__device__ inline void kv_store_out(const KvAttn& a, int64_t o, float v) {
-  if (a.dtype == 1) ((__bf16*)a.out)[o] = (__bf16)v;
-  else ((_Float16*)a.out)[o] = (_Float16)v;
-}
-
-// Over the four lane groups (lanes l ^ 16, l ^ 32), in every lane.
-__device__ inline float groups_max(float v) {
-  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  float m;
-  asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(r[0]), "v"(r[1]));
-  r = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
-  asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(r[0]), "v"(r[1]));
-  return m;
-}
-__device__ inline float groups_sum(float v) {
-  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
 
 // Query row r of the row tile (column c of the MFMA tiles), in fp16 times a power
 // of two: elements d(j) .. d(j) + 7 of lane group h into qf[j].
@@ -676,33 +506,6 @@ __device__ inline void kv_weights(f32x4v (&sc)[QT][4], const KvRow (&row)[QT], c
       }
     st.l[t] = __builtin_fmaf(sum, f[t], st.l[t]);
   }
-}
-
-__device__ inline float kv_lse(float top, float sum) {
-  return sum == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
-}
-
-// Tiles and limits of a row tile within its chunk.
-struct KvRange {
-  int t0, t1;       // tiles
-  int lo, hi;       // tokens that some row sees
-  int least, from;  // tokens from .. least - 1 are seen by every row
-};
-__device__ inline KvRange kv_range(const KvAttnArgs& p, const KvItem& it, int r0, int r1) {
-  const KvAttn& a = p.a;
-  const int pos0 = it.r.len - it.r.n, i0 = r0 / p.g, i1 = (r1 - 1) / p.g;
-  const int hi_all = (int)(it.r.len < a.q.cap ? it.r.len : a.q.cap);
-  KvRange k;
-  k.hi = a.causal && pos0 + i1 + 1 < hi_all ? pos0 + i1 + 1 : hi_all;
-  k.lo = first_seen(pos0 + i0, a.window);
-  k.least = a.causal && pos0 + i0 + 1 < k.hi ? pos0 + i0 + 1 : k.hi;
-  k.from = first_seen(pos0 + i1, a.window);
-  k.t0 = it.k.lo + it.chunk * it.len;
-  k.t1 = k.t0 + it.len;
-  if (k.t1 > it.k.lo + it.k.tiles) k.t1 = it.k.lo + it.k.tiles;
-  if (k.t0 < k.lo / kKvTile) k.t0 = k.lo / kKvTile;
-  if (k.t1 > (k.hi + kKvTile - 1) / kKvTile) k.t1 = (k.hi + kKvTile - 1) / kKvTile;
-  return {scalar(k.t0), scalar(k.t1), scalar(k.lo), scalar(k.hi), scalar(k.least), scalar(k.from)};
 }
 
 // e4m3 only.  A V code can be NaN, and 0 * NaN carries it to rows that do not see it.
@@ -1259,129 +1062,6 @@ __global__ __launch_bounds__(64 * KvPromptShape<D>::NW, D == 64 && BIG ? 3 : KvP
   }
 }
 
-// First units of more than kScanned sequences, a workgroup for each kernel: that each
-// of their workgroups added them up took it a round of loads per 64 sequences, twice
-// (4096 sequences of 100 tokens, one new each, with offsets: 2264 us, so 551).
-__global__ __launch_bounds__(1024) void k_kv_plan(KvAttnArgs few, KvAttnArgs many) {
-  const KvAttnArgs& w = blockIdx.x ? many : few;
-  if (!w.starts) return;
-  __shared__ int64_t part[1024];
-  const int tid = threadIdx.x;
-  const int64_t seqs = w.a.q.seqs, per = (seqs + 1023) / 1024;
-  const int64_t b0 = tid * per < seqs ? tid * per : seqs, b1 = b0 + per < seqs ? b0 + per : seqs;
-  auto scan = [&](int64_t v) {  // inclusive, over the workgroup
-    part[tid] = v;
-    for (int o = 1; o < 1024; o <<= 1) {
-      __syncthreads();
-      const int64_t u = tid >= o ? part[tid - o] : 0;
-      __syncthreads();
-      part[tid] += u;
-    }
-    __syncthreads();
-    return part[tid];
-  };
-  int len = w.cmin;
-  if (w.cmin < kNever) {
-    int64_t c = 0;
-#pragma unroll 4
-    for (int64_t b = b0; b < b1; ++b) c += tiles_of(kv_work(w, seq_rows(w.a.q, b)));
-    scan(c);
-    len = chunk_tiles(w, part[1023]);
-    __syncthreads();  // part is read before it is used again
-  }
-  int64_t n = 0;
-#pragma unroll 4
-  for (int64_t b = b0; b < b1; ++b) n += units_of(kv_work(w, seq_rows(w.a.q, b)), len);
-  int64_t at = scan(n) - n;
-  for (int64_t b = b0; b < b1; ++b) {
-    w.starts[b] = (int)(at < INT32_MAX ? at : INT32_MAX);
-    at += units_of(kv_work(w, seq_rows(w.a.q, b)), len);
-  }
-  if (tid == 1023) {
-    w.starts[seqs] = (int)(at < INT32_MAX ? at : INT32_MAX);
-    w.starts[seqs + 1] = len;
-  }
-}
-
-// Joins the chunks of split sequences.  Few rows (W = 4), and so long chains of
-// chunks: a workgroup per (token, query head), the chunks dealt to its four waves,
-// whose sums meet in wave order.  Many (W = 0): 16 lanes per row, so that one round
-// of waves holds them all (17500 rows of 64: 7.2 us, with a wave per row 14.6).
-template <int D, int W>
-__global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many) {
-  constexpr int L = W == 4 ? 64 : 16, V = D / L, F = W == 4 ? V : 4;  // lanes of a row, elements of a lane, in runs of F
-  const KvAttn& a = few.a;
-  const int tid = threadIdx.x, wv = W == 4 ? uniform(tid >> 6) : 0, l = tid & (L - 1);
-  const int64_t id = W == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 16 + (tid >> 4);
-  if (W != 4 && id >= a.q.total * a.heads) return;
-  const int64_t tok = id / a.heads;
-  const int hq = (int)(id % a.heads);
-  int64_t seq = 0;
-  if (a.q.cu) {  // last sequence that begins at or before the token
-    int64_t lo = 0, hi = a.q.seqs;
-    while (hi - lo > 1) {
-      const int64_t mid = (lo + hi) / 2;
-      if (a.q.cu[mid] <= tok) lo = mid;
-      else hi = mid;
-    }
-    seq = lo;
-  } else {
-    seq = tok / a.q.nper;
-  }
-  const SeqRows r = seq_rows(a.q, seq);
-  if (tok < r.first || tok >= (int64_t)r.first + r.n) return;  // in no sequence
-  const KvAttnArgs& p = r.n * few.g <= few.most ? few : many;
-  const int chunks = p.plan[2 * seq + 1];
-  if (chunks < 2) return;
-  const int row = (int)(tok - r.first) * p.g + hq % p.g;
-  const int nrt = (r.n * p.g + p.rb - 1) / p.rb, rt = row / p.rb, rr = row % p.rb;
-  const int head = hq / p.g;
-  const int64_t first = p.plan[2 * seq];
-  // offsets that do not ascend can ask for more items than there is room for
-  if (first < 0 || (first + (int64_t)chunks * nrt) * a.c.heads > p.items) return;
-  const int64_t at0 = ((first + nrt - 1 - rt) * a.c.heads + head) * p.rb + rr;
-  const int64_t step = (int64_t)nrt * a.c.heads * p.rb;
-  // the common reference: the largest sum's own exponent, so that no chunk's weight passes 2
-  float top = kNegInf;
-  for (int c = l; c < chunks; c += L) {
-    const f32x2v ml = *(const f32x2v*)(p.ml + (at0 + c * step) * 2);
-    top = __builtin_fmaxf(top, ml[0] + (float)((int)(__float_as_uint(ml[1]) >> 23) - 127));
-  }
-#pragma unroll
-  for (int x = 1; x < L; x <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, x, 64));
-  float sum = 0.0f, v[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) v[e] = 0.0f;
-  auto at = [&](int e) { return F * L * (e / F) + F * l + e % F; };
-  if (top != kNegInf) {
-#pragma unroll 4
-    for (int c = wv; c < chunks; c += W == 4 ? 4 : 1) {
-      const int64_t s = at0 + c * step;
-      const f32x2v ml = *(const f32x2v*)(p.ml + s * 2);
-      const float f = ml[1] * __builtin_amdgcn_exp2f(ml[0] - top);
-      sum += f;
-#pragma unroll
-      for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(p.po[s * D + at(e)], f, v[e]);
-    }
-  }
-  if constexpr (W == 4) {
-    __shared__ float part[4][D], sums[4];
-#pragma unroll
-    for (int e = 0; e < V; ++e) part[wv][at(e)] = v[e];
-    if (l == 0) sums[wv] = sum;
-    __syncthreads();
-    sum = sums[0] + sums[1] + sums[2] + sums[3];
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    for (int d = tid; d < D; d += 256)
-      kv_store_out(a, id * D + d, (part[0][d] + part[1][d] + part[2][d] + part[3][d]) * inv);
-  } else {
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int e = 0; e < V; ++e) kv_store_out(a, id * D + at(e), v[e] * inv);
-  }
-  if (a.lse && wv == 0 && l == 0) a.lse[id] = kv_lse(top, sum);
-}
-
 namespace {
 // Row shapes of the prompt kernel by head dim (KvPromptShape).
 template <int D>
@@ -1390,95 +1070,19 @@ int prompt_rows(int dim) {
   return dim == 64 ? kPromptRows<64> : dim == 128 ? kPromptRows<128> : dim == 192 ? kPromptRows<192> : kPromptRows<256>;
 }
 
-struct KvPlan {
-  KvAttnArgs few, many;
-  bool run_few, run_many, split, planned;
-  size_t need;
-};
-
-// Which kernels run, their row tiles and the room for split results, from what
-// the host knows (shapes; lengths and offsets stay on the device).  Sequences of
-// at most 16 rows per kv head (query tokens times heads of the group) go to the
-// few-rows kernel, the others to the prompt kernel; without offsets all have the
-// same count, with offsets both may be needed.  16 sequences of 4096 tokens, 4 kv
-// heads of 128: 32 rows 32 us in the prompt kernel, 60 in the other with two row
-// tiles a wave; 64 rows 39, and 108 with four.
-KvPlan kv_plan(const KvAttn& a, char* ws) {
-  KvPlan p;
-  const int g = a.heads / a.c.heads;
-  const int64_t H = a.c.heads, rows = a.q.nper * g, cus = device_cu_count();
-  p.run_few = a.q.cu || rows <= kFewRows;
-  p.run_many = a.q.cu ? a.q.total * g > kFewRows : rows > kFewRows;
-  const int64_t tiles = (a.q.cap + kKvTile - 1) / kKvTile;
-  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  size_t off = up((size_t)a.q.seqs * 8);
-  p.split = p.planned = false;
-  auto lay = [&](KvAttnArgs& w, bool run, int rb, int above, int most, int cmin, int64_t target, int64_t rt) {
-    w.a = a;
-    w.g = g;
-    w.rb = rb;
-    w.above = above;
-    w.most = most;
-    w.target = target;
-    const bool split = run && tiles > kWholeTiles && (most == kFewRows || rt * H < target);
-    w.cmin = split ? cmin : kNever;
-    w.items = rt * H;
-    w.plan = (int*)ws;
-    w.starts = nullptr;
-    if (run && a.q.seqs > kScanned && (a.q.cu || split)) {
-      w.starts = (int*)(ws + off);
-      off += up((size_t)(a.q.seqs + 2) * 4);
-      p.planned = true;
-    }
-    if (split) {
-      const int64_t all = rt * H * ((tiles + cmin - 1) / cmin);
-      w.items = all < target + rt * H ? all : target + rt * H;
-      w.ml = (float*)(ws + off);
-      off += up((size_t)w.items * rb * 8);
-      w.po = (float*)(ws + off);
-      off += up((size_t)w.items * rb * a.c.dim * 4);
-      p.split = true;
-    } else {
-      w.ml = w.po = nullptr;
-    }
-  };
-  const int rbf = kFewRows, rbm = prompt_rows(a.c.dim);
-  int64_t rtf = a.q.seqs * ((rows + rbf - 1) / rbf), rtm = a.q.seqs * ((rows + rbm - 1) / rbm);
-  if (a.q.cu) {  // n rows make at most n / rb + 1 tiles
-    rtf = a.q.total * g / rbf + a.q.seqs;
-    const int64_t most = a.q.seqs * ((kFewRows + rbf - 1) / rbf), longer = a.q.total * g / kFewRows;
-    if (rtf > most) rtf = most;
-    rtm = a.q.total * g / rbm + (longer < a.q.seqs ? longer : a.q.seqs);
-  }
-  // chunks even out ragged lengths, but the join walks them: at most 64 of a
-  // sequence and head, at most eight items per CU (64 sequences of 300..16384
-  // tokens: 248 / 227 / 219 us at two / four / eight; one of 131071: 61 / 65 / 80)
-  int64_t aim = 64 * a.q.seqs * H;
-  aim = aim < 2 * cus ? 2 * cus : (aim > 8 * cus ? 8 * cus : aim);
-  // a chunk has one tile a wave at least, and four where unsplit sequences fill the
-  // card twice (64 sequences of 1024: 26 and 48 us with one; 8 of 2048: 21 and 17)
-  lay(p.few, p.run_few, rbf, 0, kFewRows, rtf * H >= 2 * cus ? 16 : 4, aim, rtf);
-  lay(p.many, p.run_many, rbm, kFewRows, INT32_MAX, 4, (a.c.dim <= 128 ? 2 : 1) * cus, rtm);
-  p.need = p.split || p.planned ? off : 0;
-  if (!p.split) p.few.plan = p.many.plan = nullptr;
-  return p;
-}
 }  // namespace
 
 bool kv_attn_fits(const KvAttn& a) {
-  const KvPlan p = kv_plan(a, nullptr);
-  const int64_t prompt = a.c.dim == 64 ? 64 * KvPromptShape<64>::NW : 64 * KvPromptShape<128>::NW;
-  return (!p.run_few || p.few.items <= kMostThreads / 256) && (!p.run_many || p.many.items <= kMostThreads / prompt) &&
-         (!p.split || a.q.total * a.heads <= kMostThreads / 16);
+  return kv_plan_fits(a, kv_plan(a, nullptr, prompt_rows(a.c.dim)),
+                      a.c.dim == 64 ? 64 * KvPromptShape<64>::NW : 64 * KvPromptShape<128>::NW);
 }
 
-size_t kv_attn_workspace(const KvAttn& a) { return kv_plan(a, nullptr).need; }
+size_t kv_attn_workspace(const KvAttn& a) { return kv_plan(a, nullptr, prompt_rows(a.c.dim)).need; }
 
 hipError_t launch_kv_attn(const KvAttn& a, void* ws, hipStream_t s) {
-  const KvPlan p = kv_plan(a, (char*)ws);
+  const KvPlan p = kv_plan(a, (char*)ws, prompt_rows(a.c.dim));
   if (p.planned) {
-    hipLaunchKernelGGL(k_kv_plan, dim3(2), dim3(1024), 0, s, p.few, p.many);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_kv_starts(p, s);
     if (e != hipSuccess) return e;
   }
   auto dim = [&]<int D>() {
@@ -1496,15 +1100,7 @@ hipError_t launch_kv_attn(const KvAttn& a, void* ws, hipStream_t s) {
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    if (p.split) {
-      const int64_t rows = a.q.total * a.heads;
-      if (rows <= 16 * device_cu_count())
-        hipLaunchKernelGGL((k_kv_join<D, 4>), dim3((unsigned)rows), dim3(256), 0, s, p.few, p.many);
-      else
-        hipLaunchKernelGGL((k_kv_join<D, 0>), dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, s, p.few, p.many);
-      return hipGetLastError();
-    }
-    return hipSuccess;
+    return p.split ? launch_kv_join(p, s) : hipSuccess;
   };
   switch (a.c.dim) {
     case 64: return dim.template operator()<64>();

@@ -1,0 +1,553 @@
+// Paged 4-bit key/value cache (MXFP4 along the head dim): append of new token rows,
+// and attention of query rows over the cached tokens.  Layout: kv_common.hpp.
+#include "kv_split.hpp"
+
+namespace sparq24 {
+
+// ---------------------------------------------------------------------------
+// Append.  A wave takes whole tokens, a lane 8 dims of one head at a time, four lanes
+// a group of 32 dims: amax over its finite elements, the exponent byte of
+// mx_exponent, E2M1 codes.  A token's codes depend on it alone, so nothing is read
+// back from the cache.
+// ---------------------------------------------------------------------------
+template <class DT>
+__global__ __launch_bounds__(kBlock) void k_kv4_append(KvCache c, KvSeqs q, KvRows kr, KvRows vr, int tokens) {
+  const int lane = threadIdx.x & 63;
+  const int64_t wave = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
+  const int64_t tok0 = wave * tokens;
+  if (tok0 >= q.total) return;
+  const int upr = c.dim / 8, units = c.heads * upr;  // of a token
+  const int all = (int)((q.total - tok0 < tokens ? q.total - tok0 : tokens) * units);
+  const int b0 = q.cu ? last_reached((int)q.seqs, lane, [&](int i) { return q.cu[i] <= tok0; }) : 0;
+  for (int i0 = 0; i0 < all; i0 += 64) {
+    const int i = i0 + lane, at = i < all ? i : 0;
+    const int64_t tok = tok0 + at / units;
+    const int unit = at % units, head = unit / upr, u = unit % upr;
+    int64_t b = b0;
+    if (q.cu) {
+      while (b + 1 < q.seqs && q.cu[b + 1] <= tok) ++b;
+    } else {
+      b = tok / q.nper;
+    }
+    const SeqRows r = seq_rows(q, b);
+    const int64_t pos = (int64_t)r.len - r.n + (tok - r.first);
+    const bool mine = i < all && tok >= r.first && tok < (int64_t)r.first + r.n && pos >= 0 && pos < q.cap;
+    const int64_t blk = mine ? q.table[b * q.table_stride + (pos >> c.tsh)] : -1;
+    const int T = 1 << c.tsh, o = (int)(pos & (T - 1));
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const KvRows& rows = side ? vr : kr;
+      Unit<DT> x;
+      load_unit(x, rows.x + tok * rows.ts + head * rows.hs + u * (8 * DT::ESIZE));
+      uint32_t am = 0;
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = x.f(e);
+        const uint32_t a = __float_as_uint(y[e]) & 0x7FFFFFFFu;
+        am = a < 0x7F800000u && a > am ? a : am;
+      }
+      uint32_t w = xor_lane32<1>(am);
+      am = am > w ? am : w;
+      w = xor_lane32<2>(am);
+      am = am > w ? am : w;
+      const int ex = mx_exponent(am);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)  // (8: above the largest code, for infinities)
+        y[e] = y[e] == y[e] ? __builtin_amdgcn_fmed3f(__builtin_ldexpf(y[e], -ex), -8.0f, 8.0f) : 0.0f;
+      const uint32_t pk = enc_e2m1_x8(y);
+      if (blk >= 0 && blk < c.blocks) {
+        const int64_t at = blk * c.heads + head;
+        *(uint32_t*)((side ? c.v : c.k) + (at * T + o) * (c.dim / 2) + 4 * u) = pk;
+        if ((u & 3) == 0) (side ? c.ve : c.ke)[(at * (c.dim / 32) + (u >> 2)) * T + o] = (uint8_t)(ex + 127);
+      }
+    }
+  }
+}
+
+namespace {
+// Tokens of a wave: so many that its lanes are busy.
+int append_tokens(const KvCache& c) {
+  const int units = c.heads * (c.dim / 8);
+  return units >= 64 ? 1 : 64 / units;
+}
+int64_t append_groups(const KvCache& c, const KvSeqs& q) {
+  const int64_t per = (kBlock / 64) * append_tokens(c);
+  return (q.total + per - 1) / per;
+}
+}  // namespace
+
+bool kv4_append_fits(const KvCache& c, const KvSeqs& q) {
+  return append_groups(c, q) <= kMostThreads / kBlock && (int64_t)c.heads * c.dim <= INT32_MAX / 64;
+}
+
+hipError_t launch_kv4_append(const KvCache& c, const KvSeqs& q, const KvRows& k, const KvRows& v,
+                             int dtype, hipStream_t s) {
+  return with_dtype(dtype, [&]<class DT>() {
+    hipLaunchKernelGGL((k_kv4_append<DT>), dim3((unsigned)append_groups(c, q)), dim3(kBlock), 0, s, c, q, k, v,
+                       append_tokens(c));
+    return hipGetLastError();
+  });
+}
+
+// ---------------------------------------------------------------------------
+// Attention.  For query row i of sequence b at position pos = len - n + i and kv head
+// j = h / g (g query heads per kv head), over the visible tokens t:
+//   s_t = scale * (q . K_t),  p_t = exp(s_t),  o = (sum_t p_t V_t) / (sum_t p_t).
+// Both products run on v_mfma_f32_16x16x32 in the queries' type (bf16 or fp16), which
+// the codes enter through v_cvt_scalef32_pk_*_fp4: two codes times their power of two
+// an instruction, exact in bf16 and, within its range, in fp16.  (The power's operand
+// counts by its exponent field alone, so an exponent byte is put there by one shift,
+// whatever lies around it.)  Transposed throughout:
+//   S^T [token][row] = K Q^T    lane: row c = lane % 16, tokens of lane group h = lane / 16
+//   O^T [dim][row]   = V^T P^T  lane: row c
+// A tile is 64 tokens; row 4 q + i of MFMA tile mt of K is token 16 q + 4 i + mt, so that
+// lane group h gets the scores of its 16 tokens 16 h + 4 i + mt in slots 4 mt + i, and a
+// lane's four K rows are adjacent tokens: their exponents are one dword.  V's operand
+// has the dims as rows: row c of tile u is dim 8 c + u of a span of 128 dims (4 c + u of
+// one of 64), so that a lane reads 8 (4) adjacent dims of its group's 16 tokens, whose
+// exponents are 16 adjacent bytes; pairs of tokens are put together by byte permutes.
+// Scores, maxima, sums and O are fp32; p_t is rounded to the queries' type.
+// ---------------------------------------------------------------------------
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
+
+constexpr float kTopSet4 = 8.0f;    // a new reference puts the largest weight at 2^8 ...
+constexpr float kTopMost4 = 15.0f;  // ... and stands until one would pass 2^15 (fp16's range)
+// One fma from score to exponent rounds the reference, not the exponent: the same factor
+// for every token, harmless until the rounding itself is large.  From here on every
+// tile takes the difference of the rounded terms, so that the largest stays in range.
+constexpr float kFarTop4 = 65536.0f;
+
+template <bool F16>
+struct Kv4Type {
+  // the largest exponent byte whose codes stay finite
+  static constexpr uint32_t kMost = F16 ? 140u : 252u;
+  // codes of byte B of w times the power whose exponent field is in s
+  template <int B>
+  static __device__ inline uint32_t widen(uint32_t w, uint32_t s) {
+    if constexpr (F16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, __uint_as_float(s), B));
+    else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, __uint_as_float(s), B));
+  }
+  static __device__ inline u32x4v widen8(uint32_t w, uint32_t s) {
+    return u32x4v{widen<0>(w, s), widen<1>(w, s), widen<2>(w, s), widen<3>(w, s)};
+  }
+  static __device__ inline f32x4v mfma(u32x4v a, u32x4v b, f32x4v c) {
+    if constexpr (F16)
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8v, a), __builtin_bit_cast(bf16x8v, b), c, 0, 0, 0);
+  }
+  static __device__ inline uint32_t pack(float x, float y) {
+    if constexpr (F16) return __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)x, (_Float16)y});
+    else return __builtin_bit_cast(uint32_t, bf16x2v{(__bf16)x, (__bf16)y});
+  }
+  static constexpr uint32_t kNan = F16 ? 0x7E007E00u : 0x7FC07FC0u;
+  static constexpr uint32_t kExp = F16 ? 0x7C00u : 0x7F80u;  // exponent field
+};
+
+// Exponent byte B of w in a float's exponent field.
+template <int B>
+__device__ inline uint32_t exponent_field(uint32_t w) {
+  if constexpr (B == 3) return w >> 1;
+  else return w << (23 - 8 * B);
+}
+
+// Exponent bytes of w: those above `most` become it; 255 (NaN) becomes `nan`.  bad
+// gets a bit per byte that was 255.
+__device__ inline uint32_t tame_exponents(uint32_t w, uint32_t most, uint32_t nan, uint32_t& bad) {
+  uint32_t r = 0;
+  bad = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = (w >> (8 * i)) & 0xFFu;
+    r |= (b == 255 ? nan : (b > most ? most : b)) << (8 * i);
+    bad |= (b == 255 ? 1u : 0u) << i;
+  }
+  return r;
+}
+
+// Query row r of the row tile (column c of the MFMA tiles): elements d(j) .. d(j) + 7 of
+// this lane into qf[j].  A row with an element that is no finite number is all NaN.
+struct Kv4Row {
+  int lim, low;  // last and first position seen (lim -1: no row)
+};
+template <bool F16, int NJ, class F>
+__device__ inline Kv4Row kv4_query(const KvAttnArgs& p, const KvItem& it, int r, u32x4v (&qf)[NJ], F&& d) {
+  const KvAttn& a = p.a;
+  const bool valid = r < it.k.rows;
+  const int i = valid ? r / p.g : 0, hq = valid ? it.head * p.g + r % p.g : 0;
+  const int pos = it.r.len - it.r.n + i;
+  const int hi_all = (int)(it.r.len < a.q.cap ? it.r.len : a.q.cap);
+  Kv4Row row;
+  row.lim = !valid ? -1 : (a.causal && pos + 1 < hi_all ? pos + 1 : hi_all) - 1;
+  row.low = first_seen(pos, a.window);
+  const char* x = a.x + (it.r.first + (int64_t)i) * a.ts + hq * a.hs;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) qf[j] = *(const u32x4v*)(x + 2 * d(j));
+  constexpr uint32_t E = Kv4Type<F16>::kExp;
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bad |= (qf[j][e] & E) == E || (qf[j][e] & (E << 16)) == (E << 16);
+  if (__any(bad)) {
+    const float b = groups_max(bad ? 1.0f : 0.0f);  // over the row's lanes
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) qf[j][e] = b > 0.0f ? Kv4Type<F16>::kNan : qf[j][e];
+  }
+  return row;
+}
+
+// State of a wave's rows over the tiles.
+template <int QT, int NU>
+struct Kv4State {
+  float m[QT], l[QT];  // reference (log2), sum of this lane group's weights
+  f32x4v o[QT][NU];
+  int far;             // some row's reference is past kFarTop4
+  __device__ inline void init() {
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      m[t] = kNegInf;
+      l[t] = 0.0f;
+#pragma unroll
+      for (int u = 0; u < NU; ++u) o[t][u] = f32x4v{0.f, 0.f, 0.f, 0.f};
+    }
+    far = 0;
+  }
+};
+
+// Scores of a tile to weights: lane: QT rows, slot 4 mt + i is token tok(mt, i) of the
+// lane group's 16 (tok0 = its first).  edge: some token is not seen by some row, or is NaN
+// (bad: by slot).  The sum is of the weights before their rounding.
+template <bool F16, bool ADJACENT, int QT, int NU>
+__device__ inline void kv4_weights(f32x4v (&sc)[QT][4], const Kv4Row (&row)[QT], float c, bool there, int tok0,
+                                   bool edge, uint32_t bad, Kv4State<QT, NU>& st, u32x4v (&pf)[QT][2]) {
+  // tokens of slot (mt, i): 4 mt + i (ADJACENT), or 4 i + mt
+  auto token = [](int mt, int i) { return ADJACENT ? 4 * mt + i : 4 * i + mt; };
+  if (edge) {
+    if (__any(bad != 0)) {
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sc[t][mt][e] = (bad >> token(mt, e)) & 1 ? __builtin_nanf("") : sc[t][mt][e];
+    }
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      // tokens tok0 + x with first <= x <= last
+      const int first = there ? row[t].low - tok0 : 16, last = row[t].lim - tok0;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sc[t][mt][e] = token(mt, e) > last || token(mt, e) < first ? kNegInf : sc[t][mt][e];
+    }
+  }
+  float top[QT];
+  bool turn = false;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    float mx = kNegInf;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx = __builtin_fmaxf(mx, sc[t][mt][e]);
+    top[t] = groups_max(mx) * c;
+    turn |= top[t] - st.m[t] > kTopMost4;  // -inf - -inf is NaN: no new reference
+  }
+  if (__any(turn)) {
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      const bool g = top[t] - st.m[t] > kTopMost4;
+      float nm = top[t] - kTopSet4;
+      nm = top[t] - nm > kTopMost4 ? top[t] : nm;  // where scores have steps of 16, top - 8 may round to top - 16
+      const float al = g ? __builtin_amdgcn_exp2f(st.m[t] - nm) : 1.0f;
+      st.m[t] = g ? nm : st.m[t];
+      st.l[t] *= al;
+      st.far |= uniform((int)__any(__builtin_fabsf(st.m[t]) > kFarTop4 && st.m[t] != kNegInf));
+#pragma unroll
+      for (int u = 0; u < NU; ++u) st.o[t][u] *= al;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    const float ref = st.m[t] == kNegInf ? 0.0f : st.m[t];
+    if (st.far) {
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[t][mt][e] = sc[t][mt][e] * c - ref;
+    } else {
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[t][mt][e] = __builtin_fmaf(sc[t][mt][e], c, -ref);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sc[t][mt][e] = __builtin_amdgcn_exp2f(sc[t][mt][e]);
+        sum += sc[t][mt][e];
+      }
+      pf[t][mt / 2][2 * (mt & 1)] = Kv4Type<F16>::pack(sc[t][mt][0], sc[t][mt][1]);
+      pf[t][mt / 2][2 * (mt & 1) + 1] = Kv4Type<F16>::pack(sc[t][mt][2], sc[t][mt][3]);
+    }
+    st.l[t] += sum;
+  }
+}
+
+// Few rows per kv head (decoding): one tile of 16 rows, four waves that take the
+// chunk's tiles in turn, K and V straight from memory into MFMA operands.
+// BIG: blocks of 64 tokens and more, so a tile lies in one block (scalar addresses).
+template <int D, bool F16, bool BIG>
+__global__ __launch_bounds__(256) void k_kv4_attn(KvAttnArgs p) {
+  using X = Kv4Type<F16>;
+  // spans of 128 dims (16 bytes of a K row a lane) and of 64 (8 bytes)
+  constexpr int S128 = D / 128, S64 = D % 128 / 64, NS = S128 + S64, NJ = D / 32, NU = D / 16, G = D / 32;
+  const KvAttn& a = p.a;
+  const int lane = threadIdx.x & 63, wv = uniform((int)threadIdx.x >> 6), c16 = lane & 15, h = lane >> 4;
+  KvItem it;
+  if (!kv_item(p, blockIdx.x, lane, it)) return;
+  const int H = a.c.heads, tsh = a.c.tsh, T = 1 << tsh;
+  u32x4v qf[NJ];
+  const Kv4Row row[1] = {kv4_query<F16>(p, it, it.rt * p.rb + c16, qf, [&](int j) {
+    return j / 4 < S128 ? 128 * (j / 4) + 32 * h + 8 * (j % 4) : 128 * S128 + 16 * h + 8 * (j % 4);
+  })};
+  const float c = a.scale * 1.44269504088896340736f;
+  Kv4State<1, NU> st;
+  st.init();
+
+  const int r0 = it.rt * p.rb, r1 = r0 + 16 < it.k.rows ? r0 + 16 : it.k.rows;
+  const KvRange rg = kv_range(p, it, r0, r1);
+  const int lo = rg.lo, hi = rg.hi;
+  const int* table = a.q.table + (int64_t)it.seq * a.q.table_stride;
+
+  // Block of a tile (BIG) or of this lane group's 16 tokens of it, or -1: what no row
+  // sees and what has no block reads block 0, masked.
+  auto block_of = [&](int tt) -> int {
+    const int gp = tt * kKvTile + (BIG ? 0 : 16 * h);
+    int blk = tt < rg.t1 && gp < hi && gp + (BIG ? kKvTile : 16) > lo ? table[gp >> tsh] : -1;
+    if (blk >= a.c.blocks) blk = -1;
+    return BIG ? scalar(blk) : blk;
+  };
+  auto place = [&](int blk) -> int64_t { return (int64_t)(blk < 0 ? 0 : blk) * H + it.head; };
+  // K: rows 4 c16 .. 4 c16 + 3 of the tile; V: rows 16 h .. 16 h + 15
+  u32x4v kr[4][S128 ? S128 : 1], vs[NS];
+  uint2 k8[4];
+  uint32_t vr[16][S128 ? S128 : 1], ks[NS];
+  uint16_t v2[16];
+  auto load_k = [&](int tt, int blk) {
+    const int row0 = (tt * kKvTile + 4 * c16) & (T - 1);
+    const int64_t at = place(BIG ? blk : __shfl(blk, 16 * (c16 >> 2), 64));
+    const uint8_t* kp = a.c.k + (at * T + row0) * (D / 2);
+    const uint8_t* ep = a.c.ke + at * G * T + row0;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+      for (int s = 0; s < S128; ++s) kr[mt][s] = *(const u32x4v*)(kp + mt * (D / 2) + 64 * s + 16 * h);
+      if constexpr (S64) k8[mt] = *(const uint2*)(kp + mt * (D / 2) + 64 * S128 + 8 * h);
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) ks[s] = *(const uint32_t*)(ep + (4 * s + (s < S128 ? h : h >> 1)) * T);
+  };
+  auto load_v = [&](int tt, int blk) {
+    const int row0 = (tt * kKvTile + 16 * h) & (T - 1);
+    const int64_t at = place(blk);
+    const uint8_t* vp = a.c.v + (at * T + row0) * (D / 2);
+    const uint8_t* ep = a.c.ve + at * G * T + row0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+#pragma unroll
+      for (int s = 0; s < S128; ++s) vr[e][s] = *(const uint32_t*)(vp + e * (D / 2) + 64 * s + 4 * c16);
+      if constexpr (S64) v2[e] = *(const uint16_t*)(vp + e * (D / 2) + 64 * S128 + 2 * c16);
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) vs[s] = *(const u32x4v*)(ep + (4 * s + (s < S128 ? c16 >> 2 : c16 >> 3)) * T);
+  };
+  int tt = rg.t0 + wv, blk = -1, blk1 = -1;
+  if (tt < rg.t1) {
+    blk = block_of(tt);
+    blk1 = block_of(tt + 4);
+    load_k(tt, blk);
+    load_v(tt, blk);
+  }
+  for (; tt < rg.t1; tt += 4) {
+    const int b0 = tt * kKvTile, gp = b0 + 16 * h;
+    const bool there = blk >= 0 && (!BIG || (gp < hi && gp + 16 > lo)), more = tt + 4 < rg.t1;
+    // Exponents of 128 and more are rare: only then are their bytes looked at one by one.
+    uint32_t high = 0, bad = 0;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) high |= ks[s] | vs[s][0] | vs[s][1] | vs[s][2] | vs[s][3];
+    if (__any(high & 0x80808080u)) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        uint32_t none;
+        ks[s] = tame_exponents(ks[s], X::kMost, 255, none);  // K's NaN makes the score NaN
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t b;
+          vs[s][i] = tame_exponents(vs[s][i], X::kMost, 0, b);
+          bad |= b << (4 * i);
+        }
+      }
+      bad |= (uint32_t)__shfl_xor((int)bad, 4, 64);  // the other groups of dims
+      bad |= (uint32_t)__shfl_xor((int)bad, 8, 64);
+    }
+    f32x4v sc[1][4];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) sc[0][mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
+    auto scores = [&]<int MT>() {
+#pragma unroll
+      for (int s = 0; s < S128; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sc[0][MT] = X::mfma(X::widen8(kr[MT][s][j], exponent_field<MT>(ks[s])), qf[4 * s + j], sc[0][MT]);
+      if constexpr (S64) {
+        sc[0][MT] = X::mfma(X::widen8(k8[MT].x, exponent_field<MT>(ks[S128])), qf[4 * S128], sc[0][MT]);
+        sc[0][MT] = X::mfma(X::widen8(k8[MT].y, exponent_field<MT>(ks[S128])), qf[4 * S128 + 1], sc[0][MT]);
+      }
+    };
+    scores.template operator()<0>();
+    scores.template operator()<1>();
+    scores.template operator()<2>();
+    scores.template operator()<3>();
+    const bool edge = __any(bad != 0 || !there) || b0 + kKvTile > rg.least || b0 < rg.from;
+    int blk2 = -1;
+    if (more) {
+      load_k(tt + 4, blk1);
+      blk2 = block_of(tt + 8);
+    }
+    u32x4v pf[1][2];
+    kv4_weights<F16, false, 1, NU>(sc, row, c, there, gp, edge, bad, st, pf);
+    // slot 4 mt + i of V is token 4 i + mt: byte mt of exponent dword i
+    auto out = [&]<int U0, int NB>(auto&& word, const u32x4v& ex) {  // NB bytes: 2 NB dims a lane
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t w[8][NB];  // slots 8 x ..: dims 2 b and 2 b + 1
+        auto slot = [&]<int MT>() {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t v = word(4 * i + 2 * x + MT), s = x ? exponent_field<2 + MT>(ex[i]) : exponent_field<MT>(ex[i]);
+            w[4 * MT + i][0] = X::template widen<0>(v, s);
+            w[4 * MT + i][1] = X::template widen<1>(v, s);
+            if constexpr (NB == 4) {
+              w[4 * MT + i][2] = X::template widen<2>(v, s);
+              w[4 * MT + i][3] = X::template widen<3>(v, s);
+            }
+          }
+        };
+        slot.template operator()<0>();
+        slot.template operator()<1>();
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          u32x4v even, odd;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            even[j] = __builtin_amdgcn_perm(w[2 * j + 1][b], w[2 * j][b], 0x05040100u);
+            odd[j] = __builtin_amdgcn_perm(w[2 * j + 1][b], w[2 * j][b], 0x07060302u);
+          }
+          st.o[0][U0 + 2 * b] = X::mfma(even, pf[0][x], st.o[0][U0 + 2 * b]);
+          st.o[0][U0 + 2 * b + 1] = X::mfma(odd, pf[0][x], st.o[0][U0 + 2 * b + 1]);
+        }
+      }
+    };
+    if constexpr (S128 > 0) out.template operator()<0, 4>([&](int e) { return vr[e][0]; }, vs[0]);
+    if constexpr (S128 > 1) out.template operator()<8, 4>([&](int e) { return vr[e][1]; }, vs[1]);
+    if constexpr (S64 > 0) out.template operator()<8 * S128, 2>([&](int e) { return (uint32_t)v2[e]; }, vs[S128]);
+    if (more) load_v(tt + 4, blk1);
+    blk = blk1;
+    blk1 = blk2;
+  }
+
+  // the four waves' parts of each row meet in LDS, in wave order
+  constexpr int PITCH = D + 4;
+  __shared__ float os[4][16][PITCH];
+  __shared__ __attribute__((aligned(16))) float mls[4][16][2];  // reference, sum
+  st.l[0] = groups_sum(st.l[0]);
+  if (h == 0) *(f32x2v*)mls[wv][c16] = f32x2v{st.m[0], st.l[0]};
+#pragma unroll
+  for (int u = 0; u < NU; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = u / 8, d = s < S128 ? 128 * s + 8 * (4 * h + i) + u % 8 : 128 * S128 + 4 * (4 * h + i) + u % 8;
+      os[wv][c16][d] = st.o[0][u][i];
+    }
+  __syncthreads();
+  const int at = 4 * wv + h, sub = c16, g = scalar(p.g);
+  const int r = it.rt * p.rb + at;
+  if (r < it.k.rows) {
+    float top = kNegInf, f[4], sum = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) top = __builtin_fmaxf(top, mls[q][at][0]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      f[q] = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mls[q][at][0] - top);
+      // a wave whose scores are all NaN has no reference, and a NaN sum
+      f[q] = mls[q][at][1] == mls[q][at][1] ? f[q] : __builtin_nanf("");
+      sum += mls[q][at][1] * f[q];
+    }
+    const int64_t tok = it.r.first + r / g, hq = it.head * g + r % g;
+    const bool split = it.chunks > 1;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t base = split ? (it.slot * p.rb + at) * D : (tok * a.heads + hq) * D;
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) {
+      const int d = sub + 16 * e;
+      float v = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v += os[q][at][d] * f[q];
+      if (split) p.po[base + d] = v * inv;
+      else kv_store_out(a, base + d, v * inv);
+    }
+    if (sub == 0) {
+      if (split) {
+        const f32x2v ml = {sum == sum ? top : -kNegInf, sum};  // NaN has the last word in the join
+        *(f32x2v*)(p.ml + (it.slot * p.rb + at) * 2) = ml;
+      } else if (a.lse) {
+        a.lse[tok * a.heads + hq] = kv_lse(top, sum);
+      }
+    }
+  }
+}
+
+bool kv4_attn_fits(const KvAttn& a) { return kv_plan_fits(a, kv_plan(a, nullptr, kFewRows), 256); }
+
+size_t kv4_attn_workspace(const KvAttn& a) { return kv_plan(a, nullptr, kFewRows).need; }
+
+hipError_t launch_kv4_attn(const KvAttn& a, void* ws, hipStream_t s) {
+  const KvPlan p = kv_plan(a, (char*)ws, kFewRows);
+  if (p.planned) {
+    const hipError_t e = launch_kv_starts(p, s);
+    if (e != hipSuccess) return e;
+  }
+  auto dim = [&]<int D>() {
+    auto go = [&](const KvAttnArgs& w) {
+      const bool f16 = a.dtype == 2;
+      auto k = a.c.tsh >= 6 ? (f16 ? k_kv4_attn<D, true, true> : k_kv4_attn<D, false, true>)
+                            : (f16 ? k_kv4_attn<D, true, false> : k_kv4_attn<D, false, false>);
+      hipLaunchKernelGGL(k, dim3((unsigned)w.items), dim3(256), 0, s, w);
+      return hipGetLastError();
+    };
+    hipError_t e = hipSuccess;
+    if (p.run_many) e = go(p.many);
+    if (e == hipSuccess && p.run_few) e = go(p.few);
+    if (e == hipSuccess && p.split) e = launch_kv_join(p, s);
+    return e;
+  };
+  switch (a.c.dim) {
+    case 64: return dim.template operator()<64>();
+    case 128: return dim.template operator()<128>();
+    case 192: return dim.template operator()<192>();
+    case 256: return dim.template operator()<256>();
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace sparq24

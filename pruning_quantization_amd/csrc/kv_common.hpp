@@ -1,9 +1,11 @@
-// Paged 8-bit key/value cache as the append and attention kernels see it.
+// Paged key/value cache as the append and attention kernels see it.
 //
-// A pool of blocks of T tokens (T = 1 << tsh, 16..256).  Per block and kv
-// head: K codes [T][D], V codes [D][T] (both reductions of attention run over
+// A pool of blocks of T tokens (T = 1 << tsh, 16..256).  Per block and kv head, in
+// 8 bits: K codes [T][D], V codes [D][T] (both reductions of attention run over
 // contiguous bytes: q.k along D, p.v along the tokens), and one fp32 scale
-// each.  Position p of sequence b lives in block table[b][p >> tsh], row
+// each.  In 4 bits (MXFP4 along the dims): K and V codes [T][D/2] and exponent bytes
+// [D/32][T], so that a token's row is written by itself and the exponents of adjacent
+// tokens lie side by side.  Position p of sequence b lives in block table[b][p >> tsh], row
 // p & (T - 1).  A table entry outside 0 .. blocks - 1 names no block: nothing
 // is written there and attention sees no tokens in it, so bad tables never
 // become addresses.

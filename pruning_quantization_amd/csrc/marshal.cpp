@@ -1,5 +1,5 @@
 // Python marshalling of the calls that a serving step makes once per layer and
-// token (int8_gemm, kv_append, kv_attention): checks of the tensors, the C
+// token (rmsnorm_quantize, int8_gemm, mxfp4_gemm, kv_append, kv_attention): checks of the tensors, the C
 // descriptors, the outputs and the current stream, in native code because in
 // Python they took as long as the kernels (9 to 15 us a call against 5 to 10).
 // The C entry points themselves are handed in by bind(), as loaded by
@@ -27,6 +27,10 @@ using at::Tensor;
 decltype(&sparq24_int8_gemm) c_int8_gemm = nullptr;
 decltype(&sparq24_kv_append) c_kv_append = nullptr;
 decltype(&sparq24_kv_attention) c_kv_attention = nullptr;
+decltype(&sparq24_mxfp4_gemm) c_mxfp4_gemm = nullptr;
+decltype(&sparq24_rmsnorm_quantize) c_rmsnorm_quantize = nullptr;
+decltype(&sparq24_kv_append_mxfp4) c_kv_append_mxfp4 = nullptr;
+decltype(&sparq24_kv_attention_mxfp4) c_kv_attention_mxfp4 = nullptr;
 
 PyObject* call_error = nullptr;  // class raised for a status: (function, status)
 
@@ -122,91 +126,222 @@ PyObject* failed(const char* fn, int st) {
   return nullptr;
 }
 
-// bind(address of sparq24_int8_gemm, of sparq24_kv_append, of sparq24_kv_attention, error class)
+// bind(addresses of sparq24_int8_gemm, _kv_append, _kv_attention, _mxfp4_gemm, _rmsnorm_quantize, _kv_append_mxfp4
+// and _kv_attention_mxfp4, error class)
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    arguments(n, 4);
+    arguments(n, 8);
     c_int8_gemm = (decltype(c_int8_gemm))PyLong_AsVoidPtr(a[0]);
     c_kv_append = (decltype(c_kv_append))PyLong_AsVoidPtr(a[1]);
     c_kv_attention = (decltype(c_kv_attention))PyLong_AsVoidPtr(a[2]);
+    c_mxfp4_gemm = (decltype(c_mxfp4_gemm))PyLong_AsVoidPtr(a[3]);
+    c_rmsnorm_quantize = (decltype(c_rmsnorm_quantize))PyLong_AsVoidPtr(a[4]);
+    c_kv_append_mxfp4 = (decltype(c_kv_append_mxfp4))PyLong_AsVoidPtr(a[5]);
+    c_kv_attention_mxfp4 = (decltype(c_kv_attention_mxfp4))PyLong_AsVoidPtr(a[6]);
     if (PyErr_Occurred()) return nullptr;
     Py_XDECREF(call_error);
-    call_error = Py_NewRef(a[3]);
+    call_error = Py_NewRef(a[7]);
     Py_RETURN_NONE;
   });
 }
 
-// int8_gemm(codes_a, scale_a, codes_b, scale_b, bias, dtype, out)
-PyObject* py_int8_gemm(PyObject*, PyObject* const* a, Py_ssize_t argc) {
-  return guarded([&]() -> PyObject* {
-    arguments(argc, 7);
-    const Tensor &ca = tensor(a[0], "codes_a"), &sa = tensor(a[1], "scale_a");
-    const Tensor &cb = tensor(a[2], "codes_b"), &sb = tensor(a[3], "scale_b");
-    const Tensor *bias = optional(a[4], "bias"), *given = optional(a[6], "out");
-    if (ca.scalar_type() != ScalarType::Char || cb.scalar_type() != ScalarType::Char)
-      type_error("int8 codes expected, got " + shape_of(ca) + " and " + shape_of(cb));
+// A product of rows of codes, C = A B^T: what int8_gemm and mxfp4_gemm have in common.
+// args: codes_a, scale_a, codes_b, scale_b, bias, dtype, out; width: the codes' dim.
+struct Product {
+  const Tensor &ca, &sa, &cb, &sb;
+  const Tensor *bias, *given;
+  int64_t m = 1, n, width, lda, ldb, ldc;
+  ScalarType want;
+  int code;
+  float* pbias;
+  std::vector<int64_t> shape;
+
+  Product(PyObject* const* a, Py_ssize_t argc, ScalarType codes, const char* what)
+      : ca(tensor((arguments(argc, 7), a[0]), "codes_a")), sa(tensor(a[1], "scale_a")), cb(tensor(a[2], "codes_b")),
+        sb(tensor(a[3], "scale_b")), bias(optional(a[4], "bias")), given(optional(a[6], "out")) {
+    if (ca.scalar_type() != codes || cb.scalar_type() != codes)
+      type_error(std::string(what) + " codes expected, got " + shape_of(ca) + " and " + shape_of(cb));
     const int64_t rank = ca.dim();
     if (cb.dim() != 2 || rank < 1 || ca.size(-1) != cb.size(1))
       value_error("shapes " + shape_of(ca) + " and " + shape_of(cb) + " do not multiply");
-    const int64_t n = cb.size(0), k = cb.size(1);
-    int64_t m = 1;
+    n = cb.size(0), width = cb.size(1);
     for (int64_t i = 0; i + 1 < rank; ++i) m *= ca.size(i);
-    // Step between the m rows of t, whose leading dims have to be evenly spaced.
-    auto rows = [&](const Tensor& t, int64_t width, const char* name) -> int64_t {
-      if (m == 0) return width;
-      if (width > 1 && t.stride(-1) != 1) value_error(std::string(name) + " must be contiguous along its last dim");
-      bool one = true;
-      int64_t step = width, span = 0;
-      for (int64_t i = t.dim() - 2; i >= 0; --i) {
-        if (t.size(i) == 1) continue;
-        if (one) span = step = t.stride(i);
-        one = false;
-        if (t.stride(i) != span) value_error("the rows of " + std::string(name) + " must be evenly spaced");
-        span *= t.size(i);
-      }
-      return step;
-    };
-    const int64_t lda = rows(ca, k, "codes_a"), ldb = n > 1 ? cb.stride(0) : k;
-    if (k > 1 && n && cb.stride(1) != 1) value_error("codes_b must be contiguous along K");
+    lda = rows(ca, width, "codes_a"), ldb = n > 1 ? cb.stride(0) : width;
+    if (width > 1 && n && cb.stride(1) != 1) value_error("codes_b must be contiguous along K");
     if (!THPDtype_Check(a[5])) type_error("dtype must be a torch.dtype");
-    const ScalarType want = given ? given->scalar_type() : ((THPDtype*)a[5])->scalar_type;
-    const int code = dtype_code(want);
-    float* psa = vector<float>(sa, m, ScalarType::Float, "scale_a");
-    float* psb = vector<float>(sb, n, ScalarType::Float, "scale_b");
-    float* pbias = bias ? vector<float>(*bias, n, ScalarType::Float, "bias") : nullptr;
-    std::vector<int64_t> shape(ca.sizes().begin(), ca.sizes().end());
+    want = given ? given->scalar_type() : ((THPDtype*)a[5])->scalar_type;
+    code = dtype_code(want);
+  }
+  // Step between the m rows of t, whose leading dims have to be evenly spaced.
+  int64_t rows(const Tensor& t, int64_t width, const char* name) const {
+    if (m == 0) return width;
+    if (width > 1 && t.stride(-1) != 1) value_error(std::string(name) + " must be contiguous along its last dim");
+    bool one = true;
+    int64_t step = width, span = 0;
+    for (int64_t i = t.dim() - 2; i >= 0; --i) {
+      if (t.size(i) == 1) continue;
+      if (one) span = step = t.stride(i);
+      one = false;
+      if (t.stride(i) != span) value_error("the rows of " + std::string(name) + " must be evenly spaced");
+      span *= t.size(i);
+    }
+    return step;
+  }
+  // The checks that follow those of the scales, and the output.
+  template <class F>
+  PyObject* run(const char* fn, F&& call) {
+    pbias = bias ? vector<float>(*bias, n, ScalarType::Float, "bias") : nullptr;
+    shape.assign(ca.sizes().begin(), ca.sizes().end());
     shape.back() = n;
     if (given && given->sizes() != at::IntArrayRef(shape)) value_error("out has shape " + shape_of(*given));
-    const int64_t ldc = given ? rows(*given, n, "out") : n;
+    ldc = given ? rows(*given, n, "out") : n;
     const int dev = device_of({&ca, &sa, &cb, &sb, bias, given});
     const Tensor out = given ? *given : at::empty(shape, ca.options().dtype(want));
-    const int st = on_device(dev, [&](hipStream_t s) {
-      return c_int8_gemm((const int8_t*)ca.data_ptr(), lda, psa, m, (const int8_t*)cb.data_ptr(), ldb, psb, n, k,
-                         pbias, code, out.data_ptr(), ldc, nullptr, nullptr, s);
+    const int st = on_device(dev, [&](hipStream_t s) { return call(out.data_ptr(), s); });
+    return st ? failed(fn, st) : THPVariable_Wrap(out);
+  }
+};
+
+PyObject* py_int8_gemm(PyObject*, PyObject* const* a, Py_ssize_t argc) {
+  return guarded([&]() -> PyObject* {
+    Product p(a, argc, ScalarType::Char, "int8");
+    float* psa = vector<float>(p.sa, p.m, ScalarType::Float, "scale_a");
+    float* psb = vector<float>(p.sb, p.n, ScalarType::Float, "scale_b");
+    return p.run("sparq24_int8_gemm", [&](void* out, hipStream_t s) {
+      return c_int8_gemm((const int8_t*)p.ca.data_ptr(), p.lda, psa, p.m, (const int8_t*)p.cb.data_ptr(), p.ldb, psb,
+                         p.n, p.width, p.pbias, p.code, out, p.ldc, nullptr, nullptr, s);
     });
-    return st ? failed("sparq24_int8_gemm", st) : THPVariable_Wrap(out);
   });
 }
 
-// The cache: a tuple (k, k_scale, v, v_scale).
+PyObject* py_mxfp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t argc) {
+  return guarded([&]() -> PyObject* {
+    Product p(a, argc, ScalarType::Byte, "uint8 (two to a byte)");
+    if (p.width % 16) value_error("rows of codes hold groups of 32 (16 bytes), got " + shape_of(p.ca));
+    const int64_t groups = p.width / 16;
+    uint8_t* psa = vector<uint8_t>(p.sa, p.m * groups, ScalarType::Byte, "scale_a");
+    uint8_t* psb = vector<uint8_t>(p.sb, p.n * groups, ScalarType::Byte, "scale_b");
+    return p.run("sparq24_mxfp4_gemm", [&](void* out, hipStream_t s) {
+      return c_mxfp4_gemm((const uint8_t*)p.ca.data_ptr(), p.lda, psa, p.m, (const uint8_t*)p.cb.data_ptr(), p.ldb,
+                          psb, p.n, 2 * p.width, p.pbias, p.code, out, p.ldc, nullptr, nullptr, s);
+    });
+  });
+}
+
+// Rows of t along its last dim: rows its second to last, batches the dims before, which have to be evenly spaced.
+sparq24_tensor operand_of(const Tensor& t, const char* name) {
+  const int64_t rank = t.dim();
+  if (rank < 1) value_error(std::string(name) + " must have rows");
+  if (t.size(-1) > 1 && t.stride(-1) != 1) value_error(std::string(name) + " must be contiguous along its last dim");
+  int64_t batch = 1, step = 0;
+  bool one = true;
+  for (int64_t i = rank - 3; i >= 0; --i) {
+    if (t.size(i) == 1) continue;
+    if (one) step = t.stride(i);
+    else if (t.stride(i) != step * batch) value_error("the leading dims of " + std::string(name) + " must be evenly spaced");
+    one = false;
+    batch *= t.size(i);
+  }
+  return {t.data_ptr(), dtype_code(t.scalar_type()), batch, rank > 1 ? t.size(-2) : 1, t.size(-1),
+          step, rank > 1 ? t.stride(-2) : t.size(-1), 1};
+}
+
+// rmsnorm_quantize(x, weight, fmt, bits, eps, residual, residual_out, codes, scales)
+// -> (codes, scales) or (codes, scales, residual_out)
+PyObject* py_rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t argc) {
+  return guarded([&]() -> PyObject* {
+    arguments(argc, 9);
+    const Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "weight");
+    sparq24_qspec q{(int32_t)PyLong_AsLong(a[2]), (int32_t)PyLong_AsLong(a[3]), nullptr};
+    const double eps = PyFloat_AsDouble(a[4]);
+    if (PyErr_Occurred()) return nullptr;
+    const Tensor *res = optional(a[5], "residual"), *gsum = optional(a[6], "residual_out");
+    const Tensor *gcodes = optional(a[7], "codes"), *gscales = optional(a[8], "scales");
+    const sparq24_tensor xt = operand_of(x, "x");
+    const int64_t k = x.size(-1);
+    if (w.dim() != 1 || w.numel() != k || !w.is_contiguous())
+      value_error("weight must be contiguous with " + std::to_string(k) + " elements, got " + shape_of(w));
+    const int wcode = dtype_code(w.scalar_type());
+    if (gsum && !res) value_error("residual_out without a residual");
+    sparq24_tensor rt{}, st{};
+    if (res) {
+      if (res->sizes() != x.sizes() || res->scalar_type() != x.scalar_type())
+        value_error("residual " + shape_of(*res) + " is not of x's shape and type");
+      if (gsum && (gsum->sizes() != x.sizes() || gsum->scalar_type() != x.scalar_type()))
+        value_error("residual_out " + shape_of(*gsum) + " is not of x's shape and type");
+      rt = operand_of(*res, "residual");
+      if (gsum) st = operand_of(*gsum, "residual_out");
+    }
+    const bool mx = q.fmt == SPARQ24_Q_MXFP4;
+    if (mx && k % 32) value_error("mxfp4 needs rows of 32 elements, got " + shape_of(x));
+    std::vector<int64_t> cshape(x.sizes().begin(), x.sizes().end()), sshape(cshape);
+    if (mx) cshape.back() = k / 2, sshape.back() = k / 32;
+    else sshape.pop_back();
+    const ScalarType ctype = q.fmt == SPARQ24_Q_INT ? ScalarType::Char : ScalarType::Byte;
+    const ScalarType stype = mx ? ScalarType::Byte : ScalarType::Float;
+    auto fits = [&](const Tensor* t, const std::vector<int64_t>& shape, ScalarType type, const char* name) {
+      if (t && (t->sizes() != at::IntArrayRef(shape) || t->scalar_type() != type || !t->is_contiguous()))
+        value_error(std::string(name) + " must be contiguous " + c10::toString(type) + " of the output's shape, got " +
+                    shape_of(*t));
+    };
+    fits(gcodes, cshape, ctype, "codes");
+    fits(gscales, sshape, stype, "scales");
+    const int dev = device_of({&x, &w, res, gsum, gcodes, gscales});
+    const Tensor codes = gcodes ? *gcodes : at::empty(cshape, x.options().dtype(ctype));
+    const Tensor scales = gscales ? *gscales : at::empty(sshape, x.options().dtype(stype));
+    Tensor sum;
+    if (res) {
+      sum = gsum ? *gsum : at::empty(x.sizes(), x.options());
+      if (!gsum) st = operand_of(sum, "residual_out");
+    }
+    const int status = on_device(dev, [&](hipStream_t s) {
+      return c_rmsnorm_quantize(&xt, res ? &rt : nullptr, w.data_ptr(), wcode, (float)eps, &q, codes.data_ptr(),
+                                scales.data_ptr(), res ? &st : nullptr, s);
+    });
+    if (status) return failed("sparq24_rmsnorm_quantize", status);
+    PyObject* t = PyTuple_New(res ? 3 : 2);
+    if (!t) return nullptr;
+    PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(codes));
+    PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(scales));
+    if (res) PyTuple_SET_ITEM(t, 2, THPVariable_Wrap(sum));
+    return t;
+  });
+}
+
+// The cache: a tuple (k, k_scale, v, v_scale), of 8 bits or (uint8 scales) of 4.
 struct Cache {
   const Tensor *k, *ks, *v, *vs;
+  bool mx;
   sparq24_kvcache c;
+  sparq24_kvcache_mxfp4 c4;
 };
 Cache cache_of(PyObject* o) {
   if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) type_error("cache must be a KVCache (k, k_scale, v, v_scale)");
   Cache x{&tensor(PyTuple_GET_ITEM(o, 0), "cache.k"), &tensor(PyTuple_GET_ITEM(o, 1), "cache.k_scale"),
-          &tensor(PyTuple_GET_ITEM(o, 2), "cache.v"), &tensor(PyTuple_GET_ITEM(o, 3), "cache.v_scale"), {}};
+          &tensor(PyTuple_GET_ITEM(o, 2), "cache.v"), &tensor(PyTuple_GET_ITEM(o, 3), "cache.v_scale"), false, {}, {}};
   const Tensor &k = *x.k, &v = *x.v;
+  x.mx = x.ks->scalar_type() == ScalarType::Byte;
   if (k.dim() != 4 || v.dim() != 4)
-    value_error("cache codes must be [blocks, heads, tokens, dim] and [blocks, heads, dim, tokens]");
+    value_error("cache codes must be [blocks, heads, tokens, dim] and [blocks, heads, dim, tokens] (4 bits: both "
+                "[blocks, heads, tokens, dim / 2])");
   const int64_t blocks = k.size(0), heads = k.size(1), tokens = k.size(2), dim = k.size(3);
-  if (v.size(0) != blocks || v.size(1) != heads || v.size(2) != dim || v.size(3) != tokens ||
-      k.scalar_type() != v.scalar_type())
+  if (v.size(0) != blocks || v.size(1) != heads || v.size(2) != (x.mx ? tokens : dim) ||
+      v.size(3) != (x.mx ? dim : tokens) || k.scalar_type() != v.scalar_type())
     value_error("cache codes " + shape_of(k) + " and " + shape_of(v) + " do not match");
-  if (k.scalar_type() != ScalarType::Char && k.scalar_type() != ScalarType::Byte)
-    type_error("cache codes are int8 or uint8 (e4m3), got " + shape_of(k));
+  if (x.mx ? k.scalar_type() != ScalarType::Byte
+           : k.scalar_type() != ScalarType::Char && k.scalar_type() != ScalarType::Byte)
+    type_error("cache codes are int8 or uint8 (e4m3; 4 bits, two to a byte), got " + shape_of(k));
   if (!k.is_contiguous() || !v.is_contiguous()) value_error("cache codes must be contiguous");
+  if (x.mx) {
+    const int64_t groups = dim / 16;
+    for (const Tensor* t : {x.ks, x.vs})
+      if (t->dim() != 4 || t->size(0) != blocks || t->size(1) != heads || t->size(2) != groups || t->size(3) != tokens)
+        value_error("k_scale and v_scale of a 4-bit cache are [blocks, heads, dim / 32, tokens], got " + shape_of(*t));
+    x.c4 = {(uint8_t*)k.data_ptr(), vector<uint8_t>(*x.ks, blocks * heads * groups * tokens, ScalarType::Byte, "k_scale"),
+            (uint8_t*)v.data_ptr(), vector<uint8_t>(*x.vs, blocks * heads * groups * tokens, ScalarType::Byte, "v_scale"),
+            blocks, heads, tokens, 2 * dim};
+    return x;
+  }
   x.c = {k.data_ptr(), vector<float>(*x.ks, blocks * heads, ScalarType::Float, "k_scale"),
          v.data_ptr(), vector<float>(*x.vs, blocks * heads, ScalarType::Float, "v_scale"),
          k.scalar_type() == ScalarType::Char ? SPARQ24_Q_INT : SPARQ24_Q_FP8_E4M3,
@@ -262,8 +397,10 @@ PyObject* py_kv_append(PyObject*, PyObject* const* a, Py_ssize_t argc) {
     const sparq24_kvseqs q = seqs_of(k, table, lens, cu);
     const sparq24_tensor kr = rows_of(k), vr = rows_of(v);
     const int dev = device_of({&k, &v, &table, &lens, cu, c.k, c.ks, c.v, c.vs});
-    const int st = on_device(dev, [&](hipStream_t s) { return c_kv_append(&c.c, &q, &kr, &vr, s); });
-    if (st) return failed("sparq24_kv_append", st);
+    const int st = on_device(dev, [&](hipStream_t s) {
+      return c.mx ? c_kv_append_mxfp4(&c.c4, &q, &kr, &vr, s) : c_kv_append(&c.c, &q, &kr, &vr, s);
+    });
+    if (st) return failed(c.mx ? "sparq24_kv_append_mxfp4" : "sparq24_kv_append", st);
     Py_RETURN_NONE;
   });
 }
@@ -298,6 +435,8 @@ PyObject* py_kv_attention(PyObject*, PyObject* const* a, Py_ssize_t argc) {
     Tensor ws = work ? *work : Tensor();
     const int st = on_device(dev, [&](hipStream_t stream) -> int {
       auto call = [&](void* w, size_t* n) {
+        if (c.mx)
+          return c_kv_attention_mxfp4(&c.c4, &s, &x, (float)scale, causal, window, out.data_ptr(), plse, w, n, stream);
         return c_kv_attention(&c.c, &s, &x, (float)scale, causal, window, out.data_ptr(), plse, w, n, stream);
       };
       size_t n = work ? work->nbytes() : 0;
@@ -309,7 +448,7 @@ PyObject* py_kv_attention(PyObject*, PyObject* const* a, Py_ssize_t argc) {
       // without memory no size either: that would be the size query
       return n ? call(ws.data_ptr(), &n) : call(nullptr, nullptr);
     });
-    if (st) return failed("sparq24_kv_attention", st);
+    if (st) return failed(c.mx ? "sparq24_kv_attention_mxfp4" : "sparq24_kv_attention", st);
     if (!want_lse) return THPVariable_Wrap(out);
     PyObject* pair = PyTuple_New(2);
     PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(out));
@@ -321,6 +460,8 @@ PyObject* py_kv_attention(PyObject*, PyObject* const* a, Py_ssize_t argc) {
 PyMethodDef methods[] = {
     {"bind", (PyCFunction)(void (*)())py_bind, METH_FASTCALL, nullptr},
     {"int8_gemm", (PyCFunction)(void (*)())py_int8_gemm, METH_FASTCALL, nullptr},
+    {"mxfp4_gemm", (PyCFunction)(void (*)())py_mxfp4_gemm, METH_FASTCALL, nullptr},
+    {"rmsnorm_quantize", (PyCFunction)(void (*)())py_rmsnorm_quantize, METH_FASTCALL, nullptr},
     {"kv_append", (PyCFunction)(void (*)())py_kv_append, METH_FASTCALL, nullptr},
     {"kv_attention", (PyCFunction)(void (*)())py_kv_attention, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

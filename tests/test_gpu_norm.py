@@ -1,0 +1,176 @@
+"""GPU parity of the RMS norm with the residual's addition and a quantized output,
+bit for bit: the squares and their sum are fp64, so the mean differs from the exactly
+rounded one by a few 2^-53, which decides the one rounding to fp32 once in some 2^28
+rows; every other step is one fp32 operation."""
+import numpy as np
+import pytest
+
+import oracle as O
+import oracle.serving4 as V
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU, skipped there
+    pytest.skip("no GPU", allow_module_level=True)
+
+import pruning_quantization_amd as S  # noqa: E402
+from gpu_util import DEV, random_raw, raw_np, to_dev  # noqa: E402
+
+Q = {"fp8": ("fp8", O.QSpec("fp8")), "mxfp4": ("mxfp4", O.QSpec("mxfp4")),
+     **{f"int{b}": (("int", b), O.QSpec("int", b)) for b in (2, 4, 8)}}
+NAN = float("nan")
+
+
+def same(got, want):
+    got = raw_np(got)
+    assert got.shape == want.shape and got.dtype == want.dtype, (got.shape, got.dtype, want.shape, want.dtype)
+    assert np.array_equal(got.view(np.uint8), want.view(np.uint8)), f"{(got != want).sum()} of {got.size} differ"
+
+
+def check(out, raw, dtype, w, eps, q, res=None):
+    codes, scales, total = V.rmsnorm_quantize(raw, dtype, w, eps, q, res)
+    same(out[0], codes)
+    same(out[1], scales)
+    assert len(out) == (2 if res is None else 3)
+    if res is not None:
+        same(out[2], total)
+
+
+# every width class of the kernel (64 lanes x 1, 2 units; 256 lanes x 1 .. 16), rows that
+# do not fill them, one row and odd counts
+@pytest.mark.parametrize("fmt", sorted(Q))
+@pytest.mark.parametrize("dtype,k,rows", [
+    ("bf16", 32, 5), ("f16", 512, 3), ("f32", 544, 7), ("bf16", 1024, 9), ("f32", 1056, 2), ("f16", 2048, 1),
+    ("bf16", 4096, 33), ("bf16", 5152, 3), ("f32", 8192, 2), ("f16", 8224, 2), ("bf16", 16384, 3),
+    ("f32", 16416, 2), ("bf16", 32768, 2), ("f32", 32768, 1)])
+def test_formats(fmt, dtype, k, rows):
+    rng = np.random.default_rng(k + rows)
+    name, q = Q[fmt]
+    raw, res = random_raw(rng, (rows, k), dtype, 3.0), random_raw(rng, (rows, k), dtype)
+    w = random_raw(rng, (k,), "f32")
+    x, r, tw = to_dev(raw, dtype), to_dev(res, dtype), to_dev(w, "f32")
+    check(S.rmsnorm_quantize(x, tw, name, eps=1e-5), raw, dtype, w, 1e-5, q)
+    check(S.rmsnorm_quantize(x, tw, name, eps=0.0, residual=r), raw, dtype, w, 0.0, q, res)
+
+
+@pytest.mark.parametrize("k", [8, 24, 264, 4104, 11008])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_widths_of_eight_and_weights_of_the_rows_type(dtype, k):
+    rng = np.random.default_rng(k)
+    raw, w = random_raw(rng, (6, k), dtype), random_raw(rng, (k,), dtype)
+    w32 = O.decode_input(w[None], dtype)[0].astype(np.float32)
+    for fmt in ("int8", "fp8"):
+        check(S.rmsnorm_quantize(to_dev(raw, dtype), to_dev(w, dtype), Q[fmt][0]), raw, dtype, w32, 1e-6, Q[fmt][1])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "mxfp4"])
+def test_strides_batches_and_outputs_given(fmt):
+    rng = np.random.default_rng(3)
+    name, q = Q[fmt]
+    raw, res = random_raw(rng, (4, 6, 192), "bf16"), random_raw(rng, (4, 6, 256), "bf16")
+    w = random_raw(rng, (64,), "f32")
+    x, r, tw = to_dev(raw, "bf16"), to_dev(res, "bf16"), to_dev(w, "f32")
+    flat = lambda a: np.ascontiguousarray(a).reshape(-1, 64)  # noqa: E731
+    total = torch.zeros(4, 6, 128, dtype=torch.bfloat16, device=DEV)
+    codes, scales, got = S.rmsnorm_quantize(x[:, 1:4, 64:128], tw, name, residual=r[:, 2:5, 128:192],
+                                            residual_out=total[:, 3:6, 64:])
+    want = V.rmsnorm_quantize(flat(raw[:, 1:4, 64:128]), "bf16", w, 1e-6, q, flat(res[:, 2:5, 128:192]))
+    for a, b in zip((codes, scales, got), want):
+        a = a.contiguous().flatten(0, 1)
+        same(a, b)
+    assert not total[:, :3].any() and not total[:, :, :64].any()
+    out = torch.empty_like(codes), torch.empty_like(scales)
+    again = S.rmsnorm_quantize(x[:, 1:4, 64:128], tw, name, residual=r[:, 2:5, 128:192], out=out)
+    assert again[0] is not None and out[0].data_ptr() == again[0].data_ptr()
+    assert torch.equal(out[0], codes) and torch.equal(out[1].view(torch.uint8), scales.view(torch.uint8))
+    one = S.rmsnorm_quantize(x[2, 3, :64], tw, name)             # a single row without leading dims
+    want = V.rmsnorm_quantize(raw[2, 3:4, :64], "bf16", w, 1e-6, q)
+    same(one[0].reshape(1, -1), want[0])
+    same(one[1].reshape(want[1].shape), want[1])
+
+
+@pytest.mark.parametrize("into", ["residual", "x"])
+@pytest.mark.parametrize("k", [64, 1024, 4096, 16384])
+def test_sum_in_place(into, k):
+    rng = np.random.default_rng(k)
+    raw, res, w = random_raw(rng, (70, k), "bf16"), random_raw(rng, (70, k), "bf16"), random_raw(rng, (k,), "f32")
+    x, r = to_dev(raw, "bf16"), to_dev(res, "bf16")
+    to = r if into == "residual" else x
+    out = S.rmsnorm_quantize(x, to_dev(w, "f32"), "fp8", residual=r, residual_out=to)
+    assert out[2].data_ptr() == to.data_ptr()
+    check(out, raw, "bf16", w, 1e-6, Q["fp8"][1], res)
+
+
+def test_the_stored_sum_is_what_is_normed():
+    # a second call on the sum gives the first one's codes
+    rng = np.random.default_rng(8)
+    x, r = (to_dev(random_raw(rng, (9, 512), "f16", 30.0), "f16") for _ in range(2))
+    w = to_dev(random_raw(rng, (512,), "f32"), "f32")
+    c, s, h = S.rmsnorm_quantize(x, w, ("int", 8), residual=r)
+    c2, s2 = S.rmsnorm_quantize(h, w, ("int", 8))
+    assert torch.equal(c, c2) and torch.equal(s, s2)
+
+
+def test_rows_of_zeros_and_tiny_rows():
+    w = np.ones(64, np.float32)
+    raw = np.zeros((6, 64), np.float32)
+    raw[1] = -0.0
+    raw[2] = 1e-30                      # its square is far below eps; with eps 0 the row is normed to ones
+    raw[3, 7] = 2.0 ** -120
+    raw[4] = np.arange(64) * 2.0 ** -130
+    raw[5] = 3e38                       # the squares leave fp32's range, not fp64's
+    x = to_dev(raw, "f32")
+    for eps in (0.0, 1e-6, 1e30):
+        for fmt in ("int8", "fp8", "mxfp4"):
+            check(S.rmsnorm_quantize(x, to_dev(w, "f32"), Q[fmt][0], eps=eps), raw, "f32", w, eps, Q[fmt][1])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "mxfp4"])
+@pytest.mark.parametrize("k", [64, 4096])
+def test_elements_that_are_no_numbers_make_their_row_nan(k, fmt):
+    rng = np.random.default_rng(4)
+    raw = random_raw(rng, (5, k), "f32")
+    w = random_raw(rng, (k,), "f32")
+    x, tw = to_dev(raw, "f32"), to_dev(w, "f32")
+    x[1, 3], x[2, k - 1], x[3, 5] = NAN, float("inf"), -float("inf")
+    r = torch.zeros_like(x)
+    r[3, 5] = float("inf")              # -inf + inf
+    codes, scales, total = S.rmsnorm_quantize(x, tw, Q[fmt][0], residual=r)
+    for row in (1, 2, 3):
+        assert not codes[row].any()
+        assert (scales[row] == 255).all() if fmt == "mxfp4" else scales[row].isnan()
+    keep = [0, 4]
+    want = V.rmsnorm_quantize(raw[keep], "f32", w, 1e-6, Q[fmt][1])
+    same(codes[keep], want[0])
+    same(scales[keep], want[1])
+    assert total[1, 3].isnan() and total[2, k - 1].isinf() and total[3, 5].isnan()
+    # a weight that is no number: the row, or its group of 32
+    tw[33] = NAN
+    codes, scales = S.rmsnorm_quantize(to_dev(raw, "f32"), tw, Q[fmt][0])
+    if fmt == "mxfp4":
+        want = V.rmsnorm_quantize(raw, "f32", w, 1e-6, Q[fmt][1])
+        assert (scales[:, 1] == 255).all() and not codes[:, 16:32].any()
+        same(codes[:, :16].contiguous(), want[0][:, :16])
+        same(codes[:, 32:].contiguous(), want[0][:, 32:])
+    else:
+        assert scales.isnan().all() and not codes.any()
+
+
+def test_nothing_to_do():
+    w = torch.ones(64, device=DEV)
+    x = torch.empty(0, 64, device=DEV)
+    codes, scales, total = S.rmsnorm_quantize(x, w, "fp8", residual=x)
+    assert codes.shape == (0, 64) and scales.shape == (0,) and total.shape == (0, 64)
+
+
+def test_refusals():
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(64, device=DEV)
+    for bad in (lambda: S.rmsnorm_quantize(x, w.cpu(), "fp8"), lambda: S.rmsnorm_quantize(x, w, "fp8", residual=x.cpu())):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: S.rmsnorm_quantize(x, w.half(), "fp8"), lambda: S.rmsnorm_quantize(x, w, ("int", 9)),
+                lambda: S.rmsnorm_quantize(x, w, "fp8", eps=-1.0), lambda: S.rmsnorm_quantize(x, w, "fp8", eps=NAN),
+                lambda: S.rmsnorm_quantize(x, w, "nvfp4")):
+        with pytest.raises(S.Sparq24Error):
+            bad()
