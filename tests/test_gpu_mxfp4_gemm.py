@@ -73,6 +73,21 @@ def test_every_rest_of_k(m, n, rest):
     check(S.mxfp4_gemm(*dev(a, sa, b, sb)), a, sa, b, sb, None, "f32")
 
 
+# the tiles: whole and ragged ones of each size, K below and at a slab, odd numbers of slabs
+# and of the groups in which exponents are read
+@pytest.mark.parametrize("m,n,k,dtype", [
+    (4096, 4096, 512, "bf16"), (4000, 4200, 544, "f32"), (3841, 4097, 768, "f16"), (4096, 4352, 1312, "f32"),
+    (4096, 4096, 480, "bf16"), (2048, 4096, 512, "bf16"), (2000, 4100, 832, "f32"), (1030, 4090, 1056, "f16"),
+    (1024, 2048, 256, "f32"), (600, 1500, 96, "f32"), (5000, 4111, 1024, "bf16"), (4100, 4100, 928, "f32")])
+def test_tiles(m, n, k, dtype):
+    rng = np.random.default_rng(m + n)
+    a, sa = operand(rng, m, k, 122, 128)
+    b, sb = operand(rng, n, k, 122, 128)
+    bias = rng.standard_normal(n).astype(np.float32)
+    da, dsa, db, dsb, dbias = dev(a, sa, b, sb, bias)
+    check(S.mxfp4_gemm(da, dsa, db, dsb, bias=dbias, dtype=DT[dtype]), a, sa, b, sb, bias, dtype)
+
+
 def test_quantized_operands_and_leading_dims():
     rng = np.random.default_rng(5)
     x = torch.from_numpy(rng.standard_normal((2, 9, 512)).astype(np.float32)).to(DEV).bfloat16()
@@ -118,7 +133,7 @@ def test_scales_at_the_ends_of_the_range(m, n):
     assert (np.isinf(got) | np.isnan(got) | (want == 0)).all()
 
 
-@pytest.mark.parametrize("m,n,k", [(3, 40, 96), (3, 40, 1024), (150, 290, 544), (520, 530, 512)])
+@pytest.mark.parametrize("m,n,k", [(3, 40, 96), (3, 40, 1024), (150, 290, 544), (520, 530, 512), (4096, 4096, 1056)])
 def test_nan_scales_reach_their_row_and_column(m, n, k):
     rng = np.random.default_rng(k)
     a, sa = operand(rng, m, k)
@@ -146,7 +161,7 @@ def test_signed_zeros_and_no_reduction():
 
 def test_repeats_give_the_same_bits():
     rng = np.random.default_rng(6)
-    for m, n, k in ((1, 512, 4096), (60, 300, 2080), (400, 700, 1056)):
+    for m, n, k in ((1, 512, 4096), (60, 300, 2080), (400, 700, 1056), (4096, 4096, 2048)):
         ops = dev(*operand(rng, m, k), *operand(rng, n, k))
         first = S.mxfp4_gemm(*ops)
         assert all(torch.equal(first, S.mxfp4_gemm(*ops)) for _ in range(3))
