@@ -167,12 +167,24 @@ __device__ inline uint32_t tame_exponents(uint32_t w, uint32_t most, uint32_t na
   return r;
 }
 
+// Over lanes l and l ^ 32, in both.
+__device__ inline float halves_max(float v) {
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  float m;
+  asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(r[0]), "v"(r[1]));
+  return m;
+}
+__device__ inline float halves_sum(float v) {
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
 // Query row r of the row tile (column c of the MFMA tiles): elements d(j) .. d(j) + 7 of
 // this lane into qf[j].  A row with an element that is no finite number is all NaN.
 struct Kv4Row {
   int lim, low;  // last and first position seen (lim -1: no row)
 };
-template <bool F16, int NJ, class F>
+template <bool F16, int LANES, int NJ, class F>  // LANES of a row: four lane groups of 16, or two of 32
 __device__ inline Kv4Row kv4_query(const KvAttnArgs& p, const KvItem& it, int r, u32x4v (&qf)[NJ], F&& d) {
   const KvAttn& a = p.a;
   const bool valid = r < it.k.rows;
@@ -192,7 +204,7 @@ __device__ inline Kv4Row kv4_query(const KvAttnArgs& p, const KvItem& it, int r,
 #pragma unroll
     for (int e = 0; e < 4; ++e) bad |= (qf[j][e] & E) == E || (qf[j][e] & (E << 16)) == (E << 16);
   if (__any(bad)) {
-    const float b = groups_max(bad ? 1.0f : 0.0f);  // over the row's lanes
+    const float b = LANES == 4 ? groups_max(bad ? 1.0f : 0.0f) : halves_max(bad ? 1.0f : 0.0f);
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -317,7 +329,7 @@ __global__ __launch_bounds__(256) void k_kv4_attn(KvAttnArgs p) {
   if (!kv_item(p, blockIdx.x, lane, it)) return;
   const int H = a.c.heads, tsh = a.c.tsh, T = 1 << tsh;
   u32x4v qf[NJ];
-  const Kv4Row row[1] = {kv4_query<F16>(p, it, it.rt * p.rb + c16, qf, [&](int j) {
+  const Kv4Row row[1] = {kv4_query<F16, 4>(p, it, it.rt * p.rb + c16, qf, [&](int j) {
     return j / 4 < S128 ? 128 * (j / 4) + 32 * h + 8 * (j % 4) : 128 * S128 + 16 * h + 8 * (j % 4);
   })};
   const float c = a.scale * 1.44269504088896340736f;
@@ -517,29 +529,340 @@ __global__ __launch_bounds__(256) void k_kv4_attn(KvAttnArgs p) {
   }
 }
 
-bool kv4_attn_fits(const KvAttn& a) { return kv_plan_fits(a, kv_plan(a, nullptr, kFewRows), 256); }
+// Many rows per kv head (prompts): the waves of a workgroup hold 32 rows each and share
+// every tile of 64 tokens, which is widened once into LDS (K [64][D], V transposed to
+// [D][64], 16-byte chunks XOR-swizzled by row), one tile ahead of its use, its codes
+// loaded one tile ahead of that.  Products on v_mfma_f32_32x32x16, transposed as above:
+//   S^T  lane: row c = lane % 32, tokens 32 mt + 8 (i / 4) + 4 h + i % 4  (h = lane / 32)
+//   O^T  lane: row c, dims 32 u + 8 (i / 4) + 4 h + i % 4
+// The tokens that a lane has of each 16 are its k slots in the second product; V's
+// tokens are stored in that order (quads 0, 2 | 1, 3 of each 16).
+template <int D>
+struct Kv4PromptShape {
+  static constexpr int NW = D == 192 ? 8 : 4, WAVES = D == 256 ? 1 : 2;  // waves of a workgroup, per SIMD
+  static constexpr int ROWS = 32 * NW;
+};
+typedef float f32x16v __attribute__((ext_vector_type(16)));
 
-size_t kv4_attn_workspace(const KvAttn& a) { return kv_plan(a, nullptr, kFewRows).need; }
+template <bool F16>
+__device__ inline f32x16v kv4_mfma32(u32x4v a, u32x4v b, f32x16v c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8v, a), __builtin_bit_cast(bf16x8v, b), c, 0, 0, 0);
+}
+template <int D, bool F16, bool BIG>
+__global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVES) void k_kv4_prompt(KvAttnArgs p) {
+  using X = Kv4Type<F16>;
+  constexpr int NW = Kv4PromptShape<D>::NW, NJ = D / 16, NU = D / 32, G = D / 32;
+  constexpr int WK = D / 32, NQ = (2 * WK + NW - 1) / NW;  // 64-unit loads of K (and of V), a wave's share
+  constexpr int K_BYTES = kKvTile * D * 2, BUF = 2 * K_BYTES;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * BUF];
+  __shared__ uint32_t nan_tokens[3][2];  // tokens whose V exponent is NaN, by tile
+  const KvAttn& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63, wv = uniform(tid >> 6), c32 = lane & 31, h = lane >> 5;
+  KvItem it;
+  if (!kv_item(p, blockIdx.x, lane, it)) return;
+  const int H = a.c.heads, tsh = a.c.tsh, T = 1 << tsh;
+
+  const int w0 = it.rt * p.rb + 32 * wv;  // this wave's first row
+  u32x4v qf[NJ];
+  const Kv4Row row = kv4_query<F16, 2>(p, it, w0 + c32, qf, [&](int j) { return 16 * j + 8 * h; });
+  const float c = a.scale * 1.44269504088896340736f;
+  float m = kNegInf, l = 0.0f;
+  f32x16v o[NU];
+#pragma unroll
+  for (int u = 0; u < NU; ++u)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[u][e] = 0.0f;
+  int far = 0;
+  const int r0 = it.rt * p.rb, r1 = r0 + p.rb < it.k.rows ? r0 + p.rb : it.k.rows;
+  const KvRange rg = kv_range(p, it, r0, r1);
+  // what this wave's own rows see (none: rows past the end)
+  const int w1 = w0 + 32 < it.k.rows ? w0 + 32 : it.k.rows;
+  KvRange mine = rg;
+  if (w0 < w1) mine = kv_range(p, it, w0, w1);
+  else mine.hi = 0;
+
+  const int* table = a.q.table + (int64_t)it.seq * a.q.table_stride;
+  // Block of a tile (BIG) or, in lanes 16 g .., of its 16 tokens g, or -1 where no row
+  // sees them or there is none; its place among blocks and heads (0's if none).
+  auto block_of = [&](int tt) -> int {
+    const int gp = tt * kKvTile + (BIG ? 0 : 16 * (lane >> 4));
+    if (tt >= rg.t1 || gp >= rg.hi || (!BIG && gp + 16 <= rg.lo)) return -1;
+    int b = table[gp >> tsh];
+    b = b >= 0 && b < a.c.blocks ? b : -1;
+    return BIG ? uniform(b) : b;
+  };
+  auto place = [&](int blk) -> int64_t { return (int64_t)(blk < 0 ? 0 : blk) * H + it.head; };
+  // A 16-byte LDS access takes lanes l .. l + 7 and l + 16 .. l + 23 at a time: rows 0 .. 7
+  // and 16 .. 23 of a fragment (or eight later) have to meet sixteen slots of 16 bytes.
+  // Rows of 256 and 512 bytes: all slots by row bits 0, 1, 2, 4; rows of odd multiples of
+  // 128: the half by bit 0, the slot in it by bits 1, 2, 4.  The order of the bits and
+  // V's bits 3, 5, 6 spread the writes (of rows 8 apart, for V).
+  auto k_swizzle = [](int r) {
+    return D % 128 == 0 ? (r & 1) | ((r >> 1) & 2) | ((r << 1) & 4) | ((r >> 1) & 8)
+                        : ((r >> 1) & 1) | ((r >> 1) & 2) | ((r >> 2) & 4);
+  };
+  auto v_swizzle = [](int d) {
+    return (((d << 1) & 4) ^ ((d >> 3) & 4)) | (((d >> 1) & 2) ^ ((d >> 5) & 2)) | (((d >> 4) & 1) ^ ((d >> 3) & 1));
+  };
+
+  // This lane's first fragments; the others lie at fixed distances, but for address bits
+  // that the swizzle turns (KX).  One register each, and not one per chunk.
+  constexpr unsigned KX = D % 128 == 0 ? 255 : 127;
+  const unsigned kat = c32 * (2 * D) + (h ^ k_swizzle(c32)) * 16;
+  const unsigned vat = K_BYTES + c32 * 128 + (h ^ v_swizzle(c32)) * 16;
+
+  // Unit i = 64 wc + lane of a tile, wc = wv + NW q.  Of K (wc < WK): 32 dims i % G of token
+  // i / G.  Of V: dims 8 o .. 8 o + 7 of tokens 4 t .. 4 t + 3, o = i % (D / 8), t = i / (D / 8).
+  auto is_k = [&](int q) { return WK % NW == 0 ? q < WK / NW : wv + NW * q < WK; };
+  auto has = [&](int q) { return 2 * WK % NW == 0 || wv + NW * q < 2 * WK; };
+  u32x4v cr[NQ];
+  uint32_t ex[NQ];
+  auto fetch = [&](int tt, int blk) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      if (!has(q)) continue;
+      const int i = 64 * (wv + NW * q) + lane;
+      if (is_k(q)) {
+        const int r = i / G, g = i % G;
+        const int64_t at = place(BIG ? blk : __shfl(blk, r & 48, 64));
+        const int o = (tt * kKvTile + r) & (T - 1);
+        cr[q] = *(const u32x4v*)(a.c.k + (at * T + o) * (D / 2) + 16 * g);
+        ex[q] = a.c.ke[(at * G + g) * T + o];
+      } else {
+        const int j = i - 64 * WK, od = j % (D / 8), t = j / (D / 8);
+        const int64_t at = place(BIG ? blk : __shfl(blk, (4 * t) & 48, 64));
+        const int o = (tt * kKvTile + 4 * t) & (T - 1);
+        const uint8_t* vp = a.c.v + (at * T + o) * (D / 2) + 4 * od;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cr[q][e] = *(const uint32_t*)(vp + e * (D / 2));
+        ex[q] = *(const uint32_t*)(a.c.ve + (at * G + (od >> 2)) * T + o);
+      }
+    }
+  };
+  auto widen = [&](int tt, uint8_t* buf) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      if (!has(q)) continue;
+      const int i = 64 * (wv + NW * q) + lane;
+      if (is_k(q)) {
+        uint32_t e = ex[q];
+        e = e > X::kMost && e != 255 ? X::kMost : e;
+        const int r = i / G, g = i % G, z = k_swizzle(r);
+        uint8_t* k = buf + r * (2 * D);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) *(u32x4v*)(k + ((4 * g + x) ^ z) * 16) = X::widen8(cr[q][x], e << 23);
+      } else {
+        const int j = i - 64 * WK, od = j % (D / 8), t = j / (D / 8);
+        uint32_t e = ex[q];
+        if (__any(e & 0x80808080u)) {  // rare: 128 and more
+          uint32_t bad;
+          e = tame_exponents(e, X::kMost, 0, bad);
+          if (bad) atomicOr(&nan_tokens[tt % 3][t >> 3], bad << ((4 * t) & 31));
+        }
+        uint32_t w[4][4];
+        w[0][0] = X::template widen<0>(cr[q][0], exponent_field<0>(e));
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          auto one = [&]<int B>() {
+            w[0][B] = X::template widen<B>(cr[q][0], exponent_field<0>(e));
+            w[1][B] = X::template widen<B>(cr[q][1], exponent_field<1>(e));
+            w[2][B] = X::template widen<B>(cr[q][2], exponent_field<2>(e));
+            w[3][B] = X::template widen<B>(cr[q][3], exponent_field<3>(e));
+          };
+          if (b == 0) one.template operator()<0>();
+          if (b == 1) one.template operator()<1>();
+          if (b == 2) one.template operator()<2>();
+          if (b == 3) one.template operator()<3>();
+        }
+        const int chunk = 2 * (t >> 2) + (t & 1), half = (t >> 1) & 1;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          const uint32_t sel = d & 1 ? 0x07060302u : 0x05040100u;
+          uint2 v;
+          v.x = __builtin_amdgcn_perm(w[1][d / 2], w[0][d / 2], sel);
+          v.y = __builtin_amdgcn_perm(w[3][d / 2], w[2][d / 2], sel);
+          const int dim = 8 * od + d;
+          *(uint2*)(buf + K_BYTES + dim * 128 + (chunk ^ v_swizzle(dim)) * 16 + 8 * half) = v;
+        }
+      }
+    }
+  };
+
+  if (rg.t0 < rg.t1) {
+    int blk = block_of(rg.t0), blk1 = block_of(rg.t0 + 1);
+    fetch(rg.t0, blk);
+    if (tid < 6) nan_tokens[tid >> 1][tid & 1] = 0;
+    __syncthreads();
+    widen(rg.t0, smem);
+    fetch(rg.t0 + 1, blk1);  // past the end: block 0, unused
+    int blk2 = block_of(rg.t0 + 2);
+    __syncthreads();
+    for (int tt = rg.t0; tt < rg.t1; ++tt) {
+      const unsigned buf = ((tt - rg.t0) & 1) * BUF;
+      const int b0 = tt * kKvTile;
+      if (b0 < mine.hi && b0 + kKvTile > mine.lo) {
+        f32x16v sc[2];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sc[mt][e] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            // row 32 mt + c32, chunk 2 j + h
+            const u32x4v kf = *(const u32x4v*)(smem + ((buf + kat) ^ (32 * j & KX)) + (32 * j & ~KX) + mt * (64 * D));
+            sc[mt] = kv4_mfma32<F16>(kf, qf[j], sc[mt]);
+          }
+        // slot (mt, i): token 32 mt + 8 (i / 4) + 4 h + i % 4
+        const uint64_t some = BIG ? (blk >= 0 ? ~0ull : 0ull) : __ballot(blk >= 0);
+        const uint32_t nan0 = nan_tokens[tt % 3][0], nan1 = nan_tokens[tt % 3][1];
+        const bool whole = BIG ? blk >= 0 : some == ~0ull;
+        const bool bad = (nan0 | nan1) != 0;
+        if (!whole || bad || b0 + kKvTile > mine.least || b0 < mine.from) {
+          const int first = row.low - b0 - 4 * h, last = row.lim - b0 - 4 * h;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int x = 32 * mt + 8 * (e >> 2) + (e & 3);  // + 4 h
+              const bool there = (some >> (16 * (x >> 4))) & 1;
+              if (bad) sc[mt][e] = ((mt ? nan1 : nan0) >> ((x & 31) + 4 * h)) & 1 ? __builtin_nanf("") : sc[mt][e];
+              sc[mt][e] = x > last || x < first || !there ? kNegInf : sc[mt][e];
+            }
+        }
+        float mx = kNegInf;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) mx = __builtin_fmaxf(mx, sc[mt][e]);
+        const float top = halves_max(mx) * c;
+        const bool turn = top - m > kTopMost4;  // -inf - -inf is NaN: no new reference
+        if (__any(turn)) {
+          float nm = top - kTopSet4;
+          nm = top - nm > kTopMost4 ? top : nm;  // where scores have steps of 16, top - 8 may round to top - 16
+          const float al = turn ? __builtin_amdgcn_exp2f(m - nm) : 1.0f;
+          m = turn ? nm : m;
+          l *= al;
+          far |= uniform((int)__any(__builtin_fabsf(m) > kFarTop4 && m != kNegInf));
+#pragma unroll
+          for (int u = 0; u < NU; ++u) o[u] *= al;
+        }
+        const float ref = m == kNegInf ? 0.0f : m;
+        if (far) {
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sc[mt][e] = sc[mt][e] * c - ref;
+        } else {
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sc[mt][e] = __builtin_fmaf(sc[mt][e], c, -ref);
+        }
+        u32x4v pf[2][2];
+        float sum = 0.0f;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              const float w0 = __builtin_amdgcn_exp2f(sc[mt][8 * x + 2 * d]);
+              const float w1 = __builtin_amdgcn_exp2f(sc[mt][8 * x + 2 * d + 1]);
+              sum += w0;
+              sum += w1;
+              pf[mt][x][d] = X::pack(w0, w1);
+            }
+        l += sum;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+              // row 32 u + c32, chunk 4 mt + 2 x + h
+              const u32x4v vf = *(const u32x4v*)(smem + ((buf + vat) ^ (16 * ((4 * mt + 2 * x) ^ v_swizzle(32 * u)))) + 4096 * u);
+              o[u] = kv4_mfma32<F16>(vf, pf[mt][x], o[u]);
+            }
+      }
+      if (tid < 2) nan_tokens[(tt + 2) % 3][tid] = 0;
+      if (tt + 1 < rg.t1) {
+        widen(tt + 1, smem + ((tt + 1 - rg.t0) & 1) * BUF);
+        fetch(tt + 2, blk2);
+        blk = blk1;
+        blk1 = blk2;
+        blk2 = block_of(tt + 3);
+      }
+      __syncthreads();
+    }
+  }
+  l = halves_sum(l);
+  const int r = w0 + c32;
+  if (r >= it.k.rows) return;
+  const int64_t tok = it.r.first + r / p.g, hq = it.head * p.g + r % p.g;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (it.chunks > 1) {
+    const int64_t at = it.slot * p.rb + (r - r0);
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(f32x4v*)(p.po + at * D + 32 * u + 8 * q + 4 * h) =
+            f32x4v{o[u][4 * q] * inv, o[u][4 * q + 1] * inv, o[u][4 * q + 2] * inv, o[u][4 * q + 3] * inv};
+    const f32x2v ml = {l == l ? m : -kNegInf, l};  // NaN has the last word in the join
+    if (h == 0) *(f32x2v*)(p.ml + at * 2) = ml;
+  } else {
+    char* out = a.out + 2 * (tok * a.heads + hq) * D;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(uint2*)(out + 2 * (32 * u + 8 * q + 4 * h)) =
+            uint2{X::pack(o[u][4 * q] * inv, o[u][4 * q + 1] * inv), X::pack(o[u][4 * q + 2] * inv, o[u][4 * q + 3] * inv)};
+    if (a.lse && h == 0) a.lse[tok * a.heads + hq] = kv_lse(m, l);
+  }
+}
+
+namespace {
+int prompt4_rows(int dim) {
+  return dim == 64 ? Kv4PromptShape<64>::ROWS : dim == 128 ? Kv4PromptShape<128>::ROWS
+         : dim == 192 ? Kv4PromptShape<192>::ROWS : Kv4PromptShape<256>::ROWS;
+}
+}  // namespace
+
+bool kv4_attn_fits(const KvAttn& a) {
+  return kv_plan_fits(a, kv_plan(a, nullptr, prompt4_rows(a.c.dim)), 2 * prompt4_rows(a.c.dim));
+}
+
+size_t kv4_attn_workspace(const KvAttn& a) { return kv_plan(a, nullptr, prompt4_rows(a.c.dim)).need; }
 
 hipError_t launch_kv4_attn(const KvAttn& a, void* ws, hipStream_t s) {
-  const KvPlan p = kv_plan(a, (char*)ws, kFewRows);
+  const KvPlan p = kv_plan(a, (char*)ws, prompt4_rows(a.c.dim));
   if (p.planned) {
     const hipError_t e = launch_kv_starts(p, s);
     if (e != hipSuccess) return e;
   }
   auto dim = [&]<int D>() {
-    auto go = [&](const KvAttnArgs& w) {
-      const bool f16 = a.dtype == 2;
+    const bool f16 = a.dtype == 2;
+    if (p.run_many) {
+      auto k = a.c.tsh >= 6 ? (f16 ? k_kv4_prompt<D, true, true> : k_kv4_prompt<D, false, true>)
+                            : (f16 ? k_kv4_prompt<D, true, false> : k_kv4_prompt<D, false, false>);
+      hipLaunchKernelGGL(k, dim3((unsigned)p.many.items), dim3(64 * Kv4PromptShape<D>::NW), 0, s, p.many);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    if (p.run_few) {
       auto k = a.c.tsh >= 6 ? (f16 ? k_kv4_attn<D, true, true> : k_kv4_attn<D, false, true>)
                             : (f16 ? k_kv4_attn<D, true, false> : k_kv4_attn<D, false, false>);
-      hipLaunchKernelGGL(k, dim3((unsigned)w.items), dim3(256), 0, s, w);
-      return hipGetLastError();
-    };
-    hipError_t e = hipSuccess;
-    if (p.run_many) e = go(p.many);
-    if (e == hipSuccess && p.run_few) e = go(p.few);
-    if (e == hipSuccess && p.split) e = launch_kv_join(p, s);
-    return e;
+      hipLaunchKernelGGL(k, dim3((unsigned)p.few.items), dim3(256), 0, s, p.few);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return p.split ? launch_kv_join(p, s) : hipSuccess;
   };
   switch (a.c.dim) {
     case 64: return dim.template operator()<64>();
