@@ -537,9 +537,20 @@ __global__ __launch_bounds__(256) void k_kv4_attn(KvAttnArgs p) {
 //   O^T  lane: row c, dims 32 u + 8 (i / 4) + 4 h + i % 4
 // The tokens that a lane has of each 16 are its k slots in the second product; V's
 // tokens are stored in that order (quads 0, 2 | 1, 3 of each 16).
+// What bounds it: the exponentials, the sums and the widening on the vector unit (about
+// 1300 cycles per 32 rows and 64 tokens of 128 dims, the products 1024), LDS reads (half of
+// its rate) and the clock, 2.06 GHz under this load.  8192 tokens, 32 heads over 8 of 128:
+// 583 us, 0.94 Pflop/s (of 1.38 in a large product).  Taken and not taken: 4 waves and two
+// workgroups a CU (8 waves that multiply and weight in turns: 611, and 58 us for 42 where
+// prompts are short); a tile's scores formed while the one before is weighted: 660; a
+// block's number awaited behind the next tile's loads: 628.
+// Heads of 64 have registers for a third wave a SIMD: 349 us, two 387.  At 192 and 256 the
+// scores of 64 tokens beside the sums pass 256 registers, so they are formed 32 at a time,
+// and 8 waves share a tile, the only workgroup of its CU: 431 and 773 us (16 heads over 8),
+// for 498 of 64 tokens at a time and 995 of 4 waves with twice the registers.
 template <int D>
 struct Kv4PromptShape {
-  static constexpr int NW = D == 192 ? 8 : 4, WAVES = D == 256 ? 1 : 2;  // waves of a workgroup, per SIMD
+  static constexpr int NW = D >= 192 ? 8 : 4, WAVES = D == 64 ? 3 : 2;  // waves of a workgroup, per SIMD
   static constexpr int ROWS = 32 * NW;
 };
 typedef float f32x16v __attribute__((ext_vector_type(16)));
@@ -587,10 +598,13 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
   const int* table = a.q.table + (int64_t)it.seq * a.q.table_stride;
   // Block of a tile (BIG) or, in lanes 16 g .., of its 16 tokens g, or -1 where no row
   // sees them or there is none; its place among blocks and heads (0's if none).
-  auto block_of = [&](int tt) -> int {
+  // `entry` is asked for a tile before `known` uses it.
+  auto entry = [&](int tt) -> int {
     const int gp = tt * kKvTile + (BIG ? 0 : 16 * (lane >> 4));
     if (tt >= rg.t1 || gp >= rg.hi || (!BIG && gp + 16 <= rg.lo)) return -1;
-    int b = table[gp >> tsh];
+    return table[gp >> tsh];
+  };
+  auto known = [&](int b) -> int {
     b = b >= 0 && b < a.c.blocks ? b : -1;
     return BIG ? uniform(b) : b;
   };
@@ -692,110 +706,120 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
   };
 
   if (rg.t0 < rg.t1) {
-    int blk = block_of(rg.t0), blk1 = block_of(rg.t0 + 1);
+    int blk = known(entry(rg.t0)), blk1 = known(entry(rg.t0 + 1)), ahead = entry(rg.t0 + 2);
     fetch(rg.t0, blk);
     if (tid < 6) nan_tokens[tid >> 1][tid & 1] = 0;
     __syncthreads();
     widen(rg.t0, smem);
     fetch(rg.t0 + 1, blk1);  // past the end: block 0, unused
-    int blk2 = block_of(rg.t0 + 2);
     __syncthreads();
     for (int tt = rg.t0; tt < rg.t1; ++tt) {
       const unsigned buf = ((tt - rg.t0) & 1) * BUF;
       const int b0 = tt * kKvTile;
       if (b0 < mine.hi && b0 + kKvTile > mine.lo) {
-        f32x16v sc[2];
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) sc[mt][e] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            // row 32 mt + c32, chunk 2 j + h
-            const u32x4v kf = *(const u32x4v*)(smem + ((buf + kat) ^ (32 * j & KX)) + (32 * j & ~KX) + mt * (64 * D));
-            sc[mt] = kv4_mfma32<F16>(kf, qf[j], sc[mt]);
-          }
-        // slot (mt, i): token 32 mt + 8 (i / 4) + 4 h + i % 4
         const uint64_t some = BIG ? (blk >= 0 ? ~0ull : 0ull) : __ballot(blk >= 0);
         const uint32_t nan0 = nan_tokens[tt % 3][0], nan1 = nan_tokens[tt % 3][1];
-        const bool whole = BIG ? blk >= 0 : some == ~0ull;
-        const bool bad = (nan0 | nan1) != 0;
-        if (!whole || bad || b0 + kKvTile > mine.least || b0 < mine.from) {
-          const int first = row.low - b0 - 4 * h, last = row.lim - b0 - 4 * h;
+        const bool whole = some == ~0ull, bad = (nan0 | nan1) != 0;
+        // the tokens 32 M .. of the tile, in MT parts of 32
+        auto part = [&]<int M, int MT>() {
+          f32x16v sc[MT];
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int x = 32 * mt + 8 * (e >> 2) + (e & 3);  // + 4 h
-              const bool there = (some >> (16 * (x >> 4))) & 1;
-              if (bad) sc[mt][e] = ((mt ? nan1 : nan0) >> ((x & 31) + 4 * h)) & 1 ? __builtin_nanf("") : sc[mt][e];
-              sc[mt][e] = x > last || x < first || !there ? kNegInf : sc[mt][e];
+            for (int e = 0; e < 16; ++e) sc[mt][e] = 0.0f;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              // row 32 (M + mt) + c32, chunk 2 j + h
+              const u32x4v kf =
+                  *(const u32x4v*)(smem + ((buf + kat) ^ (32 * j & KX)) + (32 * j & ~KX) + (M + mt) * (64 * D));
+              sc[mt] = kv4_mfma32<F16>(kf, qf[j], sc[mt]);
             }
+          // slot (mt, i): token 32 (M + mt) + 8 (i / 4) + 4 h + i % 4
+          if (!whole || bad || b0 + kKvTile > mine.least || b0 < mine.from) {
+            const int first = row.low - b0 - 4 * h, last = row.lim - b0 - 4 * h;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int x = 32 * (M + mt) + 8 * (e >> 2) + (e & 3);  // + 4 h
+                const bool there = (some >> (16 * (x >> 4))) & 1;
+                if (bad) sc[mt][e] = ((x < 32 ? nan0 : nan1) >> ((x & 31) + 4 * h)) & 1 ? __builtin_nanf("") : sc[mt][e];
+                sc[mt][e] = x > last || x < first || !there ? kNegInf : sc[mt][e];
+              }
+          }
+          float mx = kNegInf;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mx = __builtin_fmaxf(mx, sc[mt][e]);
+          const float top = halves_max(mx) * c;
+          const bool turn = top - m > kTopMost4;  // -inf - -inf is NaN: no new reference
+          if (__any(turn)) {
+            float nm = top - kTopSet4;
+            nm = top - nm > kTopMost4 ? top : nm;  // where scores have steps of 16, top - 8 may round to top - 16
+            const float al = turn ? __builtin_amdgcn_exp2f(m - nm) : 1.0f;
+            m = turn ? nm : m;
+            l *= al;
+            far |= uniform((int)__any(__builtin_fabsf(m) > kFarTop4 && m != kNegInf));
+#pragma unroll
+            for (int u = 0; u < NU; ++u) o[u] *= al;
+          }
+          if constexpr (D > 128) __builtin_amdgcn_sched_barrier(0);
+          const float ref = m == kNegInf ? 0.0f : m;
+          if (far) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) sc[mt][e] = sc[mt][e] * c - ref;
+          } else {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) sc[mt][e] = __builtin_fmaf(sc[mt][e], c, -ref);
+          }
+          u32x4v pf[MT][2];
+          float sum = 0.0f;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                const float w0 = __builtin_amdgcn_exp2f(sc[mt][8 * x + 2 * d]);
+                const float w1 = __builtin_amdgcn_exp2f(sc[mt][8 * x + 2 * d + 1]);
+                sum += w0;
+                sum += w1;
+                pf[mt][x][d] = X::pack(w0, w1);
+              }
+          l += sum;
+          if constexpr (D > 128) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int u = 0; u < NU; ++u) {
+                // row 32 u + c32, chunk 4 (M + mt) + 2 x + h
+                const u32x4v vf = *(const u32x4v*)(smem + ((buf + vat) ^ (16 * ((4 * (M + mt) + 2 * x) ^ v_swizzle(32 * u)))) + 4096 * u);
+                o[u] = kv4_mfma32<F16>(vf, pf[mt][x], o[u]);
+              }
+        };
+        if constexpr (D <= 128) {
+          part.template operator()<0, 2>();
+        } else {  // the scores of 64 tokens do not fit the registers
+          part.template operator()<0, 1>();
+          part.template operator()<1, 1>();
         }
-        float mx = kNegInf;
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) mx = __builtin_fmaxf(mx, sc[mt][e]);
-        const float top = halves_max(mx) * c;
-        const bool turn = top - m > kTopMost4;  // -inf - -inf is NaN: no new reference
-        if (__any(turn)) {
-          float nm = top - kTopSet4;
-          nm = top - nm > kTopMost4 ? top : nm;  // where scores have steps of 16, top - 8 may round to top - 16
-          const float al = turn ? __builtin_amdgcn_exp2f(m - nm) : 1.0f;
-          m = turn ? nm : m;
-          l *= al;
-          far |= uniform((int)__any(__builtin_fabsf(m) > kFarTop4 && m != kNegInf));
-#pragma unroll
-          for (int u = 0; u < NU; ++u) o[u] *= al;
-        }
-        const float ref = m == kNegInf ? 0.0f : m;
-        if (far) {
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sc[mt][e] = sc[mt][e] * c - ref;
-        } else {
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sc[mt][e] = __builtin_fmaf(sc[mt][e], c, -ref);
-        }
-        u32x4v pf[2][2];
-        float sum = 0.0f;
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-              const float w0 = __builtin_amdgcn_exp2f(sc[mt][8 * x + 2 * d]);
-              const float w1 = __builtin_amdgcn_exp2f(sc[mt][8 * x + 2 * d + 1]);
-              sum += w0;
-              sum += w1;
-              pf[mt][x][d] = X::pack(w0, w1);
-            }
-        l += sum;
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-              // row 32 u + c32, chunk 4 mt + 2 x + h
-              const u32x4v vf = *(const u32x4v*)(smem + ((buf + vat) ^ (16 * ((4 * mt + 2 * x) ^ v_swizzle(32 * u)))) + 4096 * u);
-              o[u] = kv4_mfma32<F16>(vf, pf[mt][x], o[u]);
-            }
       }
       if (tid < 2) nan_tokens[(tt + 2) % 3][tid] = 0;
       if (tt + 1 < rg.t1) {
         widen(tt + 1, smem + ((tt + 1 - rg.t0) & 1) * BUF);
-        fetch(tt + 2, blk2);
         blk = blk1;
-        blk1 = blk2;
-        blk2 = block_of(tt + 3);
+        blk1 = known(ahead);
+        ahead = entry(tt + 3);
+        fetch(tt + 2, blk1);
       }
       __syncthreads();
     }
