@@ -318,8 +318,12 @@ __device__ inline void kv4_weights(f32x4v (&sc)[QT][4], const Kv4Row (&row)[QT],
 // Few rows per kv head (decoding): one tile of 16 rows, four waves that take the
 // chunk's tiles in turn, K and V straight from memory into MFMA operands.
 // BIG: blocks of 64 tokens and more, so a tile lies in one block (scalar addresses).
+// The cache's bytes bound it, where the waves hide their latency: 64 sequences of 300 to
+// 16384 tokens, 8 kv heads of 128, 134 us, 4.4 TB/s (5.1 in a large copy); with 2 waves a
+// SIMD 148, heads of 192 and 256 with one 171 and 188, now 127 and 144.  Block numbers are
+// asked for two tiles ahead, before loads that are not due yet: behind them 165 us.
 template <int D, bool F16, bool BIG>
-__global__ __launch_bounds__(256) void k_kv4_attn(KvAttnArgs p) {
+__global__ __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) void k_kv4_attn(KvAttnArgs p) {
   using X = Kv4Type<F16>;
   // spans of 128 dims (16 bytes of a K row a lane) and of 64 (8 bytes)
   constexpr int S128 = D / 128, S64 = D % 128 / 64, NS = S128 + S64, NJ = D / 32, NU = D / 16, G = D / 32;
@@ -342,10 +346,14 @@ __global__ __launch_bounds__(256) void k_kv4_attn(KvAttnArgs p) {
   const int* table = a.q.table + (int64_t)it.seq * a.q.table_stride;
 
   // Block of a tile (BIG) or of this lane group's 16 tokens of it, or -1: what no row
-  // sees and what has no block reads block 0, masked.
-  auto block_of = [&](int tt) -> int {
+  // sees and what has no block reads block 0, masked.  `entry` is asked for before the
+  // loads that `known` must not wait for.
+  auto entry = [&](int tt) -> int {
     const int gp = tt * kKvTile + (BIG ? 0 : 16 * h);
-    int blk = tt < rg.t1 && gp < hi && gp + (BIG ? kKvTile : 16) > lo ? table[gp >> tsh] : -1;
+    if (tt >= rg.t1 || gp >= hi || gp + (BIG ? kKvTile : 16) <= lo) return -1;
+    return table[gp >> tsh];
+  };
+  auto known = [&](int blk) -> int {
     if (blk >= a.c.blocks) blk = -1;
     return BIG ? scalar(blk) : blk;
   };
@@ -383,10 +391,12 @@ __global__ __launch_bounds__(256) void k_kv4_attn(KvAttnArgs p) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) vs[s] = *(const u32x4v*)(ep + (4 * s + (s < S128 ? c16 >> 2 : c16 >> 3)) * T);
   };
-  int tt = rg.t0 + wv, blk = -1, blk1 = -1;
+  int tt = rg.t0 + wv, blk = -1, blk1 = -1, ahead = -1;
   if (tt < rg.t1) {
-    blk = block_of(tt);
-    blk1 = block_of(tt + 4);
+    const int e0 = entry(tt), e1 = entry(tt + 4);
+    ahead = entry(tt + 8);
+    blk = known(e0);
+    blk1 = known(e1);
     load_k(tt, blk);
     load_v(tt, blk);
   }
@@ -433,8 +443,9 @@ __global__ __launch_bounds__(256) void k_kv4_attn(KvAttnArgs p) {
     const bool edge = __any(bad != 0 || !there) || b0 + kKvTile > rg.least || b0 < rg.from;
     int blk2 = -1;
     if (more) {
+      blk2 = known(ahead);
+      ahead = entry(tt + 12);
       load_k(tt + 4, blk1);
-      blk2 = block_of(tt + 8);
     }
     u32x4v pf[1][2];
     kv4_weights<F16, false, 1, NU>(sc, row, c, there, gp, edge, bad, st, pf);
