@@ -487,7 +487,15 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64) void k_mxfp4_tile(Mxfp4
 // thread two rows: 16 bytes [slab][lane group][step], turned into [lane group][slab][step],
 // so that a lane group gets its four in one dword, whose byte the matrix instruction
 // selects.
-__global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g) {
+// CHAINED, where rows end with such a pair of slabs: a workgroup walks through several
+// tiles, and what is asked for behind a tile's end is the next one's first slabs, which land
+// while results are stored (4096 x 14336 x 4096: 140 us, a workgroup per tile 145).
+// The products bound it, and the clock that they leave: a slab's take 2900 cycles of 3020,
+// at 1.97 GHz for 2.36 with constant data.  4096 x 14336 x 4096 140 us, 3.4 Pflop/s; at K =
+// 8192 252 us, 3.8.  A tile costs 6 us beside its slabs' 1.8 each, and 896 tiles leave half
+// of the CUs idle in the last of four rounds.
+template <bool CHAINED>
+__global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g, unsigned tiles) {
   constexpr int BM = 256, BN = 256, NT = 256, TI = 8, TJ = 8, SK = 128;
   constexpr int A_BYTES = BM * SK, STAGE = (BM + BN) * SK, E_AT = 2 * STAGE, QA = 8, QB = 8;
   __shared__ __attribute__((aligned(16))) uint8_t smem[E_AT + (BM + BN) * 32];
@@ -495,13 +503,16 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g) {
   const int wm = w >> 1, wn = w & 1;
   // XCD-aware order: each XCD owns a contiguous run of tiles, walked in
   // groups of eight row tiles, so that its L2 serves the shared slabs
-  const int64_t ntn = (g.N + BN - 1) / BN, ntm = (g.M + BM - 1) / BM, total = ntm * ntn;
-  const int64_t pid = blockIdx.x, per = total / 8;
-  const int64_t lid = pid < per * 8 ? (pid % 8) * per + pid / 8 : pid;
-  constexpr int64_t kGroupM = 8;
-  const int64_t ingroup = kGroupM * ntn, first = (lid / ingroup) * kGroupM;
-  const int64_t gsz = ntm - first < kGroupM ? ntm - first : kGroupM;
-  const int64_t m0 = (first + (lid % ingroup) % gsz) * BM, n0 = ((lid % ingroup) / gsz) * BN;
+  const unsigned ntn = (unsigned)((g.N + BN - 1) / BN), ntm = (unsigned)((g.M + BM - 1) / BM), per = tiles / 8;
+  int64_t m0, n0;
+  auto place = [&](unsigned pid) {
+    const unsigned lid = pid < per * 8 ? (pid % 8) * per + pid / 8 : pid;
+    constexpr unsigned kGroupM = 8;
+    const unsigned ingroup = kGroupM * ntn, first = (lid / ingroup) * kGroupM;
+    const unsigned gsz = ntm - first < kGroupM ? ntm - first : kGroupM;
+    m0 = (int64_t)__builtin_amdgcn_readfirstlane(first + (lid % ingroup) % gsz) * BM;
+    n0 = (int64_t)__builtin_amdgcn_readfirstlane((lid % ingroup) / gsz) * BN;
+  };
 
   // Swizzles: the sixteen lanes that a 16-byte LDS read takes at a time (rows 0 .. 7 of a
   // fragment, two lane groups) meet sixteen chunks; the rows of a B fragment are 4 j + 0 .. 3
@@ -509,29 +520,26 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g) {
   auto swizzle_a = [](int r) { return ((r >> 1) & 1) | (r & 4); };
   auto swizzle_b = [](int r) { return ((r >> 1) & 1) | ((r >> 2) & 4); };
   const int KB = (int)(g.K / 2), groups = (int)(g.K / 32);
-  const int rows_a = (int)(g.M - m0 < BM ? g.M - m0 : BM), rows_b = (int)(g.N - n0 < BN ? g.N - n0 : BN);
-  const uint8_t *base_a = g.a + m0 * g.lda, *base_b = g.b + n0 * g.ldb;
+  const uint8_t *base_a, *base_b, *exps_a, *exps_b;
   unsigned off_a[QA], off_b[QB];
+  auto aim = [&] {  // at the tile m0, n0
+    const int rows_a = (int)(g.M - m0 < BM ? g.M - m0 : BM), rows_b = (int)(g.N - n0 < BN ? g.N - n0 : BN);
+    const int t = (int)lane_value(tid);  // nothing of this is kept over a tile
+    base_a = g.a + m0 * g.lda;
+    base_b = g.b + n0 * g.ldb;
 #pragma unroll
-  for (int q = 0; q < QA; ++q) {
-    const int p = q * NT + tid, r = p >> 3;
-    off_a[q] = (unsigned)(r < rows_a ? r : rows_a - 1) * (unsigned)g.lda + 16 * ((p & 7) ^ swizzle_a(r));
-    off_b[q] = (unsigned)(r < rows_b ? r : rows_b - 1) * (unsigned)g.ldb + 16 * ((p & 7) ^ swizzle_b(r));
-  }
-  // this thread's rows of exponents: row tid of A and of B
-  const uint8_t* exps_a = g.sa + (m0 + (tid < rows_a ? tid : rows_a - 1)) * groups;
-  const uint8_t* exps_b = g.sb + (n0 + (tid < rows_b ? tid : rows_b - 1)) * groups;
+    for (int q = 0; q < QA; ++q) {
+      const int p = q * NT + t, r = p >> 3;
+      off_a[q] = (unsigned)(r < rows_a ? r : rows_a - 1) * (unsigned)g.lda + 16 * ((p & 7) ^ swizzle_a(r));
+      off_b[q] = (unsigned)(r < rows_b ? r : rows_b - 1) * (unsigned)g.ldb + 16 * ((p & 7) ^ swizzle_b(r));
+    }
+    // this thread's rows of exponents: row tid of A and of B
+    exps_a = g.sa + (m0 + (t < rows_a ? t : rows_a - 1)) * groups;
+    exps_b = g.sb + (n0 + (t < rows_b ? t : rows_b - 1)) * groups;
+  };
   // chunk c: groups 16 c .. 16 c + 15 (there are 16 at least).  The last one, where the row
   // ends in it, is put together once (exponents of 1 behind the end) and waits in LDS.
   uint8_t* rest = smem + E_AT + (BM + BN) * 16 + tid * 16;
-  if (groups % 16) {
-#pragma unroll 1
-    for (int e = 0; e < 16; ++e) {
-      const int i = groups / 16 * 16 + e;
-      rest[e] = i < groups ? exps_a[i] : 127;
-      rest[NT * 16 + e] = i < groups ? exps_b[i] : 127;
-    }
-  }
   u32x4_t next_a, next_b;
   auto ask_chunk = [&](int c) {
     const int at = 16 * c + 16 <= groups ? 16 * c : groups - 16;
@@ -544,7 +552,7 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g) {
                 __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
   };
   auto put_chunk = [&](int c) {
-    const bool ends = 16 * c + 16 > groups;
+    const bool ends = !CHAINED && 16 * c + 16 > groups;
     put_row(ends ? *(const u32x4_t*)rest : next_a, tid);
     put_row(ends ? *(const u32x4_t*)(rest + NT * 16) : next_b, BM + tid);
   };
@@ -568,10 +576,6 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g) {
   f32x4_t acc[TI][TJ];
   i32x4_t af[2][TI], bf[2][TJ];
   uint32_t ea[TI], eb[TJ];
-#pragma unroll
-  for (int i = 0; i < TI; ++i)
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   auto read = [&]<int X>(int stage) {  // step X of the slab in `stage`
     const unsigned a = lane_value((fa ^ (16 * X)) + stage * STAGE), b = lane_value((fb ^ (16 * X)) + stage * STAGE);
 #pragma unroll
@@ -597,7 +601,18 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g) {
     asm volatile("" ::: "memory");
   };
   constexpr int kLgkm0 = 0xC07F;  // s_waitcnt lgkmcnt(0)
-  if (nk) {
+  unsigned pid = blockIdx.x;
+  place(pid);
+  aim();
+  if (!CHAINED && groups % 16) {
+#pragma unroll 1
+    for (int e = 0; e < 16; ++e) {
+      const int i = groups / 16 * 16 + e;
+      rest[e] = i < groups ? exps_a[i] : 127;
+      rest[NT * 16 + e] = i < groups ? exps_b[i] : 127;
+    }
+  }
+  {
     ask_chunk(0);
     request(0, 0);
     put_chunk(0);
@@ -609,11 +624,25 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g) {
     fence();
     read_exponents();
     read.template operator()<0>(0);
-    // slab s, number Y of its chunk; a read or two loads among every four products
-    auto slab = [&]<int Y>(int s) {
+  }
+  for (;;) {  // the workgroup's tiles
+    const int64_t out_m = m0, out_n = n0;  // m0 and n0 go on to the next tile before this one is stored
+    const bool more = CHAINED && pid + gridDim.x < tiles;
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        asm volatile("" : "+a"(acc[i][j]));
+      }
+    asm volatile("s_nop 7");  // before a product takes what was just written
+    // Slab s, number Y of its chunk; asks for slab `next` in its place and (Y = 0) for
+    // chunk `chunk`, which is put down in Y = 1.  A read or two loads among every four
+    // products.
+    auto slab = [&]<int Y>(int next, int chunk) {
       constexpr int kQuads = TI * TJ / 4;
       const unsigned a1 = lane_value((fa ^ 16) + Y * STAGE), b1 = lane_value((fb ^ 16) + Y * STAGE);
-      if constexpr (Y == 0) ask_chunk(s / 2 + 1);
+      if constexpr (Y == 0) ask_chunk(chunk);
 #pragma unroll
       for (int p = 0; p < kQuads; ++p) {
         if (p < TJ) bf[1][p] = *(const i32x4_t*)(smem + b1 + 64 * SK * (p >> 2) + 4 * SK * (p & 3));
@@ -621,13 +650,13 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g) {
         multiply4.template operator()<0, Y>(p);
       }
       wait_vmcnt<0>();
-      if constexpr (Y == 1) put_chunk(s / 2 + 1);
+      if constexpr (Y == 1) put_chunk(chunk);
       __builtin_amdgcn_s_waitcnt(kLgkm0);
       fence();
       __builtin_amdgcn_s_barrier();
       fence();
       const unsigned a0 = lane_value(fa + (1 - Y) * STAGE), b0 = lane_value(fb + (1 - Y) * STAGE);
-      const int t = __builtin_amdgcn_readfirstlane(s + 2 < nk ? s + 2 : nk - 1);  // past the end: the last one again
+      const int t = __builtin_amdgcn_readfirstlane(next < nk ? next : nk - 1);  // past the end: the last one again
       uint8_t* st = smem + Y * STAGE + w * 1024;
       const uint8_t *ka = hidden(base_a + t * SK), *kb = hidden(base_b + t * SK);
 #pragma unroll
@@ -648,61 +677,74 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g) {
     };
     int s = 0;
     for (; s + 2 <= nk; s += 2) {
-      slab.template operator()<0>(s);
-      slab.template operator()<1>(s + 1);
+      const bool next = CHAINED && s + 2 == nk;
+      if (next && more) {
+        pid += gridDim.x;
+        place(pid);
+        aim();
+      }
+      const int chunk = next ? 0 : s / 2 + 1;
+      slab.template operator()<0>(next ? 0 : s + 2, chunk);
+      slab.template operator()<1>(next ? 1 : s + 3, chunk);
     }
-    if (s < nk) slab.template operator()<0>(s);
-    wait_vmcnt<0>();  // the slabs requested past the end have landed
-    __syncthreads();
-  }
-  if (KB % SK) {  // the rest of K, filled up with zeros (codes; exponents of 1)
-    auto fill = [&](uint8_t* at, const uint8_t* src, unsigned off, int chunk) {
-      i32x4_t v = {0, 0, 0, 0};
-      if (nk * SK + chunk < KB) v = *(const i32x4_t*)(src + nk * SK + off);
-      *(i32x4_t*)at = v;
-    };
-#pragma unroll
-    for (int q = 0; q < QA; ++q) {
-      const int p = q * NT + tid;
-      fill(smem + p * 16, base_a, off_a[q], 16 * ((p & 7) ^ swizzle_a(p >> 3)));
-      fill(smem + A_BYTES + p * 16, base_b, off_b[q], 16 * ((p & 7) ^ swizzle_b(p >> 3)));
+    if constexpr (!CHAINED) {
+      if (s < nk) slab.template operator()<0>(nk, s / 2 + 1);
     }
-    // the last chunk: this slab is its first or its second
-    u32x4_t va = *(const u32x4_t*)rest, vb = *(const u32x4_t*)(rest + NT * 16);
-    if (nk & 1) va = u32x4_t{va[2], va[3], va[2], va[3]}, vb = u32x4_t{vb[2], vb[3], vb[2], vb[3]};
-    put_row(va, tid);
-    put_row(vb, BM + tid);
-    __syncthreads();
-    read_exponents();
-    read.template operator()<0>(0);
-    read.template operator()<1>(0);
-#pragma unroll
-    for (int p = 0; p < TI * TJ / 4; ++p) {
-      multiply4.template operator()<0, 0>(p);
-      multiply4.template operator()<1, 0>(p);
+    if (!more) {
+      wait_vmcnt<0>();  // the slabs requested past the end have landed
+      __syncthreads();
     }
-  }
-  products_done();
-  // lane: row 16 i + fr, outputs 64 half + 16 h + 4 j + e
-  auto out = [&]<class T>(T) {
+    if (!CHAINED && KB % SK) {  // the rest of K, filled up with zeros (codes; exponents of 1)
+      auto fill = [&](uint8_t* at, const uint8_t* src, unsigned off, int chunk) {
+        i32x4_t v = {0, 0, 0, 0};
+        if (nk * SK + chunk < KB) v = *(const i32x4_t*)(src + nk * SK + off);
+        *(i32x4_t*)at = v;
+      };
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int64_t n = n0 + wn * 128 + 64 * half + 16 * h;
-      float bias[16];
+      for (int q = 0; q < QA; ++q) {
+        const int p = q * NT + tid;
+        fill(smem + p * 16, base_a, off_a[q], 16 * ((p & 7) ^ swizzle_a(p >> 3)));
+        fill(smem + A_BYTES + p * 16, base_b, off_b[q], 16 * ((p & 7) ^ swizzle_b(p >> 3)));
+      }
+      // the last chunk: this slab is its first or its second
+      u32x4_t va = *(const u32x4_t*)rest, vb = *(const u32x4_t*)(rest + NT * 16);
+      if (nk & 1) va = u32x4_t{va[2], va[3], va[2], va[3]}, vb = u32x4_t{vb[2], vb[3], vb[2], vb[3]};
+      put_row(va, tid);
+      put_row(vb, BM + tid);
+      __syncthreads();
+      read_exponents();
+      read.template operator()<0>(0);
+      read.template operator()<1>(0);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) bias[e] = g.bias ? g.bias[n + e < g.N ? n + e : g.N - 1] : -0.0f;  // y + -0 is y
-      const bool wide = n + 16 <= g.N;
-#pragma unroll
-      for (int i = 0; i < TI; ++i) {
-        const int64_t m = m0 + wm * 128 + 16 * i + fr;
-        const f32x4_t y[4] = {acc[i][4 * half], acc[i][4 * half + 1], acc[i][4 * half + 2], acc[i][4 * half + 3]};
-        if (m < g.M) mx_store16<T>(g, m, n, y, bias, wide);
+      for (int p = 0; p < TI * TJ / 4; ++p) {
+        multiply4.template operator()<0, 0>(p);
+        multiply4.template operator()<1, 0>(p);
       }
     }
-  };
-  if (g.dtype == 0) out(0.0f);
-  else if (g.dtype == 1) out((__bf16)0.0f);
-  else out((_Float16)0.0f);
+    products_done();
+    // lane: row 16 i + fr, outputs 64 half + 16 h + 4 j + e
+    const int l = (int)lane_value(lane);  // row numbers are not kept over the products
+    auto out = [&]<class T>(T) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int64_t n = out_n + wn * 128 + 64 * half + 16 * (l >> 4);
+        float bias[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) bias[e] = g.bias ? g.bias[n + e < g.N ? n + e : g.N - 1] : -0.0f;  // y + -0 is y
+        const bool wide = n + 16 <= g.N;
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+          const int64_t m = out_m + wm * 128 + 16 * i + (l & 15);
+          const f32x4_t y[4] = {acc[i][4 * half], acc[i][4 * half + 1], acc[i][4 * half + 2], acc[i][4 * half + 3]};
+          if (m < g.M) mx_store16<T>(g, m, n, y, bias, wide);
+        }
+      }
+    };
+    if (g.dtype == 0) out(0.0f);
+    else if (g.dtype == 1) out((__bf16)0.0f);
+    else out((_Float16)0.0f);
+    if (!more) break;
+  }
 }
 
 hipError_t launch_mxfp4_gemm(const Mxfp4Gemm& g, hipStream_t s) {
@@ -747,7 +789,10 @@ hipError_t launch_mxfp4_gemm(const Mxfp4Gemm& g, hipStream_t s) {
   // 256 x 256 / 256 x 128 / 128 x 128 / 64 x 64: 4096 x 14336: 141 / 168 / 193 / 278; 2048 x
   // 4096: 33 / 27 / 31 / 44; 1024 x 4096: 31 / 23 / 23 / 24.
   if (tiles(256, 256) >= cus && g.K >= 512) {
-    hipLaunchKernelGGL(k_mxfp4_wide, dim3((unsigned)tiles(256, 256)), dim3(256), 0, s, g);
+    const unsigned n = (unsigned)tiles(256, 256);
+    // (K in whole pairs of slabs: chained tiles, one workgroup a CU)
+    if (g.K % 512) hipLaunchKernelGGL(k_mxfp4_wide<false>, dim3(n), dim3(256), 0, s, g, n);
+    else hipLaunchKernelGGL(k_mxfp4_wide<true>, dim3(n < (unsigned)cus ? n : (unsigned)cus), dim3(256), 0, s, g, n);
     return hipGetLastError();
   }
   if (tiles(256, 128) >= cus) return tile.template operator()<256, 128, 64>();

@@ -88,6 +88,18 @@ def test_tiles(m, n, k, dtype):
     check(S.mxfp4_gemm(da, dsa, db, dsb, bias=dbias, dtype=DT[dtype]), a, sa, b, sb, bias, dtype)
 
 
+# more of the largest tiles than CUs, K in whole groups of exponents: a workgroup goes from
+# tile to tile (three times over the ragged edges; one, three groups of K)
+@pytest.mark.parametrize("m,n,k,dtype", [(300, 66000, 512, "f16"), (4097, 5000, 1536, "f32"), (66000, 257, 1024, "bf16")])
+def test_tiles_in_turn(m, n, k, dtype):
+    rng = np.random.default_rng(m + n)
+    a, sa = operand(rng, m, k, 122, 128)
+    b, sb = operand(rng, n, k, 122, 128)
+    bias = rng.standard_normal(n).astype(np.float32)
+    da, dsa, db, dsb, dbias = dev(a, sa, b, sb, bias)
+    check(S.mxfp4_gemm(da, dsa, db, dsb, bias=dbias, dtype=DT[dtype]), a, sa, b, sb, bias, dtype)
+
+
 def test_quantized_operands_and_leading_dims():
     rng = np.random.default_rng(5)
     x = torch.from_numpy(rng.standard_normal((2, 9, 512)).astype(np.float32)).to(DEV).bfloat16()
