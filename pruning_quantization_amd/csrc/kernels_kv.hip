@@ -1070,17 +1070,21 @@ int prompt_rows(int dim) {
   return dim == 64 ? kPromptRows<64> : dim == 128 ? kPromptRows<128> : dim == 192 ? kPromptRows<192> : kPromptRows<256>;
 }
 
+KvPlan plan_of(const KvAttn& a, void* ws) {
+  return kv_plan(a, (char*)ws, prompt_rows(a.c.dim), a.c.dim <= 128 ? 2 : 1);
+}
+
 }  // namespace
 
 bool kv_attn_fits(const KvAttn& a) {
-  return kv_plan_fits(a, kv_plan(a, nullptr, prompt_rows(a.c.dim)),
+  return kv_plan_fits(a, plan_of(a, nullptr),
                       a.c.dim == 64 ? 64 * KvPromptShape<64>::NW : 64 * KvPromptShape<128>::NW);
 }
 
-size_t kv_attn_workspace(const KvAttn& a) { return kv_plan(a, nullptr, prompt_rows(a.c.dim)).need; }
+size_t kv_attn_workspace(const KvAttn& a) { return plan_of(a, nullptr).need; }
 
 hipError_t launch_kv_attn(const KvAttn& a, void* ws, hipStream_t s) {
-  const KvPlan p = kv_plan(a, (char*)ws, prompt_rows(a.c.dim));
+  const KvPlan p = plan_of(a, ws);
   if (p.planned) {
     const hipError_t e = launch_kv_starts(p, s);
     if (e != hipSuccess) return e;

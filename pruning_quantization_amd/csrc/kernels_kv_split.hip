@@ -134,7 +134,7 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many
 // same count, with offsets both may be needed.  16 sequences of 4096 tokens, 4 kv
 // heads of 128: 32 rows 32 us in the prompt kernel, 60 in the other with two row
 // tiles a wave; 64 rows 39, and 108 with four.
-KvPlan kv_plan(const KvAttn& a, char* ws, int prompt_rows) {
+KvPlan kv_plan(const KvAttn& a, char* ws, int prompt_rows, int resident) {
   KvPlan p;
   const int g = a.heads / a.c.heads;
   const int64_t H = a.c.heads, rows = a.q.nper * g, cus = device_cu_count();
@@ -156,6 +156,7 @@ KvPlan kv_plan(const KvAttn& a, char* ws, int prompt_rows) {
     w.items = rt * H;
     w.plan = (int*)ws;
     w.starts = nullptr;
+    w.round = INT64_MAX;
     if (run && a.q.seqs > kScanned && (a.q.cu || split)) {
       w.starts = (int*)(ws + off);
       off += up((size_t)(a.q.seqs + 2) * 4);
@@ -189,7 +190,12 @@ KvPlan kv_plan(const KvAttn& a, char* ws, int prompt_rows) {
   // a chunk has one tile a wave at least, and four where unsplit sequences fill the
   // card twice (64 sequences of 1024: 26 and 48 us with one; 8 of 2048: 21 and 17)
   lay(p.few, p.run_few, rbf, 0, kFewRows, rtf * H >= 2 * cus ? 16 : 4, aim, rtf);
-  lay(p.many, p.run_many, rbm, kFewRows, INT32_MAX, 4, (a.c.dim <= 128 ? 2 : 1) * cus, rtm);
+  lay(p.many, p.run_many, rbm, kFewRows, INT32_MAX, 4, resident * cus, rtm);
+  // Causal row tiles that are all resident at once: a CU's second is dealt from the
+  // shortest up (two prompts of 1024 tokens, 32 heads over 8 of 128, in MXFP4 and FP8: 34
+  // and 44 us; the longest of the rest first, sequence by sequence, 45 and 60).
+  if (!a.q.cu && p.many.cmin == kNever && rtm * H > cus && rtm * H <= resident * cus && cus % H == 0)
+    p.many.round = cus / H;
   p.need = p.split || p.planned ? off : 0;
   if (!p.split) p.few.plan = p.many.plan = nullptr;
   return p;

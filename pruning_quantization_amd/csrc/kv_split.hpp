@@ -26,6 +26,7 @@ struct KvAttnArgs {
   int above, most;  // sequences with more than `above` and at most `most` rows
   int64_t target;   // items that the launch aims at
   int64_t items;    // items that it has room for
+  int64_t round;    // units that the CUs take up first, where a second round is dealt in reverse (else all)
   int cmin;         // least tiles of a chunk
   int* starts;      // [seqs + 2] or null: first unit of each sequence, all units, len (k_kv_plan)
   int* plan;        // [seqs][2]: first item / kv heads, chunks
@@ -118,9 +119,12 @@ __device__ inline bool kv_item(const KvAttnArgs& w, int64_t id, int lane, KvItem
   } else if (!w.a.q.cu && w.cmin == kNever) {
     const int rt = (int)((w.a.q.nper * w.g + w.rb - 1) / w.rb);
     it.len = kNever;
-    it.seq = (int)(unit / rt);
-    at = (int)(unit % rt);
-    if (it.seq >= seqs) return false;
+    if (unit >= seqs * rt) return false;
+    // the longest of all sequences first (8 prompts of 2048: 331 us, sequence by sequence
+    // 344); in a second round (`round`) the shortest first, beside the longest of the first
+    const int64_t u = unit < w.round ? unit : seqs * rt - 1 - (unit - w.round);
+    at = (int)(u / seqs);
+    it.seq = (int)(u % seqs);
   } else {
     it.len = w.cmin;
     if (w.cmin < kNever) {
@@ -212,7 +216,7 @@ struct KvPlan {
   bool run_few, run_many, split, planned;
   size_t need;
 };
-KvPlan kv_plan(const KvAttn& a, char* ws, int prompt_rows);
+KvPlan kv_plan(const KvAttn& a, char* ws, int prompt_rows, int resident);
 constexpr int64_t kMostThreads = UINT32_MAX;  // of a grid, along x
 // Whether the launches' grids hold it; threads: of a prompt workgroup.
 bool kv_plan_fits(const KvAttn& a, const KvPlan& p, int threads);

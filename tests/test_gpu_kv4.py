@@ -249,6 +249,15 @@ def test_same_count_strided(n, dtype, wide):
     check_attention(out, None, p, f64.reshape(3 * n, 12, 128)[:, :8], cu, dtype, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("seqs,dim,n", [(9, 128, 270), (13, 64, 270), (25, 64, 200)])
+def test_prompts_of_the_same_count(seqs, dim, n):
+    # two row tiles a CU (three, one), all resident at once: the second from the shortest up
+    p = Pool(seqs, [n + (7 * i) % 30 for i in range(seqs)], 8, dim, 32)
+    q, q64 = stored(p.rng.standard_normal((seqs, n, 16, dim)), "bf16")
+    out, lse = S.kv_attention(q, p.dev(), *p.args(), return_lse=True)
+    check_attention(out, lse, p, q64.reshape(seqs * n, 16, dim), np.arange(seqs + 1) * n, "bf16", dim ** -0.5)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_split_along_the_tokens(dtype):
     # far more tiles than one workgroup takes; a width that allows much more
