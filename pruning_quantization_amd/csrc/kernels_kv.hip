@@ -1071,7 +1071,7 @@ int prompt_rows(int dim) {
 }
 
 KvPlan plan_of(const KvAttn& a, void* ws) {
-  return kv_plan(a, (char*)ws, prompt_rows(a.c.dim), a.c.dim <= 128 ? 2 : 1);
+  return kv_plan(a, (char*)ws, 16, prompt_rows(a.c.dim), a.c.dim <= 128 ? 2 : 1);
 }
 
 }  // namespace

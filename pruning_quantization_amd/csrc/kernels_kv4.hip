@@ -234,11 +234,10 @@ struct Kv4State {
 // Scores of a tile to weights: lane: QT rows, slot 4 mt + i is token tok(mt, i) of the
 // lane group's 16 (tok0 = its first).  edge: some token is not seen by some row, or is NaN
 // (bad: by slot).  The sum is of the weights before their rounding.
-template <bool F16, bool ADJACENT, int QT, int NU>
+template <bool F16, int QT, int NU>
 __device__ inline void kv4_weights(f32x4v (&sc)[QT][4], const Kv4Row (&row)[QT], float c, bool there, int tok0,
                                    bool edge, uint32_t bad, Kv4State<QT, NU>& st, u32x4v (&pf)[QT][2]) {
-  // tokens of slot (mt, i): 4 mt + i (ADJACENT), or 4 i + mt
-  auto token = [](int mt, int i) { return ADJACENT ? 4 * mt + i : 4 * i + mt; };
+  auto token = [](int mt, int i) { return 4 * i + mt; };  // of slot (mt, i)
   if (edge) {
     if (__any(bad != 0)) {
 #pragma unroll
@@ -315,15 +314,19 @@ __device__ inline void kv4_weights(f32x4v (&sc)[QT][4], const Kv4Row (&row)[QT],
   }
 }
 
-// Few rows per kv head (decoding): one tile of 16 rows, four waves that take the
+// Few rows per kv head (decoding): QT tiles of 16 rows, four waves that take the
 // chunk's tiles in turn, K and V straight from memory into MFMA operands.
 // BIG: blocks of 64 tokens and more, so a tile lies in one block (scalar addresses).
 // The cache's bytes bound it, where the waves hide their latency: 64 sequences of 300 to
 // 16384 tokens, 8 kv heads of 128, 134 us, 4.4 TB/s (5.1 in a large copy); with 2 waves a
 // SIMD 148, heads of 192 and 256 with one 171 and 188, now 127 and 144.  Block numbers are
-// asked for two tiles ahead, before loads that are not due yet: behind them 165 us.
-template <int D, bool F16, bool BIG>
-__global__ __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) void k_kv4_attn(KvAttnArgs p) {
+// asked for two tiles ahead, before loads that are not due yet: behind them 165 us.  With
+// two row tiles every widened operand serves two products; they take half of the waves'
+// registers more, and a wave less a SIMD.
+template <int D, int QT>
+constexpr int Kv4FewWaves = QT == 1 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : (D == 64 ? 3 : D == 128 ? 2 : 1);  // per SIMD
+template <int D, bool F16, bool BIG, int QT>
+__global__ __launch_bounds__(256, (Kv4FewWaves<D, QT>)) void k_kv4_attn(KvAttnArgs p) {
   using X = Kv4Type<F16>;
   // spans of 128 dims (16 bytes of a K row a lane) and of 64 (8 bytes)
   constexpr int S128 = D / 128, S64 = D % 128 / 64, NS = S128 + S64, NJ = D / 32, NU = D / 16, G = D / 32;
@@ -332,15 +335,18 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) void k_kv4_att
   KvItem it;
   if (!kv_item(p, blockIdx.x, lane, it)) return;
   const int H = a.c.heads, tsh = a.c.tsh, T = 1 << tsh;
-  u32x4v qf[NJ];
-  const Kv4Row row[1] = {kv4_query<F16, 4>(p, it, it.rt * p.rb + c16, qf, [&](int j) {
-    return j / 4 < S128 ? 128 * (j / 4) + 32 * h + 8 * (j % 4) : 128 * S128 + 16 * h + 8 * (j % 4);
-  })};
+  u32x4v qf[QT][NJ];
+  Kv4Row row[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t)
+    row[t] = kv4_query<F16, 4>(p, it, it.rt * p.rb + 16 * t + c16, qf[t], [&](int j) {
+      return j / 4 < S128 ? 128 * (j / 4) + 32 * h + 8 * (j % 4) : 128 * S128 + 16 * h + 8 * (j % 4);
+    });
   const float c = a.scale * 1.44269504088896340736f;
-  Kv4State<1, NU> st;
+  Kv4State<QT, NU> st;
   st.init();
 
-  const int r0 = it.rt * p.rb, r1 = r0 + 16 < it.k.rows ? r0 + 16 : it.k.rows;
+  const int r0 = it.rt * p.rb, r1 = r0 + 16 * QT < it.k.rows ? r0 + 16 * QT : it.k.rows;
   const KvRange rg = kv_range(p, it, r0, r1);
   const int lo = rg.lo, hi = rg.hi;
   const int* table = a.q.table + (int64_t)it.seq * a.q.table_stride;
@@ -422,18 +428,27 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) void k_kv4_att
       bad |= (uint32_t)__shfl_xor((int)bad, 4, 64);  // the other groups of dims
       bad |= (uint32_t)__shfl_xor((int)bad, 8, 64);
     }
-    f32x4v sc[1][4];
+    f32x4v sc[QT][4];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) sc[0][mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) sc[t][mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
     auto scores = [&]<int MT>() {
 #pragma unroll
       for (int s = 0; s < S128; ++s)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          sc[0][MT] = X::mfma(X::widen8(kr[MT][s][j], exponent_field<MT>(ks[s])), qf[4 * s + j], sc[0][MT]);
+        for (int j = 0; j < 4; ++j) {
+          const u32x4v k = X::widen8(kr[MT][s][j], exponent_field<MT>(ks[s]));
+#pragma unroll
+          for (int t = 0; t < QT; ++t) sc[t][MT] = X::mfma(k, qf[t][4 * s + j], sc[t][MT]);
+        }
       if constexpr (S64) {
-        sc[0][MT] = X::mfma(X::widen8(k8[MT].x, exponent_field<MT>(ks[S128])), qf[4 * S128], sc[0][MT]);
-        sc[0][MT] = X::mfma(X::widen8(k8[MT].y, exponent_field<MT>(ks[S128])), qf[4 * S128 + 1], sc[0][MT]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const u32x4v k = X::widen8(j ? k8[MT].y : k8[MT].x, exponent_field<MT>(ks[S128]));
+#pragma unroll
+          for (int t = 0; t < QT; ++t) sc[t][MT] = X::mfma(k, qf[t][4 * S128 + j], sc[t][MT]);
+        }
       }
     };
     scores.template operator()<0>();
@@ -447,8 +462,8 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) void k_kv4_att
       ahead = entry(tt + 12);
       load_k(tt + 4, blk1);
     }
-    u32x4v pf[1][2];
-    kv4_weights<F16, false, 1, NU>(sc, row, c, there, gp, edge, bad, st, pf);
+    u32x4v pf[QT][2];
+    kv4_weights<F16, QT, NU>(sc, row, c, there, gp, edge, bad, st, pf);
     // slot 4 mt + i of V is token 4 i + mt: byte mt of exponent dword i
     auto out = [&]<int U0, int NB>(auto&& word, const u32x4v& ex) {  // NB bytes: 2 NB dims a lane
 #pragma unroll
@@ -476,8 +491,11 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) void k_kv4_att
             even[j] = __builtin_amdgcn_perm(w[2 * j + 1][b], w[2 * j][b], 0x05040100u);
             odd[j] = __builtin_amdgcn_perm(w[2 * j + 1][b], w[2 * j][b], 0x07060302u);
           }
-          st.o[0][U0 + 2 * b] = X::mfma(even, pf[0][x], st.o[0][U0 + 2 * b]);
-          st.o[0][U0 + 2 * b + 1] = X::mfma(odd, pf[0][x], st.o[0][U0 + 2 * b + 1]);
+#pragma unroll
+          for (int t = 0; t < QT; ++t) {
+            st.o[t][U0 + 2 * b] = X::mfma(even, pf[t][x], st.o[t][U0 + 2 * b]);
+            st.o[t][U0 + 2 * b + 1] = X::mfma(odd, pf[t][x], st.o[t][U0 + 2 * b + 1]);
+          }
         }
       }
     };
@@ -493,48 +511,52 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) void k_kv4_att
   constexpr int PITCH = D + 4;
   __shared__ float os[4][16][PITCH];
   __shared__ __attribute__((aligned(16))) float mls[4][16][2];  // reference, sum
-  st.l[0] = groups_sum(st.l[0]);
-  if (h == 0) *(f32x2v*)mls[wv][c16] = f32x2v{st.m[0], st.l[0]};
 #pragma unroll
-  for (int u = 0; u < NU; ++u)
+  for (int t = 0; t < QT; ++t) {
+    if (t) __syncthreads();  // the rows before are out
+    st.l[t] = groups_sum(st.l[t]);
+    if (h == 0) *(f32x2v*)mls[wv][c16] = f32x2v{st.m[t], st.l[t]};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int s = u / 8, d = s < S128 ? 128 * s + 8 * (4 * h + i) + u % 8 : 128 * S128 + 4 * (4 * h + i) + u % 8;
-      os[wv][c16][d] = st.o[0][u][i];
-    }
-  __syncthreads();
-  const int at = 4 * wv + h, sub = c16, g = scalar(p.g);
-  const int r = it.rt * p.rb + at;
-  if (r < it.k.rows) {
-    float top = kNegInf, f[4], sum = 0.0f;
+    for (int u = 0; u < NU; ++u)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) top = __builtin_fmaxf(top, mls[q][at][0]);
+      for (int i = 0; i < 4; ++i) {
+        const int s = u / 8, d = s < S128 ? 128 * s + 8 * (4 * h + i) + u % 8 : 128 * S128 + 4 * (4 * h + i) + u % 8;
+        os[wv][c16][d] = st.o[t][u][i];
+      }
+    __syncthreads();
+    const int at = 4 * wv + h, sub = c16, g = scalar(p.g);
+    const int r = it.rt * p.rb + 16 * t + at;
+    if (r < it.k.rows) {
+      float top = kNegInf, f[4], sum = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      f[q] = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mls[q][at][0] - top);
-      // a wave whose scores are all NaN has no reference, and a NaN sum
-      f[q] = mls[q][at][1] == mls[q][at][1] ? f[q] : __builtin_nanf("");
-      sum += mls[q][at][1] * f[q];
-    }
-    const int64_t tok = it.r.first + r / g, hq = it.head * g + r % g;
-    const bool split = it.chunks > 1;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t base = split ? (it.slot * p.rb + at) * D : (tok * a.heads + hq) * D;
+      for (int q = 0; q < 4; ++q) top = __builtin_fmaxf(top, mls[q][at][0]);
 #pragma unroll
-    for (int e = 0; e < D / 16; ++e) {
-      const int d = sub + 16 * e;
-      float v = 0.0f;
+      for (int q = 0; q < 4; ++q) {
+        f[q] = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mls[q][at][0] - top);
+        // a wave whose scores are all NaN has no reference, and a NaN sum
+        f[q] = mls[q][at][1] == mls[q][at][1] ? f[q] : __builtin_nanf("");
+        sum += mls[q][at][1] * f[q];
+      }
+      const int64_t tok = it.r.first + r / g, hq = it.head * g + r % g;
+      const bool split = it.chunks > 1;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const int64_t base = split ? (it.slot * p.rb + 16 * t + at) * D : (tok * a.heads + hq) * D;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v += os[q][at][d] * f[q];
-      if (split) p.po[base + d] = v * inv;
-      else kv_store_out(a, base + d, v * inv);
-    }
-    if (sub == 0) {
-      if (split) {
-        const f32x2v ml = {sum == sum ? top : -kNegInf, sum};  // NaN has the last word in the join
-        *(f32x2v*)(p.ml + (it.slot * p.rb + at) * 2) = ml;
-      } else if (a.lse) {
-        a.lse[tok * a.heads + hq] = kv_lse(top, sum);
+      for (int e = 0; e < D / 16; ++e) {
+        const int d = sub + 16 * e;
+        float v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v += os[q][at][d] * f[q];
+        if (split) p.po[base + d] = v * inv;
+        else kv_store_out(a, base + d, v * inv);
+      }
+      if (sub == 0) {
+        if (split) {
+          const f32x2v ml = {sum == sum ? top : -kNegInf, sum};  // NaN has the last word in the join
+          *(f32x2v*)(p.ml + (it.slot * p.rb + 16 * t + at) * 2) = ml;
+        } else if (a.lse) {
+          a.lse[tok * a.heads + hq] = kv_lse(top, sum);
+        }
       }
     }
   }
@@ -869,7 +891,11 @@ int prompt4_rows(int dim) {
 }
 // (three workgroups a CU with heads of 64: a mixed batch of 24 sequences 41.5 us, aimed at two 43.9)
 KvPlan plan_of(const KvAttn& a, void* ws) {
-  return kv_plan(a, (char*)ws, prompt4_rows(a.c.dim), a.c.dim == 64 ? 3 : a.c.dim == 128 ? 2 : 1);
+  // Two row tiles a wave where sequences have 17 to 32 rows each, or do on average (8 tokens
+  // on 64 sequences of 300..8192, 32 heads over 8: 105 us, by the prompt kernel 203; on 16 of
+  // 4096, 4 kv heads: 25.5 and 30.4; heads of 256, 300..4096: 198 and 573).
+  const int64_t rows = a.q.total * (a.heads / a.c.heads), seqs = a.q.seqs;  // (seqs: at least one)
+  return kv_plan(a, (char*)ws, rows > 16 * seqs && rows <= 32 * seqs ? 32 : 16, prompt4_rows(a.c.dim), a.c.dim == 64 ? 3 : a.c.dim == 128 ? 2 : 1);
 }
 }  // namespace
 
@@ -895,8 +921,11 @@ hipError_t launch_kv4_attn(const KvAttn& a, void* ws, hipStream_t s) {
       if (e != hipSuccess) return e;
     }
     if (p.run_few) {
-      auto k = a.c.tsh >= 6 ? (f16 ? k_kv4_attn<D, true, true> : k_kv4_attn<D, false, true>)
-                            : (f16 ? k_kv4_attn<D, true, false> : k_kv4_attn<D, false, false>);
+      auto kernel = [&]<int QT>() {
+        return a.c.tsh >= 6 ? (f16 ? k_kv4_attn<D, true, true, QT> : k_kv4_attn<D, false, true, QT>)
+                            : (f16 ? k_kv4_attn<D, true, false, QT> : k_kv4_attn<D, false, false, QT>);
+      };
+      auto k = p.few.rb == 16 ? kernel.template operator()<1>() : kernel.template operator()<2>();
       hipLaunchKernelGGL(k, dim3((unsigned)p.few.items), dim3(256), 0, s, p.few);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;

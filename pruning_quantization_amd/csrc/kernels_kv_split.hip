@@ -129,17 +129,17 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many
 
 // Which kernels run, their row tiles and the room for split results, from what
 // the host knows (shapes; lengths and offsets stay on the device).  Sequences of
-// at most 16 rows per kv head (query tokens times heads of the group) go to the
+// at most few_rows rows per kv head (query tokens times heads of the group) go to the
 // few-rows kernel, the others to the prompt kernel; without offsets all have the
 // same count, with offsets both may be needed.  16 sequences of 4096 tokens, 4 kv
 // heads of 128: 32 rows 32 us in the prompt kernel, 60 in the other with two row
 // tiles a wave; 64 rows 39, and 108 with four.
-KvPlan kv_plan(const KvAttn& a, char* ws, int prompt_rows, int resident) {
+KvPlan kv_plan(const KvAttn& a, char* ws, int few_rows, int prompt_rows, int resident) {
   KvPlan p;
   const int g = a.heads / a.c.heads;
   const int64_t H = a.c.heads, rows = a.q.nper * g, cus = device_cu_count();
-  p.run_few = a.q.cu || rows <= kFewRows;
-  p.run_many = a.q.cu ? a.q.total * g > kFewRows : rows > kFewRows;
+  p.run_few = a.q.cu || rows <= few_rows;
+  p.run_many = a.q.cu ? a.q.total * g > few_rows : rows > few_rows;
   const int64_t tiles = (a.q.cap + kKvTile - 1) / kKvTile;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   size_t off = up((size_t)a.q.seqs * 8);
@@ -151,7 +151,7 @@ KvPlan kv_plan(const KvAttn& a, char* ws, int prompt_rows, int resident) {
     w.above = above;
     w.most = most;
     w.target = target;
-    const bool split = run && tiles > kWholeTiles && (most == kFewRows || rt * H < target);
+    const bool split = run && tiles > kWholeTiles && (most == few_rows || rt * H < target);
     w.cmin = split ? cmin : kNever;
     w.items = rt * H;
     w.plan = (int*)ws;
@@ -174,11 +174,11 @@ KvPlan kv_plan(const KvAttn& a, char* ws, int prompt_rows, int resident) {
       w.ml = w.po = nullptr;
     }
   };
-  const int rbf = kFewRows, rbm = prompt_rows;
+  const int rbf = few_rows, rbm = prompt_rows;
   int64_t rtf = a.q.seqs * ((rows + rbf - 1) / rbf), rtm = a.q.seqs * ((rows + rbm - 1) / rbm);
   if (a.q.cu) {  // n rows make at most n / rb + 1 tiles
     rtf = a.q.total * g / rbf + a.q.seqs;
-    const int64_t most = a.q.seqs * ((kFewRows + rbf - 1) / rbf), longer = a.q.total * g / kFewRows;
+    const int64_t most = a.q.seqs, longer = a.q.total * g / few_rows;
     if (rtf > most) rtf = most;
     rtm = a.q.total * g / rbm + (longer < a.q.seqs ? longer : a.q.seqs);
   }
@@ -186,11 +186,19 @@ KvPlan kv_plan(const KvAttn& a, char* ws, int prompt_rows, int resident) {
   // sequence and head, at most eight items per CU (64 sequences of 300..16384
   // tokens: 248 / 227 / 219 us at two / four / eight; one of 131071: 61 / 65 / 80)
   int64_t aim = 64 * a.q.seqs * H;
-  aim = aim < 2 * cus ? 2 * cus : (aim > 8 * cus ? 8 * cus : aim);
-  // a chunk has one tile a wave at least, and four where unsplit sequences fill the
-  // card twice (64 sequences of 1024: 26 and 48 us with one; 8 of 2048: 21 and 17)
-  lay(p.few, p.run_few, rbf, 0, kFewRows, rtf * H >= 2 * cus ? 16 : 4, aim, rtf);
-  lay(p.many, p.run_many, rbm, kFewRows, INT32_MAX, 4, resident * cus, rtm);
+  // Two row tiles a wave: three a CU (8 tokens on 64 sequences of 300..8192, 32 heads over 8,
+  // MXFP4: 105 us, with two 119, with eight 113; on 32 of 2048: 37, 30, 57).
+  const int64_t per = few_rows > 16 ? 3 : 8;
+  aim = aim < 2 * cus ? 2 * cus : (aim > per * cus ? per * cus : aim);
+  // A chunk has one tile a wave at least, and four where unsplit sequences fill the
+  // card twice (64 sequences of 1024: 26 and 48 us with one; 8 of 2048: 21 and 17).  Two
+  // where that still gives every CU two (16 sequences of 4096, 4 kv heads of 128: MXFP4 18.7
+  // us, with one 21.2, e4m3 23.0 and 26.5; one of 8192, 8 heads: 14.0 and 13.1, 16.1 and
+  // 14.7), and with two row tiles a wave (5 tokens, the 16 sequences: 23.9 and 31.9).
+  const int64_t seen = a.window && a.window / kKvTile + 2 < tiles ? a.window / kKvTile + 2 : tiles;
+  const int least = rtf * H >= 2 * cus ? 16 : (few_rows > 16 || rtf * H * seen >= 16 * cus ? 8 : 4);
+  lay(p.few, p.run_few, rbf, 0, few_rows, least, aim, rtf);
+  lay(p.many, p.run_many, rbm, few_rows, INT32_MAX, 4, resident * cus, rtm);
   // Causal row tiles that are all resident at once: a CU's second is dealt from the
   // shortest up (two prompts of 1024 tokens, 32 heads over 8 of 128, in MXFP4 and FP8: 34
   // and 44 us; the longest of the rest first, sequence by sequence, 45 and 60).

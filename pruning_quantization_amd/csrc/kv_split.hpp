@@ -15,7 +15,6 @@ typedef float f32x2v __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4v __attribute__((ext_vector_type(4)));
 
 constexpr int kKvTile = 64;
-constexpr int kFewRows = 16;       // most rows per kv head of the few-rows kernel
 constexpr float kNegInf = -__builtin_inff();
 
 // Work of one launch: item = ((sequence, chunk, row tile), kv head).
@@ -216,7 +215,9 @@ struct KvPlan {
   bool run_few, run_many, split, planned;
   size_t need;
 };
-KvPlan kv_plan(const KvAttn& a, char* ws, int prompt_rows, int resident);
+// few_rows: most rows of the few-rows kernel, one row tile; prompt_rows: of a prompt
+// workgroup; resident: prompt workgroups that a CU holds.
+KvPlan kv_plan(const KvAttn& a, char* ws, int few_rows, int prompt_rows, int resident);
 constexpr int64_t kMostThreads = UINT32_MAX;  // of a grid, along x
 // Whether the launches' grids hold it; threads: of a prompt workgroup.
 bool kv_plan_fits(const KvAttn& a, const KvPlan& p, int threads);

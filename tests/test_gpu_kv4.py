@@ -258,6 +258,45 @@ def test_prompts_of_the_same_count(seqs, dim, n):
     check_attention(out, lse, p, q64.reshape(seqs * n, 16, dim), np.arange(seqs + 1) * n, "bf16", dim ** -0.5)
 
 
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,tokens,kv,group,n,kw", [
+    (64, 16, 2, 4, 5, {}), (128, 64, 1, 4, 8, {}), (192, 32, 2, 3, 6, {"window": 70}), (256, 128, 1, 8, 3, {}),
+    (128, 16, 1, 1, 17, {"causal": False}), (64, 64, 1, 32, 1, {}), (256, 16, 2, 2, 16, {"window": 5}),
+    (192, 64, 1, 7, 4, {})])
+def test_two_row_tiles(dim, tokens, kv, group, n, kw, dtype, wide):
+    # 17 to 32 rows per kv head: more tokens than the sequence has, ends in a tile, many tiles
+    lens = [n, n + 1, max(n - 2, 0), 64, 65, 700, 1023]
+    p = Pool(dim + n, lens, kv, dim, tokens, wide=wide)
+    p.ref[1][:, :, 0, :3], p.ref[3][:, :, -1, 5:7] = 255, 255
+    q, q64 = stored(p.rng.standard_normal((len(lens), n, kv * group, dim)), dtype)
+    clean = tuple(np.where(x == 255, 120, x).astype(np.uint8) if i % 2 else x for i, x in enumerate(p.ref))
+    cu = np.arange(len(lens) + 1) * n
+    out, lse = S.kv_attention(q, p.dev(clean), *p.args(), return_lse=True, **kw)
+    check_attention(out, lse, p, q64.reshape(-1, kv * group, dim), cu, dtype, dim ** -0.5, ref=clean, **kw)
+    # NaN scales of tokens that a row sees, and only they, make it NaN
+    nan = S.kv_attention(q, p.dev(), *p.args(), **kw).cpu()
+    seen = torch.zeros(len(lens), n, dtype=torch.bool)
+    for b, length in enumerate(lens):
+        for i in range(n):
+            pos = length - n + i
+            hi = min(pos + 1, length) if kw.get("causal", True) else length
+            lo = max(pos - kw["window"] + 1, 0) if kw.get("window") else 0
+            seen[b, i] = any(t % tokens in (0, 1, 2, 5, 6) for t in range(lo, hi))
+    assert nan[seen].isnan().all() and torch.equal(nan[~seen], out.cpu()[~seen])
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_counts_around_two_row_tiles(dim):
+    # offsets: 17 to 32 rows on average, from none to many in a sequence
+    news, lens = [5, 1, 0, 8, 4, 21, 7, 2], [900, 3, 50, 8, 1500, 21, 70, 2000]
+    p = Pool(dim, lens, 2, dim, 32)
+    cu, dcu = offsets(news)
+    q, q64 = stored(p.rng.standard_normal((cu[-1], 8, dim)), "bf16")
+    out, lse = S.kv_attention(q, p.dev(), *p.args(), cu_tokens=dcu, return_lse=True)
+    check_attention(out, lse, p, q64, cu, "bf16", dim ** -0.5)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_split_along_the_tokens(dtype):
     # far more tiles than one workgroup takes; a width that allows much more
