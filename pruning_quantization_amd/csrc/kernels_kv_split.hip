@@ -131,9 +131,9 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many
 // the host knows (shapes; lengths and offsets stay on the device).  Sequences of
 // at most few_rows rows per kv head (query tokens times heads of the group) go to the
 // few-rows kernel, the others to the prompt kernel; without offsets all have the
-// same count, with offsets both may be needed.  16 sequences of 4096 tokens, 4 kv
-// heads of 128: 32 rows 32 us in the prompt kernel, 60 in the other with two row
-// tiles a wave; 64 rows 39, and 108 with four.
+// same count, with offsets both may be needed.  (8 bits, 16 sequences of 4096 tokens, 4 kv
+// heads of 128: 32 rows 32 us in the prompt kernel, 60 in the other with two row tiles a
+// wave; 64 rows 39, and 108 with four.)
 KvPlan kv_plan(const KvAttn& a, char* ws, int few_rows, int prompt_rows, int resident) {
   KvPlan p;
   const int g = a.heads / a.c.heads;
