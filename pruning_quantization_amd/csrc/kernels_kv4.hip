@@ -572,11 +572,13 @@ __global__ __launch_bounds__(256, (Kv4FewWaves<D, QT>)) void k_kv4_attn(KvAttnAr
 // tokens are stored in that order (quads 0, 2 | 1, 3 of each 16).
 // What bounds it: the exponentials, the sums and the widening on the vector unit (about
 // 1300 cycles per 32 rows and 64 tokens of 128 dims, the products 1024), LDS reads (half of
-// its rate) and the clock, 2.06 GHz under this load.  8192 tokens, 32 heads over 8 of 128:
-// 583 us, 0.94 Pflop/s (of 1.38 in a large product).  Taken and not taken: 4 waves and two
-// workgroups a CU (8 waves that multiply and weight in turns: 611, and 58 us for 42 where
-// prompts are short); a tile's scores formed while the one before is weighted: 660; a
-// block's number awaited behind the next tile's loads: 628.
+// its rate) and the clock, 2.0 GHz under this load.  8192 tokens, 32 heads over 8 of 128:
+// 572 us, 0.96 Pflop/s (of 1.38 in a large product); 570 to 690 us by card.  Taken and not
+// taken, each pair on one card: 4 waves and two workgroups a CU (8 waves that multiply and
+// weight in turns: level, 476 us for 434 at heads of 192, and 58 for 43 where prompts are
+// short); a tile's scores formed while the one before is weighted: 660 for 628; waves
+// without rows that share the others' tokens: 640 for 575; codes asked for two tiles ahead:
+// level.
 // Heads of 64 have registers for a third wave a SIMD: 349 us, two 387.  At 192 and 256 the
 // scores of 64 tokens beside the sums pass 256 registers, so they are formed 32 at a time,
 // and 8 waves share a tile, the only workgroup of its CU: 431 and 773 us (16 heads over 8),
@@ -631,14 +633,17 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
   const int* table = a.q.table + (int64_t)it.seq * a.q.table_stride;
   // Block of a tile (BIG) or, in lanes 16 g .., of its 16 tokens g, or -1 where no row
   // sees them or there is none; its place among blocks and heads (0's if none).
-  // `entry` is asked for a tile before `known` uses it.
+  // `entry` is asked for a tile before `known` uses it, and without a branch, behind
+  // which the value would be copied and so waited for at once.
+  auto first_of = [&](int tt) { return tt * kKvTile + (BIG ? 0 : 16 * (lane >> 4)); };
   auto entry = [&](int tt) -> int {
-    const int gp = tt * kKvTile + (BIG ? 0 : 16 * (lane >> 4));
-    if (tt >= rg.t1 || gp >= rg.hi || (!BIG && gp + 16 <= rg.lo)) return -1;
-    return table[gp >> tsh];
+    const int gp = first_of(tt);
+    return table[(gp < rg.hi ? gp : rg.hi - 1) >> tsh];  // (hi > 0 where there is a tile)
   };
-  auto known = [&](int b) -> int {
-    b = b >= 0 && b < a.c.blocks ? b : -1;
+  auto known = [&](int b, int tt) -> int {
+    const int gp = first_of(tt);
+    const bool none = tt >= rg.t1 || gp >= rg.hi || (!BIG && gp + 16 <= rg.lo) || b < 0 || b >= a.c.blocks;
+    b = none ? -1 : b;
     return BIG ? uniform(b) : b;
   };
   auto place = [&](int blk) -> int64_t { return (int64_t)(blk < 0 ? 0 : blk) * H + it.head; };
@@ -739,7 +744,7 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
   };
 
   if (rg.t0 < rg.t1) {
-    int blk = known(entry(rg.t0)), blk1 = known(entry(rg.t0 + 1)), ahead = entry(rg.t0 + 2);
+    int blk = known(entry(rg.t0), rg.t0), blk1 = known(entry(rg.t0 + 1), rg.t0 + 1), ahead = entry(rg.t0 + 2);
     fetch(rg.t0, blk);
     if (tid < 6) nan_tokens[tid >> 1][tid & 1] = 0;
     __syncthreads();
@@ -850,7 +855,7 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
       if (tt + 1 < rg.t1) {
         widen(tt + 1, smem + ((tt + 1 - rg.t0) & 1) * BUF);
         blk = blk1;
-        blk1 = known(ahead);
+        blk1 = known(ahead, tt + 2);
         ahead = entry(tt + 3);
         fetch(tt + 2, blk1);
       }
