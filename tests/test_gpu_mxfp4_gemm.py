@@ -188,3 +188,61 @@ def test_refusals():
     wide = torch.zeros(4, 40, dtype=torch.uint8, device=DEV)
     with pytest.raises(S.Sparq24Error):                                   # rows 40 bytes apart
         S.mxfp4_gemm(wide[:, :32], s, c, s)
+
+
+def test_offsets_past_32_bits():
+    # operand, and rows 8 MiB apart (where the tiles' 32-bit offsets end)
+    rng = np.random.default_rng(41)
+    m, n, k = 70000, 40, 131072
+    b, sb = operand(rng, n, k)
+    tail, stail = operand(rng, 5, k)
+    a = torch.zeros(m, k // 2, dtype=torch.uint8, device=DEV)
+    sa = torch.full((m, k // 32), 127, dtype=torch.uint8, device=DEV)
+    a[-5:], sa[-5:] = dev(tail, stail)
+    db, dsb = dev(b, sb)
+    got = S.mxfp4_gemm(a, sa, db, dsb)
+    assert not got[:-5].any()
+    check(got[-5:], tail, stail, b, sb, None, "f32")
+    rows = a.view(-1).as_strided((37, k // 2), (1 << 23, 1))
+    few, sfew = operand(rng, 37, k)
+    rows.copy_(dev(few)[0])
+    check(S.mxfp4_gemm(rows, dev(sfew)[0], db, dsb), few, sfew, b, sb, None, "f32")
+    check(S.mxfp4_gemm(db, dsb, rows, dev(sfew)[0]), b, sb, few, sfew, None, "f32")
+
+
+def test_an_output_past_32_bits():
+    rng = np.random.default_rng(42)
+    m, n, k = 40000, 70000, 32
+    a, sa = operand(rng, m, k)
+    b, sb = operand(rng, n, k)
+    got = S.mxfp4_gemm(*dev(a, sa, b, sb), dtype=torch.bfloat16)
+    for at in (slice(0, 3), slice(m - 3, m)):
+        check(got[at], a[at], sa[at], b, sb, None, "bf16")
+
+
+def test_streams_at_once_and_a_captured_product():
+    # few rows, tiles, tiles in turn: on two side streams at once, then replayed on new operands
+    rng = np.random.default_rng(43)
+    ops = [dev(*operand(rng, m, k, 122, 128), *operand(rng, n, k, 122, 128))
+           for m, n, k in ((48, 4000, 1056), (700, 900, 512), (300, 66000, 512))]
+    want = [S.mxfp4_gemm(*o) for o in ops]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(3):
+        for s, out in zip(streams, got):
+            with torch.cuda.stream(s):
+                out.append([S.mxfp4_gemm(*o) for o in ops])
+    torch.cuda.synchronize()
+    for outs in got:
+        assert all(torch.equal(w, y) for ys in outs for w, y in zip(want, ys))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ys = [S.mxfp4_gemm(*o) for o in ops]
+    for step in range(3):
+        for o in ops:
+            o[0].copy_(o[0].roll(step + 1, 0))
+        eager = [S.mxfp4_gemm(*o) for o in ops]
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, e) for y, e in zip(ys, eager))

@@ -174,3 +174,47 @@ def test_refusals():
                 lambda: S.rmsnorm_quantize(x, w, "nvfp4")):
         with pytest.raises(S.Sparq24Error):
             bad()
+
+
+def test_offsets_past_32_bits():
+    rows, k = 1100000, 2048
+    x = torch.randn(rows, k, device=DEV).bfloat16()
+    res = torch.randn(rows, k, device=DEV).bfloat16()
+    w = torch.ones(k, device=DEV)
+    for q in ("fp8", "mxfp4"):
+        got = S.rmsnorm_quantize(x, w, q, residual=res)
+        for at in (slice(0, 2), slice(rows - 3, rows)):
+            part = S.rmsnorm_quantize(x[at].contiguous(), w, q, residual=res[at].contiguous())
+            assert all(torch.equal(a[at], b) for a, b in zip(got, part))
+
+
+def test_streams_at_once_and_a_captured_norm():
+    xs = [torch.randn(70, 4096, device=DEV).bfloat16(), torch.randn(3, 96, device=DEV).half()]
+    rs = [torch.randn_like(x) for x in xs]
+    ws = [torch.randn(x.shape[-1], device=DEV).to(x.dtype) for x in xs]
+
+    def run():
+        return [y for x, r, w in zip(xs, rs, ws) for q in ("mxfp4", ("int", 8))
+                for y in S.rmsnorm_quantize(x, w, q, residual=r)]
+
+    want = run()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(run())
+    torch.cuda.synchronize()
+    assert all(torch.equal(w, y) for ys in got for w, y in zip(want, ys))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ys = run()
+    for step in range(3):
+        for x, r in zip(xs, rs):
+            x.copy_(x.roll(1, 0))
+            r.mul_(0.5)
+        eager = run()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, e) for y, e in zip(ys, eager))
