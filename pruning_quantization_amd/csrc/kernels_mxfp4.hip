@@ -266,8 +266,8 @@ __device__ inline uint32_t load_any(const uint8_t* p, unsigned o) { return *(glo
 
 // c += b a with byte X of both exponents, c in accumulation registers and in place: with
 // the builtin the compiler gives results registers of their own, which a wave that
-// accumulates in half of its registers does not have.  What reads c afterwards waits with
-// products_done() first.
+// accumulates in half of its registers does not have.  The compiler puts no waits around it:
+// before the first product and behind the last one stands settle().
 template <int X>
 __device__ inline void mx_product_at(i32x4_t b, i32x4_t a, f32x4_t& c, uint32_t sb, uint32_t sa) {
 #define SPARQ24_MXFP4_ASM(sel)                                                                   \
@@ -278,7 +278,23 @@ __device__ inline void mx_product_at(i32x4_t b, i32x4_t a, f32x4_t& c, uint32_t 
   if constexpr (X == 2) SPARQ24_MXFP4_ASM("op_sel_hi:[1,1,0]");
   if constexpr (X == 3) SPARQ24_MXFP4_ASM("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
 }
-__device__ inline void products_done() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+// Waits until products are done, or what they start from is written.  All accumulators go
+// through asm on both sides of the wait (which yields no instruction), so that neither
+// copies out of them nor zeros into them can pass it.
+template <int TI, int TJ>
+__device__ inline void settle(f32x4_t (&c)[TI][TJ]) {
+  auto hold = [&] {
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) asm volatile("" : "+a"(c[i][j]));
+  };
+  hold();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  hold();
+}
 
 // Many rows: a BM x BN tile per workgroup, waves of WM x 64.  Slabs of 256 codes go from
 // memory straight into LDS (global_load_lds) into two buffers, their 16-byte chunks
@@ -631,11 +647,8 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g, unsigned til
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        asm volatile("" : "+a"(acc[i][j]));
-      }
-    asm volatile("s_nop 7");  // before a product takes what was just written
+      for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    settle(acc);
     // Slab s, number Y of its chunk; asks for slab `next` in its place and (Y = 0) for
     // chunk `chunk`, which is put down in Y = 1.  A read or two loads among every four
     // products.
@@ -690,6 +703,7 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g, unsigned til
     if constexpr (!CHAINED) {
       if (s < nk) slab.template operator()<0>(nk, s / 2 + 1);
     }
+    settle(acc);
     if (!more) {
       wait_vmcnt<0>();  // the slabs requested past the end have landed
       __syncthreads();
@@ -720,8 +734,8 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g, unsigned til
         multiply4.template operator()<0, 0>(p);
         multiply4.template operator()<1, 0>(p);
       }
+      settle(acc);
     }
-    products_done();
     // lane: row 16 i + fr, outputs 64 half + 16 h + 4 j + e
     const int l = (int)lane_value(lane);  // row numbers are not kept over the products
     auto out = [&]<class T>(T) {
