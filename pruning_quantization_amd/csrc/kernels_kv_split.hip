@@ -82,8 +82,10 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many
   const int nrt = (r.n * p.g + p.rb - 1) / p.rb, rt = row / p.rb, rr = row % p.rb;
   const int head = hq / p.g;
   const int64_t first = p.plan[2 * seq];
-  // offsets that do not ascend can ask for more items than there is room for
-  if (first < 0 || (first + (int64_t)chunks * nrt) * a.c.heads > p.items) return;
+  // Offsets that do not ascend can ask for more items than there is room for.  A sequence
+  // that got none has no entry in the plan: what stands there is any number, also where
+  // nothing was split.
+  if (!p.ml || first < 0 || chunks > p.items || first + (int64_t)chunks * nrt > p.items / a.c.heads) return;
   const int64_t at0 = ((first + nrt - 1 - rt) * a.c.heads + head) * p.rb + rr;
   const int64_t step = (int64_t)nrt * a.c.heads * p.rb;
   // the common reference: the largest sum's own exponent, so that no chunk's weight passes 2
