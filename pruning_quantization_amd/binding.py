@@ -704,8 +704,9 @@ def mxfp4_gemm(codes_a: torch.Tensor, scale_a: torch.Tensor, codes_b: torch.Tens
     """C = A B^T (+ bias) from the MXFP4 codes [..., K/2], [N, K/2] and E8M0
     bytes [..., K/32], [N, K/32] of :func:`quantize`, exact products in fp32 sums
     -> ``dtype`` (fp32, bf16 or fp16) [..., N].  K is a multiple of 32; the rows
-    of either operand's codes and of ``out`` may be strided; ``bias`` is fp32
-    [N].  A scale byte of 255 makes its row (column) NaN."""
+    of either operand's codes and of ``out`` may be strided; scales are contiguous,
+    with the leading dims of their codes or [rows, K/32]; ``bias`` is fp32 [N].  A
+    scale byte of 255 makes its row (column) NaN."""
     return (_serving_module or _serving()).mxfp4_gemm(codes_a, scale_a, codes_b, scale_b, bias, dtype, out)
 
 

@@ -71,6 +71,15 @@ T* vector(const Tensor& t, int64_t n, ScalarType type, const char* name) {
   return (T*)t.data_ptr();
 }
 
+// Scale bytes of rows of codes: their leading dims, or all rows in one, and then the groups.
+uint8_t* scales(const Tensor& t, const Tensor& codes, int64_t rows, int64_t groups, const char* name) {
+  const auto lead = codes.sizes().slice(0, codes.dim() - 1);
+  const bool alike = t.dim() == codes.dim() && t.sizes().slice(0, t.dim() - 1) == lead;
+  if (t.dim() < 1 || t.size(-1) != groups || !(alike || (t.dim() == 2 && t.size(0) == rows)))
+    value_error(std::string(name) + " must be [..., K / 32] beside codes " + shape_of(codes) + ", got " + shape_of(t));
+  return vector<uint8_t>(t, rows * groups, ScalarType::Byte, name);
+}
+
 // All tensors on one GPU; its index.  Last of a call's checks.
 int device_of(std::initializer_list<const Tensor*> ts) {
   const Tensor* first = *ts.begin();
@@ -219,8 +228,8 @@ PyObject* py_mxfp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t argc) {
     Product p(a, argc, ScalarType::Byte, "uint8 (two to a byte)");
     if (p.width % 16) value_error("rows of codes hold groups of 32 (16 bytes), got " + shape_of(p.ca));
     const int64_t groups = p.width / 16;
-    uint8_t* psa = vector<uint8_t>(p.sa, p.m * groups, ScalarType::Byte, "scale_a");
-    uint8_t* psb = vector<uint8_t>(p.sb, p.n * groups, ScalarType::Byte, "scale_b");
+    uint8_t* psa = scales(p.sa, p.ca, p.m, groups, "scale_a");
+    uint8_t* psb = scales(p.sb, p.cb, p.n, groups, "scale_b");
     return p.run("sparq24_mxfp4_gemm", [&](void* out, hipStream_t s) {
       return c_mxfp4_gemm((const uint8_t*)p.ca.data_ptr(), p.lda, psa, p.m, (const uint8_t*)p.cb.data_ptr(), p.ldb,
                           psb, p.n, 2 * p.width, p.pbias, p.code, out, p.ldc, nullptr, nullptr, s);
