@@ -27,8 +27,11 @@ inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 int esize(int dtype) { return dtype == SPARQ24_F32 ? 4 : 2; }
 
 // Structural checks of an operand; fills the kernel view (strides in bytes,
-// back-to-back batches folded into rows).
-sparq24_status check_tensor(const sparq24_tensor* x, bool allow_transposed, RowDesc& d) {
+// back-to-back batches folded into rows).  Most kernels have the batches that
+// are left along grid.y or grid.z, at most kMostBatches.
+constexpr int64_t kMostBatches = 65535;
+sparq24_status check_tensor(const sparq24_tensor* x, bool allow_transposed, RowDesc& d,
+                            int64_t most_batches = kMostBatches) {
   if (!x) return SPARQ24_ERR_INVALID;
   if (x->dtype != SPARQ24_F32 && x->dtype != SPARQ24_BF16 && x->dtype != SPARQ24_F16)
     return SPARQ24_ERR_INVALID;
@@ -84,7 +87,7 @@ sparq24_status check_tensor(const sparq24_tensor* x, bool allow_transposed, RowD
   } else {
     return SPARQ24_ERR_UNSUPPORTED;
   }
-  if (d.B > 65535) return SPARQ24_ERR_UNSUPPORTED;
+  if (d.B > most_batches) return SPARQ24_ERR_UNSUPPORTED;
   return SPARQ24_OK;
 }
 
@@ -842,7 +845,7 @@ sparq24_status sparq24_rmsnorm_quantize(const sparq24_tensor* x, const sparq24_t
   RmsNorm n{};
   NormRows* rows[3] = {&n.x, &n.res, &n.sum};
   for (int i = 0; i < (residual ? 3 : 1); ++i) {
-    CHECK(check_tensor(t[i], false, d[i]));
+    CHECK(check_tensor(t[i], false, d[i], INT32_MAX));  // rows are numbered over all batches
     if (t[i]->dtype != x->dtype) return SPARQ24_ERR_UNSUPPORTED;
     if (t[i]->batch != x->batch || t[i]->rows != x->rows || t[i]->k != x->k) return SPARQ24_ERR_SHAPE;
     *rows[i] = NormRows{(char*)d[i].x, d[i].R, d[i].bs, d[i].rs};

@@ -1,7 +1,10 @@
 """Refusals of the 4-bit serving calls that hold on the host."""
+import ctypes
+
 import pytest
 
 import pruning_quantization_amd as S
+import pruning_quantization_amd.binding as B
 
 torch = pytest.importorskip("torch")
 
@@ -31,3 +34,35 @@ def test_product_scales_that_do(codes, scales):
     w, ws = u8(5, codes[-1]), u8(5, codes[-1] // 16)
     with pytest.raises(ValueError, match="on a GPU"):
         S.mxfp4_gemm(u8(*codes), u8(*scales), w, ws)
+
+
+# --- the norm at the C interface ---------------------------------------------
+
+FAKE = 0x7F0000000000
+OK, INVALID, UNSUPPORTED, SHAPE, ALIGN, WORKSPACE, DEVICE = 0, 1, 2, 3, 4, 5, 6
+
+
+def rows(dtype=B.BF16, batch=1, rows=4, k=64, bs=None, rs=None, data=FAKE):
+    rs = k if rs is None else rs
+    return B.CTensor(data, dtype, batch, rows, k, rows * rs if bs is None else bs, rs, 1)
+
+
+def norm(x, res=None, total=None, fmt=B.Q_FP8):
+    ref = lambda t: ctypes.byref(t) if t is not None else None  # noqa: E731
+    q = B.CQSpec(fmt, 0, None)
+    return B.lib().sparq24_rmsnorm_quantize(ref(x), ref(res), FAKE, B.F32, 1e-6, ctypes.byref(q), FAKE, FAKE,
+                                            ref(total), None)
+
+
+@pytest.fixture()
+def no_gpu():
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+
+
+def test_norm_of_many_batches(no_gpu):
+    heads = dict(batch=70000, rows=4, bs=640)          # heads of a fused projection, token by token
+    assert norm(rows(**heads)) == DEVICE
+    assert norm(rows(**heads), rows(batch=70000), rows(**heads)) == DEVICE
+    assert norm(rows(batch=70000, rows=1, bs=640)) == DEVICE
+    assert norm(rows(batch=1 << 30, rows=4, bs=640)) == UNSUPPORTED
