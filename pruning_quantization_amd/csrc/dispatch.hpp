@@ -79,6 +79,8 @@ inline dim3 row_grid(const RowDesc& d, int team) {
   return dim3((unsigned)((d.R + rpb - 1) / rpb), (unsigned)d.B, 1);
 }
 
+constexpr int64_t kMostThreads = UINT32_MAX;  // of a grid, along x
+
 // Grid of a streaming row kernel: one team per row.  New workgroups start as
 // old ones retire, so loads of fresh rows overlap the arithmetic of others.
 inline dim3 stream_grid(int64_t nrows, int team) {

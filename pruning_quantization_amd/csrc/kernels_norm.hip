@@ -57,7 +57,7 @@ __global__ __launch_bounds__(kBlock) void k_rmsnorm(RmsNorm n) {
   __shared__ double sums[kBlock / 64];
   __shared__ uint32_t red[kBlock / 64];
   const int t = threadIdx.x % TEAM;
-  const int64_t at = (int64_t)blockIdx.x * (kBlock / TEAM) + threadIdx.x / TEAM;
+  const int64_t at = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (kBlock / TEAM) + threadIdx.x / TEAM;
   const bool act = at < n.rows;
   const int64_t row = act ? at : n.rows - 1;  // teams past the end run along
   const char* x = norm_row(n.x, row);
@@ -181,9 +181,11 @@ __global__ __launch_bounds__(kBlock) void k_rmsnorm(RmsNorm n) {
 hipError_t launch_rmsnorm_quantize(const RmsNorm& n, hipStream_t s) {
   return with_dtype(n.dtype, [&]<class DT>() {
     auto go = [&]<class WT, int TEAM, int UPL>() {
-      const int64_t per = kBlock / TEAM;
-      hipLaunchKernelGGL((k_rmsnorm<DT, WT, TEAM, UPL>), dim3((unsigned)((n.rows + per - 1) / per)), dim3(kBlock),
-                         0, s, n);
+      // more workgroups than a grid has along x (64 heads of 1M tokens) in as many lines as it takes
+      const int64_t per = kBlock / TEAM, all = (n.rows + per - 1) / per, most = kMostThreads / kBlock;
+      const int64_t lines = (all + most - 1) / most;
+      hipLaunchKernelGGL((k_rmsnorm<DT, WT, TEAM, UPL>), dim3((unsigned)((all + lines - 1) / lines), (unsigned)lines),
+                         dim3(kBlock), 0, s, n);
       return hipGetLastError();
     };
     // Up to 1024 elements a wave per row, from there on a workgroup: with a residual to e4m3,

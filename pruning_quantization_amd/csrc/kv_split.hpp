@@ -218,7 +218,6 @@ struct KvPlan {
 // few_rows: most rows of the few-rows kernel, one row tile; prompt_rows: of a prompt
 // workgroup; resident: prompt workgroups that a CU holds.
 KvPlan kv_plan(const KvAttn& a, char* ws, int few_rows, int prompt_rows, int resident);
-constexpr int64_t kMostThreads = UINT32_MAX;  // of a grid, along x
 // Whether the launches' grids hold it; threads: of a prompt workgroup.
 bool kv_plan_fits(const KvAttn& a, const KvPlan& p, int threads);
 hipError_t launch_kv_starts(const KvPlan& p, hipStream_t s);  // before the kernels, where p.planned

@@ -32,3 +32,24 @@ def test_heads_of_many_tokens(q, heads):
     want = S.rmsnorm_quantize(part.contiguous(), w, q, residual=res)
     assert same(want, got)
     assert (into[:, 0] == 7).all() and (into[:, 1 + heads:] == 7).all()
+
+
+# a grid holds 2^32 - 1 threads along x, a row takes 64 of them (2^26 rows), past 1024 elements 256 (2^24)
+@pytest.mark.parametrize("rows,k,q", [((1 << 26) + 5, 8, "fp8"), ((1 << 26) + 1, 32, "mxfp4"),
+                                      (3 * (1 << 26) + 7, 8, ("int", 8)), ((1 << 24) + 3, 1056, "mxfp4")], ids=str)
+def test_more_workgroups_than_a_grid_has_along_x(rows, k, q):
+    x = torch.randn(1 << 16, k, device=DEV).bfloat16()
+    x = x.repeat(-(-rows // (1 << 16)), 1)[:rows]
+    x[-1], x[1 << 24] = 3.0, 5.0
+    w = torch.randn(k, device=DEV)
+    codes, scales = S.rmsnorm_quantize(x, w, q)
+    step = 1 << 22                                     # whole copies of the 65536 rows
+    first = S.rmsnorm_quantize(x[:step], w, q)
+    for at in range(0, rows, step):
+        end = min(at + step, rows)
+        if at == 1 << 24 or end == rows:
+            want = S.rmsnorm_quantize(x[at:end], w, q)
+        else:
+            want = first
+        assert torch.equal(codes[at:end].view(torch.uint8), want[0].view(torch.uint8)), at
+        assert torch.equal(scales[at:end].view(torch.uint8), want[1].view(torch.uint8)), at
