@@ -393,8 +393,9 @@ sparq24_status sparq24_int8_gemm(const int8_t* a, int64_t lda, const float* scal
  * multiple of 16 where there is more than one row, at least K/2), ldc the
  * elements between rows of c (at least N); scales are dense, at any byte.  a, b,
  * c 16-byte aligned, bias 4-byte.  K % 32 == 0 and K <= SPARQ24_MAX_MXFP4_K
- * (SHAPE); K == 0 gives the bias or zeros.  Any M and N.  Workspace protocol as
- * above. */
+ * (SHAPE); K == 0 gives the bias or zeros.  Any M and N whose tiles one grid holds
+ * (UNSUPPORTED otherwise): M and N up to 2^28 with M * N up to 2^34 always fit.
+ * Workspace protocol as above. */
 #define SPARQ24_MAX_MXFP4_K 131072
 sparq24_status sparq24_mxfp4_gemm(const uint8_t* a, int64_t lda, const uint8_t* scale_a, int64_t m,
                                   const uint8_t* b, int64_t ldb, const uint8_t* scale_b, int64_t n,

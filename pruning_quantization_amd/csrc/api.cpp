@@ -827,7 +827,7 @@ sparq24_status sparq24_mxfp4_gemm(const uint8_t* a, int64_t lda, const uint8_t* 
   CHECK(workspace(ws, ws_bytes, 0, query));
   if (query) return SPARQ24_OK;
   if (m == 0 || n == 0) return SPARQ24_OK;
-  if (((m + 15) / 16) * ((n + 15) / 16) > INT32_MAX) return SPARQ24_ERR_UNSUPPORTED;
+  if (((m + 15) / 16) * ((n + 15) / 16) > INT32_MAX || !mxfp4_gemm_fits(g)) return SPARQ24_ERR_UNSUPPORTED;
   if ((k && (!a || !b || !scale_a || !scale_b)) || !c) return SPARQ24_ERR_INVALID;
   if (!aligned16(a) || !aligned16(b) || !aligned16(c) || ((uintptr_t)bias & 3u))
     return SPARQ24_ERR_ALIGN;

@@ -761,17 +761,14 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g, unsigned til
   }
 }
 
-hipError_t launch_mxfp4_gemm(const Mxfp4Gemm& g, hipStream_t s) {
-  auto few = [&]<int MT, int NT, int W, int S>() {
-    const int64_t ntm = (g.M + 16 * MT - 1) / (16 * MT), ntn = (g.N + 16 * NT - 1) / (16 * NT);
-    hipLaunchKernelGGL((k_mxfp4_stream<MT, NT, W, S>), dim3((unsigned)(ntm * ntn)), dim3(64 * W), 0, s, g, ntn);
-    return hipGetLastError();
-  };
-  auto tile = [&]<int BM, int BN, int WM>() {
-    const int64_t n = ((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN);
-    hipLaunchKernelGGL((k_mxfp4_tile<BM, BN, WM>), dim3((unsigned)n), dim3((BM / WM) * (BN / 64) * 64), 0, s, g);
-    return hipGetLastError();
-  };
+namespace {
+// The kernel of a product, its tile and its launch.
+struct Mxfp4Shape {
+  enum { STREAM, TILE, WIDE } kernel;
+  int bm, bn, threads;
+  int64_t tiles;  // and workgroups, unless those walk from tile to tile
+};
+Mxfp4Shape shape_of(const Mxfp4Gemm& g) {
   auto tiles = [&](int bm, int bn) { return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
   // k_mxfp4_stream takes time by the rounds of workgroups and the 16-row groups of a and b
   // that each streams (K = 4096, with the call: (1, 1) and (2, 4) for 1 x 4096 and 1 x
@@ -786,31 +783,58 @@ hipError_t launch_mxfp4_gemm(const Mxfp4Gemm& g, hipStream_t s) {
       const int64_t rounds = (tiles(16 * i, 16 * j) + cus - 1) / cus;
       if (rounds * (i + j) < best) best = rounds * (i + j), mt = i, nt = j;
     }
-  if (best <= 8 || far_rows) {
-    switch (mt * 8 + nt) {
-      case 9: return few.template operator()<1, 1, 8, 2>();
-      case 10: return few.template operator()<1, 2, 8, 2>();
-      case 12: return few.template operator()<1, 4, 8, 2>();
-      case 17: return few.template operator()<2, 1, 8, 2>();
-      case 18: return few.template operator()<2, 2, 8, 2>();
-      case 20: return few.template operator()<2, 4, 4, 2>();
-      case 33: return few.template operator()<4, 1, 8, 2>();
-      case 34: return few.template operator()<4, 2, 4, 2>();
-      default: return few.template operator()<4, 4, 4, 2>();
-    }
-  }
+  if (best <= 8 || far_rows)
+    return {Mxfp4Shape::STREAM, 16 * mt, 16 * nt, mt * nt < 8 ? 512 : 256, tiles(16 * mt, 16 * nt)};
   // The largest tile that still gives every CU one, else small ones.  At K = 4096, us for
   // 256 x 256 / 256 x 128 / 128 x 128 / 64 x 64: 4096 x 14336: 141 / 168 / 193 / 278; 2048 x
   // 4096: 33 / 27 / 31 / 44; 1024 x 4096: 31 / 23 / 23 / 24.
-  if (tiles(256, 256) >= cus && g.K >= 512) {
-    const unsigned n = (unsigned)tiles(256, 256);
+  if (tiles(256, 256) >= cus && g.K >= 512) return {Mxfp4Shape::WIDE, 256, 256, 256, tiles(256, 256)};
+  if (tiles(256, 128) >= cus) return {Mxfp4Shape::TILE, 256, 128, 512, tiles(256, 128)};
+  if (tiles(64, 64) > 4 * cus) return {Mxfp4Shape::TILE, 128, 128, 256, tiles(128, 128)};
+  return {Mxfp4Shape::TILE, 64, 64, 64, tiles(64, 64)};
+}
+}  // namespace
+
+bool mxfp4_gemm_fits(const Mxfp4Gemm& g) {
+  if (g.M <= 1 << 28 && g.N <= 1 << 28 && g.M * g.N <= 1ll << 34) return true;  // any shape's grid holds these
+  const Mxfp4Shape p = shape_of(g);
+  return p.tiles <= kMostThreads / p.threads;
+}
+
+hipError_t launch_mxfp4_gemm(const Mxfp4Gemm& g, hipStream_t s) {
+  const Mxfp4Shape p = shape_of(g);
+  auto few = [&]<int MT, int NT, int S>() {
+    constexpr int W = MT * NT < 8 ? 8 : 4;
+    hipLaunchKernelGGL((k_mxfp4_stream<MT, NT, W, S>), dim3((unsigned)p.tiles), dim3(64 * W), 0, s, g,
+                       (g.N + 16 * NT - 1) / (16 * NT));
+    return hipGetLastError();
+  };
+  auto tile = [&]<int BM, int BN, int WM>() {
+    hipLaunchKernelGGL((k_mxfp4_tile<BM, BN, WM>), dim3((unsigned)p.tiles), dim3((BM / WM) * (BN / 64) * 64), 0, s, g);
+    return hipGetLastError();
+  };
+  if (p.kernel == Mxfp4Shape::STREAM) {
+    switch (p.bm / 16 * 8 + p.bn / 16) {
+      case 9: return few.template operator()<1, 1, 2>();
+      case 10: return few.template operator()<1, 2, 2>();
+      case 12: return few.template operator()<1, 4, 2>();
+      case 17: return few.template operator()<2, 1, 2>();
+      case 18: return few.template operator()<2, 2, 2>();
+      case 20: return few.template operator()<2, 4, 2>();
+      case 33: return few.template operator()<4, 1, 2>();
+      case 34: return few.template operator()<4, 2, 2>();
+      default: return few.template operator()<4, 4, 2>();
+    }
+  }
+  if (p.kernel == Mxfp4Shape::WIDE) {
+    const unsigned n = (unsigned)p.tiles, cus = (unsigned)device_cu_count();
     // (K in whole pairs of slabs: chained tiles, one workgroup a CU)
     if (g.K % 512) hipLaunchKernelGGL(k_mxfp4_wide<false>, dim3(n), dim3(256), 0, s, g, n);
-    else hipLaunchKernelGGL(k_mxfp4_wide<true>, dim3(n < (unsigned)cus ? n : (unsigned)cus), dim3(256), 0, s, g, n);
+    else hipLaunchKernelGGL(k_mxfp4_wide<true>, dim3(n < cus ? n : cus), dim3(256), 0, s, g, n);
     return hipGetLastError();
   }
-  if (tiles(256, 128) >= cus) return tile.template operator()<256, 128, 64>();
-  if (tiles(64, 64) > 4 * cus) return tile.template operator()<128, 128, 64>();
+  if (p.bm == 256) return tile.template operator()<256, 128, 64>();
+  if (p.bm == 128) return tile.template operator()<128, 128, 64>();
   return tile.template operator()<64, 64, 64>();
 }
 

@@ -32,6 +32,7 @@ struct Mxfp4Gemm {
   int dtype;
 };
 hipError_t launch_mxfp4_gemm(const Mxfp4Gemm& g, hipStream_t s);
+bool mxfp4_gemm_fits(const Mxfp4Gemm& g);  // the launch's grid
 
 // RMS norm of x (+ residual) rows, quantized; cfmt is a CodeFmt.
 struct NormRows {  // strides in bytes; row = b * R + r

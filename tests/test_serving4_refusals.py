@@ -66,3 +66,25 @@ def test_norm_of_many_batches(no_gpu):
     assert norm(rows(**heads), rows(batch=70000), rows(**heads)) == DEVICE
     assert norm(rows(batch=70000, rows=1, bs=640)) == DEVICE
     assert norm(rows(batch=1 << 30, rows=4, bs=640)) == UNSUPPORTED
+
+
+# --- the product's grid --------------------------------------------------------
+
+
+def gemm(m, n, k, lda=None, ldb=None):
+    return B.lib().sparq24_mxfp4_gemm(FAKE, lda or k // 2, FAKE, m, FAKE, ldb or k // 2, FAKE, n, k, None, 0, FAKE, n,
+                                      None, None, None)
+
+
+def test_product_that_no_grid_holds():
+    # four threads a column in tiles, eight in the streaming kernel of rows far apart, 2^32 - 1 in a grid
+    assert gemm(1, 2 ** 31 - 1, 32) == gemm(2 ** 31 - 1, 1, 32) == UNSUPPORTED
+    assert gemm(1, 2 ** 30 + 1, 64) == gemm(2, 2 ** 29 + 1, 64, lda=1 << 23) == UNSUPPORTED
+
+
+def test_product_that_a_grid_holds(no_gpu):
+    most = 2 ** 28
+    for m, n in ((1, most), (most, 1), (31, most), (64, most), (most, 17), (65, (1 << 34) // 65), (1 << 17, 1 << 17)):
+        for kw in ({}, {"lda": 1 << 23}, {"ldb": 1 << 23}):
+            for k in (32, 512, 1056):
+                assert gemm(m, n, k, **kw) == DEVICE, (m, n, kw, k)
