@@ -417,7 +417,8 @@ sparq24_status sparq24_mxfp4_gemm(const uint8_t* a, int64_t lda, const uint8_t* 
  * group, with MXFP4) with a y that is.  weight: [K] of weight_dtype
  * (sparq24_dtype: fp32, or x's type).  residual and sum: x's type and shape, any
  * strides that x may have; both or neither (NULL).  sum may be residual or x
- * itself (the same rows at the same places), not overlap them otherwise.
+ * itself (the same rows at the same places), not overlap them otherwise (UNSUPPORTED
+ * where the strides are the same; with others the caller sees to it).
  * eps: finite, >= 0.  K <= SPARQ24_MAX_ROW_K, B * R < 2^31 (else UNSUPPORTED).
  * K-contiguous operands only. */
 sparq24_status sparq24_rmsnorm_quantize(const sparq24_tensor* x, const sparq24_tensor* residual,

@@ -835,6 +835,29 @@ sparq24_status sparq24_mxfp4_gemm(const uint8_t* a, int64_t lda, const uint8_t* 
   return launched(launch_mxfp4_gemm(g, stream));
 }
 
+}  // extern "C"
+
+namespace {
+// Whether rows of `bytes` bytes at two places of the same strides meet without being the
+// same ones: some of the distances between them is smaller than a row, but not zero throughout.
+bool rows_collide(const RowDesc& a, const RowDesc& b, int64_t bytes) {
+  if (a.x == b.x || a.B != b.B || a.R != b.R || (a.B > 1 && a.bs != b.bs) || (a.R > 1 && a.rs != b.rs))
+    return false;
+  const int64_t far = (int64_t)((uintptr_t)b.x - (uintptr_t)a.x);
+  auto near = [](int64_t d, int64_t step, int64_t count, auto&& f) {  // d + i step around 0, |i| < count
+    const int64_t q = count > 1 ? -d / step : 0;
+    for (int64_t i = q - 1; i <= q + 1; ++i)
+      if (i > -count && i < count && f(d + i * step)) return true;
+    return false;
+  };
+  return near(far, a.bs, a.B, [&](int64_t d) {
+    return near(d, a.rs, a.R, [&](int64_t e) { return e > -bytes && e < bytes; });
+  });
+}
+}  // namespace
+
+extern "C" {
+
 sparq24_status sparq24_rmsnorm_quantize(const sparq24_tensor* x, const sparq24_tensor* residual,
                                         const void* weight, int32_t weight_dtype, float eps,
                                         const sparq24_qspec* q, void* codes, void* scales,
@@ -861,6 +884,8 @@ sparq24_status sparq24_rmsnorm_quantize(const sparq24_tensor* x, const sparq24_t
   n.rows = x->batch * x->rows;
   if (n.rows > INT32_MAX) return SPARQ24_ERR_UNSUPPORTED;
   if (n.rows * x->k == 0) return SPARQ24_OK;
+  for (int i = 0; i < (residual ? 2 : 0); ++i)
+    if (rows_collide(d[i], d[2], x->k * esize(x->dtype))) return SPARQ24_ERR_UNSUPPORTED;
   if (!weight || !codes || !scales) return SPARQ24_ERR_INVALID;
   if (!aligned16(weight) || !aligned16(codes) || !aligned16(scales)) return SPARQ24_ERR_ALIGN;
   n.w = weight;

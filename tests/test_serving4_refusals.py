@@ -1,5 +1,6 @@
 """Refusals of the 4-bit serving calls that hold on the host."""
 import ctypes
+import random
 
 import pytest
 
@@ -88,3 +89,47 @@ def test_product_that_a_grid_holds(no_gpu):
         for kw in ({}, {"lda": 1 << 23}, {"ldb": 1 << 23}):
             for k in (32, 512, 1056):
                 assert gemm(m, n, k, **kw) == DEVICE, (m, n, kw, k)
+
+
+# --- a sum that meets the norm's inputs ------------------------------------------
+
+
+def test_sum_that_meets_its_inputs():
+    far = FAKE + (1 << 40)
+    for dtype, es in ((B.BF16, 2), (B.F32, 4)):
+        r = lambda at, **kw: rows(dtype=dtype, data=at, **kw)  # noqa: E731,B023
+        for kw in ({}, {"rs": 160}, {"batch": 3, "rs": 160, "bs": 1024}, {"batch": 3, "rows": 1, "bs": 640},
+                   {"rows": 1}):
+            for d in (16, 64 * es - 16, -16, 16 - 64 * es):
+                assert norm(r(FAKE, **kw), r(far, **kw), r(FAKE + d, **kw)) == UNSUPPORTED, (kw, d)
+                assert norm(r(far, **kw), r(FAKE, **kw), r(FAKE + d, **kw)) == UNSUPPORTED, (kw, d)
+        strided = {"batch": 3, "rs": 160, "bs": 1024}
+        for d in (160, -320, 1024, 1024 - 160, 2048 + 3 * 160 + 32, -1024 - 48):      # whole rows and batches on
+            assert norm(r(FAKE, **strided), r(far, **strided), r(FAKE + d * es, **strided)) == UNSUPPORTED, d
+        assert norm(r(FAKE), r(far), r(FAKE + 64 * es)) == UNSUPPORTED                # dense rows, one on
+
+
+def test_sum_beside_its_inputs(no_gpu):
+    far = FAKE + (1 << 40)
+    for dtype, es in ((B.BF16, 2), (B.F32, 4)):
+        r = lambda at, **kw: rows(dtype=dtype, data=at, **kw)  # noqa: E731,B023
+        strided = {"batch": 3, "rs": 160, "bs": 1024}
+        # the same rows; columns beside them, behind the last row, in between batches
+        for d in (0, 64, 96, -64, -96, 640, 608, 1024 - 64, 2048 + 4 * 160, -2048 - 640, 1 << 30):
+            assert norm(r(FAKE, **strided), r(far, **strided), r(FAKE + d * es, **strided)) == DEVICE, d
+            assert norm(r(far, **strided), r(FAKE, **strided), r(FAKE + d * es, **strided)) == DEVICE, d
+        assert norm(r(FAKE), r(far), r(FAKE + 256 * es)) == norm(r(FAKE), r(FAKE), r(FAKE)) == DEVICE
+        assert norm(r(FAKE, rs=128), r(far, rs=128), r(FAKE + 64 * es, rs=128)) == DEVICE
+
+
+def test_sum_at_any_place(no_gpu):
+    rng = random.Random(5)
+    for _ in range(400):
+        g = dict(k=rng.choice((8, 16, 40)), batch=rng.randint(1, 4), rows=rng.randint(1, 4))
+        g["rs"] = g["k"] + 8 * rng.randint(0, 4)
+        g["bs"] = (g["rows"] - 1) * g["rs"] + g["k"] + 8 * rng.randint(0, 12)
+        d = 8 * rng.randint(-60, 60)
+        at = {b * g["bs"] + r * g["rs"] for b in range(g["batch"]) for r in range(g["rows"])}
+        meet = d != 0 and any(abs(y + d - x) < g["k"] for x in at for y in at)
+        got = norm(rows(**g), rows(**{**g, "data": FAKE + (1 << 40)}), rows(**{**g, "data": FAKE + 2 * d}))
+        assert got == (UNSUPPORTED if meet else DEVICE), (g, d)
