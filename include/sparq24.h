@@ -540,9 +540,13 @@ sparq24_status sparq24_kv_append_mxfp4(const sparq24_kvcache_mxfp4* cache,
  * does not see does not reach it, whatever its bits.  An infinite or NaN query
  * element makes its row NaN; a score above fp32's range does, too, one below it
  * counts as hidden.
- * Arithmetic: K, V and queries enter the matrix units exactly in the queries'
- * type; the weights exp(s_t) are rounded to it (2^-8 of the weight at most in bf16,
- * 2^-11 in fp16), all sums, maxima and scores are fp32. */
+ * Arithmetic: K and queries enter the matrix units exactly in the queries' type, V
+ * exactly in fp16; the weights exp(s_t) are rounded to fp16 (2^-11 of the weight), all
+ * sums, maxima and scores are fp32.  With bf16 queries V and weights are bf16 (2^-8)
+ * instead for rows of a sequence and head that meet, among up to 128 that go through
+ * the cache together, a V scale outside 2^-23 .. 2^8 of a token that one of them sees
+ * and whose codes there are not all zero; and with dim 256 for all rows of a sequence
+ * that has more than 16 (32, where that is the average) of them per kv head. */
 sparq24_status sparq24_kv_attention_mxfp4(const sparq24_kvcache_mxfp4* cache,
                                           const sparq24_kvseqs* seqs, const sparq24_tensor* q,
                                           float scale, int32_t causal, int64_t window, void* out,

@@ -111,9 +111,10 @@ hipError_t launch_kv4_append(const KvCache& c, const KvSeqs& q, const KvRows& k,
 // Attention.  For query row i of sequence b at position pos = len - n + i and kv head
 // j = h / g (g query heads per kv head), over the visible tokens t:
 //   s_t = scale * (q . K_t),  p_t = exp(s_t),  o = (sum_t p_t V_t) / (sum_t p_t).
-// Both products run on v_mfma_f32_16x16x32 in the queries' type (bf16 or fp16), which
-// the codes enter through v_cvt_scalef32_pk_*_fp4: two codes times their power of two
-// an instruction, exact in bf16 and, within its range, in fp16.  (The power's operand
+// Both products run on v_mfma_f32_16x16x32, the first in the queries' type (bf16 or fp16),
+// the second in fp16 (outside_fp16 below), which the codes enter through
+// v_cvt_scalef32_pk_*_fp4: two codes times their power of two an instruction, exact in bf16
+// and, within its range, in fp16.  (The power's operand
 // counts by its exponent field alone, so an exponent byte is put there by one shift,
 // whatever lies around it.)  Transposed throughout:
 //   S^T [token][row] = K Q^T    lane: row c = lane % 16, tokens of lane group h = lane / 16
@@ -124,7 +125,7 @@ hipError_t launch_kv4_append(const KvCache& c, const KvSeqs& q, const KvRows& k,
 // has the dims as rows: row c of tile u is dim 8 c + u of a span of 128 dims (4 c + u of
 // one of 64), so that a lane reads 8 (4) adjacent dims of its group's 16 tokens, whose
 // exponents are 16 adjacent bytes; pairs of tokens are put together by byte permutes.
-// Scores, maxima, sums and O are fp32; p_t is rounded to the queries' type.
+// Scores, maxima, sums and O are fp32; p_t is rounded to V's type, for P V only.
 // ---------------------------------------------------------------------------
 typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
@@ -182,6 +183,37 @@ __device__ inline uint32_t tame_exponents(uint32_t w, uint32_t most, uint32_t na
     bad |= (b == 255 ? 1u : 0u) << i;
   }
   return r;
+}
+
+// Bit 7 of the bytes of w that are above MOST (128 to 254).
+template <uint32_t MOST>
+__device__ inline uint32_t above(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + (255 - MOST) * 0x01010101u) & w & 0x80808080u;
+}
+
+// V enters its product in fp16 whatever the queries' type, so that the weights keep fp16's
+// eleven bits (rounded to bf16's eight they were the largest error of a result: 8192 tokens
+// 1.8e-3 off, the output's own rounding 1.5e-3).  Codes times 2^-23 to 2^8 are exact there: bits
+// 7 to 5 of a byte are set where an exponent is outside of that (in the lowest such byte of a
+// word for certain: nothing is borrowed from it).  With bf16 queries, where a tile has such an
+// exponent, the wave (the prompt kernel's workgroup) goes through all of its tiles again in
+// bf16, in a loop of its own.  (Both types in one loop: registers spilled at every use, decoding
+// 6 to 35% slower.  The second loop recomputes what it needs, so that the first keeps nothing
+// for it; heads of 256 in the prompt kernel have no registers for that all the same, 782 us
+// became 900 to 1060, so they stay in bf16.)
+__device__ inline uint32_t outside_fp16(uint32_t w) { return (w - 0x68686868u) & 0xE0E0E0E0u; }
+
+// Whether exponents w of four tokens leave fp16, but for those of tokens whose codes are zero
+// or that are not within first .. last (0: the first of the four): no one sees them.
+__device__ inline bool leaves_fp16(uint32_t w, uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, int first, int last) {
+  const uint32_t c[4] = {c0, c1, c2, c3};
+  bool leaves = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = (w >> (8 * i)) & 0xFFu;
+    leaves |= outside_fp16(b | 0x80808000u) & 0xE0u && b != 255 && c[i] & 0x77777777u && i >= first && i <= last;
+  }
+  return leaves;
 }
 
 // Over lanes l and l ^ 32, in both.
@@ -248,10 +280,10 @@ struct Kv4State {
   }
 };
 
-// Scores of a tile to weights: lane: QT rows, slot 4 mt + i is token tok(mt, i) of the
-// lane group's 16 (tok0 = its first).  edge: some token is not seen by some row, or is NaN
-// (bad: by slot).  The sum is of the weights before their rounding.
-template <bool F16, int QT, int NU>
+// Scores of a tile to weights in VX's type: lane: QT rows, slot 4 mt + i is token tok(mt, i)
+// of the lane group's 16 (tok0 = its first).  edge: some token is not seen by some row, or is
+// NaN (bad: by slot).  The sum is of the weights before their rounding.
+template <class VX, int QT, int NU>
 __device__ inline void kv4_weights(f32x4v (&sc)[QT][4], const Kv4Row (&row)[QT], float c, bool there, int tok0,
                                    bool edge, uint32_t bad, Kv4State<QT, NU>& st, u32x4v (&pf)[QT][2]) {
   auto token = [](int mt, int i) { return 4 * i + mt; };  // of slot (mt, i)
@@ -324,8 +356,8 @@ __device__ inline void kv4_weights(f32x4v (&sc)[QT][4], const Kv4Row (&row)[QT],
         sc[t][mt][e] = __builtin_amdgcn_exp2f(sc[t][mt][e]);
         sum += sc[t][mt][e];
       }
-      pf[t][mt / 2][2 * (mt & 1)] = Kv4Type<F16>::pack(sc[t][mt][0], sc[t][mt][1]);
-      pf[t][mt / 2][2 * (mt & 1) + 1] = Kv4Type<F16>::pack(sc[t][mt][2], sc[t][mt][3]);
+      pf[t][mt / 2][2 * (mt & 1)] = VX::pack(sc[t][mt][0], sc[t][mt][1]);
+      pf[t][mt / 2][2 * (mt & 1) + 1] = VX::pack(sc[t][mt][2], sc[t][mt][3]);
     }
     st.l[t] += sum;
   }
@@ -348,20 +380,23 @@ __global__ __launch_bounds__(256, (Kv4FewWaves<D, QT>)) void k_kv4_attn(KvAttnAr
   // spans of 128 dims (16 bytes of a K row a lane) and of 64 (8 bytes)
   constexpr int S128 = D / 128, S64 = D % 128 / 64, NS = S128 + S64, NJ = D / 32, NU = D / 16, G = D / 32;
   const KvAttn& a = p.a;
-  const int lane = threadIdx.x & 63, wv = uniform((int)threadIdx.x >> 6), c16 = lane & 15, h = lane >> 4;
+  const int lane = threadIdx.x & 63, wv = uniform((int)threadIdx.x >> 6);
+  int c16 = lane & 15, h = lane >> 4;
   KvItem it;
   if (!kv_item(p, blockIdx.x, lane, it)) return;
   const int H = a.c.heads, tsh = a.c.tsh, T = 1 << tsh;
   u32x4v qf[QT][NJ];
   Kv4Row row[QT];
+  auto query = [&] {
 #pragma unroll
-  for (int t = 0; t < QT; ++t)
-    row[t] = kv4_query<F16, 4>(p, it, it.rt * p.rb + 16 * t + c16, qf[t], [&](int j) {
-      return j / 4 < S128 ? 128 * (j / 4) + 32 * h + 8 * (j % 4) : 128 * S128 + 16 * h + 8 * (j % 4);
-    });
+    for (int t = 0; t < QT; ++t)
+      row[t] = kv4_query<F16, 4>(p, it, it.rt * p.rb + 16 * t + c16, qf[t], [&](int j) {
+        return j / 4 < S128 ? 128 * (j / 4) + 32 * h + 8 * (j % 4) : 128 * S128 + 16 * h + 8 * (j % 4);
+      });
+  };
+  query();
   const float c = a.scale * 1.44269504088896340736f;
   Kv4State<QT, NU> st;
-  st.init();
 
   const int r0 = it.rt * p.rb, r1 = r0 + 16 * QT < it.k.rows ? r0 + 16 * QT : it.k.rows;
   const KvRange rg = kv_range(p, it, r0, r1);
@@ -414,114 +449,144 @@ __global__ __launch_bounds__(256, (Kv4FewWaves<D, QT>)) void k_kv4_attn(KvAttnAr
 #pragma unroll
     for (int s = 0; s < NS; ++s) vs[s] = *(const u32x4v*)(ep + (4 * s + (s < S128 ? c16 >> 2 : c16 >> 3)) * T);
   };
-  int tt = rg.t0 + wv, blk = -1, blk1 = -1, ahead = -1;
-  if (tt < rg.t1) {
-    const int e0 = entry(tt), e1 = entry(tt + 4);
-    ahead = entry(tt + 8);
-    blk = known(e0);
-    blk1 = known(e1);
-    load_k(tt, blk);
-    load_v(tt, blk);
-  }
-  for (; tt < rg.t1; tt += 4) {
-    const int b0 = tt * kKvTile, gp = b0 + 16 * h;
-    const bool there = blk >= 0 && (!BIG || (gp < hi && gp + 16 > lo)), more = tt + 4 < rg.t1;
-    // Exponents of 128 and more are rare: only then are their bytes looked at one by one.
-    uint32_t high = 0, bad = 0;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) high |= ks[s] | vs[s][0] | vs[s][1] | vs[s][2] | vs[s][3];
-    if (__any(high & 0x80808080u)) {
+  bool gone = false;  // V left fp16
+  auto run = [&]<class VX>() __attribute__((always_inline)) {  // with V in VX's type
+    constexpr bool kMayLeave = !F16 && __is_same(VX, Kv4Type<true>);
+    st.init();
+    int tt = rg.t0 + wv, blk = -1, blk1 = -1, ahead = -1;
+    if (tt < rg.t1) {
+      const int e0 = entry(tt), e1 = entry(tt + 4);
+      ahead = entry(tt + 8);
+      blk = known(e0);
+      blk1 = known(e1);
+      load_k(tt, blk);
+      load_v(tt, blk);
+    }
+    for (; tt < rg.t1; tt += 4) {
+      const int b0 = tt * kKvTile, gp = b0 + 16 * h;
+      const bool there = blk >= 0 && (!BIG || (gp < hi && gp + 16 > lo)), more = tt + 4 < rg.t1;
+      // Exponents that the types do not hold are rare: only then are their bytes looked at
+      // one by one.
+      uint32_t high = 0, bad = 0;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        uint32_t none;
-        ks[s] = tame_exponents(ks[s], X::kMost, 255, none);  // K's NaN makes the score NaN
+        high |= above<X::kMost>(ks[s]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t b;
-          vs[s][i] = tame_exponents(vs[s][i], X::kMost, 0, b);
-          bad |= b << (4 * i);
-        }
+        for (int i = 0; i < 4; ++i) high |= kMayLeave ? outside_fp16(vs[s][i]) : above<VX::kMost>(vs[s][i]);
       }
-      bad |= (uint32_t)__shfl_xor((int)bad, 4, 64);  // the other groups of dims
-      bad |= (uint32_t)__shfl_xor((int)bad, 8, 64);
-    }
-    f32x4v sc[QT][4];
+      if (__builtin_expect(__any(high), 0)) {
+        if constexpr (kMayLeave) {
+          bool leaves = false;
 #pragma unroll
-    for (int t = 0; t < QT; ++t)
+          for (int s = 0; s < NS; ++s) {
+            auto codes = [&](int e) { return s < S128 ? vr[e][s < S128 ? s : 0] : (uint32_t)v2[e]; };
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) sc[t][mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
-    auto scores = [&]<int MT>() {
-#pragma unroll
-      for (int s = 0; s < S128; ++s)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32x4v k = X::widen8(kr[MT][s][j], exponent_field<MT>(ks[s]));
-#pragma unroll
-          for (int t = 0; t < QT; ++t) sc[t][MT] = X::mfma(k, qf[t][4 * s + j], sc[t][MT]);
+            for (int i = 0; i < 4; ++i)
+              leaves |= leaves_fp16(vs[s][i], codes(4 * i), codes(4 * i + 1), codes(4 * i + 2), codes(4 * i + 3),
+                                    lo - gp - 4 * i, hi - 1 - gp - 4 * i);
+          }
+          gone |= __any(leaves);
         }
-      if constexpr (S64) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const u32x4v k = X::widen8(j ? k8[MT].y : k8[MT].x, exponent_field<MT>(ks[S128]));
-#pragma unroll
-          for (int t = 0; t < QT; ++t) sc[t][MT] = X::mfma(k, qf[t][4 * S128 + j], sc[t][MT]);
-        }
-      }
-    };
-    scores.template operator()<0>();
-    scores.template operator()<1>();
-    scores.template operator()<2>();
-    scores.template operator()<3>();
-    const bool edge = __any(bad != 0 || !there) || b0 + kKvTile > rg.least || b0 < rg.from;
-    int blk2 = -1;
-    if (more) {
-      blk2 = known(ahead);
-      ahead = entry(tt + 12);
-      load_k(tt + 4, blk1);
-    }
-    u32x4v pf[QT][2];
-    kv4_weights<F16, QT, NU>(sc, row, c, there, gp, edge, bad, st, pf);
-    // slot 4 mt + i of V is token 4 i + mt: byte mt of exponent dword i
-    auto out = [&]<int U0, int NB>(auto&& word, const u32x4v& ex) {  // NB bytes: 2 NB dims a lane
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t w[8][NB];  // slots 8 x ..: dims 2 b and 2 b + 1
-        auto slot = [&]<int MT>() {
+        for (int s = 0; s < NS; ++s) {
+          uint32_t none;
+          ks[s] = tame_exponents(ks[s], X::kMost, 255, none);  // K's NaN makes the score NaN
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t v = word(4 * i + 2 * x + MT), s = x ? exponent_field<2 + MT>(ex[i]) : exponent_field<MT>(ex[i]);
-            w[4 * MT + i][0] = X::template widen<0>(v, s);
-            w[4 * MT + i][1] = X::template widen<1>(v, s);
-            if constexpr (NB == 4) {
-              w[4 * MT + i][2] = X::template widen<2>(v, s);
-              w[4 * MT + i][3] = X::template widen<3>(v, s);
-            }
-          }
-        };
-        slot.template operator()<0>();
-        slot.template operator()<1>();
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          u32x4v even, odd;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            even[j] = __builtin_amdgcn_perm(w[2 * j + 1][b], w[2 * j][b], 0x05040100u);
-            odd[j] = __builtin_amdgcn_perm(w[2 * j + 1][b], w[2 * j][b], 0x07060302u);
-          }
-#pragma unroll
-          for (int t = 0; t < QT; ++t) {
-            st.o[t][U0 + 2 * b] = X::mfma(even, pf[t][x], st.o[t][U0 + 2 * b]);
-            st.o[t][U0 + 2 * b + 1] = X::mfma(odd, pf[t][x], st.o[t][U0 + 2 * b + 1]);
+            uint32_t b;
+            vs[s][i] = tame_exponents(vs[s][i], VX::kMost, 0, b);
+            bad |= b << (4 * i);
           }
         }
+        bad |= (uint32_t)__shfl_xor((int)bad, 4, 64);  // the other groups of dims
+        bad |= (uint32_t)__shfl_xor((int)bad, 8, 64);
       }
-    };
-    if constexpr (S128 > 0) out.template operator()<0, 4>([&](int e) { return vr[e][0]; }, vs[0]);
-    if constexpr (S128 > 1) out.template operator()<8, 4>([&](int e) { return vr[e][1]; }, vs[1]);
-    if constexpr (S64 > 0) out.template operator()<8 * S128, 2>([&](int e) { return (uint32_t)v2[e]; }, vs[S128]);
-    if (more) load_v(tt + 4, blk1);
-    blk = blk1;
-    blk1 = blk2;
+      f32x4v sc[QT][4];
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) sc[t][mt] = f32x4v{0.f, 0.f, 0.f, 0.f};
+      auto scores = [&]<int MT>() {
+#pragma unroll
+        for (int s = 0; s < S128; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const u32x4v k = X::widen8(kr[MT][s][j], exponent_field<MT>(ks[s]));
+#pragma unroll
+            for (int t = 0; t < QT; ++t) sc[t][MT] = X::mfma(k, qf[t][4 * s + j], sc[t][MT]);
+          }
+        if constexpr (S64) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const u32x4v k = X::widen8(j ? k8[MT].y : k8[MT].x, exponent_field<MT>(ks[S128]));
+#pragma unroll
+            for (int t = 0; t < QT; ++t) sc[t][MT] = X::mfma(k, qf[t][4 * S128 + j], sc[t][MT]);
+          }
+        }
+      };
+      scores.template operator()<0>();
+      scores.template operator()<1>();
+      scores.template operator()<2>();
+      scores.template operator()<3>();
+      const bool edge = __any(bad != 0 || !there) || b0 + kKvTile > rg.least || b0 < rg.from;
+      int blk2 = -1;
+      if (more) {
+        blk2 = known(ahead);
+        ahead = entry(tt + 12);
+        load_k(tt + 4, blk1);
+      }
+      u32x4v pf[QT][2];
+      kv4_weights<VX, QT, NU>(sc, row, c, there, gp, edge, bad, st, pf);
+      // slot 4 mt + i of V is token 4 i + mt: byte mt of exponent dword i
+      auto out = [&]<int U0, int NB>(auto&& word, const u32x4v& ex) {  // NB bytes: 2 NB dims a lane
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t w[8][NB];  // slots 8 x ..: dims 2 b and 2 b + 1
+          auto slot = [&]<int MT>() {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t v = word(4 * i + 2 * x + MT), s = x ? exponent_field<2 + MT>(ex[i]) : exponent_field<MT>(ex[i]);
+              w[4 * MT + i][0] = VX::template widen<0>(v, s);
+              w[4 * MT + i][1] = VX::template widen<1>(v, s);
+              if constexpr (NB == 4) {
+                w[4 * MT + i][2] = VX::template widen<2>(v, s);
+                w[4 * MT + i][3] = VX::template widen<3>(v, s);
+              }
+            }
+          };
+          slot.template operator()<0>();
+          slot.template operator()<1>();
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            u32x4v even, odd;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              even[j] = __builtin_amdgcn_perm(w[2 * j + 1][b], w[2 * j][b], 0x05040100u);
+              odd[j] = __builtin_amdgcn_perm(w[2 * j + 1][b], w[2 * j][b], 0x07060302u);
+            }
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+              st.o[t][U0 + 2 * b] = VX::mfma(even, pf[t][x], st.o[t][U0 + 2 * b]);
+              st.o[t][U0 + 2 * b + 1] = VX::mfma(odd, pf[t][x], st.o[t][U0 + 2 * b + 1]);
+            }
+          }
+        }
+      };
+      if constexpr (S128 > 0) out.template operator()<0, 4>([&](int e) { return vr[e][0]; }, vs[0]);
+      if constexpr (S128 > 1) out.template operator()<8, 4>([&](int e) { return vr[e][1]; }, vs[1]);
+      if constexpr (S64 > 0) out.template operator()<8 * S128, 2>([&](int e) { return (uint32_t)v2[e]; }, vs[S128]);
+      if (more) load_v(tt + 4, blk1);
+      blk = blk1;
+      blk1 = blk2;
+    }
+  };
+  run.template operator()<Kv4Type<true>>();
+  if constexpr (!F16) {
+    if (__builtin_expect(gone, 0)) {
+      asm volatile("" : "+v"(c16), "+v"(h));  // nothing of the first loop is kept for the second
+      if constexpr (QT == 1) query();
+      run.template operator()<Kv4Type<false>>();
+    }
   }
 
   // the four waves' parts of each row meet in LDS, in wave order
@@ -617,13 +682,16 @@ __device__ inline f32x16v kv4_mfma32(u32x4v a, u32x4v b, f32x16v c) {
 template <int D, bool F16, bool BIG>
 __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVES) void k_kv4_prompt(KvAttnArgs p) {
   using X = Kv4Type<F16>;
+  constexpr bool kV16 = F16 || D < 256;  // V in fp16 (outside_fp16)
   constexpr int NW = Kv4PromptShape<D>::NW, NJ = D / 16, NU = D / 32, G = D / 32;
   constexpr int WK = D / 32, NQ = (2 * WK + NW - 1) / NW;  // 64-unit loads of K (and of V), a wave's share
   constexpr int K_BYTES = kKvTile * D * 2, BUF = 2 * K_BYTES;
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * BUF];
   __shared__ uint32_t nan_tokens[3][2];  // tokens whose V exponent is NaN, by tile
+  __shared__ uint32_t gone;              // V left fp16
   const KvAttn& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 63, wv = uniform(tid >> 6), c32 = lane & 31, h = lane >> 5;
+  const int wv = uniform((int)threadIdx.x >> 6);
+  int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, h = lane >> 5;
   KvItem it;
   if (!kv_item(p, blockIdx.x, lane, it)) return;
   const int H = a.c.heads, tsh = a.c.tsh, T = 1 << tsh;
@@ -680,8 +748,12 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
   // This lane's first fragments; the others lie at fixed distances, but for address bits
   // that the swizzle turns (KX).  One register each, and not one per chunk.
   constexpr unsigned KX = D % 128 == 0 ? 255 : 127;
-  const unsigned kat = c32 * (2 * D) + (h ^ k_swizzle(c32)) * 16;
-  const unsigned vat = K_BYTES + c32 * 128 + (h ^ v_swizzle(c32)) * 16;
+  unsigned kat, vat;
+  auto first_fragments = [&] {
+    kat = c32 * (2 * D) + (h ^ k_swizzle(c32)) * 16;
+    vat = K_BYTES + c32 * 128 + (h ^ v_swizzle(c32)) * 16;
+  };
+  first_fragments();
 
   // Unit i = 64 wc + lane of a tile, wc = wv + NW q.  Of K (wc < WK): 32 dims i % G of token
   // i / G.  Of V: dims 8 o .. 8 o + 7 of tokens 4 t .. 4 t + 3, o = i % (D / 8), t = i / (D / 8).
@@ -689,6 +761,15 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
   auto has = [&](int q) { return 2 * WK % NW == 0 || wv + NW * q < 2 * WK; };
   u32x4v cr[NQ];
   uint32_t ex[NQ];
+  auto fetch_v = [&](int q, int tt, int blk, u32x4v& codes, uint32_t& exps) {
+    const int j = 64 * (wv + NW * q) + lane - 64 * WK, od = j % (D / 8), t = j / (D / 8);
+    const int64_t at = place(BIG ? blk : __shfl(blk, (4 * t) & 48, 64));
+    const int o = (tt * kKvTile + 4 * t) & (T - 1);
+    const uint8_t* vp = a.c.v + (at * T + o) * (D / 2) + 4 * od;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) codes[e] = *(const uint32_t*)(vp + e * (D / 2));
+    exps = *(const uint32_t*)(a.c.ve + (at * G + (od >> 2)) * T + o);
+  };
   auto fetch = [&](int tt, int blk) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
@@ -701,17 +782,37 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
         cr[q] = *(const u32x4v*)(a.c.k + (at * T + o) * (D / 2) + 16 * g);
         ex[q] = a.c.ke[(at * G + g) * T + o];
       } else {
-        const int j = i - 64 * WK, od = j % (D / 8), t = j / (D / 8);
-        const int64_t at = place(BIG ? blk : __shfl(blk, (4 * t) & 48, 64));
-        const int o = (tt * kKvTile + 4 * t) & (T - 1);
-        const uint8_t* vp = a.c.v + (at * T + o) * (D / 2) + 4 * od;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) cr[q][e] = *(const uint32_t*)(vp + e * (D / 2));
-        ex[q] = *(const uint32_t*)(a.c.ve + (at * G + (od >> 2)) * T + o);
+        fetch_v(q, tt, blk, cr[q], ex[q]);
       }
     }
   };
-  auto widen = [&](int tt, uint8_t* buf) {
+  // V's unit into a buffer, in VX's type
+  auto put_v = [&]<class VX>(int q, const u32x4v& codes, uint32_t e, uint8_t* buf) {
+    const int j = 64 * (wv + NW * q) + lane - 64 * WK, od = j % (D / 8), t = j / (D / 8);
+    uint32_t w[4][4];
+    auto one = [&]<int B>() {
+      w[0][B] = VX::template widen<B>(codes[0], exponent_field<0>(e));
+      w[1][B] = VX::template widen<B>(codes[1], exponent_field<1>(e));
+      w[2][B] = VX::template widen<B>(codes[2], exponent_field<2>(e));
+      w[3][B] = VX::template widen<B>(codes[3], exponent_field<3>(e));
+    };
+    one.template operator()<0>();
+    one.template operator()<1>();
+    one.template operator()<2>();
+    one.template operator()<3>();
+    const int chunk = 2 * (t >> 2) + (t & 1), half = (t >> 1) & 1;
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      const uint32_t sel = d & 1 ? 0x07060302u : 0x05040100u;
+      uint2 v;
+      v.x = __builtin_amdgcn_perm(w[1][d / 2], w[0][d / 2], sel);
+      v.y = __builtin_amdgcn_perm(w[3][d / 2], w[2][d / 2], sel);
+      const int dim = 8 * od + d;
+      *(uint2*)(buf + K_BYTES + dim * 128 + (chunk ^ v_swizzle(dim)) * 16 + 8 * half) = v;
+    }
+  };
+  auto widen = [&]<bool V16>(int tt, uint8_t* buf) {
+    constexpr bool kMayLeave = !F16 && V16;
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       if (!has(q)) continue;
@@ -724,48 +825,36 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
 #pragma unroll
         for (int x = 0; x < 4; ++x) *(u32x4v*)(k + ((4 * g + x) ^ z) * 16) = X::widen8(cr[q][x], e << 23);
       } else {
-        const int j = i - 64 * WK, od = j % (D / 8), t = j / (D / 8);
         uint32_t e = ex[q];
-        if (__any(e & 0x80808080u)) {  // rare: 128 and more
+        if (__builtin_expect(__any(kMayLeave ? outside_fp16(e) : above<Kv4Type<V16>::kMost>(e)), 0)) {
+          int l = lane;
+          if constexpr (kMayLeave) asm volatile("" : "+v"(l));  // nothing of this is kept over the loop
+          const int t = (64 * (wv + NW * q) + l - 64 * WK) / (D / 8);
+          if constexpr (kMayLeave) {
+            const int tok = tt * kKvTile + 4 * t;
+            if (leaves_fp16(e, cr[q][0], cr[q][1], cr[q][2], cr[q][3], rg.lo - tok, rg.hi - 1 - tok)) gone = 1;
+          }
           uint32_t bad;
-          e = tame_exponents(e, X::kMost, 0, bad);
+          e = tame_exponents(e, Kv4Type<V16>::kMost, 0, bad);
           if (bad) atomicOr(&nan_tokens[tt % 3][t >> 3], bad << ((4 * t) & 31));
         }
-        uint32_t w[4][4];
-        w[0][0] = X::template widen<0>(cr[q][0], exponent_field<0>(e));
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          auto one = [&]<int B>() {
-            w[0][B] = X::template widen<B>(cr[q][0], exponent_field<0>(e));
-            w[1][B] = X::template widen<B>(cr[q][1], exponent_field<1>(e));
-            w[2][B] = X::template widen<B>(cr[q][2], exponent_field<2>(e));
-            w[3][B] = X::template widen<B>(cr[q][3], exponent_field<3>(e));
-          };
-          if (b == 0) one.template operator()<0>();
-          if (b == 1) one.template operator()<1>();
-          if (b == 2) one.template operator()<2>();
-          if (b == 3) one.template operator()<3>();
-        }
-        const int chunk = 2 * (t >> 2) + (t & 1), half = (t >> 1) & 1;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) {
-          const uint32_t sel = d & 1 ? 0x07060302u : 0x05040100u;
-          uint2 v;
-          v.x = __builtin_amdgcn_perm(w[1][d / 2], w[0][d / 2], sel);
-          v.y = __builtin_amdgcn_perm(w[3][d / 2], w[2][d / 2], sel);
-          const int dim = 8 * od + d;
-          *(uint2*)(buf + K_BYTES + dim * 128 + (chunk ^ v_swizzle(dim)) * 16 + 8 * half) = v;
-        }
+        put_v.template operator()<Kv4Type<V16>>(q, cr[q], e, buf);
       }
     }
   };
 
-  if (rg.t0 < rg.t1) {
+  auto run = [&]<bool V16>() __attribute__((always_inline)) {  // with V in fp16 or bf16
+    m = kNegInf, l = 0.0f, far = 0;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[u][e] = 0.0f;
     int blk = known(entry(rg.t0), rg.t0), blk1 = known(entry(rg.t0 + 1), rg.t0 + 1), ahead = entry(rg.t0 + 2);
     fetch(rg.t0, blk);
     if (tid < 6) nan_tokens[tid >> 1][tid & 1] = 0;
+    if (V16 && tid == 0) gone = 0;
     __syncthreads();
-    widen(rg.t0, smem);
+    widen.template operator()<V16>(rg.t0, smem);
     fetch(rg.t0 + 1, blk1);  // past the end: block 0, unused
     __syncthreads();
     for (int tt = rg.t0; tt < rg.t1; ++tt) {
@@ -846,7 +935,7 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
                 const float w1 = __builtin_amdgcn_exp2f(sc[mt][8 * x + 2 * d + 1]);
                 sum += w0;
                 sum += w1;
-                pf[mt][x][d] = X::pack(w0, w1);
+                pf[mt][x][d] = Kv4Type<V16>::pack(w0, w1);
               }
           l += sum;
           if constexpr (D > 128) __builtin_amdgcn_sched_barrier(0);
@@ -858,7 +947,7 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
               for (int u = 0; u < NU; ++u) {
                 // row 32 u + c32, chunk 4 (M + mt) + 2 x + h
                 const u32x4v vf = *(const u32x4v*)(smem + ((buf + vat) ^ (16 * ((4 * (M + mt) + 2 * x) ^ v_swizzle(32 * u)))) + 4096 * u);
-                o[u] = kv4_mfma32<F16>(vf, pf[mt][x], o[u]);
+                o[u] = kv4_mfma32<V16>(vf, pf[mt][x], o[u]);
               }
         };
         if constexpr (D <= 128) {
@@ -870,13 +959,24 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
       }
       if (tid < 2) nan_tokens[(tt + 2) % 3][tid] = 0;
       if (tt + 1 < rg.t1) {
-        widen(tt + 1, smem + ((tt + 1 - rg.t0) & 1) * BUF);
+        widen.template operator()<V16>(tt + 1, smem + ((tt + 1 - rg.t0) & 1) * BUF);
         blk = blk1;
         blk1 = known(ahead, tt + 2);
         ahead = entry(tt + 3);
         fetch(tt + 2, blk1);
       }
       __syncthreads();
+    }
+  };
+  if (rg.t0 < rg.t1) {
+    run.template operator()<kV16>();
+    if constexpr (kV16 && !F16) {
+      if (__builtin_expect(uniform((int)gone), 0)) {
+        asm volatile("" : "+v"(tid));  // nothing of the first loop is kept for the second
+        lane = tid & 63, c32 = lane & 31, h = lane >> 5;
+        first_fragments();
+        run.template operator()<false>();
+      }
     }
   }
   l = halves_sum(l);
