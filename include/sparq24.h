@@ -534,7 +534,8 @@ sparq24_status sparq24_kv_append_mxfp4(const sparq24_kvcache_mxfp4* cache,
 /* Attention of query rows over a 4-bit cache: arguments, masks, outputs, refusals
  * and workspace protocol of sparq24_kv_attention, K_t and V_t the stored codes
  * times their scales.  With bf16 queries a visible V scale above 2^96 may make its
- * rows infinite or NaN; with fp16 queries K_t and V_t are rounded to fp16, and
+ * rows infinite or NaN, and scales of 2^126 and 2^127 (which the append never
+ * writes) count as 2^125; with fp16 queries K_t and V_t are rounded to fp16, and
  * scales above 2^13 (which no fp16 element gives) count as 2^13.  A scale byte
  * of 255 in K or V of a token makes the rows that see the token NaN; what a row
  * does not see does not reach it, whatever its bits.  An infinite or NaN query

@@ -147,3 +147,22 @@ def test_nan_scales_among_scales_outside_of_fp16(kernel):
         assert got[0, sees, group:].isnan().all()
         assert torch.equal(got[0, ~sees], want[0, ~sees]) and torch.equal(got[0, :, :group], want[0, :, :group])
         assert torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype,most", [("bf16", 252), ("f16", 140)])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_scales_above_the_types_range_count_as_its_largest(kernel, dtype, most):
+    n, group = KERNELS[kernel]
+    p = Pool(n, lengths(n), 2, 128, 32)
+    k, ks, v, vs = p.ref
+    high = p.rng.random(ks.shape) < 0.3
+    ks = np.where(high, p.rng.integers(most, 255, ks.shape), most - 3).astype(np.uint8)
+    q = p.rng.standard_normal((len(p.lens), n, 2 * group, 128)) * 2.0 ** (124 - most)
+    q, _ = stored(np.where(np.abs(q) < 2.0 ** -24, 0, q) if dtype == "f16" else q, dtype)
+    got = S.kv_attention(q, p.dev((k, ks, v, vs)), *p.args())
+    assert got.isfinite().all() and got.any()
+    assert torch.equal(got, S.kv_attention(q, p.dev((k, np.minimum(ks, most), v, vs)), *p.args()))
+    vs = np.where(high, p.rng.integers(most, 255, vs.shape), vs).astype(np.uint8)
+    got = S.kv_attention(q, p.dev((k, ks, v, vs)), *p.args())
+    want = S.kv_attention(q, p.dev((k, ks, v, np.minimum(vs, most))), *p.args())
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))     # infinities and NaN alike
