@@ -1014,8 +1014,10 @@ int prompt4_rows(int dim) {
 // (three workgroups a CU with heads of 64: a mixed batch of 24 sequences 41.5 us, aimed at two 43.9)
 KvPlan plan_of(const KvAttn& a, void* ws) {
   // Two row tiles a wave where sequences have 17 to 32 rows each, or do on average (8 tokens
-  // on 64 sequences of 300..8192, 32 heads over 8: 105 us, by the prompt kernel 203; on 16 of
-  // 4096, 4 kv heads: 25.5 and 30.4; heads of 256, 300..4096: 198 and 573).
+  // on 64 sequences of 300..8192, 32 heads over 8: 95 us, by the prompt kernel 200; with one
+  // token on every other sequence 93 and 228; on 16 of 4096, 4 kv heads: 25.5 and 30.4).  The
+  // host knows only the average, and pays where single tokens have it from a long prompt
+  // beside them (63 and one of 400 tokens on such sequences: 155 us, with one row tile 140).
   const int64_t rows = a.q.total * (a.heads / a.c.heads), seqs = a.q.seqs;  // (seqs: at least one)
   return kv_plan(a, (char*)ws, rows > 16 * seqs && rows <= 32 * seqs ? 32 : 16, prompt4_rows(a.c.dim), a.c.dim == 64 ? 3 : a.c.dim == 128 ? 2 : 1);
 }
