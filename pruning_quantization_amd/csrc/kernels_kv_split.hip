@@ -85,7 +85,9 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs few, KvAttnArgs many
   // Offsets that do not ascend can ask for more items than there is room for.  A sequence
   // that got none has no entry in the plan: what stands there is any number, also where
   // nothing was split.
-  if (!p.ml || first < 0 || chunks > p.items || first + (int64_t)chunks * nrt > p.items / a.c.heads) return;
+  if (!p.ml || first < 0 || chunks > p.items) return;
+  const int64_t units = first + (int64_t)chunks * nrt;
+  if (units > p.items || units * a.c.heads > p.items) return;
   const int64_t at0 = ((first + nrt - 1 - rt) * a.c.heads + head) * p.rb + rr;
   const int64_t step = (int64_t)nrt * a.c.heads * p.rb;
   // the common reference: the largest sum's own exponent, so that no chunk's weight passes 2
