@@ -367,11 +367,13 @@ __device__ inline void kv4_weights(f32x4v (&sc)[QT][4], const Kv4Row (&row)[QT],
 // chunk's tiles in turn, K and V straight from memory into MFMA operands.
 // BIG: blocks of 64 tokens and more, so a tile lies in one block (scalar addresses).
 // The cache's bytes bound it, where the waves hide their latency: 64 sequences of 300 to
-// 16384 tokens, 8 kv heads of 128, 134 us, 4.4 TB/s (5.1 in a large copy); with 2 waves a
-// SIMD 148, heads of 192 and 256 with one 171 and 188, now 127 and 144.  Block numbers are
-// asked for two tiles ahead, before loads that are not due yet: behind them 165 us.  With
-// two row tiles every widened operand serves two products; they take half of the waves'
-// registers more, and a wave less a SIMD.
+// 16384 tokens, 8 kv heads of 128, 128 us, 4.6 TB/s (6.5 in a large copy), heads of 64 82, of
+// 192 116, of 256 on 300 to 8192 136.  A third wave a SIMD took 148 us to 134, a second at heads
+// of 192 and 256 171 to 127 and 188 to 144; block numbers asked for two tiles ahead, before
+// loads that are not due yet, 165 to 148; exponents looked at byte by byte only where the type
+// does not hold them, and not from 128 on, 130 to 128 (heads of 64 89 to 82).  With two row
+// tiles every widened operand serves two products; they take half of the waves' registers
+// more, and a wave less a SIMD (heads of 64 keep 18 to 23 registers in scratch, of 256 50).
 template <int D, int QT>
 constexpr int Kv4FewWaves = QT == 1 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : (D == 64 ? 3 : D == 128 ? 2 : 1);  // per SIMD
 template <int D, bool F16, bool BIG, int QT>
@@ -655,16 +657,19 @@ __global__ __launch_bounds__(256, (Kv4FewWaves<D, QT>)) void k_kv4_attn(KvAttnAr
 // What bounds it: the exponentials, the sums and the widening on the vector unit (about
 // 1300 cycles per 32 rows and 64 tokens of 128 dims, the products 1024), LDS reads (half of
 // its rate) and the clock, 2.0 GHz under this load.  8192 tokens, 32 heads over 8 of 128:
-// 572 us, 0.96 Pflop/s (of 1.38 in a large product); 570 to 690 us by card.  Taken and not
+// 549 us, 1.0 Pflop/s (1.4 in a large product); 549 to 650 us by card and run.  Taken and not
 // taken, each pair on one card: 4 waves and two workgroups a CU (8 waves that multiply and
 // weight in turns: level, 476 us for 434 at heads of 192, and 58 for 43 where prompts are
 // short); a tile's scores formed while the one before is weighted: 660 for 628; waves
 // without rows that share the others' tokens: 640 for 575; codes asked for two tiles ahead:
 // level.
-// Heads of 64 have registers for a third wave a SIMD: 349 us, two 387.  At 192 and 256 the
-// scores of 64 tokens beside the sums pass 256 registers, so they are formed 32 at a time,
-// and 8 waves share a tile, the only workgroup of its CU: 431 and 773 us (16 heads over 8),
-// for 498 of 64 tokens at a time and 995 of 4 waves with twice the registers.
+// Heads of 64 have registers for a third wave a SIMD: 349 us, two 387 (334 now that V is in
+// fp16).  At 192 and 256 the scores of 64 tokens beside the sums pass 256 registers, so they
+// are formed 32 at a time, and 8 waves share a tile, the only workgroup of its CU: 431 and 773
+// us (16 heads over 8; now 440 and 781), for 498 of 64 tokens at a time and 995 of 4 waves with
+// twice the registers.  Heads of 256 still keep 83 to 96 registers in scratch, five of the
+// sixteen query fragments among them, which are read back for every 32 tokens; of 192 3 to 18, of
+// 64 5 to 32, few of them inside the loop.
 template <int D>
 struct Kv4PromptShape {
   static constexpr int NW = D >= 192 ? 8 : 4, WAVES = D == 64 ? 3 : 2;  // waves of a workgroup, per SIMD

@@ -506,10 +506,12 @@ __global__ __launch_bounds__((BM / WM) * (BN / 64) * 64) void k_mxfp4_tile(Mxfp4
 // CHAINED, where rows end with such a pair of slabs: a workgroup walks through several
 // tiles, and what is asked for behind a tile's end is the next one's first slabs, which land
 // while results are stored (4096 x 14336 x 4096: 140 us, a workgroup per tile 145).
-// The products bound it, and the clock that they leave: a slab's take 2900 cycles of 3020,
-// at 1.97 GHz for 2.36 with constant data.  4096 x 14336 x 4096 140 us, 3.4 Pflop/s; at K =
-// 8192 252 us, 3.8.  A tile costs 6 us beside its slabs' 1.8 each, and 896 tiles leave half
-// of the CUs idle in the last of four rounds.
+// 4096 x 14336 x 4096 140 us, 3.4 Pflop/s; at K = 8192 254 us, 3.8.  By counters the first
+// takes 298000 cycles (2.13 GHz; 2.4 without load), the matrix units busy for 115000 of them
+// (38%).  A slab takes 3570 (the difference of the two, over four rounds of tiles), 2048 of them
+// products: the rest is the one wave of a SIMD issuing reads and loads among them and waiting
+// at the barrier (26% of its cycles wait for data, 27% to issue).  A tile's start and end take
+// 17000 more, and 896 tiles leave half of the CUs idle in the last of four rounds.
 template <bool CHAINED>
 __global__ __launch_bounds__(256, 1) void k_mxfp4_wide(Mxfp4Gemm g, unsigned tiles) {
   constexpr int BM = 256, BN = 256, NT = 256, TI = 8, TJ = 8, SK = 128;

@@ -50,8 +50,10 @@ constexpr uint32_t kInfBits = 0x7F800000u;  // bits of |y| from here on: no fini
 
 // A team of TEAM lanes holds a row in registers from its one read to its codes, UPL units of
 // 8 elements a lane; the weights are read again for the codes, from cache.  The rows' bytes
-// bound it: 16384 x 4096 in bf16 with a residual to e4m3, 470 MB, 80 us, 5.85 TB/s; one such
-// row 3.5 us, the launch and two rounds of dependent loads.
+// bound it: 16384 x 4096 in bf16 with a residual to e4m3, 470 MB, 80 us, 5.85 TB/s; to MXFP4,
+// 439 MB, 72 us.  One such row takes 3.5 us: the launch and a chain of loads, each waited for
+// before the next is asked for: the row, its residual unit by unit, and behind each of the two
+// reductions the weights unit by unit (MXFP4 has one), though they do not depend on the row.
 template <class DT, class WT, int TEAM, int UPL>
 __global__ __launch_bounds__(kBlock) void k_rmsnorm(RmsNorm n) {
   __shared__ double sums[kBlock / 64];
