@@ -542,8 +542,8 @@ sparq24_status sparq24_kv_append_mxfp4(const sparq24_kvcache_mxfp4* cache,
  * element makes its row NaN; a score above fp32's range does, too, one below it
  * counts as hidden.
  * Arithmetic: K and queries enter the matrix units exactly in the queries' type, V
- * exactly in fp16; the weights exp(s_t) are rounded to fp16 (2^-11 of the weight), all
- * sums, maxima and scores are fp32.  With bf16 queries V and weights are bf16 (2^-8)
+ * exactly in fp16; the weights exp(s_t) are rounded to fp16 (2^-11 of the weight, or
+ * 2^-33 of the largest), all sums, maxima and scores are fp32.  With bf16 queries V and weights are bf16 (2^-8)
  * instead for rows of a sequence and head that meet, among up to 128 that go through
  * the cache together, a V scale outside 2^-23 .. 2^8 of a token that one of them sees
  * and whose codes there are not all zero; and with dim 256 for all rows of a sequence
