@@ -546,8 +546,7 @@ sparq24_status sparq24_kv_append_mxfp4(const sparq24_kvcache_mxfp4* cache,
  * 2^-33 of the largest), all sums, maxima and scores are fp32.  With bf16 queries V and weights are bf16 (2^-8)
  * instead for rows of a sequence and head that meet, among up to 128 that go through
  * the cache together, a V scale outside 2^-23 .. 2^8 of a token that one of them sees
- * and whose codes there are not all zero; and with dim 256 for all rows of a sequence
- * that has more than 16 (32, where that is the average) of them per kv head. */
+ * and whose codes there are not all zero. */
 sparq24_status sparq24_kv_attention_mxfp4(const sparq24_kvcache_mxfp4* cache,
                                           const sparq24_kvseqs* seqs, const sparq24_tensor* q,
                                           float scale, int32_t causal, int64_t window, void* out,

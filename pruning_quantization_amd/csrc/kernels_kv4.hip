@@ -199,8 +199,7 @@ __device__ inline uint32_t above(uint32_t w) {
 // exponent, the wave (the prompt kernel's workgroup) goes through all of its tiles again in
 // bf16, in a loop of its own.  (Both types in one loop: registers spilled at every use, decoding
 // 6 to 35% slower.  The second loop recomputes what it needs, so that the first keeps nothing
-// for it; heads of 256 in the prompt kernel have no registers for that all the same, 782 us
-// became 900 to 1060, so they stay in bf16.)
+// for it.  Prompts with heads of 256 pay for it all the same: 734 us, all in bf16 657.)
 __device__ inline uint32_t outside_fp16(uint32_t w) { return (w - 0x68686868u) & 0xE0E0E0E0u; }
 
 // Whether exponents w of four tokens leave fp16, but for those of tokens whose codes are zero
@@ -666,10 +665,10 @@ __global__ __launch_bounds__(256, (Kv4FewWaves<D, QT>)) void k_kv4_attn(KvAttnAr
 // Heads of 64 have registers for a third wave a SIMD: 349 us, two 387 (334 now that V is in
 // fp16).  At 192 and 256 the scores of 64 tokens beside the sums pass 256 registers, so they
 // are formed 32 at a time, and 8 waves share a tile, the only workgroup of its CU: 431 and 773
-// us (16 heads over 8; now 440 and 781), for 498 of 64 tokens at a time and 995 of 4 waves with
-// twice the registers.  Heads of 256 still keep 83 to 96 registers in scratch, five of the
-// sixteen query fragments among them, which are read back for every 32 tokens; of 192 3 to 18, of
-// 64 5 to 32, few of them inside the loop.
+// us (16 heads over 8; now 440 and 734), for 498 of 64 tokens at a time and 995 of 4 waves with
+// twice the registers.  Heads of 256 still keep 49 to 54 registers in scratch (bf16, over both
+// loops, 118 to 129), up to four of the sixteen query fragments among them, which are read back
+// for every 32 tokens; of 192 2 to 21, of 64 4 to 28, few of them inside the loop.
 template <int D>
 struct Kv4PromptShape {
   static constexpr int NW = D >= 192 ? 8 : 4, WAVES = D == 64 ? 3 : 2;  // waves of a workgroup, per SIMD
@@ -687,7 +686,6 @@ __device__ inline f32x16v kv4_mfma32(u32x4v a, u32x4v b, f32x16v c) {
 template <int D, bool F16, bool BIG>
 __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVES) void k_kv4_prompt(KvAttnArgs p) {
   using X = Kv4Type<F16>;
-  constexpr bool kV16 = F16 || D < 256;  // V in fp16 (outside_fp16)
   constexpr int NW = Kv4PromptShape<D>::NW, NJ = D / 16, NU = D / 32, G = D / 32;
   constexpr int WK = D / 32, NQ = (2 * WK + NW - 1) / NW;  // 64-unit loads of K (and of V), a wave's share
   constexpr int K_BYTES = kKvTile * D * 2, BUF = 2 * K_BYTES;
@@ -702,8 +700,18 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
   const int H = a.c.heads, tsh = a.c.tsh, T = 1 << tsh;
 
   const int w0 = it.rt * p.rb + 32 * wv;  // this wave's first row
+  // Query fragments in LDS, as many as it has room for, where the registers do not hold all:
+  // heads of 256 773 us (16 heads over 8, fp16), with two in LDS 675, with three 637.
+  constexpr int QL = D == 256 ? 3 : 0, NR = NJ - QL;
+  __shared__ u32x4v q_last[QL ? NW * QL * 64 : 1];
   u32x4v qf[NJ];
-  const Kv4Row row = kv4_query<F16, 2>(p, it, w0 + c32, qf, [&](int j) { return 16 * j + 8 * h; });
+  Kv4Row row;
+  auto query = [&] {
+    row = kv4_query<F16, 2>(p, it, w0 + c32, qf, [&](int j) { return 16 * j + 8 * h; });
+  };
+  query();
+#pragma unroll
+  for (int j = 0; j < QL; ++j) q_last[(wv * QL + j) * 64 + lane] = qf[NR + j];
   const float c = a.scale * 1.44269504088896340736f;
   float m = kNegInf, l = 0.0f;
   f32x16v o[NU];
@@ -883,7 +891,7 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
               // row 32 (M + mt) + c32, chunk 2 j + h
               const u32x4v kf =
                   *(const u32x4v*)(smem + ((buf + kat) ^ (32 * j & KX)) + (32 * j & ~KX) + (M + mt) * (64 * D));
-              sc[mt] = kv4_mfma32<F16>(kf, qf[j], sc[mt]);
+              sc[mt] = kv4_mfma32<F16>(kf, j < NR ? qf[j] : q_last[(wv * QL + j - NR) * 64 + lane], sc[mt]);
             }
           // slot (mt, i): token 32 (M + mt) + 8 (i / 4) + 4 h + i % 4
           if (!whole || bad || b0 + kKvTile > mine.least || b0 < mine.from) {
@@ -974,12 +982,13 @@ __global__ __launch_bounds__(64 * Kv4PromptShape<D>::NW, Kv4PromptShape<D>::WAVE
     }
   };
   if (rg.t0 < rg.t1) {
-    run.template operator()<kV16>();
-    if constexpr (kV16 && !F16) {
+    run.template operator()<true>();
+    if constexpr (!F16) {
       if (__builtin_expect(uniform((int)gone), 0)) {
         asm volatile("" : "+v"(tid));  // nothing of the first loop is kept for the second
         lane = tid & 63, c32 = lane & 31, h = lane >> 5;
         first_fragments();
+        if constexpr (D == 256) query();
         run.template operator()<false>();
       }
     }

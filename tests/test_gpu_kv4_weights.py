@@ -3,7 +3,7 @@
 They enter it in fp16 for queries of either type, so a weight is off by 2^-11 of itself,
 and below fp16's 2^-14, where the largest stands at 2^8 or more, by 2^-25: 2^-33 of the
 largest |V| a token.  With bf16 queries it is bf16, 2^-8, where a V scale of a seen token lies
-outside 2^-23 .. 2^8, and in the prompt kernel with heads of 256.  The other terms of a bound are those of test_gpu_kv4.py: with P =
+outside 2^-23 .. 2^8.  The other terms of a bound are those of test_gpu_kv4.py: with P =
 sum_t p_t |V_t| / sum_t p_t, a score's error twice (numerator and sum), the fp32 sums over
 the tokens, and half a step of the output."""
 import numpy as np
@@ -45,10 +45,6 @@ def check(p, n, group, dtype, weight, scale=None, lens=None, **kw):
     assert ok.all(), f"{(~ok).sum()} of {ok.size} outside; worst {np.nanmax(np.abs(got - out) / tol):.3g}"
 
 
-def fp16_weight(kernel, dim, dtype):
-    return 2.0 ** -8 if (kernel, dim, dtype) == ("prompt", 256, "bf16") else 2.0 ** -11
-
-
 def lengths(n):
     return [max(n, 2) + i for i in (0, 5, 62, 300, 1100)]
 
@@ -63,7 +59,7 @@ def test_weights_of_two_tokens_whose_values_cancel(dtype, kernel, dim, tokens):
     odd = (np.arange(tokens) % 2).reshape(1, 1, tokens, 1)
     p.ref = (p.ref[0], p.ref[1] - 3, np.broadcast_to(np.where(odd, 0xAA, 0x22), p.ref[2].shape).astype(np.uint8),
              np.full_like(p.ref[3], 127))
-    check(p, n, group, dtype, fp16_weight(kernel, dim, dtype), window=2)
+    check(p, n, group, dtype, 2.0 ** -11, window=2)
 
 
 @pytest.mark.parametrize("dim,tokens", [(64, 16), (128, 64), (192, 32), (256, 64)])
@@ -121,10 +117,10 @@ def test_scales_at_the_ends_of_fp16(dim, kernel):
         p = Pool(dim + n, lengths(n), 2, dim, 32)
         p.ref[3][:] = low
         p.ref[2][:] = p.rng.choice([0x11, 0x77, 0x17, 0x91, 0xF7], p.ref[2].shape)
-        check(p, n, group, "bf16", fp16_weight(kernel, dim, "bf16"))
+        check(p, n, group, "bf16", 2.0 ** -11)
         p = Pool(dim + n, lengths(n), 2, dim, 64)
         p.ref[3][:] = p.rng.integers(104, 136, p.ref[3].shape)
-        check(p, n, group, "bf16", fp16_weight(kernel, dim, "bf16"))
+        check(p, n, group, "bf16", 2.0 ** -11)
 
 
 @pytest.mark.parametrize("kernel", KERNELS)
