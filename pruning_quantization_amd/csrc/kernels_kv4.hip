@@ -199,7 +199,9 @@ __device__ inline uint32_t above(uint32_t w) {
 // exponent, the wave (the prompt kernel's workgroup) goes through all of its tiles again in
 // bf16, in a loop of its own.  (Both types in one loop: registers spilled at every use, decoding
 // 6 to 35% slower.  The second loop recomputes what it needs, so that the first keeps nothing
-// for it.  Prompts with heads of 256 pay for it all the same: 734 us, all in bf16 657.)
+// for it.  Prompts with heads of 256 pay for it all the same: 734 us, all in bf16 657.  Where every
+// tile has such exponents, 64 sequences of 300..16384 take 133 us for 128, but two row tiles a wave
+// and prompts, which do not end their first loop early, twice the time: 8192 tokens 1110 us.)
 __device__ inline uint32_t outside_fp16(uint32_t w) { return (w - 0x68686868u) & 0xE0E0E0E0u; }
 
 // Whether exponents w of four tokens leave fp16, but for those of tokens whose codes are zero
@@ -486,7 +488,10 @@ __global__ __launch_bounds__(256, (Kv4FewWaves<D, QT>)) void k_kv4_attn(KvAttnAr
               leaves |= leaves_fp16(vs[s][i], codes(4 * i), codes(4 * i + 1), codes(4 * i + 2), codes(4 * i + 3),
                                     lo - gp - 4 * i, hi - 1 - gp - 4 * i);
           }
-          gone |= __any(leaves);
+          if (__any(leaves)) {
+            gone = true;
+            if constexpr (QT == 1) return;  // (with two, at heads of 256, this took 151 us to 179)
+          }
         }
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
